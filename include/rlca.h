@@ -392,6 +392,200 @@ rlca_status rlca_ppo_clip_loss(const float *advantages, const double *stats,
                                double *loss, void *workspace, size_t workspace_bytes,
                                hipStream_t stream);
 
+/* ------------------------------------- operators of a recurrent policy or model
+ * The forward affine recurrence as the core of a sequence model: a short
+ * causal convolution and a selective state space scan over rows of T steps,
+ * each with its gradients and its form for single steps, and the clipping of
+ * the model's gradients by their global norm.
+ *
+ * Layout:   a row of T steps is contiguous in time, as everywhere in this
+ *           header: activations are [num_seqs, channels, T] with free strides
+ *           (in elements, not negative) between sequences and between
+ *           channels, so a channel range of a projection's output
+ *           [num_seqs, more channels, T] is read in place.  Outputs are
+ *           dense; so are states and parameters.  Arrays must be aligned to
+ *           their element size; speed, not results, depends on more.
+ * Types:    `dtype` (RLCA_F32, RLCA_BF16 or RLCA_F16) is the storage type of
+ *           the activations and of their gradients; arithmetic is fp32 and
+ *           each output is rounded once.  Parameters, their gradients and the
+ *           scan's states are float32 (a state is a running sum: rounding it
+ *           to 16 bits at every step would lose what slow decays remember).
+ *           The convolution's states are past inputs and have their type.
+ * Episodes: `flags` [num_seqs, T] (nullable) marks episode boundaries inside
+ *           the rows, under `convention` as for the forward scans above.  No
+ *           state and no tap reaches across a start, not even a NaN or
+ *           infinity; the state after the last step is 0 if that step's flag
+ *           ends an episode (RLCA_RESET_AFTER_DONE).
+ * Lengths:  `lengths` [num_seqs] int32 (nullable) gives each row's number of
+ *           steps, in 0..T (values outside are taken as the nearer end).
+ *           Steps past it change no state, get output and gradients 0, and
+ *           what the inputs hold there is not used.
+ * Sizes:    num_seqs * channels < 2^31 and T <= RLCA_MAX_T; a call with
+ *           num_seqs, channels or T of 0 is a valid no-op where it has no
+ *           state to hand on; with T = 0 the final state is the state, and
+ *           the gradients of an empty sum are 0.
+ * Errors and memory: as stated at the top.  Workspaces need no
+ *           initialisation, except rlca_clip_grad_norm's (as the fused
+ *           consumers': zero-filled before its first use, and left so). */
+
+/* The convolution:  pre_t = bias + sum_{k < width} weight[k] * x[t - (width-1) + k],
+ * out_t = silu(pre_t) = pre_t / (1 + exp(-pre_t)), or pre_t with silu == 0.
+ * Inputs before the row's first step are those of `state`, oldest first, or 0. */
+typedef struct {
+    int64_t num_seqs, channels, T;
+    int32_t width;      /* taps: 2, 3 or 4 */
+    int32_t silu;       /* nonzero: out = silu(pre) */
+    int32_t dtype;      /* of x, out, state, grad_* of them */
+    int32_t convention; /* rlca_reset_convention, for flags */
+    const void *x;      /* [num_seqs, channels, T] */
+    int64_t x_stride_seq, x_stride_channel;
+    const float *weight;    /* [channels, width] */
+    const float *bias;      /* [channels], nullable */
+    const void *state;      /* [num_seqs, channels, width-1], nullable (=> 0) */
+    const uint8_t *flags;   /* [num_seqs, T], nullable */
+    const int32_t *lengths; /* [num_seqs], nullable */
+    /* rlca_causal_conv */
+    void *out;         /* [num_seqs, channels, T] */
+    void *final_state; /* [num_seqs, channels, width-1], nullable: the state for the next row */
+    /* rlca_causal_conv_backward */
+    const void *grad_out; /* [num_seqs, channels, T] */
+    int64_t grad_stride_seq, grad_stride_channel;
+    const void *grad_final_state; /* [num_seqs, channels, width-1], nullable (=> 0) */
+    void *grad_x;                 /* [num_seqs, channels, T] */
+    float *grad_weight;           /* [channels, width] */
+    float *grad_bias;             /* [channels], nullable */
+    void *grad_state;             /* [num_seqs, channels, width-1], nullable */
+} rlca_conv_call;
+
+rlca_status rlca_causal_conv(const rlca_conv_call *call, hipStream_t stream);
+
+/* The gradients of the call whose inputs `call` holds: pre is computed again
+ * from x.  Sums over sequences and steps run in a fixed order (reproducible
+ * bit for bit).  The workspace holds each row's partial sums. */
+size_t rlca_causal_conv_backward_workspace_size(const rlca_conv_call *call);
+rlca_status rlca_causal_conv_backward(const rlca_conv_call *call, void *workspace,
+                                      size_t workspace_bytes, hipStream_t stream);
+
+/* The scan, for each channel d with `states` running values:
+ *   dt_t = softplus(delta_t + delta_bias), or delta_t + delta_bias with softplus == 0
+ *   h_t  = exp(dt_t A) h_{t-1} + dt_t u_t B_t        (h: [states]; h_{t-1} = 0 at a start)
+ *   y_t  = (sum_s C_t[s] h_t[s] + D u_t) * silu(z_t)   (the gate only where z is given)
+ * B and C are shared by the channels / groups consecutive channels of a group. */
+#define RLCA_MAX_STATES 128
+
+typedef struct {
+    int64_t num_seqs, channels, T;
+    int32_t states;   /* 1 .. RLCA_MAX_STATES */
+    int32_t groups;   /* divides channels */
+    int32_t softplus; /* nonzero: dt = softplus(...) */
+    int32_t dtype;    /* of u, delta, B, C, z, y and of their gradients */
+    int32_t convention;
+    const void *u, *delta; /* [num_seqs, channels, T] */
+    int64_t u_stride_seq, u_stride_channel, delta_stride_seq, delta_stride_channel;
+    const float *A;    /* [channels, states]; below 0 for a decaying state */
+    const void *B, *C; /* [num_seqs, groups, states, T] */
+    int64_t B_stride_seq, B_stride_group, B_stride_state;
+    int64_t C_stride_seq, C_stride_group, C_stride_state;
+    const float *D;          /* [channels], nullable (=> 0) */
+    const float *delta_bias; /* [channels], nullable (=> 0) */
+    const void *z;           /* [num_seqs, channels, T], nullable: no gate */
+    int64_t z_stride_seq, z_stride_channel;
+    const float *state;     /* [num_seqs, channels, states], nullable (=> 0) */
+    const uint8_t *flags;   /* [num_seqs, T], nullable */
+    const int32_t *lengths; /* [num_seqs], nullable */
+    /* rlca_selective_scan.  checkpoints (nullable) is what the backward call
+     * needs of the forward one: states at fixed steps, laid out for it. */
+    void *y;            /* [num_seqs, channels, T] */
+    float *final_state; /* [num_seqs, channels, states], nullable */
+    float *checkpoints; /* rlca_selective_scan_checkpoints_size bytes */
+    /* rlca_selective_scan_backward (reads checkpoints) */
+    const void *grad_y; /* [num_seqs, channels, T] */
+    int64_t grad_stride_seq, grad_stride_channel;
+    const float *grad_final_state; /* [num_seqs, channels, states], nullable (=> 0) */
+    void *grad_u, *grad_delta;     /* [num_seqs, channels, T] */
+    float *grad_A;                 /* [channels, states] */
+    void *grad_B, *grad_C;         /* [num_seqs, groups, states, T] */
+    float *grad_D, *grad_delta_bias; /* [channels], nullable */
+    void *grad_z;                    /* [num_seqs, channels, T]; required iff z */
+    float *grad_state;               /* [num_seqs, channels, states], nullable */
+} rlca_scan_call;
+
+size_t rlca_selective_scan_checkpoints_size(const rlca_scan_call *call);
+rlca_status rlca_selective_scan(const rlca_scan_call *call, hipStream_t stream);
+
+/* The gradients of the call whose inputs and checkpoints `call` holds.
+ * Nothing is accumulated into what the outputs held before, and all sums run
+ * in a fixed order (reproducible bit for bit).  Sums over the channels of a
+ * group, over sequences and over steps are float32 or wider. */
+size_t rlca_selective_scan_backward_workspace_size(const rlca_scan_call *call);
+rlca_status rlca_selective_scan_backward(const rlca_scan_call *call, void *workspace,
+                                         size_t workspace_bytes, hipStream_t stream);
+
+/* One step of the convolution and of the scan for each of `num_seqs`
+ * sequences (a generated token, an environment's next action).  Sequence n's
+ * state is place slots[n] of a pool of `places` states (slots == NULL: place
+ * n, and places >= num_seqs), read and rewritten in place.  A slot outside
+ * 0..places-1 is an empty seat of the batch: its output is 0 and no state is
+ * touched.  The slots of one call must differ (two sequences would race on
+ * one state).  starts [num_seqs] (nullable): nonzero begins an episode with
+ * this step, so the state is taken as 0. */
+typedef struct {
+    int64_t num_seqs, channels, places;
+    int32_t width, silu, dtype;
+    const void *x; /* [num_seqs, channels], rows x_stride_seq elements apart */
+    int64_t x_stride_seq;
+    const float *weight, *bias;
+    void *state;           /* [places, channels, width-1], in and out */
+    const int32_t *slots;  /* [num_seqs], nullable */
+    const uint8_t *starts; /* [num_seqs], nullable */
+    void *out;             /* [num_seqs, channels] */
+} rlca_conv_step_call;
+
+rlca_status rlca_causal_conv_step(const rlca_conv_step_call *call, hipStream_t stream);
+
+typedef struct {
+    int64_t num_seqs, channels, places;
+    int32_t states, groups, softplus, dtype;
+    const void *u, *delta; /* [num_seqs, channels] */
+    int64_t u_stride_seq, delta_stride_seq;
+    const float *A;
+    const void *B, *C; /* [num_seqs, groups, states] */
+    int64_t B_stride_seq, B_stride_group, C_stride_seq, C_stride_group;
+    const float *D, *delta_bias;
+    const void *z; /* [num_seqs, channels], nullable */
+    int64_t z_stride_seq;
+    float *state; /* [places, channels, states], in and out */
+    const int32_t *slots;
+    const uint8_t *starts;
+    void *y; /* [num_seqs, channels] */
+} rlca_scan_step_call;
+
+rlca_status rlca_selective_step(const rlca_scan_step_call *call, hipStream_t stream);
+
+/* The global norm of a model's gradients, and the gradients scaled to at most
+ * max_norm:
+ *   norm[0] = sqrt(sum over all tensors of x^2)      (double; squares and sums in fp64)
+ *   out = x * min(1, max_norm / (norm[0] + eps))
+ * (and out = x where the norm is 0).  out may be data itself (in place, the
+ * usual case) or another array that overlaps no array of the call.  With
+ * max_norm = +infinity only the norm is computed, and out is not used.  A NaN gradient makes the norm and every scaled value NaN, as the
+ * formula says; with an infinite one the scale is 0 and infinite values
+ * become NaN.  max_norm >= 0, eps >= 0 and finite.  `tensors` is host memory,
+ * read before the function returns; tensors of count 0 are skipped, and with
+ * nothing to sum the norm is 0.  The sums run in a fixed order: the norm is
+ * reproducible bit for bit. */
+typedef struct {
+    const void *data;
+    void *out;
+    int64_t count;
+    int32_t dtype;
+} rlca_grad_tensor;
+
+#define RLCA_CLIP_WORKSPACE_BYTES 20736
+rlca_status rlca_clip_grad_norm(const rlca_grad_tensor *tensors, int64_t num_tensors,
+                                double max_norm, double eps, double *norm, void *workspace,
+                                size_t workspace_bytes, hipStream_t stream);
+
 /* Static description of a status code (never NULL). */
 const char *rlca_status_string(rlca_status status);
 

@@ -5,6 +5,9 @@ discounted returns, V-Trace, Retrace(lambda), eligibility traces, episodic
 prefix sums), the generic affine scan over caller-built coefficients, batches
 of those calls, and the fused PPO consumers of the advantages (gae_stats,
 ppo_clip_loss), each HIP kernel launches behind the C ABI of include/rlca.h.
+For policies and models with a recurrent core: the short causal convolution and
+the selective state space scan over the same rows, with gradients and
+single-step forms, and gradient clipping by the global norm (sequence.py).
 Real-valued arrays may be float32, bfloat16 or float16 (fp32 arithmetic).
 PyTorch supplies device memory and the stream; the computation is entirely in
 librlca.so, which must be built (``python -m linear_recurrence_scan_row_amd.build``).
@@ -28,4 +31,15 @@ from .rlca import (  # noqa: F401
     retrace,
     td_lambda,
     vtrace,
+)
+from .sequence import (  # noqa: F401
+    ConvGrads,
+    ScanGrads,
+    causal_conv,
+    causal_conv_backward,
+    causal_conv_step,
+    clip_grad_norm,
+    selective_scan,
+    selective_scan_backward,
+    selective_step,
 )

@@ -1,0 +1,277 @@
+// grad_clip.hip -- the global norm of many gradient tensors, and the gradients
+// scaled to at most max_norm.
+//
+// Bound by memory: every element is read for the norm, and read and written
+// again for the scaling, which cannot begin before the last element was seen
+// (the second reading of up to 256 MB comes from the last-level cache).  The
+// tensors' addresses travel as kernel arguments, so nothing is copied to the
+// device; one launch takes up to kMaxTensors tensors as a list of chunks of
+// kChunk elements, so many small tensors fill the chip like one large one.
+#include <stdlib.h>
+
+#include <algorithm>
+
+#include "kernels.hpp"
+#include "seq.hpp"
+
+namespace rlca {
+namespace clip {
+
+constexpr int kThreads = 256;
+constexpr int kPerThread = 16;
+constexpr int kChunk = kThreads * kPerThread;
+constexpr int kMaxTensors = 96;  // 32 bytes each, of 4 KB kernel arguments
+constexpr uint32_t kClipGrid = 2048;
+
+// The workspace: ticket counters, one partial sum per workgroup, then the
+// running total of the launches before and the scale.
+struct Head {
+    double total;
+    double scale;
+};
+constexpr size_t kHeadAt = kTicketBytes + kClipGrid * sizeof(double);
+static_assert(kHeadAt + 128 == RLCA_CLIP_WORKSPACE_BYTES, "the header's workspace size");
+
+struct Tensor {
+    const void *data;
+    void *out;
+    uint64_t count;
+    uint32_t first_chunk;
+    int32_t dtype;
+};
+
+struct Launch {
+    Tensor tensors[kMaxTensors];
+    uint32_t num_tensors, chunks;
+    double *partials;
+    Head *head;
+    double *norm;
+    double max_norm, eps;
+    int32_t first, last;  // of the launches of one call
+};
+
+// The tensor that holds a chunk: the last one whose first chunk is not after it.
+__device__ __forceinline__ uint32_t tensor_of(const Launch &l, uint32_t chunk) {
+    uint32_t lo = 0, hi = l.num_tensors;
+    while (hi - lo > 1) {
+        const uint32_t mid = (lo + hi) / 2;
+        if (l.tensors[mid].first_chunk <= chunk)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    return lo;
+}
+
+// A thread's elements of a chunk: kBlocks blocks of 16 bytes, a workgroup's
+// next to each other.
+template <typename E>
+struct Blocks {
+    static constexpr int kElems = 16 / sizeof(E);
+    static constexpr int kBlocks = kPerThread / kElems;
+};
+
+template <typename E, typename F>
+__device__ __forceinline__ void for_blocks(const Tensor &t, uint32_t chunk, F f) {
+    constexpr int K = Blocks<E>::kElems, N = Blocks<E>::kBlocks;
+    const uint64_t begin = (uint64_t)chunk * kChunk;
+    const int64_t left = (int64_t)(t.count - begin);
+    float v[N][K];
+#pragma unroll
+    for (int b = 0; b < N; ++b) {
+        const int at = (b * kThreads + (int)threadIdx.x) * K;
+        const int64_t n = left - at;
+        seq::load_steps<K>(static_cast<const E *>(t.data) + begin + at, n < K ? (int)(n < 0 ? 0 : n) : K,
+                           v[b]);
+    }
+#pragma unroll
+    for (int b = 0; b < N; ++b) {
+        const int at = (b * kThreads + (int)threadIdx.x) * K;
+        const int64_t n = left - at;
+        f(v[b], begin + at, n < K ? (int)(n < 0 ? 0 : n) : K);
+    }
+}
+
+// Squares and sums in fp64: a float32 square overflows from 1.8e19 on and is
+// 0 below 1e-23, and fp64 sums of 10^9 terms keep ten digits.
+template <typename E>
+__device__ __forceinline__ double chunk_square_sum(const Tensor &t, uint32_t chunk) {
+    double sum = 0.0;
+    for_blocks<E>(t, chunk, [&](const float(&v)[Blocks<E>::kElems], uint64_t, int) {
+#pragma unroll
+        for (int k = 0; k < Blocks<E>::kElems; ++k) sum = fma((double)v[k], (double)v[k], sum);
+    });
+    return sum;
+}
+
+__global__ __launch_bounds__(kThreads) void grad_norm(Launch l) {
+    double sum = 0.0;
+    for (uint32_t c = blockIdx.x; c < l.chunks; c += gridDim.x) {
+        const Tensor &t = l.tensors[tensor_of(l, c)];
+        const uint32_t chunk = c - t.first_chunk;
+        sum += t.dtype == RLCA_F32    ? chunk_square_sum<float>(t, chunk)
+               : t.dtype == RLCA_BF16 ? chunk_square_sum<__bf16>(t, chunk)
+                                      : chunk_square_sum<_Float16>(t, chunk);
+    }
+    double unused = 0.0;
+    workgroup_sum2<kThreads / kWave>(sum, unused);
+    Head *head = l.head;
+    double *norm = l.norm;
+    const double max_norm = l.max_norm, eps = l.eps;
+    const bool first = l.first != 0, last = l.last != 0;
+    finish_in_last_workgroup<kThreads, 1>(l.partials, sum, 0.0, [=](double s, double) {
+        const double total = first ? s : load_coherent(&head->total) + s;
+        store_coherent(&head->total, total);
+        if (!last) return;
+        const double n = sqrt(total), scale = max_norm / (n + eps);
+        norm[0] = n;
+        // a NaN stays one
+        store_coherent(&head->scale, n == 0.0 || scale >= 1.0 ? 1.0 : scale);
+    });
+}
+
+template <typename E>
+__device__ __forceinline__ void scale_chunk(const Tensor &t, uint32_t chunk, float scale) {
+    for_blocks<E>(t, chunk, [&](float(&v)[Blocks<E>::kElems], uint64_t at, int n) {
+#pragma unroll
+        for (int k = 0; k < Blocks<E>::kElems; ++k) v[k] *= scale;
+        seq::store_steps<Blocks<E>::kElems>(static_cast<E *>(t.out) + at, n, v);
+    });
+}
+
+__global__ __launch_bounds__(kThreads) void grad_scale(Launch l) {
+    const float scale = (float)load_coherent(&l.head->scale);
+    for (uint32_t c = blockIdx.x; c < l.chunks; c += gridDim.x) {
+        const Tensor &t = l.tensors[tensor_of(l, c)];
+        if (scale == 1.f && t.out == t.data) continue;  // nothing changes
+        const uint32_t chunk = c - t.first_chunk;
+        if (t.dtype == RLCA_F32)
+            scale_chunk<float>(t, chunk, scale);
+        else if (t.dtype == RLCA_BF16)
+            scale_chunk<__bf16>(t, chunk, scale);
+        else
+            scale_chunk<_Float16>(t, chunk, scale);
+    }
+}
+
+// ------------------------------------------------------------------- host side
+struct Range {
+    uintptr_t begin, end;
+    bool written;
+};
+
+// No written range may overlap another range: one pass over them in order.
+static bool disjoint(Range *r, size_t n) {
+    std::sort(r, r + n, [](const Range &a, const Range &b) { return a.begin < b.begin; });
+    uintptr_t any = 0, written = 0;  // the ends of the ranges so far
+    for (size_t i = 0; i < n; ++i) {
+        if (r[i].begin < (r[i].written ? any : written)) return false;
+        any = std::max(any, r[i].end);
+        if (r[i].written) written = std::max(written, r[i].end);
+    }
+    return true;
+}
+
+static rlca_status check_tensors(const rlca_grad_tensor *tensors, int64_t n, bool scaled,
+                                 double *norm, void *workspace) {
+    constexpr int64_t kOnStack = 256;
+    Range local[2 * kOnStack + 2], *ranges = local;
+    if (n > kOnStack) {
+        ranges = static_cast<Range *>(malloc((2 * (size_t)n + 2) * sizeof(Range)));
+        if (ranges == nullptr) return RLCA_ERR_INVALID_SIZE;
+    }
+    size_t count = 0;
+    rlca_status st = RLCA_OK;
+    for (int64_t i = 0; i < n && st == RLCA_OK; ++i) {
+        const rlca_grad_tensor &t = tensors[i];
+        const size_t e = seq::element_bytes(t.dtype);
+        if (t.count < 0 || t.count >= (int64_t)1 << 43)
+            st = RLCA_ERR_INVALID_SIZE;
+        else if (e == 0)
+            st = RLCA_ERR_INVALID_VALUE;
+        else if (t.count == 0)
+            continue;
+        else if (t.data == nullptr || (scaled && t.out == nullptr))
+            st = RLCA_ERR_NULL_POINTER;
+        else if ((uintptr_t)t.data % e != 0 || (scaled && (uintptr_t)t.out % e != 0))
+            st = RLCA_ERR_MISALIGNED;
+        else {
+            const size_t bytes = (size_t)t.count * e;
+            const uintptr_t data = (uintptr_t)t.data, out = (uintptr_t)t.out;
+            ranges[count++] = {data, data + bytes, scaled && out == data};
+            if (scaled && out != data) ranges[count++] = {out, out + bytes, true};
+        }
+    }
+    if (st == RLCA_OK) {
+        ranges[count++] = {(uintptr_t)norm, (uintptr_t)norm + 8, true};
+        ranges[count++] = {(uintptr_t)workspace, (uintptr_t)workspace + RLCA_CLIP_WORKSPACE_BYTES,
+                           true};
+        if (!disjoint(ranges, count)) st = RLCA_ERR_ALIASING;
+    }
+    if (ranges != local) free(ranges);
+    return st;
+}
+
+// Fills `l` with tensors from *next on, up to a launch's worth of tensors and
+// chunks (a tensor has fewer than 2^43 elements, 2^31 chunks).
+static void fill(Launch *l, const rlca_grad_tensor *tensors, int64_t n, int64_t *next) {
+    l->num_tensors = 0;
+    uint64_t chunks = 0;
+    for (; *next < n && l->num_tensors < (uint32_t)kMaxTensors; ++*next) {
+        const rlca_grad_tensor &t = tensors[*next];
+        if (t.count == 0) continue;
+        const uint64_t c = ((uint64_t)t.count + kChunk - 1) / kChunk;
+        if (l->num_tensors != 0 && chunks + c > (1ull << 31)) break;
+        l->tensors[l->num_tensors++] = {t.data, t.out, (uint64_t)t.count, (uint32_t)chunks,
+                                        t.dtype};
+        chunks += c;
+    }
+    l->chunks = (uint32_t)chunks;
+}
+
+}  // namespace clip
+}  // namespace rlca
+
+using rlca::kTicketBytes;
+using namespace rlca::clip;
+
+extern "C" rlca_status rlca_clip_grad_norm(const rlca_grad_tensor *tensors, int64_t num_tensors,
+                                           double max_norm, double eps, double *norm,
+                                           void *workspace, size_t workspace_bytes,
+                                           hipStream_t stream) {
+    if (num_tensors < 0 || num_tensors > (1 << 24)) return RLCA_ERR_INVALID_SIZE;
+    if (!(max_norm >= 0.0) || !(eps >= 0.0 && isfinite(eps))) return RLCA_ERR_INVALID_VALUE;
+    if ((tensors == nullptr && num_tensors != 0) || norm == nullptr || workspace == nullptr)
+        return RLCA_ERR_NULL_POINTER;
+    if ((uintptr_t)norm % 8 != 0 || (uintptr_t)workspace % 8 != 0) return RLCA_ERR_MISALIGNED;
+    if (workspace_bytes < RLCA_CLIP_WORKSPACE_BYTES) return RLCA_ERR_INVALID_SIZE;
+    const bool scaled = !isinf(max_norm);
+    rlca_status st = check_tensors(tensors, num_tensors, scaled, norm, workspace);
+    if (st != RLCA_OK) return st;
+    char *ws = static_cast<char *>(workspace);
+    Launch l;
+    l.partials = reinterpret_cast<double *>(ws + kTicketBytes);
+    l.head = reinterpret_cast<Head *>(ws + kHeadAt);
+    l.norm = norm;
+    l.max_norm = max_norm;
+    l.eps = eps;
+    for (int pass = 0; pass < (scaled ? 2 : 1); ++pass) {
+        int64_t next = 0;
+        l.first = 1;
+        do {
+            fill(&l, tensors, num_tensors, &next);
+            int64_t rest = next;
+            while (rest < num_tensors && tensors[rest].count == 0) ++rest;
+            l.last = rest == num_tensors;
+            if (l.chunks != 0 || pass == 0) {
+                const uint32_t grid = l.chunks < 1 ? 1 : l.chunks < kClipGrid ? l.chunks : kClipGrid;
+                st = rlca::seq::launch(pass == 0 ? (const void *)grad_norm : (const void *)grad_scale,
+                                 dim3(grid), kThreads, 0, l, stream);
+                if (st != RLCA_OK) return st;
+            }
+            next = rest;
+            l.first = 0;
+        } while (next < num_tensors);
+    }
+    return RLCA_OK;
+}

@@ -1,0 +1,235 @@
+// seq_scan.hip -- the selective scan over rows of T steps, forward:
+//   h_t = exp(dt_t A) h_{t-1} + dt_t u_t B_t,   y_t = (C_t . h_t + D u_t) silu(z_t).
+// How a wave scans a state is told in seq_scan.hpp.
+//
+// Bound by the vector units: each (step, state) takes one exponential and the
+// products of the fold, of the second pass over the maps and of y, against
+// one or two stored values per step.  A workgroup's 16 channels share the
+// tile's B and C, staged in LDS in fp32 and read there 16 bytes a lane.
+#include "seq_scan.hpp"
+
+namespace rlca {
+namespace seq {
+
+template <typename E, bool FLAGS>
+__global__ __launch_bounds__(kScanThreads) void selective_scan(ScanParams p) {
+    extern __shared__ __attribute__((aligned(16))) char lds_bytes[];
+    __shared__ TileRow B_tile[kScanStates], C_tile[kScanStates];
+    const ScanLane l = scan_lane(p);
+    const int S = (int)p.states;
+    // [rows][S]: the states entering the tile, and A log2(e)
+    float *carry = reinterpret_cast<float *>(lds_bytes) + l.local * S;
+    float *A2 = reinterpret_cast<float *>(lds_bytes) + (kScanRows + l.local) * S;
+    for (int s = l.lane; s < S; s += kScanLanes) {
+        carry[s] = p.state == nullptr ? 0.f : p.state[(int64_t)l.row * S + s];
+        A2[s] = p.A[(int64_t)l.d * S + s] * kLog2e;
+    }
+    const int end = row_end(p.lengths, l.n, p.T);
+    const E *u_row = static_cast<const E *>(p.u) + l.n * p.u_n + l.d * p.u_d;
+    const E *delta_row = static_cast<const E *>(p.delta) + l.n * p.delta_n + l.d * p.delta_d;
+    const E *z_row =
+        p.z == nullptr ? nullptr : static_cast<const E *>(p.z) + l.n * p.z_n + l.d * p.z_d;
+    const E *B = static_cast<const E *>(p.B) + l.n * p.B_n + l.g * p.B_g;
+    const E *C = static_cast<const E *>(p.C) + l.n * p.C_n + l.g * p.C_g;
+    const uint8_t *flags = FLAGS ? p.flags + (int64_t)l.n * p.T : nullptr;
+    const float bias = p.delta_bias == nullptr ? 0.f : p.delta_bias[l.d];
+    const float skip = p.D == nullptr ? 0.f : p.D[l.d];
+    E *y_row = static_cast<E *>(p.y) + (int64_t)l.row * p.T;
+
+    for (int tile = 0; tile < p.tiles; ++tile) {
+        const int t0 = tile * kScanTile, t = t0 + l.lane * kScanK;
+        if (p.checkpoints != nullptr && l.live)
+            for (int s = l.lane; s < S; s += kScanLanes)
+                p.checkpoints[((int64_t)l.row * p.tiles + tile) * S + s] = carry[s];
+        float dt[kScanK], raw[kScanK], u[kScanK], cut[kScanK], y[kScanK];
+        load_inputs<E, FLAGS>(p, u_row, delta_row, flags, bias, t, end, end, dt, raw, u, cut);
+        float dtu[kScanK], dt_sum = 0.f;
+        bool starts = false;
+#pragma unroll
+        for (int k = 0; k < kScanK; ++k) {
+            dtu[k] = t + k < end ? dt[k] * u[k] : 0.f;
+            dt_sum += dt[k];
+            if constexpr (FLAGS) starts |= cut[k] != 0.f;
+            y[k] = skip * u[k];
+        }
+        for (int s0 = 0; s0 < S; s0 += kScanStates) {
+            const int count = S - s0 < kScanStates ? S - s0 : kScanStates;
+            __syncthreads();  // the tiles before are used up
+            stage_rows(B_tile, B, p.B_s, s0, count, t0, end);
+            stage_rows(C_tile, C, p.C_s, s0, count, t0, end);
+            __syncthreads();
+            for (int i = 0; i < count; ++i) {
+                const float a2 = A2[s0 + i], enter = carry[s0 + i];
+                float a[kScanK], b[kScanK], c[kScanK];
+                read_tile(B_tile[i], l.lane, b);
+                read_tile(C_tile[i], l.lane, c);
+                float h = 0.f;
+#pragma unroll
+                for (int k = 0; k < kScanK; ++k) {
+                    a[k] = decay<FLAGS>(dt[k], cut[k], a2);
+                    b[k] *= dtu[k];
+                    h = step_map<FLAGS>(a[k], b[k], h);
+                }
+                float prod = lane_product<FLAGS>(dt_sum, starts, a2);
+                row_scan<FLAGS, false>(prod, h);
+                const float after = step_map<FLAGS>(prod, h, enter);
+                if (l.lane == kScanLanes - 1) carry[s0 + i] = after;
+                h = row_shift<false>(after, enter);
+#pragma unroll
+                for (int k = 0; k < kScanK; ++k) {
+                    h = step_map<FLAGS>(a[k], b[k], h);
+                    y[k] = fmaf(c[k], h, y[k]);
+                }
+            }
+        }
+        wave_order();
+        if (l.live && t < p.T) {
+            if (z_row != nullptr) {
+                float z[kScanK];
+                load_steps<kScanK>(z_row + t, end - t, z);
+#pragma unroll
+                for (int k = 0; k < kScanK; ++k) y[k] *= silu(z[k]);
+            }
+#pragma unroll
+            for (int k = 0; k < kScanK; ++k) y[k] = t + k < end ? y[k] : 0.f;
+            store_steps<kScanK>(y_row + t, p.T - t, y);
+        }
+    }
+    if (p.final_state != nullptr && l.live) {
+        const bool over = FLAGS && p.after_done != 0 && end > 0 && flags[end - 1] != 0;
+        for (int s = l.lane; s < S; s += kScanLanes)
+            p.final_state[(int64_t)l.row * S + s] = over ? 0.f : carry[s];
+    }
+}
+
+// ------------------------------------------------------------------- host side
+ScanParams scan_params(const rlca_scan_call &c) {
+    ScanParams p = {};
+    p.u = c.u;
+    p.delta = c.delta;
+    p.B = c.B;
+    p.C = c.C;
+    p.z = c.z;
+    p.grad_y = c.grad_y;
+    p.A = c.A;
+    p.D = c.D;
+    p.delta_bias = c.delta_bias;
+    p.state = c.state;
+    p.grad_final = c.grad_final_state;
+    p.flags = c.flags;
+    p.lengths = c.lengths;
+    p.y = c.y;
+    p.final_state = c.final_state;
+    p.checkpoints = c.checkpoints;
+    p.grad_u = c.grad_u;
+    p.grad_delta = c.grad_delta;
+    p.grad_z = c.grad_z;
+    p.grad_state = c.grad_state;
+    p.u_n = c.u_stride_seq, p.u_d = c.u_stride_channel;
+    p.delta_n = c.delta_stride_seq, p.delta_d = c.delta_stride_channel;
+    p.z_n = c.z_stride_seq, p.z_d = c.z_stride_channel;
+    p.g_n = c.grad_stride_seq, p.g_d = c.grad_stride_channel;
+    p.B_n = c.B_stride_seq, p.B_g = c.B_stride_group, p.B_s = c.B_stride_state;
+    p.C_n = c.C_stride_seq, p.C_g = c.C_stride_group, p.C_s = c.C_stride_state;
+    p.num_seqs = (uint32_t)c.num_seqs;
+    p.channels = (uint32_t)c.channels;
+    p.groups = (uint32_t)c.groups;
+    p.per_group = p.channels / p.groups;
+    p.states = (uint32_t)c.states;
+    p.blocks_per_group = (p.per_group + kScanRows - 1) / kScanRows;
+    p.T = (int32_t)c.T;
+    p.tiles = (p.T + kScanTile - 1) / kScanTile;
+    p.softplus = c.softplus;
+    p.after_done = c.convention == RLCA_RESET_AFTER_DONE;
+    return p;
+}
+
+static int64_t checkpoint_values(const rlca_scan_call &c) {
+    return c.num_seqs * c.channels * ((c.T + kScanTile - 1) / kScanTile) * c.states;
+}
+
+rlca_status check_scan(const rlca_scan_call &c, bool backward, Arrays *a) {
+    const int64_t N = c.num_seqs, D = c.channels, T = c.T, S = c.states, G = c.groups;
+    if (!sizes_ok(N, D, T)) return RLCA_ERR_INVALID_SIZE;
+    const size_t e = element_bytes(c.dtype);
+    if (e == 0 || S < 1 || S > RLCA_MAX_STATES || G < 1 || D % G != 0 ||
+        (c.convention != RLCA_RESET_ON_START && c.convention != RLCA_RESET_AFTER_DONE))
+        return RLCA_ERR_INVALID_VALUE;
+    if (T != 0 && N * D > INT64_MAX / 8 / S / T) return RLCA_ERR_INVALID_SIZE;
+    // a launch holds less than 2^32 threads
+    const int64_t blocks = D == 0 ? 0 : N * G * ((D / G + kScanRows - 1) / kScanRows);
+    if (blocks >= ((int64_t)1 << 32) / kScanThreads) return RLCA_ERR_INVALID_SIZE;
+    const int64_t params = N == 0 ? 0 : D, rows = D == 0 ? 0 : N;
+    const Dim dense[] = {{N, D * T}, {D, T}, {T, 1}};
+    const Dim state[] = {{N * D, S}, {S, 1}};
+    const Dim b[] = {{rows, c.B_stride_seq}, {G, c.B_stride_group}, {S, c.B_stride_state}, {T, 1}};
+    const Dim cc[] = {{rows, c.C_stride_seq}, {G, c.C_stride_group}, {S, c.C_stride_state}, {T, 1}};
+    a->in(c.u, e, true, {{N, c.u_stride_seq}, {D, c.u_stride_channel}, {T, 1}});
+    a->in(c.delta, e, true, {{N, c.delta_stride_seq}, {D, c.delta_stride_channel}, {T, 1}});
+    a->in(c.z, e, false, {{N, c.z_stride_seq}, {D, c.z_stride_channel}, {T, 1}});
+    a->in(c.A, 4, true, {{params, S}, {S, 1}});
+    a->in(c.B, e, true, b);
+    a->in(c.C, e, true, cc);
+    a->in(c.D, 4, false, {{params, 1}});
+    a->in(c.delta_bias, 4, false, {{params, 1}});
+    a->in(c.flags, 1, false, {{N * T, 1}});
+    a->in(c.lengths, 4, false, {{N, 1}});
+    const Dim checkpoints[] = {{checkpoint_values(c), 1}};
+    if (!backward) {
+        a->in(c.state, 4, false, state);
+        a->out(c.y, e, true, dense);
+        a->out(c.final_state, 4, false, state);
+        a->out(c.checkpoints, 4, false, checkpoints);
+    } else {
+        a->in(c.checkpoints, 4, true, checkpoints);
+        a->in(c.grad_y, e, true, {{N, c.grad_stride_seq}, {D, c.grad_stride_channel}, {T, 1}});
+        a->in(c.grad_final_state, 4, false, state);
+        const Dim bc[] = {{rows * G * S, T}, {T, 1}};
+        a->out(c.grad_u, e, true, dense);
+        a->out(c.grad_delta, e, true, dense);
+        a->out(c.grad_A, 4, true, {{D, S}, {S, 1}});
+        a->out(c.grad_B, e, true, bc);
+        a->out(c.grad_C, e, true, bc);
+        a->out(c.grad_D, 4, false, {{D, 1}});
+        a->out(c.grad_delta_bias, 4, false, {{D, 1}});
+        if (c.z != nullptr) a->out(c.grad_z, e, true, dense);
+        a->out(c.grad_state, 4, false, state);
+    }
+    return RLCA_OK;
+}
+
+}  // namespace seq
+}  // namespace rlca
+
+using namespace rlca::seq;
+
+extern "C" {
+
+size_t rlca_selective_scan_checkpoints_size(const rlca_scan_call *call) {
+    Arrays a;
+    if (call == nullptr || check_scan(*call, false, &a) != RLCA_OK) return 0;
+    return (size_t)checkpoint_values(*call) * 4;
+}
+
+rlca_status rlca_selective_scan(const rlca_scan_call *call, hipStream_t stream) {
+    if (call == nullptr) return RLCA_ERR_NULL_POINTER;
+    const rlca_scan_call &c = *call;
+    Arrays a;
+    rlca_status st = check_scan(c, false, &a);
+    if (st == RLCA_OK) st = a.status();
+    if (st != RLCA_OK) return st;
+    if (c.num_seqs * c.channels == 0 || (c.T == 0 && c.final_state == nullptr)) return RLCA_OK;
+    ScanParams p = scan_params(c);
+    const bool flags = c.flags != nullptr;
+    const void *kernel =
+        c.dtype == RLCA_F32    ? (flags ? (const void *)selective_scan<float, true>
+                                        : (const void *)selective_scan<float, false>)
+        : c.dtype == RLCA_BF16 ? (flags ? (const void *)selective_scan<__bf16, true>
+                                        : (const void *)selective_scan<__bf16, false>)
+                               : (flags ? (const void *)selective_scan<_Float16, true>
+                                        : (const void *)selective_scan<_Float16, false>);
+    return launch(kernel, dim3(p.num_seqs * p.groups * p.blocks_per_group), kScanThreads,
+                  2 * kScanRows * p.states * 4, p, stream);
+}
+
+}  // extern "C"

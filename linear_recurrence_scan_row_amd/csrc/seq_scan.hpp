@@ -1,0 +1,196 @@
+// seq_scan.hpp -- the selective scan's shared parts: parameters, tiles and the
+// scan of one state's affine maps over the lanes of a row.
+//
+// For each channel and state,  h_t = a_t h_{t-1} + b_t  with a_t = exp(dt_t A)
+// and b_t = dt_t u_t B_t, is the forward affine recurrence of this library; a
+// wave scans it as the other kernels do.  A row of 16 lanes (one DPP row) owns
+// a channel and a tile of 128 steps, 8 consecutive steps a lane:
+//   * each lane folds its 8 maps serially into one; the product of its a's is
+//     exp(A sum dt), one exponential;
+//   * four DPP row shifts scan the 16 lane maps;
+//   * the tile's incoming state is a carry per (channel, state) kept in LDS;
+//   * each lane then applies its maps again from the state that enters it.
+// A wave holds 4 channels, so even one sequence of a thousand channels gives
+// every SIMD work, and a row of any length walks its tiles.
+#pragma once
+
+#include "seq.hpp"
+
+namespace rlca {
+namespace seq {
+
+constexpr int kScanK = 8;                        // steps of a lane
+constexpr int kScanLanes = 16;                   // lanes of a row
+constexpr int kScanTile = kScanK * kScanLanes;   // 128 steps
+constexpr int kScanWaves = 4;                    // waves of a workgroup
+constexpr int kScanThreads = kScanWaves * kWave;
+constexpr int kScanRows = kScanThreads / kScanLanes;  // channels of a workgroup
+constexpr int kScanStates = 8;  // states whose B and C are staged in LDS together
+
+struct ScanParams {
+    const void *u, *delta, *B, *C, *z, *grad_y;
+    const float *A, *D, *delta_bias;
+    const float *state, *grad_final;
+    const uint8_t *flags;
+    const int32_t *lengths;
+    void *y;
+    float *final_state;
+    float *checkpoints;  // [num_seqs * channels][tiles][states]: states entering each tile
+    void *grad_u, *grad_delta, *grad_z;
+    float *grad_state;
+    float *bc_partials;  // [num_seqs][groups][blocks of a group][2][states][tiles * kScanTile]
+    float *row_partials; // [num_seqs][channels][states + 2]: grad_A, grad_D, grad_delta_bias
+    int64_t u_n, u_d, delta_n, delta_d, z_n, z_d, g_n, g_d;
+    int64_t B_n, B_g, B_s, C_n, C_g, C_s;
+    uint32_t num_seqs, channels, groups, per_group, states;
+    uint32_t blocks_per_group;  // workgroups that share a group's channels
+    int32_t T, tiles;
+    int32_t softplus, after_done;
+};
+
+// Where a lane works: its sequence, group and channel (clamped to the group's
+// last one; `live` says whether it is the lane's own), and its lane in the row.
+struct ScanLane {
+    uint32_t n, g, block, d, row;
+    int lane, local;  // lane of the row; row of the workgroup
+    bool live;
+};
+
+__device__ __forceinline__ ScanLane scan_lane(const ScanParams &p) {
+    ScanLane l;
+    const uint32_t b = blockIdx.x;
+    const uint32_t ng = b / p.blocks_per_group;
+    l.block = b - ng * p.blocks_per_group;
+    l.n = ng / p.groups;
+    l.g = ng - l.n * p.groups;
+    l.lane = threadIdx.x & (kScanLanes - 1);
+    l.local = threadIdx.x / kScanLanes;
+    const uint32_t c = l.block * kScanRows + l.local;
+    l.live = c < p.per_group;
+    l.d = l.g * p.per_group + (l.live ? c : p.per_group - 1);
+    l.row = l.n * p.channels + l.d;
+    return l;
+}
+
+// One map: a later run's (a, h) after an earlier run's (pa, ph).  CUT: the
+// runs may hold episode starts, where a is 0 and whatever lies before, a NaN
+// or infinity too, must not pass (apply_map and compose of scan_core.hpp, with
+// the legacy multiply whose product with 0 is 0; a is never infinite there,
+// exp(dt A) <= 1 for A <= 0).  Without starts a plain fused step.
+template <bool CUT>
+__device__ __forceinline__ float step_map(float a, float b, float h) {
+    if constexpr (CUT) return b + rlca_fmul_legacy(a, h);
+    return fmaf(a, h, b);
+}
+
+template <bool CUT>
+__device__ __forceinline__ float product(float a, float b) {
+    if constexpr (CUT) return rlca_fmul_legacy(a, b);
+    return a * b;
+}
+
+// Inclusive scan of the row's 16 lane maps, towards higher lanes (row_shr) or,
+// REVERSE, towards lower ones (row_shl).  Lanes whose source lies outside the
+// row see the identity.
+template <bool CUT, bool REVERSE>
+__device__ __forceinline__ void row_scan(float &a, float &h) {
+    constexpr int kShift = REVERSE ? 0x100 : 0x110;
+    const auto step = [&](auto ctrl) {
+        constexpr int kCtrl = decltype(ctrl)::value;
+        const float ph = dpp_move<kCtrl, 0xf>(h, 0.f);
+        const float pa = dpp_move<kCtrl, 0xf>(a, 1.f);
+        h = step_map<CUT>(a, h, ph);
+        a = product<CUT>(a, pa);
+    };
+    step(std::integral_constant<int, kShift + 1>{});
+    step(std::integral_constant<int, kShift + 2>{});
+    step(std::integral_constant<int, kShift + 4>{});
+    step(std::integral_constant<int, kShift + 8>{});
+}
+
+// The neighbouring lane's value in scan order; the row's first lane gets `x0`.
+template <bool REVERSE>
+__device__ __forceinline__ float row_shift(float x, float x0) {
+    return dpp_move<(REVERSE ? 0x101 : 0x111), 0xf>(x, x0);
+}
+
+// Waves run their LDS accesses in order, so lanes of one wave hand values to
+// each other without a barrier; this keeps the compiler's order too.
+__device__ __forceinline__ void wave_order() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+}
+
+// A tile of one state's B or C in LDS, fp32: a lane's 8 steps as two blocks of
+// four, each lane's next to its neighbours', so that the 16-byte reads of 16
+// lanes cover all banks once.
+typedef float float4v __attribute__((ext_vector_type(4)));
+struct TileRow {
+    float4v half[2][kScanLanes];
+};
+
+__device__ __forceinline__ void read_tile(const TileRow &r, int lane, float (&v)[kScanK]) {
+    const float4v x = r.half[0][lane], y = r.half[1][lane];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = x[k], v[4 + k] = y[k];
+}
+
+// Stage `count` states' rows of B or C for one tile from state s0.
+template <typename E>
+__device__ __forceinline__ void stage_rows(TileRow *to, const E *from, int64_t stride, int s0,
+                                           int count, int t0, int end) {
+    for (int i = threadIdx.x; i < count * kScanLanes; i += kScanThreads) {
+        const int s = i / kScanLanes, lane = i % kScanLanes, t = t0 + lane * kScanK;
+        float v[kScanK];
+        load_steps<kScanK>(from + (s0 + s) * stride + t, end - t, v);
+        float4v x, y;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[k] = v[k], y[k] = v[4 + k];
+        to[s].half[0][lane] = x;
+        to[s].half[1][lane] = y;
+    }
+}
+
+// A lane's steps of one tile: dt and u (0 past `end`, where a step then
+// changes nothing) and, where episodes start within the row's steps, what
+// switches a_t to 0: cut is 0 or -infinity, added to a's exponent.
+template <typename E, bool FLAGS>
+__device__ __forceinline__ void load_inputs(const ScanParams &p, const E *u_row,
+                                            const E *delta_row, const uint8_t *flags, float bias,
+                                            int t, int end, int row_steps, float (&dt)[kScanK],
+                                            float (&raw)[kScanK], float (&u)[kScanK],
+                                            float (&cut)[kScanK]) {
+    load_steps<kScanK>(u_row + t, end - t, u);
+    load_steps<kScanK>(delta_row + t, end - t, raw);
+#pragma unroll
+    for (int k = 0; k < kScanK; ++k) {
+        raw[k] += bias;
+        const float x = p.softplus != 0 ? softplus(raw[k]) : raw[k];
+        dt[k] = t + k < end ? x : 0.f;
+    }
+    if constexpr (FLAGS) {
+        const uint32_t starts = start_bits<kScanK>(flags, t, p.T, p.after_done);
+#pragma unroll
+        for (int k = 0; k < kScanK; ++k)
+            cut[k] = t + k < row_steps && (starts >> k & 1) ? -INFINITY : 0.f;
+    }
+}
+
+// The product of a lane's a's for one state: exp(A sum dt), or 0 where an
+// episode starts in the lane, whatever the steps before the start hold.
+template <bool FLAGS>
+__device__ __forceinline__ float lane_product(float dt_sum, bool starts, float A2) {
+    const float a = exp2_fast(dt_sum * A2);
+    return FLAGS && starts ? 0.f : a;
+}
+
+// a_k of a lane's steps for one state, A2 = A log2(e).
+template <bool FLAGS>
+__device__ __forceinline__ float decay(float dt, float cut, float A2) {
+    return exp2_fast(FLAGS ? fmaf(dt, A2, cut) : dt * A2);
+}
+
+ScanParams scan_params(const rlca_scan_call &c);
+rlca_status check_scan(const rlca_scan_call &c, bool backward, Arrays *a);
+
+}  // namespace seq
+}  // namespace rlca

@@ -41,13 +41,12 @@ __global__ __launch_bounds__(kScanThreads) void selective_scan(ScanParams p) {
         if (p.checkpoints != nullptr && l.live)
             for (int s = l.lane; s < S; s += kScanLanes)
                 p.checkpoints[((int64_t)l.row * p.tiles + tile) * S + s] = carry[s];
-        float dt[kScanK], raw[kScanK], u[kScanK], cut[kScanK], y[kScanK];
-        load_inputs<E, FLAGS>(p, u_row, delta_row, flags, bias, t, end, end, dt, raw, u, cut);
-        float dtu[kScanK], dt_sum = 0.f;
+        float dt[kScanK], raw[kScanK], u[kScanK], dtu[kScanK], cut[kScanK], y[kScanK];
+        load_inputs<E, FLAGS>(p, u_row, delta_row, flags, bias, t, end, end, dt, raw, u, dtu, cut);
+        float dt_sum = 0.f;
         bool starts = false;
 #pragma unroll
         for (int k = 0; k < kScanK; ++k) {
-            dtu[k] = t + k < end ? dt[k] * u[k] : 0.f;
             dt_sum += dt[k];
             if constexpr (FLAGS) starts |= cut[k] != 0.f;
             y[k] = skip * u[k];

@@ -150,15 +150,16 @@ __device__ __forceinline__ void stage_rows(TileRow *to, const E *from, int64_t s
     }
 }
 
-// A lane's steps of one tile: dt and u (0 past `end`, where a step then
-// changes nothing) and, where episodes start within the row's steps, what
-// switches a_t to 0: cut is 0 or -infinity, added to a's exponent.
+// A lane's steps of one tile: dt, u and dt u (0 past `end`, where a step then
+// changes nothing; raw is dt before softplus).  Where an episode starts within
+// the row's steps a_t has to be 0 whatever the step's dt is, a NaN too: cut,
+// which is added to a's exponent, is -infinity there (else 0) and dt is 0.
 template <typename E, bool FLAGS>
 __device__ __forceinline__ void load_inputs(const ScanParams &p, const E *u_row,
                                             const E *delta_row, const uint8_t *flags, float bias,
                                             int t, int end, int row_steps, float (&dt)[kScanK],
                                             float (&raw)[kScanK], float (&u)[kScanK],
-                                            float (&cut)[kScanK]) {
+                                            float (&dtu)[kScanK], float (&cut)[kScanK]) {
     load_steps<kScanK>(u_row + t, end - t, u);
     load_steps<kScanK>(delta_row + t, end - t, raw);
 #pragma unroll
@@ -166,12 +167,16 @@ __device__ __forceinline__ void load_inputs(const ScanParams &p, const E *u_row,
         raw[k] += bias;
         const float x = p.softplus != 0 ? softplus(raw[k]) : raw[k];
         dt[k] = t + k < end ? x : 0.f;
+        dtu[k] = t + k < end ? x * u[k] : 0.f;
     }
     if constexpr (FLAGS) {
         const uint32_t starts = start_bits<kScanK>(flags, t, p.T, p.after_done);
 #pragma unroll
-        for (int k = 0; k < kScanK; ++k)
-            cut[k] = t + k < row_steps && (starts >> k & 1) ? -INFINITY : 0.f;
+        for (int k = 0; k < kScanK; ++k) {
+            const bool start = t + k < row_steps && (starts >> k & 1);
+            cut[k] = start ? -INFINITY : 0.f;
+            dt[k] = start ? 0.f : dt[k];
+        }
     }
 }
 

@@ -88,9 +88,9 @@ __global__ __launch_bounds__(kScanThreads) void selective_scan_backward(ScanPara
 
     for (int tile = p.tiles - 1; tile >= 0; --tile) {
         const int t0 = tile * kScanTile, t = t0 + l.lane * kScanK;
-        float dt[kScanK], raw[kScanK], u[kScanK], cut[kScanK], gy[kScanK], y[kScanK];
+        float dt[kScanK], raw[kScanK], u[kScanK], dtu[kScanK], cut[kScanK], gy[kScanK], y[kScanK];
         load_inputs<E, FLAGS>(p, u_row, delta_row, flags, bias, t, end, row_steps, dt, raw, u,
-                              cut);
+                              dtu, cut);
         load_steps<kScanK>(g_row + t, end - t, gy);
         if (z_row != nullptr) {
             float z[kScanK];
@@ -98,11 +98,10 @@ __global__ __launch_bounds__(kScanThreads) void selective_scan_backward(ScanPara
 #pragma unroll
             for (int k = 0; k < kScanK; ++k) gy[k] = t + k < end ? gy[k] * silu(z[k]) : 0.f;
         }
-        float dtu[kScanK], grad_dt[kScanK], gB[kScanK], dt_sum = 0.f;
+        float grad_dt[kScanK], gB[kScanK], dt_sum = 0.f;
         bool starts = false;
 #pragma unroll
         for (int k = 0; k < kScanK; ++k) {
-            dtu[k] = t + k < end ? dt[k] * u[k] : 0.f;
             dt_sum += dt[k];
             if constexpr (FLAGS) starts |= cut[k] != 0.f;
             y[k] = skip * u[k];
@@ -155,7 +154,7 @@ __global__ __launch_bounds__(kScanThreads) void selective_scan_backward(ScanPara
                     v[k] = g * dtu[k];
                     gB[k] = fmaf(g, b[k], gB[k]);
                     const float q = g * w[k];
-                    dA = fmaf(q, dt[k], dA);
+                    dA = fmaf(q, dt[k], dA);  // at a start w is 0, and dt put to 0
                     grad_dt[k] = fmaf(q, A_s, grad_dt[k]);
                 }
                 bc[wave][i][threadIdx.x & (kWave - 1)] = sum_rows(v);
@@ -190,7 +189,11 @@ __global__ __launch_bounds__(kScanThreads) void selective_scan_backward(ScanPara
 #pragma unroll
             for (int k = 0; k < kScanK; ++k) {
                 const bool in = t + k < end;
-                gu[k] = in ? fmaf(dt[k], gB[k], skip * gy[k]) : 0.f;
+                // an episode's first step has its dt put to 0 for a alone
+                const float step = !FLAGS || cut[k] == 0.f ? dt[k]
+                                   : p.softplus != 0       ? softplus(raw[k])
+                                                           : raw[k];
+                gu[k] = in ? fmaf(step, gB[k], skip * gy[k]) : 0.f;
                 float gd = fmaf(u[k], gB[k], grad_dt[k]);
                 if (p.softplus != 0) gd *= sigmoid(raw[k]);
                 grad_dt[k] = in ? gd : 0.f;

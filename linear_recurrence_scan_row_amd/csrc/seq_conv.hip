@@ -279,26 +279,41 @@ __global__ __launch_bounds__(kConvThreads) void causal_conv_backward(ConvParams 
         }
 }
 
-// One wave per channel adds its partials in fp64.
+// A workgroup per channel adds its partials in fp64, its waves' sums in order.
+constexpr int kSumThreads = 1024;
+
 template <int W>
-__global__ __launch_bounds__(kWave) void conv_weight_sums(const float *partials,
-                                                          uint64_t per_channel, uint32_t channels,
-                                                          float *grad_weight, float *grad_bias) {
+__global__ __launch_bounds__(kSumThreads) void conv_weight_sums(const float *partials,
+                                                                uint64_t per_channel,
+                                                                uint32_t channels,
+                                                                float *grad_weight,
+                                                                float *grad_bias) {
+    __shared__ double sums[kSumThreads / kWave][W + 1];
     for (uint32_t d = blockIdx.x; d < channels; d += gridDim.x) {
         const float *in = partials + d * per_channel * (W + 1);
         double s[W + 1] = {};
-        for (uint64_t i = threadIdx.x; i < per_channel; i += kWave)
+#pragma unroll 4
+        for (uint64_t i = threadIdx.x; i < per_channel; i += blockDim.x)
 #pragma unroll
             for (int j = 0; j <= W; ++j) s[j] += (double)in[i * (W + 1) + j];
 #pragma unroll
         for (int m = 1; m < kWave; m <<= 1)
 #pragma unroll
             for (int j = 0; j <= W; ++j) s[j] += __shfl_xor(s[j], m);
-        if (threadIdx.x == 0) {
+        if (threadIdx.x % kWave == 0)
 #pragma unroll
-            for (int j = 0; j < W; ++j) grad_weight[(int64_t)d * W + j] = (float)s[j];
-            if (grad_bias != nullptr) grad_bias[d] = (float)s[W];
+            for (int j = 0; j <= W; ++j) sums[threadIdx.x / kWave][j] = s[j];
+        __syncthreads();
+        const uint32_t j = threadIdx.x;
+        if (j <= W) {
+            double total = 0.0;
+            for (uint32_t w = 0; w < blockDim.x / kWave; ++w) total += sums[w][j];
+            if (j < W)
+                grad_weight[(int64_t)d * W + j] = (float)total;
+            else if (grad_bias != nullptr)
+                grad_bias[d] = (float)total;
         }
+        __syncthreads();
     }
 }
 
@@ -468,9 +483,10 @@ rlca_status rlca_causal_conv_backward(const rlca_conv_call *call, void *workspac
     const void *kernel = call->width == 2   ? (const void *)conv_weight_sums<2>
                          : call->width == 3 ? (const void *)conv_weight_sums<3>
                                             : (const void *)conv_weight_sums<4>;
-    const hipError_t e =
-        hipLaunchKernel(kernel, dim3(channels < (1u << 20) ? channels : 1u << 20), dim3(rlca::kWave),
-                        args, 0, stream);
+    uint32_t threads = rlca::kWave;
+    while (threads < (uint32_t)kSumThreads && threads < per_channel) threads *= 2;
+    const hipError_t e = hipLaunchKernel(
+        kernel, dim3(channels < (1u << 20) ? channels : 1u << 20), dim3(threads), args, 0, stream);
     return e == hipSuccess ? RLCA_OK : RLCA_ERR_HIP;
 }
 

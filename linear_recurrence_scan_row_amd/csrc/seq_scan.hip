@@ -16,13 +16,13 @@ __global__ __launch_bounds__(kScanThreads) void selective_scan(ScanParams p) {
     extern __shared__ __attribute__((aligned(16))) char lds_bytes[];
     __shared__ TileRow B_tile[kScanStates], C_tile[kScanStates];
     const ScanLane l = scan_lane(p);
-    const int S = (int)p.states;
-    // [rows][S]: the states entering the tile, and A log2(e)
-    float *carry = reinterpret_cast<float *>(lds_bytes) + l.local * S;
-    float *A2 = reinterpret_cast<float *>(lds_bytes) + (kScanRows + l.local) * S;
-    for (int s = l.lane; s < S; s += kScanLanes) {
-        carry[s] = p.state == nullptr ? 0.f : p.state[(int64_t)l.row * S + s];
-        A2[s] = p.A[(int64_t)l.d * S + s] * kLog2e;
+    const int S = (int)p.states, padded = padded_states(S);
+    // [rows][padded]: the states entering the tile, and A log2(e)
+    float *carry = reinterpret_cast<float *>(lds_bytes) + l.local * padded;
+    float *A2 = carry + kScanRows * padded;
+    for (int s = l.lane; s < padded; s += kScanLanes) {
+        carry[s] = p.state == nullptr || s >= S ? 0.f : p.state[(int64_t)l.row * S + s];
+        A2[s] = s >= S ? 0.f : p.A[(int64_t)l.d * S + s] * kLog2e;
     }
     const int end = row_end(p.lengths, l.n, p.T);
     const E *u_row = static_cast<const E *>(p.u) + l.n * p.u_n + l.d * p.u_d;
@@ -54,30 +54,37 @@ __global__ __launch_bounds__(kScanThreads) void selective_scan(ScanParams p) {
         for (int s0 = 0; s0 < S; s0 += kScanStates) {
             const int count = S - s0 < kScanStates ? S - s0 : kScanStates;
             __syncthreads();  // the tiles before are used up
-            stage_rows(B_tile, B, p.B_s, s0, count, t0, end);
-            stage_rows(C_tile, C, p.C_s, s0, count, t0, end);
+            stage_rows(B_tile, B, p.B_s, s0, S, t0, end);
+            stage_rows(C_tile, C, p.C_s, s0, S, t0, end);
             __syncthreads();
-            for (int i = 0; i < count; ++i) {
-                const float a2 = A2[s0 + i], enter = carry[s0 + i];
-                float a[kScanK], b[kScanK], c[kScanK];
-                read_tile(B_tile[i], l.lane, b);
-                read_tile(C_tile[i], l.lane, c);
-                float h = 0.f;
+            for (int i = 0; i < count; i += 2) {
+                float a[2][kScanK], b[2][kScanK], h[2], prod[2], enter[2];
 #pragma unroll
-                for (int k = 0; k < kScanK; ++k) {
-                    a[k] = decay<FLAGS>(dt[k], cut[k], a2);
-                    b[k] *= dtu[k];
-                    h = step_map<FLAGS>(a[k], b[k], h);
+                for (int j = 0; j < 2; ++j) {
+                    const float a2 = A2[s0 + i + j];
+                    enter[j] = carry[s0 + i + j];
+                    read_tile(B_tile[i + j], l.lane, b[j]);
+#pragma unroll
+                    for (int k = 0; k < kScanK; ++k) {
+                        a[j][k] = decay<FLAGS>(dt[k], cut[k], a2);
+                        b[j][k] *= dtu[k];
+                        h[j] = k == 0 ? b[j][0] : step_map<FLAGS>(a[j][k], b[j][k], h[j]);
+                    }
+                    prod[j] = lane_product<FLAGS>(dt_sum, starts, a2);
                 }
-                float prod = lane_product<FLAGS>(dt_sum, starts, a2);
                 row_scan<FLAGS, false>(prod, h);
-                const float after = step_map<FLAGS>(prod, h, enter);
-                if (l.lane == kScanLanes - 1) carry[s0 + i] = after;
-                h = row_shift<false>(after, enter);
 #pragma unroll
-                for (int k = 0; k < kScanK; ++k) {
-                    h = step_map<FLAGS>(a[k], b[k], h);
-                    y[k] = fmaf(c[k], h, y[k]);
+                for (int j = 0; j < 2; ++j) {
+                    const float after = step_map<FLAGS>(prod[j], h[j], enter[j]);
+                    carry[s0 + i + j] = row_last<false>(after);
+                    h[j] = row_shift<false>(after, enter[j]);
+                    float c[kScanK];
+                    read_tile(C_tile[i + j], l.lane, c);
+#pragma unroll
+                    for (int k = 0; k < kScanK; ++k) {
+                        h[j] = step_map<FLAGS>(a[j][k], b[j][k], h[j]);
+                        y[k] = fmaf(c[k], h[j], y[k]);
+                    }
                 }
             }
         }
@@ -228,7 +235,7 @@ rlca_status rlca_selective_scan(const rlca_scan_call *call, hipStream_t stream) 
                                : (flags ? (const void *)selective_scan<_Float16, true>
                                         : (const void *)selective_scan<_Float16, false>);
     return launch(kernel, dim3(p.num_seqs * p.groups * p.blocks_per_group), kScanThreads,
-                  2 * kScanRows * p.states * 4, p, stream);
+                  2 * kScanRows * padded_states(c.states) * 4, p, stream);
 }
 
 }  // extern "C"

@@ -27,6 +27,10 @@ constexpr int kScanThreads = kScanWaves * kWave;
 constexpr int kScanRows = kScanThreads / kScanLanes;  // channels of a workgroup
 constexpr int kScanStates = 8;  // states whose B and C are staged in LDS together
 
+// States of a workgroup's LDS arrays: whole pairs, since the kernels take two
+// states at a time.
+__host__ __device__ constexpr int padded_states(int S) { return (S + 1) & ~1; }
+
 struct ScanParams {
     const void *u, *delta, *B, *C, *z, *grad_y;
     const float *A, *D, *delta_bias;
@@ -89,29 +93,61 @@ __device__ __forceinline__ float product(float a, float b) {
     return a * b;
 }
 
-// Inclusive scan of the row's 16 lane maps, towards higher lanes (row_shr) or,
-// REVERSE, towards lower ones (row_shl).  Lanes whose source lies outside the
-// row see the identity.
+// Inclusive scan of the row's 16 lane maps of two states, towards higher lanes
+// (row_shr) or, REVERSE, towards lower ones (row_shl).  Lanes whose source
+// lies outside the row keep their map.
+//
+// Without cuts a step is two instructions a state, an FMA and a product that
+// fetch their operand from the other lane themselves; the compiler would move
+// it to a register first, and fill that register before (8 instructions).  The
+// two states take turns, so that two instructions always lie between a write
+// and the lane-crossing read of it, as the hardware requires.
 template <bool CUT, bool REVERSE>
-__device__ __forceinline__ void row_scan(float &a, float &h) {
-    constexpr int kShift = REVERSE ? 0x100 : 0x110;
-    const auto step = [&](auto ctrl) {
-        constexpr int kCtrl = decltype(ctrl)::value;
-        const float ph = dpp_move<kCtrl, 0xf>(h, 0.f);
-        const float pa = dpp_move<kCtrl, 0xf>(a, 1.f);
-        h = step_map<CUT>(a, h, ph);
-        a = product<CUT>(a, pa);
-    };
-    step(std::integral_constant<int, kShift + 1>{});
-    step(std::integral_constant<int, kShift + 2>{});
-    step(std::integral_constant<int, kShift + 4>{});
-    step(std::integral_constant<int, kShift + 8>{});
+__device__ __forceinline__ void row_scan(float (&a)[2], float (&h)[2]) {
+    if constexpr (CUT) {
+        constexpr int kShift = REVERSE ? 0x100 : 0x110;
+        const auto step = [&](auto ctrl) {
+            constexpr int kCtrl = decltype(ctrl)::value;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const float ph = dpp_move<kCtrl, 0xf>(h[j], 0.f);
+                const float pa = dpp_move<kCtrl, 0xf>(a[j], 1.f);
+                h[j] = step_map<CUT>(a[j], h[j], ph);
+                a[j] = product<CUT>(a[j], pa);
+            }
+        };
+        step(std::integral_constant<int, kShift + 1>{});
+        step(std::integral_constant<int, kShift + 2>{});
+        step(std::integral_constant<int, kShift + 4>{});
+        step(std::integral_constant<int, kShift + 8>{});
+    } else {
+#define RLCA_STEP(SHIFT)                                                   \
+    "v_fmac_f32_dpp %1, %1, %0 " SHIFT " row_mask:0xf bank_mask:0xf\n\t"   \
+    "v_fmac_f32_dpp %3, %3, %2 " SHIFT " row_mask:0xf bank_mask:0xf\n\t"   \
+    "v_mul_f32_dpp %0, %0, %0 " SHIFT " row_mask:0xf bank_mask:0xf\n\t"    \
+    "v_mul_f32_dpp %2, %2, %2 " SHIFT " row_mask:0xf bank_mask:0xf\n\t"
+        if constexpr (REVERSE)
+            asm("s_nop 1\n\t" RLCA_STEP("row_shl:1") RLCA_STEP("row_shl:2")
+                    RLCA_STEP("row_shl:4") RLCA_STEP("row_shl:8")
+                : "+v"(a[0]), "+v"(h[0]), "+v"(a[1]), "+v"(h[1]));
+        else
+            asm("s_nop 1\n\t" RLCA_STEP("row_shr:1") RLCA_STEP("row_shr:2")
+                    RLCA_STEP("row_shr:4") RLCA_STEP("row_shr:8")
+                : "+v"(a[0]), "+v"(h[0]), "+v"(a[1]), "+v"(h[1]));
+#undef RLCA_STEP
+    }
 }
 
 // The neighbouring lane's value in scan order; the row's first lane gets `x0`.
 template <bool REVERSE>
 __device__ __forceinline__ float row_shift(float x, float x0) {
     return dpp_move<(REVERSE ? 0x101 : 0x111), 0xf>(x, x0);
+}
+
+// The value of the row's last lane in scan order, in all its lanes.
+template <bool REVERSE>
+__device__ __forceinline__ float row_last(float x) {
+    return dpp_move<(REVERSE ? 0x150 : 0x15f), 0xf>(x, x);
 }
 
 // Waves run their LDS accesses in order, so lanes of one wave hand values to
@@ -134,14 +170,15 @@ __device__ __forceinline__ void read_tile(const TileRow &r, int lane, float (&v)
     for (int k = 0; k < 4; ++k) v[k] = x[k], v[4 + k] = y[k];
 }
 
-// Stage `count` states' rows of B or C for one tile from state s0.
+// Stage kScanStates states' rows of B or C for one tile from state s0, as zeros
+// past the last of S states.
 template <typename E>
 __device__ __forceinline__ void stage_rows(TileRow *to, const E *from, int64_t stride, int s0,
-                                           int count, int t0, int end) {
-    for (int i = threadIdx.x; i < count * kScanLanes; i += kScanThreads) {
+                                           int S, int t0, int end) {
+    for (int i = threadIdx.x; i < kScanStates * kScanLanes; i += kScanThreads) {
         const int s = i / kScanLanes, lane = i % kScanLanes, t = t0 + lane * kScanK;
         float v[kScanK];
-        load_steps<kScanK>(from + (s0 + s) * stride + t, end - t, v);
+        load_steps<kScanK>(from + (s0 + s) * stride + t, s0 + s < S ? end - t : 0, v);
         float4v x, y;
 #pragma unroll
         for (int k = 0; k < 4; ++k) x[k] = v[k], y[k] = v[4 + k];

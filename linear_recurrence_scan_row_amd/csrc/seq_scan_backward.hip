@@ -40,13 +40,18 @@ __device__ __forceinline__ float4v sum_rows(float (&v)[16]) {
     return r;
 }
 
-// Sum over a row's 16 lanes, complete in lane 15.
-__device__ __forceinline__ float row_sum(float x) {
-    x += dpp_move<0x111, 0xf>(x, 0.f);
-    x += dpp_move<0x112, 0xf>(x, 0.f);
-    x += dpp_move<0x114, 0xf>(x, 0.f);
-    x += dpp_move<0x118, 0xf>(x, 0.f);
-    return x;
+// Sums over a row's 16 lanes of two values, complete in lane 15.
+__device__ __forceinline__ void row_sum(float (&x)[2]) {
+    // the two take turns, and one idle instruction keeps the required two
+    // between a write and the lane-crossing read of it
+#define RLCA_STEP(SHIFT)                                                  \
+    "v_add_f32_dpp %0, %0, %0 " SHIFT " row_mask:0xf bank_mask:0xf\n\t"   \
+    "v_add_f32_dpp %1, %1, %1 " SHIFT " row_mask:0xf bank_mask:0xf\n\t"   \
+    "s_nop 0\n\t"
+    asm("s_nop 1\n\t" RLCA_STEP("row_shr:1") RLCA_STEP("row_shr:2") RLCA_STEP("row_shr:4")
+            RLCA_STEP("row_shr:8")
+        : "+v"(x[0]), "+v"(x[1]));
+#undef RLCA_STEP
 }
 
 template <typename E, bool FLAGS>
@@ -55,19 +60,19 @@ __global__ __launch_bounds__(kScanThreads) void selective_scan_backward(ScanPara
     __shared__ TileRow B_tile[kScanStates], C_tile[kScanStates];
     __shared__ float4v bc[kScanWaves][kScanStates][kWave];
     const ScanLane l = scan_lane(p);
-    const int S = (int)p.states;
-    // [rows][S]: A, the gradient a_t g_t entering the tile from its right, and
+    const int S = (int)p.states, padded = padded_states(S);
+    // [rows][padded]: A, the gradient a_t g_t entering the tile from its right, and
     // the sums of grad_A
-    float *A = reinterpret_cast<float *>(lds_bytes) + l.local * S;
-    float *carry = A + kScanRows * S;
-    float *grad_A = carry + kScanRows * S;
+    float *A = reinterpret_cast<float *>(lds_bytes) + l.local * padded;
+    float *carry = A + kScanRows * padded;
+    float *grad_A = carry + kScanRows * padded;
     const int row_steps = row_end(p.lengths, l.n, p.T);
     const int end = l.live ? row_steps : 0;  // a clamped row computes on zeros
     const uint8_t *flags = FLAGS ? p.flags + (int64_t)l.n * p.T : nullptr;
     const bool over = FLAGS && p.after_done != 0 && end > 0 && flags[end - 1] != 0;
-    for (int s = l.lane; s < S; s += kScanLanes) {
-        A[s] = p.A[(int64_t)l.d * S + s];
-        carry[s] = p.grad_final == nullptr || over || !l.live
+    for (int s = l.lane; s < padded; s += kScanLanes) {
+        A[s] = s >= S ? 0.f : p.A[(int64_t)l.d * S + s];
+        carry[s] = p.grad_final == nullptr || over || !l.live || s >= S
                        ? 0.f
                        : p.grad_final[(int64_t)l.row * S + s];
         grad_A[s] = 0.f;
@@ -111,55 +116,74 @@ __global__ __launch_bounds__(kScanThreads) void selective_scan_backward(ScanPara
         for (int s0 = 0; s0 < S; s0 += kScanStates) {
             const int count = S - s0 < kScanStates ? S - s0 : kScanStates;
             __syncthreads();  // the tiles and sums before are used up
-            stage_rows(B_tile, B, p.B_s, s0, count, t0, row_steps);
-            stage_rows(C_tile, C, p.C_s, s0, count, t0, row_steps);
+            stage_rows(B_tile, B, p.B_s, s0, S, t0, row_steps);
+            stage_rows(C_tile, C, p.C_s, s0, S, t0, row_steps);
             __syncthreads();
-            for (int i = 0; i < count; ++i) {
-                const float A_s = A[s0 + i], a2 = A_s * kLog2e;
-                const float enter = l.live ? enter_row[s0 + i] : 0.f;
-                float a[kScanK], b[kScanK], c[kScanK], w[kScanK], v[16];
-                read_tile(B_tile[i], l.lane, b);
-                read_tile(C_tile[i], l.lane, c);
-                float h = 0.f;
+            for (int i = 0; i < count; i += 2) {
+                float a[2][kScanK], w[2][kScanK], g[2], prod[2], dA[2];
+                float h[2], prefix[2], enter[2];
 #pragma unroll
-                for (int k = 0; k < kScanK; ++k) {
-                    a[k] = decay<FLAGS>(dt[k], cut[k], a2);
-                    h = step_map<FLAGS>(a[k], b[k] * dtu[k], h);
+                for (int j = 0; j < 2; ++j) {
+                    const float a2 = A[s0 + i + j] * kLog2e;
+                    enter[j] = l.live && s0 + i + j < S ? enter_row[s0 + i + j] : 0.f;
+                    float b[kScanK];
+                    read_tile(B_tile[i + j], l.lane, b);
+#pragma unroll
+                    for (int k = 0; k < kScanK; ++k) {
+                        a[j][k] = decay<FLAGS>(dt[k], cut[k], a2);
+                        const float x = b[k] * dtu[k];
+                        h[j] = k == 0 ? x : step_map<FLAGS>(a[j][k], x, h[j]);
+                    }
+                    prefix[j] = prod[j] = lane_product<FLAGS>(dt_sum, starts, a2);
                 }
-                const float prod = lane_product<FLAGS>(dt_sum, starts, a2);
-                float prefix = prod;
                 row_scan<FLAGS, false>(prefix, h);
-                h = row_shift<false>(step_map<FLAGS>(prefix, h, enter), enter);
+                float v[2][16], r[2], c[2][kScanK];
 #pragma unroll
-                for (int k = 0; k < kScanK; ++k) {
-                    w[k] = product<FLAGS>(a[k], h);
-                    h = fmaf(b[k], dtu[k], w[k]);
-                    v[8 + k] = gy[k] * h;
-                    y[k] = fmaf(c[k], h, y[k]);
-                    c[k] *= gy[k];  // what y's gradient adds to g
+                for (int j = 0; j < 2; ++j) {
+                    h[j] = row_shift<false>(step_map<FLAGS>(prefix[j], h[j], enter[j]), enter[j]);
+                    float b[kScanK];
+                    read_tile(B_tile[i + j], l.lane, b);
+                    read_tile(C_tile[i + j], l.lane, c[j]);
+#pragma unroll
+                    for (int k = 0; k < kScanK; ++k) {
+                        w[j][k] = product<FLAGS>(a[j][k], h[j]);
+                        h[j] = fmaf(b[k], dtu[k], w[j][k]);
+                        v[j][8 + k] = gy[k] * h[j];
+                        y[k] = fmaf(c[j][k], h[j], y[k]);
+                        c[j][k] *= gy[k];  // what y's gradient adds to g
+                    }
+                    g[j] = c[j][kScanK - 1];
+#pragma unroll
+                    for (int k = kScanK - 2; k >= 0; --k)
+                        g[j] = step_map<FLAGS>(a[j][k + 1], c[j][k], g[j]);
+                    r[j] = product<FLAGS>(a[j][0], g[j]);
                 }
-                float g = c[kScanK - 1];
+                row_scan<FLAGS, true>(prod, r);
 #pragma unroll
-                for (int k = kScanK - 2; k >= 0; --k) g = step_map<FLAGS>(a[k + 1], c[k], g);
-                float r = product<FLAGS>(a[0], g), suffix = prod;
-                row_scan<FLAGS, true>(suffix, r);
-                const float right = carry[s0 + i];
-                r = step_map<FLAGS>(suffix, r, right);
-                if (l.lane == 0) carry[s0 + i] = r;
-                g = row_shift<true>(r, right);  // a_{t+8} g_{t+8}
-                float dA = 0.f;
+                for (int j = 0; j < 2; ++j) {
+                    const float right = carry[s0 + i + j], A_s = A[s0 + i + j];
+                    r[j] = step_map<FLAGS>(prod[j], r[j], right);
+                    carry[s0 + i + j] = row_last<true>(r[j]);
+                    g[j] = row_shift<true>(r[j], right);  // a_{t+8} g_{t+8}
+                    float b[kScanK];
+                    read_tile(B_tile[i + j], l.lane, b);
+                    dA[j] = 0.f;
 #pragma unroll
-                for (int k = kScanK - 1; k >= 0; --k) {
-                    g = k == kScanK - 1 ? c[k] + g : step_map<FLAGS>(a[k + 1], c[k], g);
-                    v[k] = g * dtu[k];
-                    gB[k] = fmaf(g, b[k], gB[k]);
-                    const float q = g * w[k];
-                    dA = fmaf(q, dt[k], dA);  // at a start w is 0, and dt put to 0
-                    grad_dt[k] = fmaf(q, A_s, grad_dt[k]);
+                    for (int k = kScanK - 1; k >= 0; --k) {
+                        g[j] = k == kScanK - 1 ? c[j][k] + g[j]
+                                               : step_map<FLAGS>(a[j][k + 1], c[j][k], g[j]);
+                        v[j][k] = g[j] * dtu[k];
+                        gB[k] = fmaf(g[j], b[k], gB[k]);
+                        const float q = g[j] * w[j][k];
+                        dA[j] = fmaf(q, dt[k], dA[j]);  // at a start w is 0, and dt put to 0
+                        grad_dt[k] = fmaf(q, A_s, grad_dt[k]);
+                    }
+                    bc[wave][i + j][threadIdx.x & (kWave - 1)] = sum_rows(v[j]);
                 }
-                bc[wave][i][threadIdx.x & (kWave - 1)] = sum_rows(v);
-                dA = row_sum(dA);
-                if (l.lane == kScanLanes - 1) grad_A[s0 + i] += dA;
+                row_sum(dA);
+                if (l.lane == kScanLanes - 1)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) grad_A[s0 + i + j] += dA[j];
             }
             __syncthreads();
             // lane x of a wave holds, for state i, four steps of grad_B (rows 0
@@ -204,8 +228,8 @@ __global__ __launch_bounds__(kScanThreads) void selective_scan_backward(ScanPara
             store_steps<kScanK>(static_cast<E *>(p.grad_delta) + out_row + t, p.T - t, grad_dt);
         }
     }
-    grad_D = row_sum(grad_D);
-    grad_bias = row_sum(grad_bias);
+    float totals[2] = {grad_D, grad_bias};
+    row_sum(totals);
     if (!l.live) return;
     float *out = p.row_partials + (int64_t)l.row * (S + 2);
     for (int s = l.lane; s < S; s += kScanLanes) {
@@ -213,23 +237,30 @@ __global__ __launch_bounds__(kScanThreads) void selective_scan_backward(ScanPara
         if (p.grad_state != nullptr) p.grad_state[(int64_t)l.row * S + s] = carry[s];
     }
     if (l.lane == kScanLanes - 1) {
-        out[S] = grad_D;
-        out[S + 1] = grad_bias;
+        out[S] = totals[0];
+        out[S + 1] = totals[1];
     }
 }
 
 // grad_B and grad_C: the sum of a group's workgroups, in order, 4 steps a lane.
+// 2^lane_bits lanes share a row (a sequence, group and state of one of the
+// two), so that short rows fill a workgroup too.
 struct BcSums {
     const float *partials;
     void *grad_B, *grad_C;
     const int32_t *lengths;
     uint32_t blocks, states, groups, rows;  // rows: num_seqs * groups * 2 * states
-    int32_t T, padded;                      // padded: tiles * kScanTile
+    uint32_t lane_bits;
+    int32_t T, padded;  // padded: tiles * kScanTile
 };
 
 template <typename E>
 __global__ __launch_bounds__(kScanThreads) void bc_sums(BcSums p) {
-    for (uint32_t r = blockIdx.x; r < p.rows; r += gridDim.x) {
+    const uint32_t lanes = 1u << p.lane_bits, rows = kScanThreads >> p.lane_bits;
+    const int lane = (int)(threadIdx.x & (lanes - 1));
+    for (uint64_t r64 = (uint64_t)blockIdx.x * rows + (threadIdx.x >> p.lane_bits); r64 < p.rows;
+         r64 += (uint64_t)gridDim.x * rows) {
+        const uint32_t r = (uint32_t)r64;
         const uint32_t ng = r / (2 * p.states), which = r / p.states & 1, s = r % p.states;
         const int end = row_end(p.lengths, ng / p.groups, p.T);
         const int64_t step = (int64_t)2 * p.states * p.padded;
@@ -237,9 +268,10 @@ __global__ __launch_bounds__(kScanThreads) void bc_sums(BcSums p) {
                             ((int64_t)which * p.states + s) * p.padded;
         E *to = static_cast<E *>(which == 0 ? p.grad_B : p.grad_C) +
                 ((int64_t)ng * p.states + s) * p.T;
-        for (int t = (int)(blockIdx.y * kScanThreads + threadIdx.x) * 4; t < p.T;
-             t += (int)(gridDim.y * kScanThreads * 4)) {
+        for (int t = ((int)(blockIdx.y << p.lane_bits) + lane) * 4; t < p.T;
+             t += (int)(gridDim.y << p.lane_bits) * 4) {
             float4v sum = *reinterpret_cast<const float4v *>(from + t);
+#pragma unroll 4
             for (uint32_t b = 1; b < p.blocks; ++b)
                 sum += *reinterpret_cast<const float4v *>(from + b * step + t);
             float v[4];
@@ -250,26 +282,44 @@ __global__ __launch_bounds__(kScanThreads) void bc_sums(BcSums p) {
     }
 }
 
-// grad_A, grad_D and grad_delta_bias: the sum over sequences, in fp64; a wave
-// takes 64 neighbouring values.
-__global__ __launch_bounds__(kWave) void row_sums(const float *partials, uint32_t num_seqs,
-                                                  uint32_t channels, uint32_t states,
-                                                  float *grad_A, float *grad_D,
-                                                  float *grad_bias) {
+// grad_A, grad_D and grad_delta_bias: the sums over sequences, in fp64.  A
+// workgroup takes kSumValues neighbouring values; its lanes of one value take
+// every so many sequences and meet in LDS in a fixed tree.
+constexpr int kSumValues = 16, kSumThreads = 1024;
+
+__global__ __launch_bounds__(kSumThreads) void row_sums(const float *partials, uint32_t num_seqs,
+                                                        uint32_t channels, uint32_t states,
+                                                        float *grad_A, float *grad_D,
+                                                        float *grad_bias) {
+    __shared__ double sums[kSumThreads];
     const int64_t width = states + 2, count = (int64_t)channels * width;
-    for (int64_t i = (int64_t)blockIdx.x * kWave + threadIdx.x; i < count;
-         i += (int64_t)gridDim.x * kWave) {
+    const uint32_t lanes = blockDim.x / kSumValues;  // a power of two
+    const uint32_t lane = threadIdx.x / kSumValues;
+    for (int64_t i0 = (int64_t)blockIdx.x * kSumValues; i0 < count;
+         i0 += (int64_t)gridDim.x * kSumValues) {
+        const int64_t i = i0 + threadIdx.x % kSumValues;
         double sum = 0.0;
-        for (uint32_t n = 0; n < num_seqs; ++n) sum += (double)partials[n * count + i];
-        const int64_t d = i / width;
-        const int s = (int)(i - d * width);
-        if (s < (int)states)
-            grad_A[d * states + s] = (float)sum;
-        else if (s == (int)states) {
-            if (grad_D != nullptr) grad_D[d] = (float)sum;
-        } else if (grad_bias != nullptr) {
-            grad_bias[d] = (float)sum;
+        if (i < count)
+#pragma unroll 8
+            for (uint32_t n = lane; n < num_seqs; n += lanes) sum += (double)partials[n * count + i];
+        sums[threadIdx.x] = sum;
+        for (uint32_t m = lanes / 2; m > 0; m /= 2) {
+            __syncthreads();
+            if (lane < m) sums[threadIdx.x] += sums[threadIdx.x + m * kSumValues];
         }
+        if (lane == 0 && i < count) {
+            const float total = (float)sums[threadIdx.x];
+            const int64_t d = i / width;
+            const int s = (int)(i - d * width);
+            if (s < (int)states)
+                grad_A[d * states + s] = total;
+            else if (s == (int)states) {
+                if (grad_D != nullptr) grad_D[d] = total;
+            } else if (grad_bias != nullptr) {
+                grad_bias[d] = total;
+            }
+        }
+        __syncthreads();
     }
 }
 
@@ -326,7 +376,7 @@ rlca_status rlca_selective_scan_backward(const rlca_scan_call *call, void *works
                                           ? (const void *)selective_scan_backward<_Float16, true>
                                           : (const void *)selective_scan_backward<_Float16, false>);
         st = launch(kernel, dim3(p.num_seqs * p.groups * p.blocks_per_group), kScanThreads,
-                    3 * kScanRows * p.states * 4, p, stream);
+                    3 * kScanRows * padded_states(c.states) * 4, p, stream);
         if (st != RLCA_OK) return st;
         if (p.T != 0) {
             BcSums b = {};
@@ -340,11 +390,14 @@ rlca_status rlca_selective_scan_backward(const rlca_scan_call *call, void *works
             b.rows = p.num_seqs * p.groups * 2 * p.states;
             b.T = p.T;
             b.padded = p.tiles * kScanTile;
-            const uint32_t across = (p.T + kScanThreads * 4 - 1) / (kScanThreads * 4);
+            while ((4 << b.lane_bits) < p.T && (1 << b.lane_bits) < kScanThreads) ++b.lane_bits;
+            const uint32_t across = (p.T + (4 << b.lane_bits) - 1) / (4 << b.lane_bits);
+            const uint32_t at_once = kScanThreads >> b.lane_bits;
+            const uint32_t down = (b.rows + at_once - 1) / at_once;
             const void *sums = c.dtype == RLCA_F32    ? (const void *)bc_sums<float>
                                : c.dtype == RLCA_BF16 ? (const void *)bc_sums<__bf16>
                                                       : (const void *)bc_sums<_Float16>;
-            st = launch(sums, dim3(b.rows < (1u << 18) ? b.rows : 1u << 18, across < 64 ? across : 64),
+            st = launch(sums, dim3(down < (1u << 18) ? down : 1u << 18, across < 64 ? across : 64),
                         kScanThreads, 0, b, stream);
             if (st != RLCA_OK) return st;
         }
@@ -353,10 +406,12 @@ rlca_status rlca_selective_scan_backward(const rlca_scan_call *call, void *works
     uint32_t num_seqs = p.num_seqs, channels = p.channels, states = p.states;
     float *gA = c.grad_A, *gD = c.grad_D, *gb = c.grad_delta_bias;
     void *args[] = {&partials, &num_seqs, &channels, &states, &gA, &gD, &gb};
-    const uint64_t waves = ((uint64_t)channels * (states + 2) + rlca::kWave - 1) / rlca::kWave;
+    const uint64_t groups = ((uint64_t)channels * (states + 2) + kSumValues - 1) / kSumValues;
+    uint32_t threads = 64;
+    while (threads < (uint32_t)kSumThreads && threads / kSumValues < num_seqs) threads *= 2;
     const hipError_t e =
-        hipLaunchKernel((const void *)row_sums, dim3(waves < (1u << 20) ? waves : 1u << 20),
-                        dim3(rlca::kWave), args, 0, stream);
+        hipLaunchKernel((const void *)row_sums, dim3(groups < (1u << 20) ? groups : 1u << 20),
+                        dim3(threads), args, 0, stream);
     return e == hipSuccess ? RLCA_OK : RLCA_ERR_HIP;
 }
 

@@ -35,6 +35,26 @@ __device__ __forceinline__ void load_steps(const E *p, int n, float (&v)[K]) {
     }
 }
 
+// As load_steps, in the storage type: loads that are issued long before their
+// use keep 16-bit steps in half the registers.
+template <int K, typename E>
+struct Steps {
+    typedef E block __attribute__((ext_vector_type(K)));
+    block b;
+    __device__ __forceinline__ void load(const E *p, int n) {
+        if (n >= K) {
+            __builtin_memcpy(&b, p, sizeof b);
+        } else {
+#pragma unroll
+            for (int k = 0; k < K; ++k) b[k] = k < n ? p[k] : (E)0.f;
+        }
+    }
+    __device__ __forceinline__ void widen(float (&v)[K]) const {
+#pragma unroll
+        for (int k = 0; k < K; ++k) v[k] = (float)b[k];
+    }
+};
+
 // The K steps before p, of which the last n exist.
 template <int K, typename E>
 __device__ __forceinline__ void load_steps_before(const E *p, int n, float (&v)[K]) {

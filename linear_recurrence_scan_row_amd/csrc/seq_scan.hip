@@ -11,53 +11,124 @@
 namespace rlca {
 namespace seq {
 
-template <typename E, bool FLAGS>
-__global__ __launch_bounds__(kScanThreads) void selective_scan(ScanParams p) {
+// States staged in LDS together, in two buffers: the next stage's rows are
+// loaded while one is computed, and one barrier a stage suffices.
+constexpr int kForwardStates = 8;
+
+// SPLIT waves share four channels: each takes every SPLIT-th pair of states
+// over all the steps, and prepares and finishes 8 / SPLIT of a lane's steps.
+// They meet in LDS twice a tile, in dt and dt u before and in y's partial sums
+// after (split_of below says when that pays).
+template <typename E, bool FLAGS, int SPLIT>
+__global__ __launch_bounds__(kScanThreads, sizeof(E) == 2 && !FLAGS ? 4 : 3) void selective_scan(ScanParams p) {
+    constexpr int kQuads = kScanWaves / SPLIT, kRows = 4 * kQuads, kOwn = kScanK / SPLIT;
     extern __shared__ __attribute__((aligned(16))) char lds_bytes[];
-    __shared__ TileRow B_tile[kScanStates], C_tile[kScanStates];
-    const ScanLane l = scan_lane(p);
+    __shared__ TileRow tiles[2][2][kForwardStates];  // [buffer][B, C][state]
+    __shared__ float steps[kQuads][SPLIT > 1 ? (FLAGS ? 3 : 2) * kScanK : 1][kWave];
+    __shared__ float sums[SPLIT > 1 ? kScanWaves : 1][SPLIT > 1 ? kScanK : 1][kWave];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int in_wave = threadIdx.x % kWave;
+    const int quad = wave / SPLIT, part = wave % SPLIT;
+    const ScanLane l = scan_lane(p, quad * 4 + in_wave / kScanLanes, kRows);
     const int S = (int)p.states, padded = padded_states(S);
     // [rows][padded]: the states entering the tile, and A log2(e)
     float *carry = reinterpret_cast<float *>(lds_bytes) + l.local * padded;
-    float *A2 = carry + kScanRows * padded;
-    for (int s = l.lane; s < padded; s += kScanLanes) {
-        carry[s] = p.state == nullptr || s >= S ? 0.f : p.state[(int64_t)l.row * S + s];
-        A2[s] = s >= S ? 0.f : p.A[(int64_t)l.d * S + s] * kLog2e;
-    }
+    float *A2 = carry + kRows * padded;
+    // a wave initialises and hands on the states that it computes
+    const auto mine = [&](int s) { return SPLIT == 1 || (s / 2) % SPLIT == part; };
+    for (int s = l.lane; s < padded; s += kScanLanes)
+        if (mine(s)) {
+            carry[s] = p.state == nullptr || s >= S ? 0.f : p.state[(int64_t)l.row * S + s];
+            A2[s] = s >= S ? 0.f : p.A[(int64_t)l.d * S + s] * kLog2e;
+        }
     const int end = row_end(p.lengths, l.n, p.T);
-    const E *u_row = static_cast<const E *>(p.u) + l.n * p.u_n + l.d * p.u_d;
-    const E *delta_row = static_cast<const E *>(p.delta) + l.n * p.delta_n + l.d * p.delta_d;
+    const int own = l.lane * kScanK + part * kOwn;  // the lane's own steps in a tile
+    const E *u_row = static_cast<const E *>(p.u) + l.n * p.u_n + l.d * p.u_d + own;
+    const E *delta_row = static_cast<const E *>(p.delta) + l.n * p.delta_n + l.d * p.delta_d + own;
     const E *z_row =
-        p.z == nullptr ? nullptr : static_cast<const E *>(p.z) + l.n * p.z_n + l.d * p.z_d;
-    const E *B = static_cast<const E *>(p.B) + l.n * p.B_n + l.g * p.B_g;
-    const E *C = static_cast<const E *>(p.C) + l.n * p.C_n + l.g * p.C_g;
+        p.z == nullptr ? nullptr : static_cast<const E *>(p.z) + l.n * p.z_n + l.d * p.z_d + own;
     const uint8_t *flags = FLAGS ? p.flags + (int64_t)l.n * p.T : nullptr;
     const float bias = p.delta_bias == nullptr ? 0.f : p.delta_bias[l.d];
     const float skip = p.D == nullptr ? 0.f : p.D[l.d];
-    E *y_row = static_cast<E *>(p.y) + (int64_t)l.row * p.T;
+    E *y_row = static_cast<E *>(p.y) + (int64_t)l.row * p.T + own;
 
-    for (int tile = 0; tile < p.tiles; ++tile) {
-        const int t0 = tile * kScanTile, t = t0 + l.lane * kScanK;
+    // What a thread stages: 8 steps of one state, of B in the first two waves
+    // and of C in the others.
+    const int stage_c = wave / 2, stage_s = threadIdx.x / kScanLanes % kForwardStates;
+    const int64_t stage_stride = stage_c ? p.C_s : p.B_s;
+    const E *stage_row = (stage_c ? static_cast<const E *>(p.C) + l.n * p.C_n + l.g * p.C_g
+                                  : static_cast<const E *>(p.B) + l.n * p.B_n + l.g * p.B_g) +
+                         stage_s * stage_stride + l.lane * kScanK;
+    Steps<kScanK, E> next_stage;
+    Steps<kOwn, E> next_u, next_delta;
+    const auto load_stage = [&](int t0, int s0) {
+        next_stage.load(stage_row + s0 * stage_stride + t0,
+                        s0 + stage_s < S ? end - t0 - l.lane * kScanK : 0);
+    };
+    const auto load_tile = [&](int t0) {
+        next_u.load(u_row + t0, end - t0 - own);
+        next_delta.load(delta_row + t0, end - t0 - own);
+    };
+    // Past the row's steps y is 0.
+    const int live_tiles = (end + kScanTile - 1) / kScanTile;
+    int buffer = 0;
+    load_stage(0, 0);
+    load_tile(0);
+
+    for (int tile = 0; tile < live_tiles; ++tile) {
+        const int t0 = tile * kScanTile;
         if (p.checkpoints != nullptr && l.live)
             for (int s = l.lane; s < S; s += kScanLanes)
-                p.checkpoints[((int64_t)l.row * p.tiles + tile) * S + s] = carry[s];
-        float dt[kScanK], raw[kScanK], u[kScanK], dtu[kScanK], cut[kScanK], y[kScanK];
-        load_inputs<E, FLAGS>(p, u_row, delta_row, flags, bias, t, end, end, dt, raw, u, dtu, cut);
+                if (mine(s)) p.checkpoints[((int64_t)l.row * p.tiles + tile) * S + s] = carry[s];
+        float skipped[kOwn], dt[kScanK], dtu[kScanK], cut[kScanK], y[kScanK] = {};
+        Steps<kOwn, E> z;
+        if (z_row != nullptr) z.load(z_row + t0, end - t0 - own);
+        {
+            float u[kOwn], raw[kOwn], own_dt[kOwn], own_dtu[kOwn], own_cut[kOwn];
+            next_u.widen(u);
+            next_delta.widen(raw);
+            make_steps<FLAGS>(p, flags, bias, t0 + own, end, end, u, raw, own_dt, own_dtu, own_cut);
+            if (tile + 1 < live_tiles) load_tile(t0 + kScanTile);
+#pragma unroll
+            for (int k = 0; k < kOwn; ++k) {
+                if constexpr (SPLIT > 1) {
+                    steps[quad][part * kOwn + k][in_wave] = own_dt[k];
+                    steps[quad][kScanK + part * kOwn + k][in_wave] = own_dtu[k];
+                    if constexpr (FLAGS)
+                        steps[quad][2 * kScanK + part * kOwn + k][in_wave] = own_cut[k];
+                } else {
+                    dt[k] = own_dt[k];
+                    dtu[k] = own_dtu[k];
+                    if constexpr (FLAGS) cut[k] = own_cut[k];
+                }
+                skipped[k] = skip * u[k];
+                if constexpr (SPLIT == 1) y[k] = skipped[k];
+            }
+        }
         float dt_sum = 0.f;
         bool starts = false;
-#pragma unroll
-        for (int k = 0; k < kScanK; ++k) {
-            dt_sum += dt[k];
-            if constexpr (FLAGS) starts |= cut[k] != 0.f;
-            y[k] = skip * u[k];
-        }
-        for (int s0 = 0; s0 < S; s0 += kScanStates) {
-            const int count = S - s0 < kScanStates ? S - s0 : kScanStates;
-            __syncthreads();  // the tiles before are used up
-            stage_rows(B_tile, B, p.B_s, s0, S, t0, end);
-            stage_rows(C_tile, C, p.C_s, s0, S, t0, end);
+        for (int s0 = 0; s0 < S; s0 += kForwardStates) {
+            stage(tiles[buffer][stage_c][stage_s], next_stage, l.lane);
+            if (s0 + kForwardStates < S)
+                load_stage(t0, s0 + kForwardStates);
+            else if (tile + 1 < live_tiles)
+                load_stage(t0 + kScanTile, 0);
             __syncthreads();
-            for (int i = 0; i < count; i += 2) {
+            if (s0 == 0) {
+#pragma unroll
+                for (int k = 0; k < kScanK; ++k) {
+                    if constexpr (SPLIT > 1) {
+                        dt[k] = steps[quad][k][in_wave];
+                        dtu[k] = steps[quad][kScanK + k][in_wave];
+                        if constexpr (FLAGS) cut[k] = steps[quad][2 * kScanK + k][in_wave];
+                    }
+                    dt_sum += dt[k];
+                    if constexpr (FLAGS) starts |= cut[k] != 0.f;
+                }
+            }
+            const TileRow *B_tile = tiles[buffer][0], *C_tile = tiles[buffer][1];
+            const int count = S - s0 < kForwardStates ? S - s0 : kForwardStates;
+            for (int i = 2 * part; i < count; i += 2 * SPLIT) {
                 float a[2][kScanK], b[2][kScanK], h[2], prod[2], enter[2];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
@@ -87,29 +158,52 @@ __global__ __launch_bounds__(kScanThreads) void selective_scan(ScanParams p) {
                     }
                 }
             }
+            buffer ^= 1;
         }
         wave_order();
+        float out[kOwn];
+        if constexpr (SPLIT > 1) {
+#pragma unroll
+            for (int k = 0; k < kScanK; ++k) sums[wave][k][in_wave] = y[k];
+            __syncthreads();
+#pragma unroll
+            for (int k = 0; k < kOwn; ++k) {
+                out[k] = skipped[k];
+#pragma unroll
+                for (int q = 0; q < SPLIT; ++q)
+                    out[k] += sums[quad * SPLIT + q][part * kOwn + k][in_wave];
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < kOwn; ++k) out[k] = y[k];
+        }
+        const int t = t0 + own;
         if (l.live && t < p.T) {
             if (z_row != nullptr) {
-                float z[kScanK];
-                load_steps<kScanK>(z_row + t, end - t, z);
+                float gate[kOwn];
+                z.widen(gate);
 #pragma unroll
-                for (int k = 0; k < kScanK; ++k) y[k] *= silu(z[k]);
+                for (int k = 0; k < kOwn; ++k) out[k] *= silu(gate[k]);
             }
 #pragma unroll
-            for (int k = 0; k < kScanK; ++k) y[k] = t + k < end ? y[k] : 0.f;
-            store_steps<kScanK>(y_row + t, p.T - t, y);
+            for (int k = 0; k < kOwn; ++k) out[k] = t + k < end ? out[k] : 0.f;
+            store_steps<kOwn>(y_row + t0, p.T - t, out);
         }
     }
-    if (p.final_state != nullptr && l.live) {
+    if (!l.live) return;
+    for (int t0 = live_tiles * kScanTile; t0 + own < p.T; t0 += kScanTile) {
+        const float zeros[kOwn] = {};
+        store_steps<kOwn>(y_row + t0, p.T - t0 - own, zeros);
+    }
+    if (p.final_state != nullptr) {
         const bool over = FLAGS && p.after_done != 0 && end > 0 && flags[end - 1] != 0;
         for (int s = l.lane; s < S; s += kScanLanes)
-            p.final_state[(int64_t)l.row * S + s] = over ? 0.f : carry[s];
+            if (mine(s)) p.final_state[(int64_t)l.row * S + s] = over ? 0.f : carry[s];
     }
 }
 
 // ------------------------------------------------------------------- host side
-ScanParams scan_params(const rlca_scan_call &c) {
+ScanParams scan_params(const rlca_scan_call &c, int rows) {
     ScanParams p = {};
     p.u = c.u;
     p.delta = c.delta;
@@ -142,12 +236,38 @@ ScanParams scan_params(const rlca_scan_call &c) {
     p.groups = (uint32_t)c.groups;
     p.per_group = p.channels / p.groups;
     p.states = (uint32_t)c.states;
-    p.blocks_per_group = (p.per_group + kScanRows - 1) / kScanRows;
+    p.blocks_per_group = (p.per_group + rows - 1) / rows;
     p.T = (int32_t)c.T;
     p.tiles = (p.T + kScanTile - 1) / kScanTile;
     p.softplus = c.softplus;
     p.after_done = c.convention == RLCA_RESET_AFTER_DONE;
     return p;
+}
+
+// Waves that share four channels: enough that the launch gives the 1024 SIMDs
+// several waves each, as long as every wave has a pair of states.  Measured
+// with 1, 2 and 4 (16 states, bf16): 1024 waves at one a quad (1x4096x4096)
+// 151, 131 and 127 us; 2304 (6x1536x2049, ragged) 112, 92 and 93; 4096
+// (8x2048x2048) 180, 194 and 216.
+constexpr int kFewestRows = 4;
+
+static int split_of(const rlca_scan_call &c) {
+    const int64_t waves = c.num_seqs * c.channels / 4;
+    const int pairs = padded_states(c.states) / 2;
+    return waves <= 1536 && pairs >= 4 ? 4 : waves <= 3072 && pairs >= 2 ? 2 : 1;
+}
+
+template <typename E, int SPLIT>
+static const void *scan_kernel(bool flags) {
+    return flags ? (const void *)selective_scan<E, true, SPLIT>
+                 : (const void *)selective_scan<E, false, SPLIT>;
+}
+
+template <typename E>
+static const void *scan_kernel(bool flags, int split) {
+    return split == 4   ? scan_kernel<E, 4>(flags)
+           : split == 2 ? scan_kernel<E, 2>(flags)
+                        : scan_kernel<E, 1>(flags);
 }
 
 static int64_t checkpoint_values(const rlca_scan_call &c) {
@@ -163,7 +283,7 @@ rlca_status check_scan(const rlca_scan_call &c, bool backward, Arrays *a) {
         return RLCA_ERR_INVALID_VALUE;
     if (T != 0 && N * D > INT64_MAX / 8 / S / T) return RLCA_ERR_INVALID_SIZE;
     // a launch holds less than 2^32 threads
-    const int64_t blocks = D == 0 ? 0 : N * G * ((D / G + kScanRows - 1) / kScanRows);
+    const int64_t blocks = D == 0 ? 0 : N * G * ((D / G + kFewestRows - 1) / kFewestRows);
     if (blocks >= ((int64_t)1 << 32) / kScanThreads) return RLCA_ERR_INVALID_SIZE;
     const int64_t params = N == 0 ? 0 : D, rows = D == 0 ? 0 : N;
     const Dim dense[] = {{N, D * T}, {D, T}, {T, 1}};
@@ -225,17 +345,13 @@ rlca_status rlca_selective_scan(const rlca_scan_call *call, hipStream_t stream) 
     if (st == RLCA_OK) st = a.status();
     if (st != RLCA_OK) return st;
     if (c.num_seqs * c.channels == 0 || (c.T == 0 && c.final_state == nullptr)) return RLCA_OK;
-    ScanParams p = scan_params(c);
-    const bool flags = c.flags != nullptr;
-    const void *kernel =
-        c.dtype == RLCA_F32    ? (flags ? (const void *)selective_scan<float, true>
-                                        : (const void *)selective_scan<float, false>)
-        : c.dtype == RLCA_BF16 ? (flags ? (const void *)selective_scan<__bf16, true>
-                                        : (const void *)selective_scan<__bf16, false>)
-                               : (flags ? (const void *)selective_scan<_Float16, true>
-                                        : (const void *)selective_scan<_Float16, false>);
+    const int split = split_of(c);
+    ScanParams p = scan_params(c, kScanRows / split);
+    const void *kernel = c.dtype == RLCA_F32    ? scan_kernel<float>(c.flags != nullptr, split)
+                         : c.dtype == RLCA_BF16 ? scan_kernel<__bf16>(c.flags != nullptr, split)
+                                                : scan_kernel<_Float16>(c.flags != nullptr, split);
     return launch(kernel, dim3(p.num_seqs * p.groups * p.blocks_per_group), kScanThreads,
-                  2 * kScanRows * padded_states(c.states) * 4, p, stream);
+                  2 * (kScanRows / split) * padded_states(c.states) * 4, p, stream);
 }
 
 }  // extern "C"

@@ -25,7 +25,7 @@ constexpr int kScanTile = kScanK * kScanLanes;   // 128 steps
 constexpr int kScanWaves = 4;                    // waves of a workgroup
 constexpr int kScanThreads = kScanWaves * kWave;
 constexpr int kScanRows = kScanThreads / kScanLanes;  // channels of a workgroup
-constexpr int kScanStates = 8;  // states whose B and C are staged in LDS together
+constexpr int kScanStates = 8;  // backward: states staged in LDS together
 
 // States of a workgroup's LDS arrays: whole pairs, since the kernels take two
 // states at a time.
@@ -53,23 +53,23 @@ struct ScanParams {
 };
 
 // Where a lane works: its sequence, group and channel (clamped to the group's
-// last one; `live` says whether it is the lane's own), and its lane in the row.
+// last one; `live` says whether it is the lane's own), its lane in the row and
+// the row in the workgroup, which holds `rows` channels.
 struct ScanLane {
-    uint32_t n, g, block, d, row;
-    int lane, local;  // lane of the row; row of the workgroup
+    uint32_t n, g, d, row;
+    int lane, local;
     bool live;
 };
 
-__device__ __forceinline__ ScanLane scan_lane(const ScanParams &p) {
+__device__ __forceinline__ ScanLane scan_lane(const ScanParams &p, int local, uint32_t rows) {
     ScanLane l;
     const uint32_t b = blockIdx.x;
     const uint32_t ng = b / p.blocks_per_group;
-    l.block = b - ng * p.blocks_per_group;
     l.n = ng / p.groups;
     l.g = ng - l.n * p.groups;
     l.lane = threadIdx.x & (kScanLanes - 1);
-    l.local = threadIdx.x / kScanLanes;
-    const uint32_t c = l.block * kScanRows + l.local;
+    l.local = local;
+    const uint32_t c = (b - ng * p.blocks_per_group) * rows + local;
     l.live = c < p.per_group;
     l.d = l.g * p.per_group + (l.live ? c : p.per_group - 1);
     l.row = l.n * p.channels + l.d;
@@ -170,46 +170,38 @@ __device__ __forceinline__ void read_tile(const TileRow &r, int lane, float (&v)
     for (int k = 0; k < 4; ++k) v[k] = x[k], v[4 + k] = y[k];
 }
 
-// Stage kScanStates states' rows of B or C for one tile from state s0, as zeros
-// past the last of S states.
 template <typename E>
-__device__ __forceinline__ void stage_rows(TileRow *to, const E *from, int64_t stride, int s0,
-                                           int S, int t0, int end) {
-    for (int i = threadIdx.x; i < kScanStates * kScanLanes; i += kScanThreads) {
-        const int s = i / kScanLanes, lane = i % kScanLanes, t = t0 + lane * kScanK;
-        float v[kScanK];
-        load_steps<kScanK>(from + (s0 + s) * stride + t, s0 + s < S ? end - t : 0, v);
-        float4v x, y;
+__device__ __forceinline__ void stage(TileRow &to, const Steps<kScanK, E> &from, int lane) {
+    float v[kScanK];
+    from.widen(v);
+    float4v x, y;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) x[k] = v[k], y[k] = v[4 + k];
-        to[s].half[0][lane] = x;
-        to[s].half[1][lane] = y;
-    }
+    for (int k = 0; k < 4; ++k) x[k] = v[k], y[k] = v[4 + k];
+    to.half[0][lane] = x;
+    to.half[1][lane] = y;
 }
 
-// A lane's steps of one tile: dt, u and dt u (0 past `end`, where a step then
-// changes nothing; raw is dt before softplus).  Where an episode starts within
-// the row's steps a_t has to be 0 whatever the step's dt is, a NaN too: cut,
-// which is added to a's exponent, is -infinity there (else 0) and dt is 0.
-template <typename E, bool FLAGS>
-__device__ __forceinline__ void load_inputs(const ScanParams &p, const E *u_row,
-                                            const E *delta_row, const uint8_t *flags, float bias,
-                                            int t, int end, int row_steps, float (&dt)[kScanK],
-                                            float (&raw)[kScanK], float (&u)[kScanK],
-                                            float (&dtu)[kScanK], float (&cut)[kScanK]) {
-    load_steps<kScanK>(u_row + t, end - t, u);
-    load_steps<kScanK>(delta_row + t, end - t, raw);
+// K steps of a lane from step t: dt and dt u from raw = delta and u (0 past
+// `end`, where a step then changes nothing; raw becomes dt before softplus).
+// Where an episode starts within the row's steps a_t has to be 0 whatever the
+// step's dt is, a NaN too: cut, which is added to a's exponent, is -infinity
+// there (else 0) and dt is 0.
+template <bool FLAGS, int K>
+__device__ __forceinline__ void make_steps(const ScanParams &p, const uint8_t *flags, float bias,
+                                           int t, int end, int row_steps, const float (&u)[K],
+                                           float (&raw)[K], float (&dt)[K], float (&dtu)[K],
+                                           float (&cut)[K]) {
 #pragma unroll
-    for (int k = 0; k < kScanK; ++k) {
+    for (int k = 0; k < K; ++k) {
         raw[k] += bias;
         const float x = p.softplus != 0 ? softplus(raw[k]) : raw[k];
         dt[k] = t + k < end ? x : 0.f;
         dtu[k] = t + k < end ? x * u[k] : 0.f;
     }
     if constexpr (FLAGS) {
-        const uint32_t starts = start_bits<kScanK>(flags, t, p.T, p.after_done);
+        const uint32_t starts = start_bits<K>(flags, t, p.T, p.after_done);
 #pragma unroll
-        for (int k = 0; k < kScanK; ++k) {
+        for (int k = 0; k < K; ++k) {
             const bool start = t + k < row_steps && (starts >> k & 1);
             cut[k] = start ? -INFINITY : 0.f;
             dt[k] = start ? 0.f : dt[k];
@@ -231,7 +223,7 @@ __device__ __forceinline__ float decay(float dt, float cut, float A2) {
     return exp2_fast(FLAGS ? fmaf(dt, A2, cut) : dt * A2);
 }
 
-ScanParams scan_params(const rlca_scan_call &c);
+ScanParams scan_params(const rlca_scan_call &c, int rows);
 rlca_status check_scan(const rlca_scan_call &c, bool backward, Arrays *a);
 
 }  // namespace seq

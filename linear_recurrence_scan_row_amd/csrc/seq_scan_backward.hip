@@ -15,6 +15,8 @@
 // gradient) meet in 12 lane-half swaps and 12 additions, after which each row
 // holds the sums of four of them.  The waves' sums meet in LDS, the
 // workgroups' in a workspace that bc_sums adds in order.
+#include <stdlib.h>
+
 #include "seq_scan.hpp"
 
 namespace rlca {
@@ -54,78 +56,170 @@ __device__ __forceinline__ void row_sum(float (&x)[2]) {
 #undef RLCA_STEP
 }
 
-template <typename E, bool FLAGS>
-__global__ __launch_bounds__(kScanThreads) void selective_scan_backward(ScanParams p) {
+// The shape of a workgroup: QUADS sets of four channels, SPLIT waves to each.
+// Waves of one quad take every SPLIT-th pair of states, and prepare and finish
+// 8 / SPLIT of a lane's steps, as in the forward scan.
+template <typename E, bool FLAGS, bool GATE, int SPLIT, int QUADS>
+__global__ __launch_bounds__(kWave *SPLIT *QUADS, 2) void selective_scan_backward(ScanParams p) {
+    constexpr int kRows = 4 * QUADS, kOwn = kScanK / SPLIT, kThreads = kWave * SPLIT * QUADS;
+    constexpr int kBefore = FLAGS ? 4 : 3, kAfter = GATE ? 3 : 2;  // values a step that waves share
     extern __shared__ __attribute__((aligned(16))) char lds_bytes[];
-    __shared__ TileRow B_tile[kScanStates], C_tile[kScanStates];
-    __shared__ float4v bc[kScanWaves][kScanStates][kWave];
-    const ScanLane l = scan_lane(p);
+    __shared__ TileRow tiles[2][2][kScanStates];  // [buffer][B, C][state]
+    __shared__ float4v bc[QUADS][kScanStates][kWave];
+    __shared__ float before[SPLIT > 1 ? QUADS : 1][SPLIT > 1 ? kBefore * kScanK : 1][kWave];
+    __shared__ float after[SPLIT > 1 ? SPLIT * QUADS : 1][SPLIT > 1 ? kAfter * kScanK : 1][kWave];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int in_wave = threadIdx.x % kWave;
+    const int quad = wave / SPLIT, part = wave % SPLIT;
+    const ScanLane l = scan_lane(p, quad * 4 + in_wave / kScanLanes, kRows);
     const int S = (int)p.states, padded = padded_states(S);
-    // [rows][padded]: A, the gradient a_t g_t entering the tile from its right, and
-    // the sums of grad_A
+    // [rows][padded]: A, the gradient a_t g_t entering the tile from its right,
+    // the states entering it from its left, and the sums of grad_A
     float *A = reinterpret_cast<float *>(lds_bytes) + l.local * padded;
-    float *carry = A + kScanRows * padded;
-    float *grad_A = carry + kScanRows * padded;
+    float *carry = A + kRows * padded;
+    float *enter_states = carry + kRows * padded;
+    float *grad_A = enter_states + kRows * padded;
+    const auto mine = [&](int s) { return SPLIT == 1 || (s / 2) % SPLIT == part; };
     const int row_steps = row_end(p.lengths, l.n, p.T);
     const int end = l.live ? row_steps : 0;  // a clamped row computes on zeros
     const uint8_t *flags = FLAGS ? p.flags + (int64_t)l.n * p.T : nullptr;
     const bool over = FLAGS && p.after_done != 0 && end > 0 && flags[end - 1] != 0;
-    for (int s = l.lane; s < padded; s += kScanLanes) {
-        A[s] = s >= S ? 0.f : p.A[(int64_t)l.d * S + s];
-        carry[s] = p.grad_final == nullptr || over || !l.live || s >= S
-                       ? 0.f
-                       : p.grad_final[(int64_t)l.row * S + s];
-        grad_A[s] = 0.f;
-    }
-    const E *u_row = static_cast<const E *>(p.u) + l.n * p.u_n + l.d * p.u_d;
-    const E *delta_row = static_cast<const E *>(p.delta) + l.n * p.delta_n + l.d * p.delta_d;
-    const E *g_row = static_cast<const E *>(p.grad_y) + l.n * p.g_n + l.d * p.g_d;
-    const E *z_row =
-        p.z == nullptr ? nullptr : static_cast<const E *>(p.z) + l.n * p.z_n + l.d * p.z_d;
-    const E *B = static_cast<const E *>(p.B) + l.n * p.B_n + l.g * p.B_g;
-    const E *C = static_cast<const E *>(p.C) + l.n * p.C_n + l.g * p.C_g;
+    for (int s = l.lane; s < padded; s += kScanLanes)
+        if (mine(s)) {
+            A[s] = s >= S ? 0.f : p.A[(int64_t)l.d * S + s];
+            carry[s] = p.grad_final == nullptr || over || !l.live || s >= S
+                           ? 0.f
+                           : p.grad_final[(int64_t)l.row * S + s];
+            grad_A[s] = 0.f;
+        }
+    const int own = l.lane * kScanK + part * kOwn;  // the lane's own steps in a tile
+    const E *u_row = static_cast<const E *>(p.u) + l.n * p.u_n + l.d * p.u_d + own;
+    const E *delta_row = static_cast<const E *>(p.delta) + l.n * p.delta_n + l.d * p.delta_d + own;
+    const E *g_row = static_cast<const E *>(p.grad_y) + l.n * p.g_n + l.d * p.g_d + own;
+    const E *z_row = GATE ? static_cast<const E *>(p.z) + l.n * p.z_n + l.d * p.z_d + own : nullptr;
     const float bias = p.delta_bias == nullptr ? 0.f : p.delta_bias[l.d];
     const float skip = p.D == nullptr ? 0.f : p.D[l.d];
-    const int64_t out_row = (int64_t)l.row * p.T;
-    const int wave = threadIdx.x / kWave;
+    const int64_t out_row = (int64_t)l.row * p.T + own;
+    E *grad_u = static_cast<E *>(p.grad_u) + out_row;
+    E *grad_delta = static_cast<E *>(p.grad_delta) + out_row;
+    E *grad_z = GATE ? static_cast<E *>(p.grad_z) + out_row : nullptr;
     float *partials = p.bc_partials + (int64_t)blockIdx.x * 2 * S * p.tiles * kScanTile;
-    float grad_D = 0.f, grad_bias = 0.f;
+    float totals[2] = {0.f, 0.f};  // of grad_D and grad_delta_bias
 
-    for (int tile = p.tiles - 1; tile >= 0; --tile) {
-        const int t0 = tile * kScanTile, t = t0 + l.lane * kScanK;
-        float dt[kScanK], raw[kScanK], u[kScanK], dtu[kScanK], cut[kScanK], gy[kScanK], y[kScanK];
-        load_inputs<E, FLAGS>(p, u_row, delta_row, flags, bias, t, end, row_steps, dt, raw, u,
-                              dtu, cut);
-        load_steps<kScanK>(g_row + t, end - t, gy);
-        if (z_row != nullptr) {
-            float z[kScanK];
-            load_steps<kScanK>(z_row + t, end - t, z);
-#pragma unroll
-            for (int k = 0; k < kScanK; ++k) gy[k] = t + k < end ? gy[k] * silu(z[k]) : 0.f;
+    // What a thread of the first four waves stages: 8 steps of one state of B
+    // (two waves) or C.
+    const int stage_c = wave / 2 % 2, stage_s = threadIdx.x / kScanLanes % kScanStates;
+    const bool stages = kThreads == 256 || wave < 4;
+    const int64_t stage_stride = stage_c ? p.C_s : p.B_s;
+    const E *stage_row = (stage_c ? static_cast<const E *>(p.C) + l.n * p.C_n + l.g * p.C_g
+                                  : static_cast<const E *>(p.B) + l.n * p.B_n + l.g * p.B_g) +
+                         stage_s * stage_stride + l.lane * kScanK;
+    Steps<kScanK, E> next_stage;
+    Steps<kOwn, E> u, delta, go, z, next_u, next_delta, next_go, next_z;
+    const auto load_stage = [&](int t0, int s0) {
+        if (stages)
+            next_stage.load(stage_row + s0 * stage_stride + t0,
+                            s0 + stage_s < S ? row_steps - t0 - l.lane * kScanK : 0);
+    };
+    const auto load_tile = [&](int t0) {
+        next_u.load(u_row + t0, end - t0 - own);
+        next_delta.load(delta_row + t0, end - t0 - own);
+        next_go.load(g_row + t0, end - t0 - own);
+        if constexpr (GATE) next_z.load(z_row + t0, end - t0 - own);
+    };
+
+    // tiles past the row's steps are zeros, and their sums are not read
+    const int live_tiles = (row_steps + kScanTile - 1) / kScanTile;
+    for (int t0 = live_tiles * kScanTile; l.live && t0 + own < p.T; t0 += kScanTile) {
+        const float zeros[kOwn] = {};
+        const int n = p.T - t0 - own;
+        store_steps<kOwn>(grad_u + t0, n, zeros);
+        store_steps<kOwn>(grad_delta + t0, n, zeros);
+        if constexpr (GATE) store_steps<kOwn>(grad_z + t0, n, zeros);
+    }
+    // Each tile's rows are loaded a tile ahead, where registers allow it.
+    constexpr bool kAhead = !GATE || (sizeof(E) == 2 && !(FLAGS && QUADS == 8)) || SPLIT > 1;
+    int buffer = 0;
+    if (live_tiles > 0) {  // an empty row has no last tile
+        load_stage((live_tiles - 1) * kScanTile, 0);
+        if constexpr (kAhead) load_tile((live_tiles - 1) * kScanTile);
+    }
+
+    for (int tile = live_tiles - 1; tile >= 0; --tile) {
+        const int t0 = tile * kScanTile;
+        if constexpr (!kAhead) load_tile(t0);
+        u = next_u;
+        delta = next_delta;
+        go = next_go;
+        if constexpr (GATE) z = next_z;
+        {
+            const float *from = p.checkpoints + ((int64_t)l.row * p.tiles + tile) * S;
+            for (int s = l.lane; s < padded; s += kScanLanes)
+                if (mine(s)) enter_states[s] = l.live && s < S ? from[s] : 0.f;
         }
-        float grad_dt[kScanK], gB[kScanK], dt_sum = 0.f;
+        if (kAhead && tile > 0) load_tile(t0 - kScanTile);
+        float dt[kScanK], dtu[kScanK], cut[kScanK], gy[kScanK];
+        float y[kScanK] = {}, grad_dt[kScanK] = {}, gB[kScanK] = {};
+        {
+            float v[kOwn], raw[kOwn], own_dt[kOwn], own_dtu[kOwn], own_cut[kOwn], own_gy[kOwn];
+            u.widen(v);
+            delta.widen(raw);
+            make_steps<FLAGS>(p, flags, bias, t0 + own, end, row_steps, v, raw, own_dt, own_dtu,
+                              own_cut);
+            go.widen(own_gy);
+            if constexpr (GATE) {
+                z.widen(v);
+#pragma unroll
+                for (int k = 0; k < kOwn; ++k)
+                    own_gy[k] = t0 + own + k < end ? own_gy[k] * silu(v[k]) : 0.f;
+            }
+#pragma unroll
+            for (int k = 0; k < kOwn; ++k) {
+                if constexpr (SPLIT > 1) {
+                    const int at = part * kOwn + k;
+                    before[quad][at][in_wave] = own_dt[k];
+                    before[quad][kScanK + at][in_wave] = own_dtu[k];
+                    before[quad][2 * kScanK + at][in_wave] = own_gy[k];
+                    if constexpr (FLAGS) before[quad][3 * kScanK + at][in_wave] = own_cut[k];
+                } else {
+                    dt[k] = own_dt[k];
+                    dtu[k] = own_dtu[k];
+                    gy[k] = own_gy[k];
+                    if constexpr (FLAGS) cut[k] = own_cut[k];
+                }
+            }
+        }
+        float dt_sum = 0.f;
         bool starts = false;
-#pragma unroll
-        for (int k = 0; k < kScanK; ++k) {
-            dt_sum += dt[k];
-            if constexpr (FLAGS) starts |= cut[k] != 0.f;
-            y[k] = skip * u[k];
-            grad_dt[k] = gB[k] = 0.f;
-        }
-        const float *enter_row = p.checkpoints + ((int64_t)l.row * p.tiles + tile) * S;
         for (int s0 = 0; s0 < S; s0 += kScanStates) {
             const int count = S - s0 < kScanStates ? S - s0 : kScanStates;
-            __syncthreads();  // the tiles and sums before are used up
-            stage_rows(B_tile, B, p.B_s, s0, S, t0, row_steps);
-            stage_rows(C_tile, C, p.C_s, s0, S, t0, row_steps);
+            if (stages) stage(tiles[buffer][stage_c][stage_s], next_stage, l.lane);
+            if (s0 + kScanStates < S)
+                load_stage(t0, s0 + kScanStates);
+            else if (tile > 0)
+                load_stage(t0 - kScanTile, 0);
             __syncthreads();
-            for (int i = 0; i < count; i += 2) {
+            if (s0 == 0) {
+#pragma unroll
+                for (int k = 0; k < kScanK; ++k) {
+                    if constexpr (SPLIT > 1) {
+                        dt[k] = before[quad][k][in_wave];
+                        dtu[k] = before[quad][kScanK + k][in_wave];
+                        gy[k] = before[quad][2 * kScanK + k][in_wave];
+                        if constexpr (FLAGS) cut[k] = before[quad][3 * kScanK + k][in_wave];
+                    }
+                    dt_sum += dt[k];
+                    if constexpr (FLAGS) starts |= cut[k] != 0.f;
+                }
+            }
+            const TileRow *B_tile = tiles[buffer][0], *C_tile = tiles[buffer][1];
+            for (int i = 2 * part; i < count; i += 2 * SPLIT) {
                 float a[2][kScanK], w[2][kScanK], g[2], prod[2], dA[2];
                 float h[2], prefix[2], enter[2];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     const float a2 = A[s0 + i + j] * kLog2e;
-                    enter[j] = l.live && s0 + i + j < S ? enter_row[s0 + i + j] : 0.f;
+                    enter[j] = enter_states[s0 + i + j];
                     float b[kScanK];
                     read_tile(B_tile[i + j], l.lane, b);
 #pragma unroll
@@ -149,7 +243,7 @@ __global__ __launch_bounds__(kScanThreads) void selective_scan_backward(ScanPara
                         w[j][k] = product<FLAGS>(a[j][k], h[j]);
                         h[j] = fmaf(b[k], dtu[k], w[j][k]);
                         v[j][8 + k] = gy[k] * h[j];
-                        y[k] = fmaf(c[j][k], h[j], y[k]);
+                        if constexpr (GATE) y[k] = fmaf(c[j][k], h[j], y[k]);
                         c[j][k] *= gy[k];  // what y's gradient adds to g
                     }
                     g[j] = c[j][kScanK - 1];
@@ -178,65 +272,113 @@ __global__ __launch_bounds__(kScanThreads) void selective_scan_backward(ScanPara
                         dA[j] = fmaf(q, dt[k], dA[j]);  // at a start w is 0, and dt put to 0
                         grad_dt[k] = fmaf(q, A_s, grad_dt[k]);
                     }
-                    bc[wave][i + j][threadIdx.x & (kWave - 1)] = sum_rows(v[j]);
+                    bc[quad][i + j][in_wave] = sum_rows(v[j]);
                 }
                 row_sum(dA);
-                if (l.lane == kScanLanes - 1)
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) grad_A[s0 + i + j] += dA[j];
+                for (int j = 0; j < 2; ++j)  // all lanes of the row write the same value
+                    grad_A[s0 + i + j] += row_last<false>(dA[j]);
+            }
+            buffer ^= 1;
+            if constexpr (SPLIT > 1) {
+                if (s0 + kScanStates >= S) {  // the tile's last stage
+#pragma unroll
+                    for (int k = 0; k < kScanK; ++k) {
+                        after[wave][k][in_wave] = gB[k];
+                        after[wave][kScanK + k][in_wave] = grad_dt[k];
+                        if constexpr (GATE) after[wave][2 * kScanK + k][in_wave] = y[k];
+                    }
+                }
             }
             __syncthreads();
             // lane x of a wave holds, for state i, four steps of grad_B (rows 0
             // and 1) or grad_C (rows 2 and 3)
-            for (int j = threadIdx.x; j < count * kWave; j += kScanThreads) {
+            for (int j = threadIdx.x; j < count * kWave; j += kThreads) {
                 const int i = j / kWave, x = j % kWave, q = x / kScanLanes;
                 float4v sum = bc[0][i][x];
 #pragma unroll
-                for (int m = 1; m < kScanWaves; ++m) sum += bc[m][i][x];
+                for (int m = 1; m < QUADS; ++m) sum += bc[m][i][x];
                 float *to = partials + ((int64_t)(q >> 1) * S + s0 + i) * p.tiles * kScanTile + t0 +
                             (x % kScanLanes) * kScanK + (q & 1) * 4;
                 *reinterpret_cast<float4v *>(to) = sum;
             }
         }
         wave_order();
+        float sum_gB[kOwn], sum_dt[kOwn], sum_y[kOwn];
+#pragma unroll
+        for (int k = 0; k < kOwn; ++k) {
+            if constexpr (SPLIT > 1) {
+                sum_gB[k] = sum_dt[k] = sum_y[k] = 0.f;
+                const int at = part * kOwn + k;
+#pragma unroll
+                for (int q = 0; q < SPLIT; ++q) {
+                    sum_gB[k] += after[quad * SPLIT + q][at][in_wave];
+                    sum_dt[k] += after[quad * SPLIT + q][kScanK + at][in_wave];
+                    if constexpr (GATE) sum_y[k] += after[quad * SPLIT + q][2 * kScanK + at][in_wave];
+                }
+            } else {
+                sum_gB[k] = gB[k];
+                sum_dt[k] = grad_dt[k];
+                sum_y[k] = y[k];
+            }
+        }
+        const int t = t0 + own;
         if (l.live && t < p.T) {
-            float gz[kScanK], gu[kScanK];
-            if (z_row != nullptr) {
-                float z[kScanK], go[kScanK];
-                load_steps<kScanK>(z_row + t, end - t, z);
-                load_steps<kScanK>(g_row + t, end - t, go);
+            float own_u[kOwn], raw[kOwn], out_u[kOwn], out_delta[kOwn], own_gy[kOwn];
+            u.widen(own_u);
+            delta.widen(raw);
+            go.widen(own_gy);
+            if constexpr (GATE) {
+                float own_z[kOwn], out_z[kOwn];
+                z.widen(own_z);
 #pragma unroll
-                for (int k = 0; k < kScanK; ++k)
-                    gz[k] = t + k < end ? go[k] * y[k] * silu_slope(z[k], sigmoid(z[k])) : 0.f;
-                store_steps<kScanK>(static_cast<E *>(p.grad_z) + out_row + t, p.T - t, gz);
+                for (int k = 0; k < kOwn; ++k) {
+                    const float sig = sigmoid(own_z[k]);
+                    const float y0 = fmaf(skip, own_u[k], sum_y[k]);
+                    out_z[k] = t + k < end ? own_gy[k] * y0 * silu_slope(own_z[k], sig) : 0.f;
+                    own_gy[k] *= own_z[k] * sig;
+                }
+                store_steps<kOwn>(grad_z + t0, p.T - t, out_z);
             }
 #pragma unroll
-            for (int k = 0; k < kScanK; ++k) {
+            for (int k = 0; k < kOwn; ++k) {
                 const bool in = t + k < end;
-                // an episode's first step has its dt put to 0 for a alone
-                const float step = !FLAGS || cut[k] == 0.f ? dt[k]
-                                   : p.softplus != 0       ? softplus(raw[k])
-                                                           : raw[k];
-                gu[k] = in ? fmaf(step, gB[k], skip * gy[k]) : 0.f;
-                float gd = fmaf(u[k], gB[k], grad_dt[k]);
+                raw[k] += bias;
+                const float step = p.softplus != 0 ? softplus(raw[k]) : raw[k];
+                out_u[k] = in ? fmaf(step, sum_gB[k], skip * own_gy[k]) : 0.f;
+                float gd = fmaf(own_u[k], sum_gB[k], sum_dt[k]);
                 if (p.softplus != 0) gd *= sigmoid(raw[k]);
-                grad_dt[k] = in ? gd : 0.f;
-                grad_D += in ? gy[k] * u[k] : 0.f;
-                grad_bias += grad_dt[k];
+                out_delta[k] = in ? gd : 0.f;
+                totals[0] += in ? own_gy[k] * own_u[k] : 0.f;
+                totals[1] += out_delta[k];
             }
-            store_steps<kScanK>(static_cast<E *>(p.grad_u) + out_row + t, p.T - t, gu);
-            store_steps<kScanK>(static_cast<E *>(p.grad_delta) + out_row + t, p.T - t, grad_dt);
+            store_steps<kOwn>(grad_u + t0, p.T - t, out_u);
+            store_steps<kOwn>(grad_delta + t0, p.T - t, out_delta);
         }
     }
-    float totals[2] = {grad_D, grad_bias};
     row_sum(totals);
+    if constexpr (SPLIT > 1) {  // the parts' totals, in order
+        __syncthreads();
+        if (l.lane == kScanLanes - 1)
+#pragma unroll
+            for (int q = 0; q < 2; ++q) after[wave][q][in_wave] = totals[q];
+        __syncthreads();
+        if (l.lane == kScanLanes - 1)
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                totals[q] = 0.f;
+#pragma unroll
+                for (int m = 0; m < SPLIT; ++m) totals[q] += after[quad * SPLIT + m][q][in_wave];
+            }
+    }
     if (!l.live) return;
     float *out = p.row_partials + (int64_t)l.row * (S + 2);
-    for (int s = l.lane; s < S; s += kScanLanes) {
-        out[s] = grad_A[s];
-        if (p.grad_state != nullptr) p.grad_state[(int64_t)l.row * S + s] = carry[s];
-    }
-    if (l.lane == kScanLanes - 1) {
+    for (int s = l.lane; s < S; s += kScanLanes)
+        if (mine(s)) {
+            out[s] = grad_A[s];
+            if (p.grad_state != nullptr) p.grad_state[(int64_t)l.row * S + s] = carry[s];
+        }
+    if (part == 0 && l.lane == kScanLanes - 1) {
         out[S] = totals[0];
         out[S + 1] = totals[1];
     }
@@ -270,10 +412,11 @@ __global__ __launch_bounds__(kScanThreads) void bc_sums(BcSums p) {
                 ((int64_t)ng * p.states + s) * p.T;
         for (int t = ((int)(blockIdx.y << p.lane_bits) + lane) * 4; t < p.T;
              t += (int)(gridDim.y << p.lane_bits) * 4) {
-            float4v sum = *reinterpret_cast<const float4v *>(from + t);
+            float4v sum = {};
+            if (t < end)  // beyond, nothing was written
 #pragma unroll 4
-            for (uint32_t b = 1; b < p.blocks; ++b)
-                sum += *reinterpret_cast<const float4v *>(from + b * step + t);
+                for (uint32_t b = 0; b < p.blocks; ++b)
+                    sum += *reinterpret_cast<const float4v *>(from + b * step + t);
             float v[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) v[k] = t + k < end ? sum[k] : 0.f;
@@ -327,12 +470,40 @@ struct Workspace {
     size_t bc, rows;  // floats
 };
 
+struct Shape {
+    int split, quads;
+    int rows() const { return 4 * quads; }
+};
+
+static Shape shape_of(const rlca_scan_call &c) {
+    const char *e = getenv("BSHAPE");
+    if (e) return {atoi(e) / 10, atoi(e) % 10};
+    return {1, 4};
+}
+
 static Workspace workspace_of(const rlca_scan_call &c) {
     const int64_t tiles = (c.T + kScanTile - 1) / kScanTile;
     const int64_t per_group = c.groups == 0 ? 0 : c.channels / c.groups;
-    const int64_t blocks = c.num_seqs * c.groups * ((per_group + kScanRows - 1) / kScanRows);
+    const int rows = shape_of(c).rows();
+    const int64_t blocks = c.num_seqs * c.groups * ((per_group + rows - 1) / rows);
     return {(size_t)(blocks * 2 * c.states * tiles * kScanTile),
             (size_t)(c.num_seqs * c.channels * (c.states + 2))};
+}
+
+template <typename E, int SPLIT, int QUADS>
+static const void *backward_kernel(const rlca_scan_call &c) {
+    const bool flags = c.flags != nullptr, gate = c.z != nullptr;
+    return flags ? (gate ? (const void *)selective_scan_backward<E, true, true, SPLIT, QUADS>
+                         : (const void *)selective_scan_backward<E, true, false, SPLIT, QUADS>)
+                 : (gate ? (const void *)selective_scan_backward<E, false, true, SPLIT, QUADS>
+                         : (const void *)selective_scan_backward<E, false, false, SPLIT, QUADS>);
+}
+
+template <typename E>
+static const void *backward_kernel(const rlca_scan_call &c, Shape s) {
+    return s.split == 2 ? backward_kernel<E, 2, 4>(c)
+           : s.quads == 8 ? backward_kernel<E, 1, 8>(c)
+                          : backward_kernel<E, 1, 4>(c);
 }
 
 }  // namespace seq
@@ -362,21 +533,17 @@ rlca_status rlca_selective_scan_backward(const rlca_scan_call *call, void *works
     if (st != RLCA_OK) return st;
     if (workspace_bytes < (w.bc + w.rows) * 4) return RLCA_ERR_INVALID_SIZE;
     if (c.channels == 0) return RLCA_OK;
-    ScanParams p = scan_params(c);
+    const Shape shape = shape_of(c);
+    ScanParams p = scan_params(c, shape.rows());
     p.bc_partials = static_cast<float *>(workspace);
     p.row_partials = p.bc_partials + w.bc;
-    const bool flags = c.flags != nullptr;
     if (c.num_seqs != 0) {
-        const void *kernel =
-            c.dtype == RLCA_F32    ? (flags ? (const void *)selective_scan_backward<float, true>
-                                            : (const void *)selective_scan_backward<float, false>)
-            : c.dtype == RLCA_BF16 ? (flags ? (const void *)selective_scan_backward<__bf16, true>
-                                            : (const void *)selective_scan_backward<__bf16, false>)
-                                   : (flags
-                                          ? (const void *)selective_scan_backward<_Float16, true>
-                                          : (const void *)selective_scan_backward<_Float16, false>);
-        st = launch(kernel, dim3(p.num_seqs * p.groups * p.blocks_per_group), kScanThreads,
-                    3 * kScanRows * padded_states(c.states) * 4, p, stream);
+        const void *kernel = c.dtype == RLCA_F32    ? backward_kernel<float>(c, shape)
+                             : c.dtype == RLCA_BF16 ? backward_kernel<__bf16>(c, shape)
+                                                    : backward_kernel<_Float16>(c, shape);
+        st = launch(kernel, dim3(p.num_seqs * p.groups * p.blocks_per_group),
+                    rlca::kWave * shape.split * shape.quads,
+                    4 * shape.rows() * padded_states(c.states) * 4, p, stream);
         if (st != RLCA_OK) return st;
         if (p.T != 0) {
             BcSums b = {};

@@ -26,6 +26,7 @@ __global__ __launch_bounds__(kScanThreads, sizeof(E) == 2 && !FLAGS ? 4 : 3) voi
     __shared__ TileRow tiles[2][2][kForwardStates];  // [buffer][B, C][state]
     __shared__ float steps[kQuads][SPLIT > 1 ? (FLAGS ? 3 : 2) * kScanK : 1][kWave];
     __shared__ float sums[SPLIT > 1 ? kScanWaves : 1][SPLIT > 1 ? kScanK : 1][kWave];
+    __shared__ uint32_t stage_tame[2][kScanWaves];  // [buffer]: whether what a wave staged is
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int in_wave = threadIdx.x % kWave;
     const int quad = wave / SPLIT, part = wave % SPLIT;
@@ -36,10 +37,13 @@ __global__ __launch_bounds__(kScanThreads, sizeof(E) == 2 && !FLAGS ? 4 : 3) voi
     float *A2 = carry + kRows * padded;
     // a wave initialises and hands on the states that it computes
     const auto mine = [&](int s) { return SPLIT == 1 || (s / 2) % SPLIT == part; };
+    bool decays = true;
     for (int s = l.lane; s < padded; s += kScanLanes)
         if (mine(s)) {
+            const float x = s >= S ? 0.f : p.A[(int64_t)l.d * S + s] * kLog2e;
             carry[s] = p.state == nullptr || s >= S ? 0.f : p.state[(int64_t)l.row * S + s];
-            A2[s] = s >= S ? 0.f : p.A[(int64_t)l.d * S + s] * kLog2e;
+            A2[s] = x;
+            if constexpr (FLAGS) decays &= x <= 0.f && tame(x, kTameStep);
         }
     const int end = row_end(p.lengths, l.n, p.T);
     const int own = l.lane * kScanK + part * kOwn;  // the lane's own steps in a tile
@@ -80,6 +84,10 @@ __global__ __launch_bounds__(kScanThreads, sizeof(E) == 2 && !FLAGS ? 4 : 3) voi
         if (p.checkpoints != nullptr && l.live)
             for (int s = l.lane; s < S; s += kScanLanes)
                 if (mine(s)) p.checkpoints[((int64_t)l.row * p.tiles + tile) * S + s] = carry[s];
+        bool all_ok = decays;  // of the lane's values in this tile: tame
+        if constexpr (FLAGS)
+            for (int s = l.lane; s < padded; s += kScanLanes)
+                if (mine(s)) all_ok &= tame(carry[s], kTameState);
         float skipped[kOwn], dt[kScanK], dtu[kScanK], cut[kScanK], y[kScanK] = {};
         Steps<kOwn, E> z;
         if (z_row != nullptr) z.load(z_row + t0, end - t0 - own);
@@ -109,6 +117,10 @@ __global__ __launch_bounds__(kScanThreads, sizeof(E) == 2 && !FLAGS ? 4 : 3) voi
         bool starts = false;
         for (int s0 = 0; s0 < S; s0 += kForwardStates) {
             stage(tiles[buffer][stage_c][stage_s], next_stage, l.lane);
+            if constexpr (FLAGS) {
+                const bool ok = whole_wave(all_tame(next_stage));
+                if (in_wave == 0) stage_tame[buffer][wave] = ok ? 1u : 0u;
+            }
             if (s0 + kForwardStates < S)
                 load_stage(t0, s0 + kForwardStates);
             else if (tile + 1 < live_tiles)
@@ -125,38 +137,53 @@ __global__ __launch_bounds__(kScanThreads, sizeof(E) == 2 && !FLAGS ? 4 : 3) voi
                     dt_sum += dt[k];
                     if constexpr (FLAGS) starts |= cut[k] != 0.f;
                 }
+                if constexpr (FLAGS) all_ok = whole_wave(all_ok && steps_tame(dt, dtu));
             }
             const TileRow *B_tile = tiles[buffer][0], *C_tile = tiles[buffer][1];
             const int count = S - s0 < kForwardStates ? S - s0 : kForwardStates;
-            for (int i = 2 * part; i < count; i += 2 * SPLIT) {
-                float a[2][kScanK], b[2][kScanK], h[2], prod[2], enter[2];
+            const auto scan_states = [&](auto careful) {
+                constexpr bool CUT = decltype(careful)::value;
+                for (int i = 2 * part; i < count; i += 2 * SPLIT) {
+                    float a[2][kScanK], b[2][kScanK], h[2], prod[2], enter[2];
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const float a2 = A2[s0 + i + j];
-                    enter[j] = carry[s0 + i + j];
-                    read_tile(B_tile[i + j], l.lane, b[j]);
+                    for (int j = 0; j < 2; ++j) {
+                        const float a2 = A2[s0 + i + j];
+                        enter[j] = carry[s0 + i + j];
+                        read_tile(B_tile[i + j], l.lane, b[j]);
 #pragma unroll
-                    for (int k = 0; k < kScanK; ++k) {
-                        a[j][k] = decay<FLAGS>(dt[k], cut[k], a2);
-                        b[j][k] *= dtu[k];
-                        h[j] = k == 0 ? b[j][0] : step_map<FLAGS>(a[j][k], b[j][k], h[j]);
+                        for (int k = 0; k < kScanK; ++k) {
+                            a[j][k] = decay<FLAGS>(dt[k], cut[k], a2);
+                            b[j][k] *= dtu[k];
+                            h[j] = k == 0 ? b[j][0] : step_map<CUT>(a[j][k], b[j][k], h[j]);
+                        }
+                        prod[j] = lane_product<FLAGS>(dt_sum, starts, a2);
                     }
-                    prod[j] = lane_product<FLAGS>(dt_sum, starts, a2);
-                }
-                row_scan<FLAGS, false>(prod, h);
+                    row_scan<CUT, false>(prod, h);
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const float after = step_map<FLAGS>(prod[j], h[j], enter[j]);
-                    carry[s0 + i + j] = row_last<false>(after);
-                    h[j] = row_shift<false>(after, enter[j]);
-                    float c[kScanK];
-                    read_tile(C_tile[i + j], l.lane, c);
+                    for (int j = 0; j < 2; ++j) {
+                        const float after = step_map<CUT>(prod[j], h[j], enter[j]);
+                        carry[s0 + i + j] = row_last<false>(after);
+                        h[j] = row_shift<false>(after, enter[j]);
+                        float c[kScanK];
+                        read_tile(C_tile[i + j], l.lane, c);
 #pragma unroll
-                    for (int k = 0; k < kScanK; ++k) {
-                        h[j] = step_map<FLAGS>(a[j][k], b[j][k], h[j]);
-                        y[k] = fmaf(c[k], h[j], y[k]);
+                        for (int k = 0; k < kScanK; ++k) {
+                            h[j] = step_map<CUT>(a[j][k], b[j][k], h[j]);
+                            y[k] = fmaf(c[k], h[j], y[k]);
+                        }
                     }
                 }
+            };
+            if constexpr (FLAGS) {
+                uint32_t staged = 1u;
+#pragma unroll
+                for (int w = 0; w < kScanWaves; ++w) staged &= stage_tame[buffer][w];
+                if (all_ok && __builtin_amdgcn_readfirstlane(staged) != 0u)
+                    scan_states(std::false_type{});
+                else
+                    scan_states(std::true_type{});
+            } else {
+                scan_states(std::false_type{});
             }
             buffer ^= 1;
         }

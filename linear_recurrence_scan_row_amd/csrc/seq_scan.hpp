@@ -78,18 +78,19 @@ __device__ __forceinline__ ScanLane scan_lane(const ScanParams &p, int local, ui
 
 // One map: a later run's (a, h) after an earlier run's (pa, ph).  CUT: the
 // runs may hold episode starts, where a is 0 and whatever lies before, a NaN
-// or infinity too, must not pass (apply_map and compose of scan_core.hpp, with
-// the legacy multiply whose product with 0 is 0; a is never infinite there,
-// exp(dt A) <= 1 for A <= 0).  Without starts a plain fused step.
+// or infinity too, must not pass, so the product is selected away (as in
+// apply_map and compose of scan_core.hpp).  Otherwise a plain fused step, which
+// is enough for rows with starts too while all values are tame (below): 0
+// times a finite number is 0.  For finite values both give the same bits.
 template <bool CUT>
 __device__ __forceinline__ float step_map(float a, float b, float h) {
-    if constexpr (CUT) return b + rlca_fmul_legacy(a, h);
+    if constexpr (CUT) return a == 0.f ? b : fmaf(a, h, b);
     return fmaf(a, h, b);
 }
 
 template <bool CUT>
 __device__ __forceinline__ float product(float a, float b) {
-    if constexpr (CUT) return rlca_fmul_legacy(a, b);
+    if constexpr (CUT) return a == 0.f ? 0.f : a * b;
     return a * b;
 }
 
@@ -221,6 +222,36 @@ __device__ __forceinline__ float lane_product(float dt_sum, bool starts, float A
 template <bool FLAGS>
 __device__ __forceinline__ float decay(float dt, float cut, float A2) {
     return exp2_fast(FLAGS ? fmaf(dt, A2, cut) : dt * A2);
+}
+
+// Tame values: too small for any state, gradient or product of the scans to
+// overflow within a tile.  With a in [0, 1] (dt >= 0 and A <= 0), dt u, B, C and
+// gy below 2^40 and entering values below 2^100, sums over 128 steps stay
+// below 2^101.  A NaN is not tame.
+constexpr float kTameStep = 0x1p40f, kTameState = 0x1p100f;
+__device__ __forceinline__ bool tame(float x, float limit) { return fabsf(x) < limit; }
+
+template <int K, typename E>
+__device__ __forceinline__ bool all_tame(const Steps<K, E> &s) {
+    float v[K];
+    s.widen(v);
+    bool ok = true;
+#pragma unroll
+    for (int k = 0; k < K; ++k) ok &= tame(v[k], kTameStep);
+    return ok;
+}
+
+// Whether a lane's steps are: dt not negative, dt and dt u small.
+__device__ __forceinline__ bool steps_tame(const float (&dt)[kScanK], const float (&dtu)[kScanK]) {
+    bool ok = true;
+#pragma unroll
+    for (int k = 0; k < kScanK; ++k)
+        ok &= dt[k] >= 0.f && tame(dt[k], kTameStep) && tame(dtu[k], kTameStep);
+    return ok;
+}
+
+__device__ __forceinline__ bool whole_wave(bool x) {
+    return __builtin_amdgcn_ballot_w64(!x) == 0;
 }
 
 ScanParams scan_params(const rlca_scan_call &c, int rows);

@@ -56,18 +56,20 @@ __device__ __forceinline__ void row_sum(float (&x)[2]) {
 #undef RLCA_STEP
 }
 
-// The shape of a workgroup: QUADS sets of four channels, SPLIT waves to each.
-// Waves of one quad take every SPLIT-th pair of states, and prepare and finish
-// 8 / SPLIT of a lane's steps, as in the forward scan.
-template <typename E, bool FLAGS, bool GATE, int SPLIT, int QUADS>
-__global__ __launch_bounds__(kWave *SPLIT *QUADS, 2) void selective_scan_backward(ScanParams p) {
-    constexpr int kRows = 4 * QUADS, kOwn = kScanK / SPLIT, kThreads = kWave * SPLIT * QUADS;
+// A workgroup holds four sets of four channels, SPLIT waves to each.  Waves of
+// one set take every SPLIT-th pair of states, and prepare and finish 8 / SPLIT
+// of a lane's steps, as in the forward scan.
+template <typename E, bool FLAGS, bool GATE, int SPLIT>
+__global__ __launch_bounds__(kScanThreads *SPLIT, 2) void selective_scan_backward(ScanParams p) {
+    constexpr int kQuads = kScanWaves, kRows = kScanRows;
+    constexpr int kOwn = kScanK / SPLIT, kThreads = kScanThreads * SPLIT;
     constexpr int kBefore = FLAGS ? 4 : 3, kAfter = GATE ? 3 : 2;  // values a step that waves share
     extern __shared__ __attribute__((aligned(16))) char lds_bytes[];
     __shared__ TileRow tiles[2][2][kScanStates];  // [buffer][B, C][state]
-    __shared__ float4v bc[QUADS][kScanStates][kWave];
-    __shared__ float before[SPLIT > 1 ? QUADS : 1][SPLIT > 1 ? kBefore * kScanK : 1][kWave];
-    __shared__ float after[SPLIT > 1 ? SPLIT * QUADS : 1][SPLIT > 1 ? kAfter * kScanK : 1][kWave];
+    __shared__ float4v bc[kQuads][kScanStates][kWave];
+    __shared__ float before[SPLIT > 1 ? kQuads : 1][SPLIT > 1 ? kBefore * kScanK : 1][kWave];
+    __shared__ float after[SPLIT > 1 ? SPLIT * kQuads : 1][SPLIT > 1 ? kAfter * kScanK : 1][kWave];
+    __shared__ uint32_t stage_tame[2][kThreads / kWave];  // [buffer]: whether what a wave staged is
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int in_wave = threadIdx.x % kWave;
     const int quad = wave / SPLIT, part = wave % SPLIT;
@@ -84,9 +86,12 @@ __global__ __launch_bounds__(kWave *SPLIT *QUADS, 2) void selective_scan_backwar
     const int end = l.live ? row_steps : 0;  // a clamped row computes on zeros
     const uint8_t *flags = FLAGS ? p.flags + (int64_t)l.n * p.T : nullptr;
     const bool over = FLAGS && p.after_done != 0 && end > 0 && flags[end - 1] != 0;
+    bool decays = true;
     for (int s = l.lane; s < padded; s += kScanLanes)
         if (mine(s)) {
-            A[s] = s >= S ? 0.f : p.A[(int64_t)l.d * S + s];
+            const float x = s >= S ? 0.f : p.A[(int64_t)l.d * S + s];
+            A[s] = x;
+            if constexpr (FLAGS) decays &= x <= 0.f && tame(x, kTameStep);
             carry[s] = p.grad_final == nullptr || over || !l.live || s >= S
                            ? 0.f
                            : p.grad_final[(int64_t)l.row * S + s];
@@ -138,7 +143,10 @@ __global__ __launch_bounds__(kWave *SPLIT *QUADS, 2) void selective_scan_backwar
         if constexpr (GATE) store_steps<kOwn>(grad_z + t0, n, zeros);
     }
     // Each tile's rows are loaded a tile ahead, where registers allow it.
-    constexpr bool kAhead = !GATE || (sizeof(E) == 2 && !(FLAGS && QUADS == 8)) || SPLIT > 1;
+    constexpr bool kAhead = !GATE || ((sizeof(E) == 2 || SPLIT > 1) && !FLAGS);
+    // With both episodes and a gate they are loaded again at a tile's end instead
+    // of kept over its states.
+    constexpr bool kReload = FLAGS && GATE;
     int buffer = 0;
     if (live_tiles > 0) {  // an empty row has no last tile
         load_stage((live_tiles - 1) * kScanTile, 0);
@@ -147,6 +155,7 @@ __global__ __launch_bounds__(kWave *SPLIT *QUADS, 2) void selective_scan_backwar
 
     for (int tile = live_tiles - 1; tile >= 0; --tile) {
         const int t0 = tile * kScanTile;
+        bool all_ok = decays;  // of the lane's values in this tile: tame
         if constexpr (!kAhead) load_tile(t0);
         u = next_u;
         delta = next_delta;
@@ -155,7 +164,12 @@ __global__ __launch_bounds__(kWave *SPLIT *QUADS, 2) void selective_scan_backwar
         {
             const float *from = p.checkpoints + ((int64_t)l.row * p.tiles + tile) * S;
             for (int s = l.lane; s < padded; s += kScanLanes)
-                if (mine(s)) enter_states[s] = l.live && s < S ? from[s] : 0.f;
+                if (mine(s)) {
+                    const float x = l.live && s < S ? from[s] : 0.f;
+                    enter_states[s] = x;
+                    if constexpr (FLAGS)
+                        all_ok &= tame(x, kTameState) && tame(carry[s], kTameState);
+                }
         }
         if (kAhead && tile > 0) load_tile(t0 - kScanTile);
         float dt[kScanK], dtu[kScanK], cut[kScanK], gy[kScanK];
@@ -194,6 +208,10 @@ __global__ __launch_bounds__(kWave *SPLIT *QUADS, 2) void selective_scan_backwar
         for (int s0 = 0; s0 < S; s0 += kScanStates) {
             const int count = S - s0 < kScanStates ? S - s0 : kScanStates;
             if (stages) stage(tiles[buffer][stage_c][stage_s], next_stage, l.lane);
+            if constexpr (FLAGS) {
+                const bool ok = whole_wave(!stages || all_tame(next_stage));
+                if (in_wave == 0) stage_tame[buffer][wave] = ok ? 1u : 0u;
+            }
             if (s0 + kScanStates < S)
                 load_stage(t0, s0 + kScanStates);
             else if (tile > 0)
@@ -211,73 +229,93 @@ __global__ __launch_bounds__(kWave *SPLIT *QUADS, 2) void selective_scan_backwar
                     dt_sum += dt[k];
                     if constexpr (FLAGS) starts |= cut[k] != 0.f;
                 }
+                if constexpr (FLAGS) {
+                    all_ok &= steps_tame(dt, dtu);
+#pragma unroll
+                    for (int k = 0; k < kScanK; ++k) all_ok &= tame(gy[k], kTameStep);
+                    all_ok = whole_wave(all_ok);
+                }
             }
             const TileRow *B_tile = tiles[buffer][0], *C_tile = tiles[buffer][1];
-            for (int i = 2 * part; i < count; i += 2 * SPLIT) {
-                float a[2][kScanK], w[2][kScanK], g[2], prod[2], dA[2];
-                float h[2], prefix[2], enter[2];
+            const auto scan_states = [&](auto careful) {
+                constexpr bool CUT = decltype(careful)::value;
+                for (int i = 2 * part; i < count; i += 2 * SPLIT) {
+                    float a[2][kScanK], w[2][kScanK], g[2], prod[2], dA[2];
+                    float h[2], prefix[2], enter[2];
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const float a2 = A[s0 + i + j] * kLog2e;
-                    enter[j] = enter_states[s0 + i + j];
-                    float b[kScanK];
-                    read_tile(B_tile[i + j], l.lane, b);
+                    for (int j = 0; j < 2; ++j) {
+                        const float a2 = A[s0 + i + j] * kLog2e;
+                        enter[j] = enter_states[s0 + i + j];
+                        float b[kScanK];
+                        read_tile(B_tile[i + j], l.lane, b);
 #pragma unroll
-                    for (int k = 0; k < kScanK; ++k) {
-                        a[j][k] = decay<FLAGS>(dt[k], cut[k], a2);
-                        const float x = b[k] * dtu[k];
-                        h[j] = k == 0 ? x : step_map<FLAGS>(a[j][k], x, h[j]);
+                        for (int k = 0; k < kScanK; ++k) {
+                            a[j][k] = decay<FLAGS>(dt[k], cut[k], a2);
+                            const float x = b[k] * dtu[k];
+                            h[j] = k == 0 ? x : step_map<CUT>(a[j][k], x, h[j]);
+                        }
+                        prefix[j] = prod[j] = lane_product<FLAGS>(dt_sum, starts, a2);
                     }
-                    prefix[j] = prod[j] = lane_product<FLAGS>(dt_sum, starts, a2);
-                }
-                row_scan<FLAGS, false>(prefix, h);
-                float v[2][16], r[2], c[2][kScanK];
+                    row_scan<CUT, false>(prefix, h);
+                    float v[2][16], r[2], c[2][kScanK];
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    h[j] = row_shift<false>(step_map<FLAGS>(prefix[j], h[j], enter[j]), enter[j]);
-                    float b[kScanK];
-                    read_tile(B_tile[i + j], l.lane, b);
-                    read_tile(C_tile[i + j], l.lane, c[j]);
+                    for (int j = 0; j < 2; ++j) {
+                        h[j] = row_shift<false>(step_map<CUT>(prefix[j], h[j], enter[j]), enter[j]);
+                        float b[kScanK];
+                        read_tile(B_tile[i + j], l.lane, b);
+                        read_tile(C_tile[i + j], l.lane, c[j]);
 #pragma unroll
-                    for (int k = 0; k < kScanK; ++k) {
-                        w[j][k] = product<FLAGS>(a[j][k], h[j]);
-                        h[j] = fmaf(b[k], dtu[k], w[j][k]);
-                        v[j][8 + k] = gy[k] * h[j];
-                        if constexpr (GATE) y[k] = fmaf(c[j][k], h[j], y[k]);
-                        c[j][k] *= gy[k];  // what y's gradient adds to g
+                        for (int k = 0; k < kScanK; ++k) {
+                            w[j][k] = product<CUT>(a[j][k], h[j]);
+                            h[j] = fmaf(b[k], dtu[k], w[j][k]);
+                            v[j][8 + k] = gy[k] * h[j];
+                            if constexpr (GATE) y[k] = fmaf(c[j][k], h[j], y[k]);
+                            c[j][k] *= gy[k];  // what y's gradient adds to g
+                        }
+                        g[j] = c[j][kScanK - 1];
+#pragma unroll
+                        for (int k = kScanK - 2; k >= 0; --k)
+                            g[j] = step_map<CUT>(a[j][k + 1], c[j][k], g[j]);
+                        r[j] = product<CUT>(a[j][0], g[j]);
                     }
-                    g[j] = c[j][kScanK - 1];
+                    row_scan<CUT, true>(prod, r);
 #pragma unroll
-                    for (int k = kScanK - 2; k >= 0; --k)
-                        g[j] = step_map<FLAGS>(a[j][k + 1], c[j][k], g[j]);
-                    r[j] = product<FLAGS>(a[j][0], g[j]);
-                }
-                row_scan<FLAGS, true>(prod, r);
+                    for (int j = 0; j < 2; ++j) {
+                        const float right = carry[s0 + i + j], A_s = A[s0 + i + j];
+                        r[j] = step_map<CUT>(prod[j], r[j], right);
+                        carry[s0 + i + j] = row_last<true>(r[j]);
+                        g[j] = row_shift<true>(r[j], right);  // a_{t+8} g_{t+8}
+                        float b[kScanK];
+                        read_tile(B_tile[i + j], l.lane, b);
+                        dA[j] = 0.f;
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const float right = carry[s0 + i + j], A_s = A[s0 + i + j];
-                    r[j] = step_map<FLAGS>(prod[j], r[j], right);
-                    carry[s0 + i + j] = row_last<true>(r[j]);
-                    g[j] = row_shift<true>(r[j], right);  // a_{t+8} g_{t+8}
-                    float b[kScanK];
-                    read_tile(B_tile[i + j], l.lane, b);
-                    dA[j] = 0.f;
-#pragma unroll
-                    for (int k = kScanK - 1; k >= 0; --k) {
-                        g[j] = k == kScanK - 1 ? c[j][k] + g[j]
-                                               : step_map<FLAGS>(a[j][k + 1], c[j][k], g[j]);
-                        v[j][k] = g[j] * dtu[k];
-                        gB[k] = fmaf(g[j], b[k], gB[k]);
-                        const float q = g[j] * w[j][k];
-                        dA[j] = fmaf(q, dt[k], dA[j]);  // at a start w is 0, and dt put to 0
-                        grad_dt[k] = fmaf(q, A_s, grad_dt[k]);
+                        for (int k = kScanK - 1; k >= 0; --k) {
+                            g[j] = k == kScanK - 1 ? c[j][k] + g[j]
+                                                   : step_map<CUT>(a[j][k + 1], c[j][k], g[j]);
+                            v[j][k] = g[j] * dtu[k];
+                            gB[k] = fmaf(g[j], b[k], gB[k]);
+                            const float q = g[j] * w[j][k];
+                            dA[j] = fmaf(q, dt[k], dA[j]);  // at a start w is 0, and dt put to 0
+                            grad_dt[k] = fmaf(q, A_s, grad_dt[k]);
+                        }
+                        bc[quad][i + j][in_wave] = sum_rows(v[j]);
                     }
-                    bc[quad][i + j][in_wave] = sum_rows(v[j]);
-                }
-                row_sum(dA);
+                    row_sum(dA);
 #pragma unroll
-                for (int j = 0; j < 2; ++j)  // all lanes of the row write the same value
-                    grad_A[s0 + i + j] += row_last<false>(dA[j]);
+                    for (int j = 0; j < 2; ++j)  // all lanes of the row write the same value
+                        grad_A[s0 + i + j] += row_last<false>(dA[j]);
+                }
+            };
+            if constexpr (FLAGS) {
+                uint32_t staged = 1u;
+#pragma unroll
+                for (int w = 0; w < kThreads / kWave; ++w) staged &= stage_tame[buffer][w];
+                if (all_ok && __builtin_amdgcn_readfirstlane(staged) != 0u)
+                    scan_states(std::false_type{});
+                else
+                    scan_states(std::true_type{});
+            } else {
+                scan_states(std::false_type{});
             }
             buffer ^= 1;
             if constexpr (SPLIT > 1) {
@@ -297,7 +335,7 @@ __global__ __launch_bounds__(kWave *SPLIT *QUADS, 2) void selective_scan_backwar
                 const int i = j / kWave, x = j % kWave, q = x / kScanLanes;
                 float4v sum = bc[0][i][x];
 #pragma unroll
-                for (int m = 1; m < QUADS; ++m) sum += bc[m][i][x];
+                for (int m = 1; m < kQuads; ++m) sum += bc[m][i][x];
                 float *to = partials + ((int64_t)(q >> 1) * S + s0 + i) * p.tiles * kScanTile + t0 +
                             (x % kScanLanes) * kScanK + (q & 1) * 4;
                 *reinterpret_cast<float4v *>(to) = sum;
@@ -325,6 +363,13 @@ __global__ __launch_bounds__(kWave *SPLIT *QUADS, 2) void selective_scan_backwar
         const int t = t0 + own;
         if (l.live && t < p.T) {
             float own_u[kOwn], raw[kOwn], out_u[kOwn], out_delta[kOwn], own_gy[kOwn];
+            if constexpr (kReload) {
+                load_tile(t0);
+                u = next_u;
+                delta = next_delta;
+                go = next_go;
+                z = next_z;
+            }
             u.widen(own_u);
             delta.widen(raw);
             go.widen(own_gy);
@@ -427,83 +472,103 @@ __global__ __launch_bounds__(kScanThreads) void bc_sums(BcSums p) {
 
 // grad_A, grad_D and grad_delta_bias: the sums over sequences, in fp64.  A
 // workgroup takes kSumValues neighbouring values; its lanes of one value take
-// every so many sequences and meet in LDS in a fixed tree.
-constexpr int kSumValues = 16, kSumThreads = 1024;
+// every so many sequences and meet in LDS in a fixed tree.  Many sequences are
+// first summed in ranges (blockIdx.y) into `ranges`, and those by a second launch.
+constexpr int kSumValues = 16, kSumThreads = 1024, kSumRange = 256;
+constexpr uint32_t kMostRanges = 1u << 15;
 
-__global__ __launch_bounds__(kSumThreads) void row_sums(const float *partials, uint32_t num_seqs,
+template <typename In>
+__global__ __launch_bounds__(kSumThreads) void row_sums(const In *partials, uint32_t parts,
                                                         uint32_t channels, uint32_t states,
+                                                        uint32_t range, double *ranges,
                                                         float *grad_A, float *grad_D,
                                                         float *grad_bias) {
     __shared__ double sums[kSumThreads];
     const int64_t width = states + 2, count = (int64_t)channels * width;
     const uint32_t lanes = blockDim.x / kSumValues;  // a power of two
     const uint32_t lane = threadIdx.x / kSumValues;
+    const uint64_t begin = (uint64_t)blockIdx.y * range;
+    const uint32_t end = begin + range < parts ? (uint32_t)(begin + range) : parts;
     for (int64_t i0 = (int64_t)blockIdx.x * kSumValues; i0 < count;
          i0 += (int64_t)gridDim.x * kSumValues) {
         const int64_t i = i0 + threadIdx.x % kSumValues;
         double sum = 0.0;
         if (i < count)
-#pragma unroll 8
-            for (uint32_t n = lane; n < num_seqs; n += lanes) sum += (double)partials[n * count + i];
+#pragma unroll 4
+            for (uint64_t n = begin + lane; n < end; n += lanes)
+                sum += (double)partials[n * count + i];
         sums[threadIdx.x] = sum;
         for (uint32_t m = lanes / 2; m > 0; m /= 2) {
             __syncthreads();
             if (lane < m) sums[threadIdx.x] += sums[threadIdx.x + m * kSumValues];
         }
         if (lane == 0 && i < count) {
-            const float total = (float)sums[threadIdx.x];
+            const double total = sums[threadIdx.x];
             const int64_t d = i / width;
             const int s = (int)(i - d * width);
-            if (s < (int)states)
-                grad_A[d * states + s] = total;
-            else if (s == (int)states) {
-                if (grad_D != nullptr) grad_D[d] = total;
+            if (ranges != nullptr) {
+                ranges[blockIdx.y * count + i] = total;
+            } else if (s < (int)states) {
+                grad_A[d * states + s] = (float)total;
+            } else if (s == (int)states) {
+                if (grad_D != nullptr) grad_D[d] = (float)total;
             } else if (grad_bias != nullptr) {
-                grad_bias[d] = total;
+                grad_bias[d] = (float)total;
             }
         }
         __syncthreads();
     }
 }
 
+// The workspace, in floats: the partial sums of grad_B and grad_C, those of
+// each sequence's rows, and (fp64) those of ranges of sequences.
 struct Workspace {
-    size_t bc, rows;  // floats
+    size_t bc, rows, ranges;
+    size_t total() const { return bc + rows + ranges; }
 };
 
-struct Shape {
-    int split, quads;
-    int rows() const { return 4 * quads; }
+// How many sequences a range holds, and how many ranges (0: too few to need them).
+struct Ranges {
+    uint32_t size, count;
 };
 
-static Shape shape_of(const rlca_scan_call &c) {
-    const char *e = getenv("BSHAPE");
-    if (e) return {atoi(e) / 10, atoi(e) % 10};
-    return {1, 4};
+static Ranges ranges_of(int64_t num_seqs) {
+    if (num_seqs <= 2 * kSumRange) return {(uint32_t)num_seqs, 0};
+    int64_t size = kSumRange;
+    while ((num_seqs + size - 1) / size > kMostRanges) size *= 2;
+    return {(uint32_t)size, (uint32_t)((num_seqs + size - 1) / size)};
+}
+
+// Waves that share four channels: two where one would leave SIMDs with a
+// single wave (SPLITB_FIGURES).
+static int split_of(const rlca_scan_call &c) {
+    const char *e = getenv("BSPLIT");
+    if (e) return atoi(e);
+    // (with more than 64 states two waves would need over 160 KB of LDS)
+    return c.num_seqs * c.channels <= 4096 && c.states > 2 && c.states <= 64 ? 2 : 1;
 }
 
 static Workspace workspace_of(const rlca_scan_call &c) {
     const int64_t tiles = (c.T + kScanTile - 1) / kScanTile;
     const int64_t per_group = c.groups == 0 ? 0 : c.channels / c.groups;
-    const int rows = shape_of(c).rows();
-    const int64_t blocks = c.num_seqs * c.groups * ((per_group + rows - 1) / rows);
+    const int64_t blocks = c.num_seqs * c.groups * ((per_group + kScanRows - 1) / kScanRows);
     return {(size_t)(blocks * 2 * c.states * tiles * kScanTile),
-            (size_t)(c.num_seqs * c.channels * (c.states + 2))};
+            (size_t)((c.num_seqs * c.channels * (c.states + 2) + 3) / 4 * 4),
+            (size_t)(2 * ranges_of(c.num_seqs).count * c.channels * (c.states + 2))};
 }
 
-template <typename E, int SPLIT, int QUADS>
+template <typename E, int SPLIT>
 static const void *backward_kernel(const rlca_scan_call &c) {
     const bool flags = c.flags != nullptr, gate = c.z != nullptr;
-    return flags ? (gate ? (const void *)selective_scan_backward<E, true, true, SPLIT, QUADS>
-                         : (const void *)selective_scan_backward<E, true, false, SPLIT, QUADS>)
-                 : (gate ? (const void *)selective_scan_backward<E, false, true, SPLIT, QUADS>
-                         : (const void *)selective_scan_backward<E, false, false, SPLIT, QUADS>);
+    return flags ? (gate ? (const void *)selective_scan_backward<E, true, true, SPLIT>
+                         : (const void *)selective_scan_backward<E, true, false, SPLIT>)
+                 : (gate ? (const void *)selective_scan_backward<E, false, true, SPLIT>
+                         : (const void *)selective_scan_backward<E, false, false, SPLIT>);
 }
 
 template <typename E>
-static const void *backward_kernel(const rlca_scan_call &c, Shape s) {
-    return s.split == 2 ? backward_kernel<E, 2, 4>(c)
-           : s.quads == 8 ? backward_kernel<E, 1, 8>(c)
-                          : backward_kernel<E, 1, 4>(c);
+static const void *backward_kernel(const rlca_scan_call &c, int split) {
+    return split == 2 ? backward_kernel<E, 2>(c) : backward_kernel<E, 1>(c);
 }
 
 }  // namespace seq
@@ -517,7 +582,7 @@ size_t rlca_selective_scan_backward_workspace_size(const rlca_scan_call *call) {
     Arrays a;
     if (call == nullptr || check_scan(*call, true, &a) != RLCA_OK) return 0;
     const Workspace w = workspace_of(*call);
-    return (w.bc + w.rows) * 4;
+    return w.total() * 4;
 }
 
 rlca_status rlca_selective_scan_backward(const rlca_scan_call *call, void *workspace,
@@ -528,22 +593,21 @@ rlca_status rlca_selective_scan_backward(const rlca_scan_call *call, void *works
     rlca_status st = check_scan(c, true, &a);
     if (st != RLCA_OK) return st;
     const Workspace w = workspace_of(c);
-    a.out(workspace, 16, true, {{(int64_t)((w.bc + w.rows + 3) / 4), 1}});
+    a.out(workspace, 16, true, {{(int64_t)((w.total() + 3) / 4), 1}});
     st = a.status();
     if (st != RLCA_OK) return st;
-    if (workspace_bytes < (w.bc + w.rows) * 4) return RLCA_ERR_INVALID_SIZE;
+    if (workspace_bytes < w.total() * 4) return RLCA_ERR_INVALID_SIZE;
     if (c.channels == 0) return RLCA_OK;
-    const Shape shape = shape_of(c);
-    ScanParams p = scan_params(c, shape.rows());
+    const int split = split_of(c);
+    ScanParams p = scan_params(c, kScanRows);
     p.bc_partials = static_cast<float *>(workspace);
     p.row_partials = p.bc_partials + w.bc;
     if (c.num_seqs != 0) {
-        const void *kernel = c.dtype == RLCA_F32    ? backward_kernel<float>(c, shape)
-                             : c.dtype == RLCA_BF16 ? backward_kernel<__bf16>(c, shape)
-                                                    : backward_kernel<_Float16>(c, shape);
+        const void *kernel = c.dtype == RLCA_F32    ? backward_kernel<float>(c, split)
+                             : c.dtype == RLCA_BF16 ? backward_kernel<__bf16>(c, split)
+                                                    : backward_kernel<_Float16>(c, split);
         st = launch(kernel, dim3(p.num_seqs * p.groups * p.blocks_per_group),
-                    rlca::kWave * shape.split * shape.quads,
-                    4 * shape.rows() * padded_states(c.states) * 4, p, stream);
+                    kScanThreads * split, 4 * kScanRows * padded_states(c.states) * 4, p, stream);
         if (st != RLCA_OK) return st;
         if (p.T != 0) {
             BcSums b = {};
@@ -569,17 +633,27 @@ rlca_status rlca_selective_scan_backward(const rlca_scan_call *call, void *works
             if (st != RLCA_OK) return st;
         }
     }
-    const float *partials = p.row_partials;
-    uint32_t num_seqs = p.num_seqs, channels = p.channels, states = p.states;
-    float *gA = c.grad_A, *gD = c.grad_D, *gb = c.grad_delta_bias;
-    void *args[] = {&partials, &num_seqs, &channels, &states, &gA, &gD, &gb};
-    const uint64_t groups = ((uint64_t)channels * (states + 2) + kSumValues - 1) / kSumValues;
-    uint32_t threads = 64;
-    while (threads < (uint32_t)kSumThreads && threads / kSumValues < num_seqs) threads *= 2;
-    const hipError_t e =
-        hipLaunchKernel((const void *)row_sums, dim3(groups < (1u << 20) ? groups : 1u << 20),
-                        dim3(threads), args, 0, stream);
-    return e == hipSuccess ? RLCA_OK : RLCA_ERR_HIP;
+    const Ranges ranges = ranges_of(c.num_seqs);
+    const uint64_t groups = ((uint64_t)p.channels * (p.states + 2) + kSumValues - 1) / kSumValues;
+    const uint32_t across = (uint32_t)(groups < (1u << 20) ? groups : 1u << 20);
+    double *range_sums = reinterpret_cast<double *>(p.row_partials + w.rows);
+    for (int pass = ranges.count == 0 ? 1 : 0; pass < 2; ++pass) {
+        // pass 0: rows into ranges; pass 1: ranges, or rows if few, into the gradients
+        const bool into_ranges = pass == 0, of_rows = into_ranges || ranges.count == 0;
+        const void *in = of_rows ? (const void *)p.row_partials : (const void *)range_sums;
+        uint32_t parts = of_rows ? p.num_seqs : ranges.count;
+        uint32_t range = into_ranges ? ranges.size : parts;
+        double *out = into_ranges ? range_sums : nullptr;
+        float *gA = c.grad_A, *gD = c.grad_D, *gb = c.grad_delta_bias;
+        void *args[] = {&in, &parts, &p.channels, &p.states, &range, &out, &gA, &gD, &gb};
+        uint32_t threads = rlca::kWave;
+        while (threads < (uint32_t)kSumThreads && threads / kSumValues < range) threads *= 2;
+        const hipError_t e = hipLaunchKernel(
+            of_rows ? (const void *)row_sums<float> : (const void *)row_sums<double>,
+            dim3(across, into_ranges ? ranges.count : 1), dim3(threads), args, 0, stream);
+        if (e != hipSuccess) return RLCA_ERR_HIP;
+    }
+    return RLCA_OK;
 }
 
 }  // extern "C"

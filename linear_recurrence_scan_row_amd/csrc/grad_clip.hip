@@ -2,8 +2,9 @@
 // scaled to at most max_norm.
 //
 // Bound by memory: every element is read for the norm, and read and written
-// again for the scaling, which cannot begin before the last element was seen
-// (the second reading of up to 256 MB comes from the last-level cache).  The
+// again for the scaling, which cannot begin before the last element was seen.
+// The scaling goes through the list from its end: what the norm read last, up
+// to 256 MB, still lies in the last-level cache.  The
 // tensors' addresses travel as kernel arguments, so nothing is copied to the
 // device; one launch takes up to kMaxTensors tensors as a list of chunks of
 // kChunk elements, so many small tensors fill the chip like one large one.
@@ -141,7 +142,8 @@ __device__ __forceinline__ void scale_chunk(const Tensor &t, uint32_t chunk, flo
 
 __global__ __launch_bounds__(kThreads) void grad_scale(Launch l) {
     const float scale = (float)load_coherent(&l.head->scale);
-    for (uint32_t c = blockIdx.x; c < l.chunks; c += gridDim.x) {
+    for (uint32_t i = blockIdx.x; i < l.chunks; i += gridDim.x) {
+        const uint32_t c = l.chunks - 1 - i;
         const Tensor &t = l.tensors[tensor_of(l, c)];
         if (scale == 1.f && t.out == t.data) continue;  // nothing changes
         const uint32_t chunk = c - t.first_chunk;
@@ -212,21 +214,38 @@ static rlca_status check_tensors(const rlca_grad_tensor *tensors, int64_t n, boo
     return st;
 }
 
-// Fills `l` with tensors from *next on, up to a launch's worth of tensors and
-// chunks (a tensor has fewer than 2^43 elements, 2^31 chunks).
-static void fill(Launch *l, const rlca_grad_tensor *tensors, int64_t n, int64_t *next) {
-    l->num_tensors = 0;
+// Fills `l` with a launch's worth of the tensors in [*begin, *end), from the
+// front or the back, and takes them out of that range; empty tensors are
+// dropped.  (A tensor has fewer than 2^43 elements, 2^31 chunks.)
+static void fill(Launch *l, const rlca_grad_tensor *tensors, int64_t *begin, int64_t *end,
+                 bool from_back) {
+    int64_t first = *begin, last = *end;  // the launch's tensors
+    uint32_t count = 0;
     uint64_t chunks = 0;
-    for (; *next < n && l->num_tensors < (uint32_t)kMaxTensors; ++*next) {
-        const rlca_grad_tensor &t = tensors[*next];
-        if (t.count == 0) continue;
-        const uint64_t c = ((uint64_t)t.count + kChunk - 1) / kChunk;
-        if (l->num_tensors != 0 && chunks + c > (1ull << 31)) break;
-        l->tensors[l->num_tensors++] = {t.data, t.out, (uint64_t)t.count, (uint32_t)chunks,
-                                        t.dtype};
+    for (int64_t left = *end - *begin; left > 0; --left) {
+        const int64_t i = from_back ? *end - 1 : *begin;
+        const uint64_t c = ((uint64_t)tensors[i].count + kChunk - 1) / kChunk;
+        if (c != 0 && (count == (uint32_t)kMaxTensors || (count != 0 && chunks + c > 1ull << 31)))
+            break;
+        if (from_back)
+            --*end;
+        else
+            ++*begin;
+        if (c != 0) ++count;
         chunks += c;
     }
-    l->chunks = (uint32_t)chunks;
+    if (from_back)
+        first = *end;
+    else
+        last = *begin;
+    l->num_tensors = 0;
+    l->chunks = 0;
+    for (int64_t i = first; i < last; ++i) {
+        const rlca_grad_tensor &t = tensors[i];
+        if (t.count == 0) continue;
+        l->tensors[l->num_tensors++] = {t.data, t.out, (uint64_t)t.count, l->chunks, t.dtype};
+        l->chunks += (uint32_t)(((uint64_t)t.count + kChunk - 1) / kChunk);
+    }
 }
 
 }  // namespace clip
@@ -256,22 +275,20 @@ extern "C" rlca_status rlca_clip_grad_norm(const rlca_grad_tensor *tensors, int6
     l.max_norm = max_norm;
     l.eps = eps;
     for (int pass = 0; pass < (scaled ? 2 : 1); ++pass) {
-        int64_t next = 0;
+        int64_t begin = 0, end = num_tensors;
         l.first = 1;
         do {
-            fill(&l, tensors, num_tensors, &next);
-            int64_t rest = next;
-            while (rest < num_tensors && tensors[rest].count == 0) ++rest;
-            l.last = rest == num_tensors;
+            fill(&l, tensors, &begin, &end, pass == 1);
+            l.last = begin == end;
             if (l.chunks != 0 || pass == 0) {
                 const uint32_t grid = l.chunks < 1 ? 1 : l.chunks < kClipGrid ? l.chunks : kClipGrid;
-                st = rlca::seq::launch(pass == 0 ? (const void *)grad_norm : (const void *)grad_scale,
-                                 dim3(grid), kThreads, 0, l, stream);
+                st = rlca::seq::launch(
+                    pass == 0 ? (const void *)grad_norm : (const void *)grad_scale, dim3(grid),
+                    kThreads, 0, l, stream);
                 if (st != RLCA_OK) return st;
             }
-            next = rest;
             l.first = 0;
-        } while (next < num_tensors);
+        } while (begin < end);
     }
     return RLCA_OK;
 }

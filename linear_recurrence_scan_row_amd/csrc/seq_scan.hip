@@ -212,8 +212,9 @@ __global__ __launch_bounds__(kScanThreads, sizeof(E) == 2 && !FLAGS ? 4 : 3) voi
 #pragma unroll
                 for (int k = 0; k < kOwn; ++k) out[k] *= silu(gate[k]);
             }
+            if (t + kOwn > end)  // few lanes
 #pragma unroll
-            for (int k = 0; k < kOwn; ++k) out[k] = t + k < end ? out[k] : 0.f;
+                for (int k = 0; k < kOwn; ++k) out[k] = t + k < end ? out[k] : 0.f;
             store_steps<kOwn>(y_row + t0, p.T - t, out);
         }
     }

@@ -195,18 +195,26 @@ __device__ __forceinline__ void make_steps(const ScanParams &p, const uint8_t *f
 #pragma unroll
     for (int k = 0; k < K; ++k) {
         raw[k] += bias;
-        const float x = p.softplus != 0 ? softplus(raw[k]) : raw[k];
-        dt[k] = t + k < end ? x : 0.f;
-        dtu[k] = t + k < end ? x * u[k] : 0.f;
+        dt[k] = p.softplus != 0 ? softplus(raw[k]) : raw[k];
+        dtu[k] = dt[k] * u[k];
+        if constexpr (FLAGS) cut[k] = 0.f;
     }
-    if constexpr (FLAGS) {
-        const uint32_t starts = start_bits<K>(flags, t, p.T, p.after_done);
+    if (t + K > end)  // few lanes
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const bool start = t + k < row_steps && (starts >> k & 1);
-            cut[k] = start ? -INFINITY : 0.f;
-            dt[k] = start ? 0.f : dt[k];
+            dt[k] = t + k < end ? dt[k] : 0.f;
+            dtu[k] = t + k < end ? dtu[k] : 0.f;
         }
+    if constexpr (FLAGS) {
+        uint32_t starts = start_bits<K>(flags, t, p.T, p.after_done);
+        if (t + K > row_steps) starts &= t < row_steps ? (1u << (row_steps - t)) - 1 : 0u;
+        if (starts != 0)
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                if (starts >> k & 1) {
+                    cut[k] = -INFINITY;
+                    dt[k] = 0.f;
+                }
     }
 }
 

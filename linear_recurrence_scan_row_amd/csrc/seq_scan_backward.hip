@@ -184,8 +184,7 @@ __global__ __launch_bounds__(kScanThreads *SPLIT, 2) void selective_scan_backwar
             if constexpr (GATE) {
                 z.widen(v);
 #pragma unroll
-                for (int k = 0; k < kOwn; ++k)
-                    own_gy[k] = t0 + own + k < end ? own_gy[k] * silu(v[k]) : 0.f;
+                for (int k = 0; k < kOwn; ++k) own_gy[k] *= silu(v[k]);  // 0 past the end
             }
 #pragma unroll
             for (int k = 0; k < kOwn; ++k) {
@@ -380,21 +379,39 @@ __global__ __launch_bounds__(kScanThreads *SPLIT, 2) void selective_scan_backwar
                 for (int k = 0; k < kOwn; ++k) {
                     const float sig = sigmoid(own_z[k]);
                     const float y0 = fmaf(skip, own_u[k], sum_y[k]);
-                    out_z[k] = t + k < end ? own_gy[k] * y0 * silu_slope(own_z[k], sig) : 0.f;
-                    own_gy[k] *= own_z[k] * sig;
+                    out_z[k] = own_gy[k] * y0 * silu_slope(own_z[k], sig);
+                    own_gy[k] = SPLIT == 1 ? gy[k] : own_gy[k] * (own_z[k] * sig);
                 }
+                if (t + kOwn > end)  // few lanes
+#pragma unroll
+                    for (int k = 0; k < kOwn; ++k) out_z[k] = t + k < end ? out_z[k] : 0.f;
                 store_steps<kOwn>(grad_z + t0, p.T - t, out_z);
             }
 #pragma unroll
             for (int k = 0; k < kOwn; ++k) {
-                const bool in = t + k < end;
                 raw[k] += bias;
-                const float step = p.softplus != 0 ? softplus(raw[k]) : raw[k];
-                out_u[k] = in ? fmaf(step, sum_gB[k], skip * own_gy[k]) : 0.f;
-                float gd = fmaf(own_u[k], sum_gB[k], sum_dt[k]);
-                if (p.softplus != 0) gd *= sigmoid(raw[k]);
-                out_delta[k] = in ? gd : 0.f;
-                totals[0] += in ? own_gy[k] * own_u[k] : 0.f;
+                // dt of this step; dt[] holds it, but for an episode's first
+                // step, and at a place that depends on the part with several
+                float step;
+                if (SPLIT == 1 && (!FLAGS || cut[k] == 0.f))
+                    step = dt[k];
+                else
+                    step = p.softplus != 0 ? softplus(raw[k]) : raw[k];
+                out_u[k] = fmaf(step, sum_gB[k], skip * own_gy[k]);
+                out_delta[k] = fmaf(own_u[k], sum_gB[k], sum_dt[k]);
+                if (p.softplus != 0) out_delta[k] *= sigmoid(raw[k]);
+            }
+            if (t + kOwn > end)  // few lanes
+#pragma unroll
+                for (int k = 0; k < kOwn; ++k) {
+                    const bool in = t + k < end;
+                    out_u[k] = in ? out_u[k] : 0.f;
+                    out_delta[k] = in ? out_delta[k] : 0.f;
+                    own_gy[k] = in ? own_gy[k] : 0.f;
+                }
+#pragma unroll
+            for (int k = 0; k < kOwn; ++k) {
+                totals[0] = fmaf(own_gy[k], own_u[k], totals[0]);
                 totals[1] += out_delta[k];
             }
             store_steps<kOwn>(grad_u + t0, p.T - t, out_u);

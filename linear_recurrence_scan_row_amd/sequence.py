@@ -132,25 +132,31 @@ def _view(name, t, shape, dtype, device):
     may have any strides that do not run backwards."""
     if t is None:
         raise ValueError(f"{name} is required")
+    # every check in one expression first; the detailed ones below name the
+    # failure
+    if t.dtype is dtype and t.shape == shape and t.device == device \
+            and (t.stride(-1) == 1 or t.shape[-1] <= 1):
+        return t
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError(f"{name} must be contiguous in its last dimension")
-    return t
+    raise ValueError(f"{name} must be contiguous in its last dimension")
 
 
 def _activations(name, t, dims):
     """[num_seqs, channels(, T)] on a GPU; its shape, device and storage type."""
-    if t.dim() != len(dims):
-        raise ValueError(f"{name} is [{', '.join(dims)}]")
-    if t.device.type != "cuda":
+    shape = t.shape
+    if len(shape) != dims:
+        raise ValueError(f"{name} is [num_seqs, channels{', T' if dims == 3 else ''}]")
+    if not t.is_cuda:
         raise ValueError("inputs must be GPU tensors")
     dtype = _real_dtype(name, t)
-    return _view(name, t, t.shape, dtype, t.device), tuple(t.shape), t.device, dtype
+    if t.stride(-1) != 1 and shape[-1] > 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+    return shape, t.device, dtype
 
 
 def _episodes(flags, lengths, N, T, dev):
@@ -182,7 +188,7 @@ def _scratch(nbytes, dev):
 
 # ------------------------------------------------------------- the convolution
 def _conv_call(x, weight, bias, state, flags, convention, lengths, silu):
-    x, (N, D, T), dev, dtype = _activations("x", x, ("num_seqs", "channels", "T"))
+    (N, D, T), dev, dtype = _activations("x", x, 3)
     if weight is None or weight.dim() != 2:
         raise ValueError("weight is [channels, width]")
     W = weight.shape[1]
@@ -192,11 +198,9 @@ def _conv_call(x, weight, bias, state, flags, convention, lengths, silu):
     b = _f32("bias", bias, (D,), dev, optional=True)
     s = _steps("state", state, (N, D, W - 1), dtype, dev, optional=True)
     f, ln = _episodes(flags, lengths, N, T, dev)
-    call = ConvCall(
-        num_seqs=N, channels=D, T=T, width=W, silu=1 if silu else 0, dtype=REAL_DTYPES[dtype],
-        convention=int(convention), x=_ptr(x), x_stride_seq=x.stride(0),
-        x_stride_channel=x.stride(1), weight=_ptr(w), bias=_ptr(b), state=_ptr(s), flags=_ptr(f),
-        lengths=_ptr(ln))
+    call = ConvCall(N, D, T, W, 1 if silu else 0, REAL_DTYPES[dtype], int(convention),
+                    x.data_ptr(), x.stride(0), x.stride(1), w.data_ptr(), _ptr(b), _ptr(s),
+                    _ptr(f), _ptr(ln))
     return call, (N, D, T, W), dev, dtype
 
 
@@ -263,7 +267,7 @@ def causal_conv_step(x, weight, bias, state, slots=None, flags=None, silu=True, 
     slots [num_seqs] int32 gives each sequence's place in the pool (one out of
     range is an empty seat: output 0); flags [num_seqs] marks sequences whose
     episode begins with this step.  Returns out [num_seqs, channels]."""
-    x, (N, D), dev, dtype = _activations("x", x, ("num_seqs", "channels"))
+    (N, D), dev, dtype = _activations("x", x, 2)
     if weight is None or weight.dim() != 2:
         raise ValueError("weight is [channels, width]")
     W = weight.shape[1]
@@ -273,10 +277,9 @@ def causal_conv_step(x, weight, bias, state, slots=None, flags=None, silu=True, 
     b = _f32("bias", bias, (D,), dev, optional=True)
     s, i, f = _seats(state, slots, flags, N, (D, W - 1), dtype, dev)
     o = _out(out, (N, D), dev, dtype)
-    call = ConvStepCall(
-        num_seqs=N, channels=D, places=s.shape[0], width=W, silu=1 if silu else 0,
-        dtype=REAL_DTYPES[dtype], x=_ptr(x), x_stride_seq=x.stride(0), weight=_ptr(w),
-        bias=_ptr(b), state=_ptr(s), slots=_ptr(i), starts=_ptr(f), out=_ptr(o))
+    call = ConvStepCall(N, D, s.shape[0], W, 1 if silu else 0, REAL_DTYPES[dtype], x.data_ptr(),
+                        x.stride(0), w.data_ptr(), _ptr(b), s.data_ptr(), _ptr(i), _ptr(f),
+                        o.data_ptr())
     _check(lib().rlca_causal_conv_step(ctypes.byref(call), _current_stream(dev)),
            "rlca_causal_conv_step")
     return o
@@ -303,7 +306,7 @@ def _groups(B, C, channels):
 
 
 def _scan_call(u, delta, A, B, C, D, z, delta_bias, flags, convention, lengths, softplus):
-    u, (N, channels, T), dev, dtype = _activations("u", u, ("num_seqs", "channels", "T"))
+    (N, channels, T), dev, dtype = _activations("u", u, 3)
     shape = (N, channels, T)
     delta = _view("delta", delta, shape, dtype, dev)
     S, A, D, delta_bias = _scan_params(A, D, delta_bias, channels, dev)
@@ -313,16 +316,12 @@ def _scan_call(u, delta, A, B, C, D, z, delta_bias, flags, convention, lengths, 
     if z is not None:
         z = _view("z", z, shape, dtype, dev)
     f, ln = _episodes(flags, lengths, N, T, dev)
-    call = ScanCall(
-        num_seqs=N, channels=channels, T=T, states=S, groups=G, softplus=1 if softplus else 0,
-        dtype=REAL_DTYPES[dtype], convention=int(convention), u=_ptr(u), delta=_ptr(delta),
-        u_stride_seq=u.stride(0), u_stride_channel=u.stride(1), delta_stride_seq=delta.stride(0),
-        delta_stride_channel=delta.stride(1), A=_ptr(A), B=_ptr(B), C=_ptr(C),
-        B_stride_seq=B.stride(0), B_stride_group=B.stride(1), B_stride_state=B.stride(2),
-        C_stride_seq=C.stride(0), C_stride_group=C.stride(1), C_stride_state=C.stride(2),
-        D=_ptr(D), delta_bias=_ptr(delta_bias), flags=_ptr(f), lengths=_ptr(ln))
-    if z is not None:
-        call.z, call.z_stride_seq, call.z_stride_channel = _ptr(z), z.stride(0), z.stride(1)
+    gate = (None, 0, 0) if z is None else (z.data_ptr(), *z.stride()[:2])
+    call = ScanCall(N, channels, T, S, G, 1 if softplus else 0, REAL_DTYPES[dtype],
+                    int(convention), u.data_ptr(), delta.data_ptr(), *u.stride()[:2],
+                    *delta.stride()[:2], A.data_ptr(), B.data_ptr(), C.data_ptr(),
+                    *B.stride()[:3], *C.stride()[:3], _ptr(D), _ptr(delta_bias), *gate, None,
+                    _ptr(f), _ptr(ln))
     return call, (N, channels, T, S, G), dev, dtype
 
 
@@ -399,7 +398,7 @@ def selective_step(u, delta, A, B, C, state, D=None, z=None, delta_bias=None, sl
     channels], B and C [num_seqs, groups, states] (or without groups), state
     [places, channels, states] float32 updated in place.  slots and flags as
     for causal_conv_step.  Returns y [num_seqs, channels]."""
-    u, (N, channels), dev, dtype = _activations("u", u, ("num_seqs", "channels"))
+    (N, channels), dev, dtype = _activations("u", u, 2)
     delta = _view("delta", delta, (N, channels), dtype, dev)
     S, A, D, delta_bias = _scan_params(A, D, delta_bias, channels, dev)
     B = _grouped("B", B, N, S, (), dtype, dev)
@@ -407,16 +406,14 @@ def selective_step(u, delta, A, B, C, state, D=None, z=None, delta_bias=None, sl
     G = _groups(B, C, channels)
     s, i, f = _seats(state, slots, flags, N, (channels, S), torch.float32, dev)
     o = _out(y, (N, channels), dev, dtype, name="y")
-    call = ScanStepCall(
-        num_seqs=N, channels=channels, places=s.shape[0], states=S, groups=G,
-        softplus=1 if softplus else 0, dtype=REAL_DTYPES[dtype], u=_ptr(u), delta=_ptr(delta),
-        u_stride_seq=u.stride(0), delta_stride_seq=delta.stride(0), A=_ptr(A), B=_ptr(B),
-        C=_ptr(C), B_stride_seq=B.stride(0), B_stride_group=B.stride(1),
-        C_stride_seq=C.stride(0), C_stride_group=C.stride(1), D=_ptr(D),
-        delta_bias=_ptr(delta_bias), state=_ptr(s), slots=_ptr(i), starts=_ptr(f), y=_ptr(o))
+    gate = (None, 0)
     if z is not None:
-        z = _view("z", z, (N, channels), dtype, dev)
-        call.z, call.z_stride_seq = _ptr(z), z.stride(0)
+        gate = (_view("z", z, (N, channels), dtype, dev).data_ptr(), z.stride(0))
+    call = ScanStepCall(N, channels, s.shape[0], S, G, 1 if softplus else 0, REAL_DTYPES[dtype],
+                        u.data_ptr(), delta.data_ptr(), u.stride(0), delta.stride(0),
+                        A.data_ptr(), B.data_ptr(), C.data_ptr(), *B.stride()[:2],
+                        *C.stride()[:2], _ptr(D), _ptr(delta_bias), *gate, s.data_ptr(), _ptr(i),
+                        _ptr(f), o.data_ptr())
     _check(lib().rlca_selective_step(ctypes.byref(call), _current_stream(dev)),
            "rlca_selective_step")
     return o
@@ -437,8 +434,6 @@ def _clip_workspace(dev, stream):
 
 def _dense(t):
     """Whether the tensor's elements fill one run of memory in some order."""
-    if t.is_contiguous():
-        return True
     order = sorted(range(t.dim()), key=lambda i: (t.stride(i), t.shape[i]))
     return t.permute(order[::-1]).is_contiguous()
 
@@ -459,19 +454,20 @@ def clip_grad_norm(grads, max_norm, eps=1e-6, out=None, norm=None):
     outs = grads if out is None else list(out)
     if len(outs) != len(grads):
         raise ValueError(f"out has {len(outs)} tensors, expected {len(grads)}")
-    arr = (GradTensor * len(grads))()
+    entries = []
     for i, (g, o) in enumerate(zip(grads, outs)):
-        if g.device != dev:
-            raise ValueError(f"grads[{i}] is on {g.device}, expected {dev}")
-        dtype = _real_dtype(f"grads[{i}]", g)
-        if not _dense(g):
-            raise ValueError(f"grads[{i}] must be dense in memory")
-        if o is not g and (o.device != dev or o.dtype != dtype or o.shape != g.shape
-                           or o.stride() != g.stride()):
-            raise ValueError(f"out[{i}] must be like grads[{i}]")
-        e = arr[i]
-        e.data, e.out, e.count, e.dtype = g.data_ptr(), o.data_ptr(), g.numel(), \
-            REAL_DTYPES[dtype]
+        dtype = REAL_DTYPES.get(g.dtype)
+        if dtype is None or g.device != dev or not (g.is_contiguous() or _dense(g)):
+            _real_dtype(f"grads[{i}]", g)
+            raise ValueError(f"grads[{i}] must be dense in memory and on {dev}")
+        at = to = g.data_ptr()
+        if o is not g:
+            if o.dtype != g.dtype or o.shape != g.shape or o.stride() != g.stride() \
+                    or o.device != dev:
+                raise ValueError(f"out[{i}] must be like grads[{i}]")
+            to = o.data_ptr()
+        entries.append((at, to, g.numel(), dtype))
+    arr = (GradTensor * len(entries))(*entries)
     n = _out(norm, (1,), dev, torch.float64, name="norm")
     h = _current_stream(dev)
     ws = _clip_workspace(dev, h)

@@ -8,13 +8,15 @@ and workspace allocation through torch, and the current HIP stream.
 from __future__ import annotations
 
 import ctypes
+import struct
+from array import array
 from typing import NamedTuple, Optional
 
 import torch
 
 from .rlca import (
-    REAL_DTYPES, RESET_ON_START, SIGNATURES, SIZE_QUERIES, _check, _current_stream, _out, _p,
-    _ptr, _real_dtype, _steps, _sz, _workspaces, _workspaces_lock, lib,
+    REAL_DTYPES, RESET_ON_START, SIGNATURES, SIZE_QUERIES, _FLAG_DTYPES, _check,
+    _current_stream, _out, _p, _real_dtype, _steps, _sz, _workspaces, _workspaces_lock, lib,
 )
 
 MAX_STATES = 128
@@ -85,23 +87,38 @@ class GradTensor(ctypes.Structure):
     _fields_ = [("data", _p), ("out", _p), ("count", _i64), ("dtype", _i32)]
 
 
-_conv = ctypes.POINTER(ConvCall)
-_scan = ctypes.POINTER(ScanCall)
+# The entry points read these records before they return.  They are taken as
+# plain addresses, so that a call can pass a packed copy of one (below) and
+# code that fills in a structure can pass that.
 SIGNATURES.update({
-    "rlca_causal_conv": [_conv, _p],
-    "rlca_causal_conv_backward": [_conv, _p, _sz, _p],
-    "rlca_selective_scan": [_scan, _p],
-    "rlca_selective_scan_backward": [_scan, _p, _sz, _p],
-    "rlca_causal_conv_step": [ctypes.POINTER(ConvStepCall), _p],
-    "rlca_selective_step": [ctypes.POINTER(ScanStepCall), _p],
-    "rlca_clip_grad_norm": [ctypes.POINTER(GradTensor), _i64, ctypes.c_double, ctypes.c_double,
-                            _p, _p, _sz, _p],
+    "rlca_causal_conv": [_p, _p],
+    "rlca_causal_conv_backward": [_p, _p, _sz, _p],
+    "rlca_selective_scan": [_p, _p],
+    "rlca_selective_scan_backward": [_p, _p, _sz, _p],
+    "rlca_causal_conv_step": [_p, _p],
+    "rlca_selective_step": [_p, _p],
+    "rlca_clip_grad_norm": [_p, _i64, ctypes.c_double, ctypes.c_double, _p, _p, _sz, _p],
 })
 SIZE_QUERIES.update({
-    "rlca_causal_conv_backward_workspace_size": [_conv],
-    "rlca_selective_scan_checkpoints_size": [_scan],
-    "rlca_selective_scan_backward_workspace_size": [_scan],
+    "rlca_causal_conv_backward_workspace_size": [_p],
+    "rlca_selective_scan_checkpoints_size": [_p],
+    "rlca_selective_scan_backward_workspace_size": [_p],
 })
+
+
+def _packer(cls):
+    """Packs a record's values, in the order of its fields, into bytes laid out
+    as the structure is: a quarter of the time that filling one takes."""
+    codes = {_i64: "q", _i32: "i", _p: "P"}
+    return struct.Struct("@" + "".join(codes[kind] for _, kind in cls._fields_)).pack
+
+
+_pack_conv, _pack_scan, _pack_conv_step, _pack_scan_step = (
+    _packer(cls) for cls in (ConvCall, ScanCall, ConvStepCall, ScanStepCall))
+
+
+def _ptr(t):
+    return 0 if t is None else t.data_ptr()
 
 
 class ConvGrads(NamedTuple):
@@ -134,7 +151,7 @@ def _view(name, t, shape, dtype, device):
         raise ValueError(f"{name} is required")
     # every check in one expression first; the detailed ones below name the
     # failure
-    if t.dtype is dtype and t.shape == shape and t.device == device \
+    if t.dtype is dtype and t.shape == shape and t.get_device() == device.index \
             and (t.stride(-1) == 1 or t.shape[-1] <= 1):
         return t
     if t.device != device:
@@ -144,6 +161,24 @@ def _view(name, t, shape, dtype, device):
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     raise ValueError(f"{name} must be contiguous in its last dimension")
+
+
+def _dense_in(name, t, shape, dtype, device):
+    """A dense tensor's address, or 0 for None (an optional input)."""
+    if t is None:
+        return 0
+    if t.dtype is dtype and t.shape == shape and t.get_device() == device.index \
+            and t.is_contiguous():
+        return t.data_ptr()
+    return _steps(name, t, tuple(shape), dtype, device).data_ptr()
+
+
+def _flags_in(t, shape, device):
+    if t is None:
+        return 0
+    if t.dtype in _FLAG_DTYPES:
+        return _dense_in("flags", t, shape, t.dtype, device)
+    return _steps("flags", t, tuple(shape), "flag", device).data_ptr()
 
 
 def _activations(name, t, dims):
@@ -159,13 +194,18 @@ def _activations(name, t, dims):
     return shape, t.device, dtype
 
 
-def _episodes(flags, lengths, N, T, dev):
-    return (_steps("flags", flags, (N, T), "flag", dev, optional=True),
-            _steps("lengths", lengths, (N,), torch.int32, dev, optional=True))
+def _new(out, shape, dtype, device, name="out"):
+    """An output tensor, the caller's or a new one."""
+    if out is None:
+        return torch.empty(tuple(shape), dtype=dtype, device=device)
+    return _out(out, tuple(shape), device, dtype, name=name)
 
 
-def _f32(name, t, shape, dev, optional=False):
-    return _steps(name, t, shape, torch.float32, dev, optional=optional)
+def _new_step(out, like, shape, dtype, device, name):
+    """As _new for one step's output; the cheapest allocation where it fits."""
+    if out is None and like.is_contiguous():
+        return torch.empty_like(like)
+    return _new(out, shape, dtype, device, name)
 
 
 def _grouped(name, t, N, S, last, dtype, dev):
@@ -177,7 +217,7 @@ def _grouped(name, t, N, S, last, dtype, dev):
         t = t.unsqueeze(1)
     if t.dim() != full:
         raise ValueError(f"{name} is [num_seqs, groups, states{', T' if last else ''}]")
-    return _view(name, t, (N, t.shape[1], S) + last, dtype, dev)
+    return _view(name, t, (N, t.shape[1], S, *last), dtype, dev)
 
 
 def _scratch(nbytes, dev):
@@ -187,21 +227,27 @@ def _scratch(nbytes, dev):
 
 
 # ------------------------------------------------------------- the convolution
-def _conv_call(x, weight, bias, state, flags, convention, lengths, silu):
-    (N, D, T), dev, dtype = _activations("x", x, 3)
+def _taps(weight):
     if weight is None or weight.dim() != 2:
         raise ValueError("weight is [channels, width]")
     W = weight.shape[1]
     if not 2 <= W <= 4:
         raise ValueError(f"weight has {W} taps, expected 2, 3 or 4")
-    w = _f32("weight", weight, (D, W), dev)
-    b = _f32("bias", bias, (D,), dev, optional=True)
-    s = _steps("state", state, (N, D, W - 1), dtype, dev, optional=True)
-    f, ln = _episodes(flags, lengths, N, T, dev)
-    call = ConvCall(N, D, T, W, 1 if silu else 0, REAL_DTYPES[dtype], int(convention),
-                    x.data_ptr(), x.stride(0), x.stride(1), w.data_ptr(), _ptr(b), _ptr(s),
-                    _ptr(f), _ptr(ln))
-    return call, (N, D, T, W), dev, dtype
+    return W
+
+
+def _conv_inputs(x, weight, bias, state, flags, convention, lengths, silu):
+    """The record's fields up to lengths, and what the outputs are made of."""
+    shape, dev, dtype = _activations("x", x, 3)
+    N, D, T = shape
+    W = _taps(weight)
+    fields = (N, D, T, W, 1 if silu else 0, REAL_DTYPES[dtype], int(convention), x.data_ptr(),
+              x.stride(0), x.stride(1), _dense_in("weight", weight, (D, W), torch.float32, dev),
+              _dense_in("bias", bias, (D,), torch.float32, dev),
+              _dense_in("state", state, (N, D, W - 1), dtype, dev),
+              _flags_in(flags, (N, T), dev),
+              _dense_in("lengths", lengths, (N,), torch.int32, dev))
+    return fields, shape, W, dev, dtype
 
 
 def causal_conv(x, weight, bias=None, state=None, flags=None, convention=RESET_ON_START,
@@ -214,14 +260,14 @@ def causal_conv(x, weight, bias=None, state=None, flags=None, convention=RESET_O
     2, 3 or 4; state [num_seqs, channels, W-1] the inputs before the row;
     flags [num_seqs, T] episode boundaries; lengths [num_seqs] int32.
     Returns (out, final state | None)."""
-    call, (N, D, T, W), dev, dtype = _conv_call(x, weight, bias, state, flags, convention,
+    fields, shape, W, dev, dtype = _conv_inputs(x, weight, bias, state, flags, convention,
                                                 lengths, silu)
-    o = _out(out, (N, D, T), dev, dtype)
+    o = _new(out, shape, dtype, dev)
     f = None
     if with_state or final_state is not None:
-        f = _out(final_state, (N, D, W - 1), dev, dtype, name="final_state")
-    call.out, call.final_state = _ptr(o), _ptr(f)
-    _check(lib().rlca_causal_conv(ctypes.byref(call), _current_stream(dev)), "rlca_causal_conv")
+        f = _new(final_state, (shape[0], shape[1], W - 1), dtype, dev, "final_state")
+    call = _pack_conv(*fields, o.data_ptr(), _ptr(f), 0, 0, 0, 0, 0, 0, 0, 0)
+    _check(lib().rlca_causal_conv(call, _current_stream(dev)), "rlca_causal_conv")
     return o, f
 
 
@@ -229,36 +275,32 @@ def causal_conv_backward(grad_out, x, weight, bias=None, state=None, flags=None,
                          convention=RESET_ON_START, lengths=None, silu=True, grad_state=None):
     """Gradients of causal_conv with these inputs, from its output's gradient
     (and, with grad_state, its final state's).  Returns ConvGrads."""
-    call, (N, D, T, W), dev, dtype = _conv_call(x, weight, bias, state, flags, convention,
+    fields, shape, W, dev, dtype = _conv_inputs(x, weight, bias, state, flags, convention,
                                                 lengths, silu)
-    g = _view("grad_out", grad_out, (N, D, T), dtype, dev)
-    gf = _steps("grad_state", grad_state, (N, D, W - 1), dtype, dev, optional=True)
+    N, D, _ = shape
+    g = _view("grad_out", grad_out, shape, dtype, dev)
+    gf = _dense_in("grad_state", grad_state, (N, D, W - 1), dtype, dev)
     grads = ConvGrads(
-        x=torch.empty((N, D, T), dtype=dtype, device=dev),
-        weight=torch.empty((D, W), dtype=torch.float32, device=dev),
-        bias=None if bias is None else torch.empty(D, dtype=torch.float32, device=dev),
-        state=None if state is None else torch.empty((N, D, W - 1), dtype=dtype, device=dev))
-    call.grad_out, call.grad_stride_seq, call.grad_stride_channel = _ptr(g), g.stride(0), \
-        g.stride(1)
-    call.grad_final_state = _ptr(gf)
-    call.grad_x, call.grad_weight = _ptr(grads.x), _ptr(grads.weight)
-    call.grad_bias, call.grad_state = _ptr(grads.bias), _ptr(grads.state)
-    ws = _scratch(lib().rlca_causal_conv_backward_workspace_size(ctypes.byref(call)), dev)
-    _check(lib().rlca_causal_conv_backward(ctypes.byref(call), _ptr(ws), ws.numel(),
+        x=_new(None, shape, dtype, dev), weight=_new(None, (D, W), torch.float32, dev),
+        bias=None if bias is None else _new(None, (D,), torch.float32, dev),
+        state=None if state is None else _new(None, (N, D, W - 1), dtype, dev))
+    call = _pack_conv(*fields, 0, 0, g.data_ptr(), g.stride(0), g.stride(1), gf,
+                      *(_ptr(t) for t in grads))
+    ws = _scratch(lib().rlca_causal_conv_backward_workspace_size(call), dev)
+    _check(lib().rlca_causal_conv_backward(call, ws.data_ptr(), ws.numel(),
                                            _current_stream(dev)), "rlca_causal_conv_backward")
     return grads
 
 
-def _seats(state, slots, flags, N, shape, dtype, dev):
-    """A step's pool of states [places, ...], its slots and its start flags."""
-    if state is None or state.dim() != 1 + len(shape):
+def _pool(state, slots, N, shape, dtype, dev):
+    """A step's pool of states [places, ...]: its number of places and address."""
+    if state is None or state.dim() != 3:
         raise ValueError(f"state is [places, {', '.join(str(n) for n in shape)}]")
-    s = _steps("state", state, (state.shape[0],) + shape, dtype, dev)
-    i = _steps("slots", slots, (N,), torch.int32, dev, optional=True)
-    f = _steps("flags", flags, (N,), "flag", dev, optional=True)
-    if i is None and s.shape[0] < N:
-        raise ValueError(f"state has {s.shape[0]} places for {N} sequences")
-    return s, i, f
+    places = state.shape[0]
+    at = _dense_in("state", state, (places, *shape), dtype, dev)
+    if slots is None and places < N:
+        raise ValueError(f"state has {places} places for {N} sequences")
+    return places, at
 
 
 def causal_conv_step(x, weight, bias, state, slots=None, flags=None, silu=True, out=None):
@@ -267,21 +309,18 @@ def causal_conv_step(x, weight, bias, state, slots=None, flags=None, silu=True, 
     slots [num_seqs] int32 gives each sequence's place in the pool (one out of
     range is an empty seat: output 0); flags [num_seqs] marks sequences whose
     episode begins with this step.  Returns out [num_seqs, channels]."""
-    (N, D), dev, dtype = _activations("x", x, 2)
-    if weight is None or weight.dim() != 2:
-        raise ValueError("weight is [channels, width]")
-    W = weight.shape[1]
-    if not 2 <= W <= 4:
-        raise ValueError(f"weight has {W} taps, expected 2, 3 or 4")
-    w = _f32("weight", weight, (D, W), dev)
-    b = _f32("bias", bias, (D,), dev, optional=True)
-    s, i, f = _seats(state, slots, flags, N, (D, W - 1), dtype, dev)
-    o = _out(out, (N, D), dev, dtype)
-    call = ConvStepCall(N, D, s.shape[0], W, 1 if silu else 0, REAL_DTYPES[dtype], x.data_ptr(),
-                        x.stride(0), w.data_ptr(), _ptr(b), s.data_ptr(), _ptr(i), _ptr(f),
-                        o.data_ptr())
-    _check(lib().rlca_causal_conv_step(ctypes.byref(call), _current_stream(dev)),
-           "rlca_causal_conv_step")
+    shape, dev, dtype = _activations("x", x, 2)
+    N, D = shape
+    W = _taps(weight)
+    w = _dense_in("weight", weight, (D, W), torch.float32, dev)
+    b = _dense_in("bias", bias, (D,), torch.float32, dev)
+    places, s = _pool(state, slots, N, (D, W - 1), dtype, dev)
+    i = _dense_in("slots", slots, (N,), torch.int32, dev)
+    f = _flags_in(flags, (N,), dev)
+    o = _new_step(out, x, shape, dtype, dev, "out")
+    call = _pack_conv_step(N, D, places, W, 1 if silu else 0, REAL_DTYPES[dtype], x.data_ptr(),
+                           x.stride(0), w, b, s, i, f, o.data_ptr())
+    _check(lib().rlca_causal_conv_step(call, _current_stream(dev)), "rlca_causal_conv_step")
     return o
 
 
@@ -292,8 +331,9 @@ def _scan_params(A, D, delta_bias, channels, dev):
     S = A.shape[1]
     if not 1 <= S <= MAX_STATES:
         raise ValueError(f"A has {S} states, expected 1 to {MAX_STATES}")
-    return (S, _f32("A", A, (channels, S), dev), _f32("D", D, (channels,), dev, optional=True),
-            _f32("delta_bias", delta_bias, (channels,), dev, optional=True))
+    return (S, _dense_in("A", A, (channels, S), torch.float32, dev),
+            _dense_in("D", D, (channels,), torch.float32, dev),
+            _dense_in("delta_bias", delta_bias, (channels,), torch.float32, dev))
 
 
 def _groups(B, C, channels):
@@ -305,24 +345,27 @@ def _groups(B, C, channels):
     return G
 
 
-def _scan_call(u, delta, A, B, C, D, z, delta_bias, flags, convention, lengths, softplus):
-    (N, channels, T), dev, dtype = _activations("u", u, 3)
-    shape = (N, channels, T)
+def _scan_inputs(u, delta, A, B, C, D, z, delta_bias, state, flags, convention, lengths,
+                 softplus):
+    """The record's fields up to lengths, and what the outputs are made of."""
+    shape, dev, dtype = _activations("u", u, 3)
+    N, channels, T = shape
     delta = _view("delta", delta, shape, dtype, dev)
-    S, A, D, delta_bias = _scan_params(A, D, delta_bias, channels, dev)
+    S, a, d, bias = _scan_params(A, D, delta_bias, channels, dev)
     B = _grouped("B", B, N, S, (T,), dtype, dev)
     C = _grouped("C", C, N, S, (T,), dtype, dev)
     G = _groups(B, C, channels)
+    gate = (0, 0, 0)
     if z is not None:
         z = _view("z", z, shape, dtype, dev)
-    f, ln = _episodes(flags, lengths, N, T, dev)
-    gate = (None, 0, 0) if z is None else (z.data_ptr(), *z.stride()[:2])
-    call = ScanCall(N, channels, T, S, G, 1 if softplus else 0, REAL_DTYPES[dtype],
-                    int(convention), u.data_ptr(), delta.data_ptr(), *u.stride()[:2],
-                    *delta.stride()[:2], A.data_ptr(), B.data_ptr(), C.data_ptr(),
-                    *B.stride()[:3], *C.stride()[:3], _ptr(D), _ptr(delta_bias), *gate, None,
-                    _ptr(f), _ptr(ln))
-    return call, (N, channels, T, S, G), dev, dtype
+        gate = (z.data_ptr(), z.stride(0), z.stride(1))
+    fields = (N, channels, T, S, G, 1 if softplus else 0, REAL_DTYPES[dtype], int(convention),
+              u.data_ptr(), delta.data_ptr(), u.stride(0), u.stride(1), delta.stride(0),
+              delta.stride(1), a, B.data_ptr(), C.data_ptr(), *B.stride()[:3], *C.stride()[:3],
+              d, bias, *gate, _dense_in("state", state, (N, channels, S), torch.float32, dev),
+              _flags_in(flags, (N, T), dev),
+              _dense_in("lengths", lengths, (N,), torch.int32, dev))
+    return fields, shape, S, G, dev, dtype
 
 
 def selective_scan(u, delta, A, B, C, D=None, z=None, delta_bias=None, state=None, flags=None,
@@ -339,19 +382,17 @@ def selective_scan(u, delta, A, B, C, D=None, z=None, delta_bias=None, state=Non
     float32; flags [num_seqs, T] episode boundaries; lengths [num_seqs] int32.
     Returns (y, final state | None, checkpoints | None); the checkpoints are
     what selective_scan_backward needs of this call."""
-    call, (N, channels, T, S, _), dev, dtype = _scan_call(
-        u, delta, A, B, C, D, z, delta_bias, flags, convention, lengths, softplus)
-    s = _f32("state", state, (N, channels, S), dev, optional=True)
-    o = _out(y, (N, channels, T), dev, dtype, name="y")
+    fields, shape, S, _, dev, dtype = _scan_inputs(u, delta, A, B, C, D, z, delta_bias, state,
+                                                   flags, convention, lengths, softplus)
+    o = _new(y, shape, dtype, dev, "y")
     f = c = None
     if with_state or final_state is not None:
-        f = _out(final_state, (N, channels, S), dev, name="final_state")
+        f = _new(final_state, (shape[0], shape[1], S), torch.float32, dev, "final_state")
     if with_checkpoints:
-        c = torch.empty(lib().rlca_selective_scan_checkpoints_size(ctypes.byref(call)) // 4,
-                        dtype=torch.float32, device=dev)
-    call.state, call.y, call.final_state, call.checkpoints = _ptr(s), _ptr(o), _ptr(f), _ptr(c)
-    _check(lib().rlca_selective_scan(ctypes.byref(call), _current_stream(dev)),
-           "rlca_selective_scan")
+        n = lib().rlca_selective_scan_checkpoints_size(_pack_scan(*fields, *(0,) * 16))
+        c = _new(None, (n // 4,), torch.float32, dev)
+    call = _pack_scan(*fields, o.data_ptr(), _ptr(f), _ptr(c), *(0,) * 13)
+    _check(lib().rlca_selective_scan(call, _current_stream(dev)), "rlca_selective_scan")
     return o, f, c
 
 
@@ -361,32 +402,30 @@ def selective_scan_backward(grad_y, u, delta, A, B, C, checkpoints, D=None, z=No
     """Gradients of selective_scan with these inputs, from its output's
     gradient (and, with grad_state, its final state's) and the checkpoints it
     returned.  Returns ScanGrads; B's and C's have four dimensions."""
-    call, (N, channels, T, S, G), dev, dtype = _scan_call(
-        u, delta, A, B, C, D, z, delta_bias, flags, convention, lengths, softplus)
-    g = _view("grad_y", grad_y, (N, channels, T), dtype, dev)
-    gf = _f32("grad_state", grad_state, (N, channels, S), dev, optional=True)
-    _f32("state", state, (N, channels, S), dev, optional=True)
-    n = lib().rlca_selective_scan_checkpoints_size(ctypes.byref(call)) // 4
-    c = _f32("checkpoints", checkpoints, (n,), dev)
-
-    def like(*shape, dtype=torch.float32):
-        return torch.empty(shape, dtype=dtype, device=dev)
-
-    rows = (N, channels, T)
+    fields, shape, S, G, dev, dtype = _scan_inputs(u, delta, A, B, C, D, z, delta_bias, state,
+                                                   flags, convention, lengths, softplus)
+    N, channels, T = shape
+    g = _view("grad_y", grad_y, shape, dtype, dev)
+    gf = _dense_in("grad_state", grad_state, (N, channels, S), torch.float32, dev)
+    if checkpoints is None:
+        raise ValueError("checkpoints is required")
+    n = lib().rlca_selective_scan_checkpoints_size(_pack_scan(*fields, *(0,) * 16)) // 4
+    c = _dense_in("checkpoints", checkpoints, (n,), torch.float32, dev)
+    f32 = torch.float32
     grads = ScanGrads(
-        u=like(*rows, dtype=dtype), delta=like(*rows, dtype=dtype), A=like(channels, S),
-        B=like(N, G, S, T, dtype=dtype), C=like(N, G, S, T, dtype=dtype),
-        D=None if D is None else like(channels),
-        z=None if z is None else like(*rows, dtype=dtype),
-        delta_bias=None if delta_bias is None else like(channels),
-        state=None if state is None else like(N, channels, S))
-    call.checkpoints, call.grad_y = _ptr(c), _ptr(g)
-    call.grad_stride_seq, call.grad_stride_channel = g.stride(0), g.stride(1)
-    call.grad_final_state = _ptr(gf)
-    for name, t in zip(grads._fields, grads):
-        setattr(call, "grad_" + name, _ptr(t))
-    ws = _scratch(lib().rlca_selective_scan_backward_workspace_size(ctypes.byref(call)), dev)
-    _check(lib().rlca_selective_scan_backward(ctypes.byref(call), _ptr(ws), ws.numel(),
+        u=_new(None, shape, dtype, dev), delta=_new(None, shape, dtype, dev),
+        A=_new(None, (channels, S), f32, dev), B=_new(None, (N, G, S, T), dtype, dev),
+        C=_new(None, (N, G, S, T), dtype, dev),
+        D=None if D is None else _new(None, (channels,), f32, dev),
+        z=None if z is None else _new(None, shape, dtype, dev),
+        delta_bias=None if delta_bias is None else _new(None, (channels,), f32, dev),
+        state=None if state is None else _new(None, (N, channels, S), f32, dev))
+    call = _pack_scan(*fields, 0, 0, c, g.data_ptr(), g.stride(0), g.stride(1), gf,
+                      grads.u.data_ptr(), grads.delta.data_ptr(), grads.A.data_ptr(),
+                      grads.B.data_ptr(), grads.C.data_ptr(), _ptr(grads.D),
+                      _ptr(grads.delta_bias), _ptr(grads.z), _ptr(grads.state))
+    ws = _scratch(lib().rlca_selective_scan_backward_workspace_size(call), dev)
+    _check(lib().rlca_selective_scan_backward(call, ws.data_ptr(), ws.numel(),
                                               _current_stream(dev)),
            "rlca_selective_scan_backward")
     return grads
@@ -398,24 +437,25 @@ def selective_step(u, delta, A, B, C, state, D=None, z=None, delta_bias=None, sl
     channels], B and C [num_seqs, groups, states] (or without groups), state
     [places, channels, states] float32 updated in place.  slots and flags as
     for causal_conv_step.  Returns y [num_seqs, channels]."""
-    (N, channels), dev, dtype = _activations("u", u, 2)
-    delta = _view("delta", delta, (N, channels), dtype, dev)
-    S, A, D, delta_bias = _scan_params(A, D, delta_bias, channels, dev)
+    shape, dev, dtype = _activations("u", u, 2)
+    N, channels = shape
+    delta = _view("delta", delta, shape, dtype, dev)
+    S, a, d, bias = _scan_params(A, D, delta_bias, channels, dev)
     B = _grouped("B", B, N, S, (), dtype, dev)
     C = _grouped("C", C, N, S, (), dtype, dev)
     G = _groups(B, C, channels)
-    s, i, f = _seats(state, slots, flags, N, (channels, S), torch.float32, dev)
-    o = _out(y, (N, channels), dev, dtype, name="y")
-    gate = (None, 0)
+    places, s = _pool(state, slots, N, (channels, S), torch.float32, dev)
+    i = _dense_in("slots", slots, (N,), torch.int32, dev)
+    f = _flags_in(flags, (N,), dev)
+    gate = (0, 0)
     if z is not None:
-        gate = (_view("z", z, (N, channels), dtype, dev).data_ptr(), z.stride(0))
-    call = ScanStepCall(N, channels, s.shape[0], S, G, 1 if softplus else 0, REAL_DTYPES[dtype],
-                        u.data_ptr(), delta.data_ptr(), u.stride(0), delta.stride(0),
-                        A.data_ptr(), B.data_ptr(), C.data_ptr(), *B.stride()[:2],
-                        *C.stride()[:2], _ptr(D), _ptr(delta_bias), *gate, s.data_ptr(), _ptr(i),
-                        _ptr(f), o.data_ptr())
-    _check(lib().rlca_selective_step(ctypes.byref(call), _current_stream(dev)),
-           "rlca_selective_step")
+        gate = (_view("z", z, shape, dtype, dev).data_ptr(), z.stride(0))
+    o = _new_step(y, u, shape, dtype, dev, "y")
+    call = _pack_scan_step(N, channels, places, S, G, 1 if softplus else 0, REAL_DTYPES[dtype],
+                           u.data_ptr(), delta.data_ptr(), u.stride(0), delta.stride(0), a,
+                           B.data_ptr(), C.data_ptr(), B.stride(0), B.stride(1), C.stride(0),
+                           C.stride(1), d, bias, *gate, s, i, f, o.data_ptr())
+    _check(lib().rlca_selective_step(call, _current_stream(dev)), "rlca_selective_step")
     return o
 
 
@@ -454,23 +494,37 @@ def clip_grad_norm(grads, max_norm, eps=1e-6, out=None, norm=None):
     outs = grads if out is None else list(out)
     if len(outs) != len(grads):
         raise ValueError(f"out has {len(outs)} tensors, expected {len(grads)}")
-    entries = []
-    for i, (g, o) in enumerate(zip(grads, outs)):
-        dtype = REAL_DTYPES.get(g.dtype)
-        if dtype is None or g.device != dev or not (g.is_contiguous() or _dense(g)):
+    # Properties of all tensors at once, the checks over those lists; a loop
+    # names the tensor that fails one.
+    tensor = torch.Tensor
+    dtypes = [g.dtype for g in grads]
+    codes = list(map(REAL_DTYPES.get, dtypes))
+    addresses = list(map(tensor.data_ptr, grads))
+    if None in codes or any(i != dev.index for i in map(tensor.get_device, grads)) \
+            or not (all(map(tensor.is_contiguous, grads)) or all(map(_dense, grads))):
+        for i, g in enumerate(grads):
             _real_dtype(f"grads[{i}]", g)
-            raise ValueError(f"grads[{i}] must be dense in memory and on {dev}")
-        at = to = g.data_ptr()
-        if o is not g:
-            if o.dtype != g.dtype or o.shape != g.shape or o.stride() != g.stride() \
-                    or o.device != dev:
-                raise ValueError(f"out[{i}] must be like grads[{i}]")
-            to = o.data_ptr()
-        entries.append((at, to, g.numel(), dtype))
-    arr = (GradTensor * len(entries))(*entries)
+            if g.device != dev or not _dense(g):
+                raise ValueError(f"grads[{i}] must be dense in memory and on {dev}")
+    targets = addresses
+    if out is not None:
+        targets = list(map(tensor.data_ptr, outs))
+        if any(i != dev.index for i in map(tensor.get_device, outs)) \
+                or [o.dtype for o in outs] != dtypes \
+                or [o.shape for o in outs] != [g.shape for g in grads] \
+                or list(map(tensor.stride, outs)) != list(map(tensor.stride, grads)):
+            raise ValueError("every tensor of out must be like the one of grads: device, type, "
+                             "shape and strides")
+    # address, output's address, count, type: four 8-byte fields a tensor
+    packed = array("Q", [0]) * (4 * len(grads))
+    packed[0::4] = array("Q", addresses)
+    packed[1::4] = array("Q", targets)
+    packed[2::4] = array("Q", list(map(tensor.numel, grads)))
+    packed[3::4] = array("Q", codes)
     n = _out(norm, (1,), dev, torch.float64, name="norm")
     h = _current_stream(dev)
     ws = _clip_workspace(dev, h)
-    _check(lib().rlca_clip_grad_norm(arr, len(grads), float(max_norm), float(eps), _ptr(n),
-                                     _ptr(ws), ws.numel(), h), "rlca_clip_grad_norm")
+    _check(lib().rlca_clip_grad_norm(packed.buffer_info()[0], len(grads), max_norm, eps,
+                                     n.data_ptr(), ws.data_ptr(), ws.numel(), h),
+           "rlca_clip_grad_norm")
     return n

@@ -121,18 +121,24 @@ __device__ __forceinline__ float softplus(float x) {
 }
 
 // Bit k of the result: an episode starts at step t0 + k (k < K <= 8), from a
-// row of T flags.  AFTER_DONE: a flag at t - 1 makes t a start.
+// row of T flags.  AFTER_DONE: a flag at t - 1 makes t a start.  Eight flags are
+// one load, moved inside the row where they would begin before it or end past
+// it, and the bits moved back.
 template <int K>
 __device__ __forceinline__ uint32_t start_bits(const uint8_t *flags, int t0, int T, int after_done) {
     const int first = t0 - after_done;
     uint32_t bits = 0;
-    if (K == 8 && first >= 0 && first + 8 <= T) {
+    if (T >= 8) {
+        const int at = first < 0 ? 0 : first > T - 8 ? T - 8 : first;
         uint64_t w;
-        __builtin_memcpy(&w, flags + first, 8);
+        __builtin_memcpy(&w, flags + at, 8);
         // nonzero bytes -> their top bit -> one bit each, in order
         w |= (w & 0x7f7f7f7f7f7f7f7full) + 0x7f7f7f7f7f7f7f7full;
         w = (w >> 7) & 0x0101010101010101ull;
-        bits = (uint32_t)((w * 0x0102040810204080ull) >> 56);
+        const uint64_t found = (w * 0x0102040810204080ull) >> 56;
+        const int d = at - first;  // -7 .. 7 where any of the flags lies in the row
+        bits = d >= 8 || d <= -8 ? 0u : d >= 0 ? (uint32_t)(found << d) : (uint32_t)(found >> -d);
+        bits &= (1u << K) - 1;
     } else {
 #pragma unroll
         for (int k = 0; k < K; ++k) {

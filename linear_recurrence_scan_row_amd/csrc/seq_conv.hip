@@ -58,14 +58,33 @@ __device__ __forceinline__ ConvLane conv_lane(const ConvParams &p, uint32_t row_
     return l;
 }
 
+// Which taps stay within their step's episode.  `starts` bit i: an episode
+// starts at step t0 - 2 + i.  Tap j of step k reads across a start if one lies
+// in steps k-j+1 .. k; within[j - 1] has bit k + 2 set where none does.
+template <int W>
+struct Episodes {
+    uint32_t within[W - 1];
+    __device__ __forceinline__ explicit Episodes(uint32_t starts) {
+        uint32_t across = starts;
+#pragma unroll
+        for (int j = 1; j < W; ++j) {
+            within[j - 1] = ~across;
+            across |= starts << j;
+        }
+    }
+    // x where the tap stays within, else 0 (whatever x is)
+    __device__ __forceinline__ float keep(float x, int k, int j) const {
+        const int mask = (int)(within[j - 1] << (29 - k)) >> 31;
+        return from_bits<float>(as_bits(x) & mask);
+    }
+};
+
 // A tap's input: the value j steps before step k, or 0 across a start.
-// `starts` bit i: an episode starts at step t0 - 2 + i.
 template <int W, bool FLAGS, int N>
-__device__ __forceinline__ float tap(const float (&x)[N], uint32_t starts, int k, int j) {
+__device__ __forceinline__ float tap(const float (&x)[N], const Episodes<W> &e, int k, int j) {
     const float v = x[kBack + k - j];
     if (!FLAGS || j == 0) return v;
-    const uint32_t between = ((1u << j) - 1) << (k + 3 - j);  // steps k-j+1 .. k
-    return (starts & between) != 0 ? 0.f : v;
+    return e.keep(v, k, j);
 }
 
 // The state's input at time -1-q (q = 0 the newest), 0 without a state.
@@ -105,10 +124,10 @@ __global__ __launch_bounds__(kConvThreads) void causal_conv(ConvParams p) {
                         for (int q = 0; q < W - 1; ++q)
                             back[kBack - 1 - q] = state_at<W, E>(p.state, l.row, q);
                     uint32_t starts = 0;
-                    if constexpr (FLAGS) {
-                        starts = start_bits<8>(flags, l.t0, p.T, p.after_done) << 2;
-                        starts |= start_bits<2>(flags, l.t0 - 2, p.T, p.after_done);
-                    }
+                    if constexpr (FLAGS)
+                        starts = start_bits<8>(flags, l.t0 - 2, p.T, p.after_done) |
+                                 start_bits<2>(flags, l.t0 + 6, p.T, p.after_done) << 8;
+                    const Episodes<W> episodes(starts);
 #pragma unroll
                     for (int k = 0; k < kBack; ++k) v[k] = back[k];
 #pragma unroll
@@ -122,7 +141,7 @@ __global__ __launch_bounds__(kConvThreads) void causal_conv(ConvParams p) {
                         float pre = bias;
 #pragma unroll
                         for (int j = 0; j < W; ++j)
-                            pre = fmaf(w[W - 1 - j], tap<W, FLAGS>(v, starts, k, j), pre);
+                            pre = fmaf(w[W - 1 - j], tap<W, FLAGS>(v, episodes, k, j), pre);
                         pre = p.silu != 0 ? silu(pre) : pre;
                         o[k] = k < n ? pre : 0.f;
                     }
@@ -188,18 +207,17 @@ __global__ __launch_bounds__(kConvThreads) void causal_conv_backward(ConvParams 
                             v[kBack + kConvK + k] = ahead[k], go[kConvK + k] = gahead[k];
                     }
                     uint32_t starts = 0;  // bit i: step t0 - 2 + i
-                    if constexpr (FLAGS) {
-                        starts = start_bits<2>(flags, l.t0 - 2, p.T, p.after_done) |
-                                 start_bits<8>(flags, l.t0, p.T, p.after_done) << 2 |
-                                 start_bits<3>(flags, l.t0 + 8, p.T, p.after_done) << 10;
-                    }
+                    if constexpr (FLAGS)
+                        starts = start_bits<8>(flags, l.t0 - 2, p.T, p.after_done) |
+                                 start_bits<5>(flags, l.t0 + 6, p.T, p.after_done) << 8;
+                    const Episodes<W> episodes(starts);
                     float dpre[kSteps];
 #pragma unroll
                     for (int k = 0; k < kSteps; ++k) {
                         float pre = bias;
 #pragma unroll
                         for (int j = 0; j < W; ++j)
-                            pre = fmaf(w[W - 1 - j], tap<W, FLAGS>(v, starts, k, j), pre);
+                            pre = fmaf(w[W - 1 - j], tap<W, FLAGS>(v, episodes, k, j), pre);
                         const float slope = p.silu != 0 ? silu_slope(pre, sigmoid(pre)) : 1.f;
                         dpre[k] = k < n ? go[k] * slope : 0.f;
                     }
@@ -209,15 +227,15 @@ __global__ __launch_bounds__(kConvThreads) void causal_conv_backward(ConvParams 
 #pragma unroll
                         for (int j = 0; j < W; ++j) {
                             // step k is tap j of step k + j
-                            const bool cut =
-                                FLAGS && j > 0 && (starts & (((1u << j) - 1) << (k + 3))) != 0;
-                            s = fmaf(w[W - 1 - j], cut ? 0.f : dpre[k + j], s);
+                            const float g = FLAGS && j > 0 ? episodes.keep(dpre[k + j], k + j, j)
+                                                           : dpre[k + j];
+                            s = fmaf(w[W - 1 - j], g, s);
                         }
                         dx[k] = k < n ? s : 0.f;
                         db += dpre[k];
 #pragma unroll
                         for (int j = 0; j < W; ++j)
-                            dw[W - 1 - j] = fmaf(dpre[k], tap<W, FLAGS>(v, starts, k, j),
+                            dw[W - 1 - j] = fmaf(dpre[k], tap<W, FLAGS>(v, episodes, k, j),
                                                  dw[W - 1 - j]);
                     }
                     if (p.grad_state != nullptr && l.t0 == 0) {

@@ -11,21 +11,21 @@
 namespace rlca {
 namespace seq {
 
-// States staged in LDS together, in two buffers: the next stage's rows are
-// loaded while one is computed, and one barrier a stage suffices.
-constexpr int kForwardStates = 8;
-
+// B and C are staged in two buffers: the next stage's rows are loaded while one
+// is computed, and one barrier a stage suffices.
+//
 // SPLIT waves share four channels: each takes every SPLIT-th pair of states
-// over all the steps, and prepares and finishes 8 / SPLIT of a lane's steps.
+// over all the steps, and prepares and finishes K / SPLIT of a lane's steps.
 // They meet in LDS twice a tile, in dt and dt u before and in y's partial sums
 // after (split_of below says when that pays).
-template <typename E, bool FLAGS, int SPLIT>
+template <typename E, bool FLAGS, int SPLIT, int K>
 __global__ __launch_bounds__(kScanThreads, sizeof(E) == 2 && !FLAGS ? 4 : 3) void selective_scan(ScanParams p) {
-    constexpr int kQuads = kScanWaves / SPLIT, kRows = 4 * kQuads, kOwn = kScanK / SPLIT;
+    constexpr int kQuads = kScanWaves / SPLIT, kRows = 4 * kQuads, kOwn = K / SPLIT;
+    constexpr int kTile = tile_of(K);
     extern __shared__ __attribute__((aligned(16))) char lds_bytes[];
-    __shared__ TileRow tiles[2][2][kForwardStates];  // [buffer][B, C][state]
-    __shared__ float steps[kQuads][SPLIT > 1 ? (FLAGS ? 3 : 2) * kScanK : 1][kWave];
-    __shared__ float sums[SPLIT > 1 ? kScanWaves : 1][SPLIT > 1 ? kScanK : 1][kWave];
+    __shared__ TileRow<K> tiles[2][2][kScanStates];  // [buffer][B, C][state]
+    __shared__ float steps[kQuads][SPLIT > 1 ? (FLAGS ? 3 : 2) * K : 1][kWave];
+    __shared__ float sums[SPLIT > 1 ? kScanWaves : 1][SPLIT > 1 ? K : 1][kWave];
     __shared__ uint32_t stage_tame[2][kScanWaves];  // [buffer]: whether what a wave staged is
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int in_wave = threadIdx.x % kWave;
@@ -46,7 +46,7 @@ __global__ __launch_bounds__(kScanThreads, sizeof(E) == 2 && !FLAGS ? 4 : 3) voi
             if constexpr (FLAGS) decays &= x <= 0.f && tame(x, kTameStep);
         }
     const int end = row_end(p.lengths, l.n, p.T);
-    const int own = l.lane * kScanK + part * kOwn;  // the lane's own steps in a tile
+    const int own = l.lane * K + part * kOwn;  // the lane's own steps in a tile
     const E *u_row = static_cast<const E *>(p.u) + l.n * p.u_n + l.d * p.u_d + own;
     const E *delta_row = static_cast<const E *>(p.delta) + l.n * p.delta_n + l.d * p.delta_d + own;
     const E *z_row =
@@ -58,29 +58,29 @@ __global__ __launch_bounds__(kScanThreads, sizeof(E) == 2 && !FLAGS ? 4 : 3) voi
 
     // What a thread stages: 8 steps of one state, of B in the first two waves
     // and of C in the others.
-    const int stage_c = wave / 2, stage_s = threadIdx.x / kScanLanes % kForwardStates;
+    const int stage_c = wave / 2, stage_s = threadIdx.x / kScanLanes % kScanStates;
     const int64_t stage_stride = stage_c ? p.C_s : p.B_s;
     const E *stage_row = (stage_c ? static_cast<const E *>(p.C) + l.n * p.C_n + l.g * p.C_g
                                   : static_cast<const E *>(p.B) + l.n * p.B_n + l.g * p.B_g) +
-                         stage_s * stage_stride + l.lane * kScanK;
-    Steps<kScanK, E> next_stage;
+                         stage_s * stage_stride + l.lane * K;
+    Steps<K, E> next_stage;
     Steps<kOwn, E> next_u, next_delta;
     const auto load_stage = [&](int t0, int s0) {
         next_stage.load(stage_row + s0 * stage_stride + t0,
-                        s0 + stage_s < S ? end - t0 - l.lane * kScanK : 0);
+                        s0 + stage_s < S ? end - t0 - l.lane * K : 0);
     };
     const auto load_tile = [&](int t0) {
         next_u.load(u_row + t0, end - t0 - own);
         next_delta.load(delta_row + t0, end - t0 - own);
     };
     // Past the row's steps y is 0.
-    const int live_tiles = (end + kScanTile - 1) / kScanTile;
+    const int live_tiles = (end + kTile - 1) / kTile;
     int buffer = 0;
     load_stage(0, 0);
     load_tile(0);
 
     for (int tile = 0; tile < live_tiles; ++tile) {
-        const int t0 = tile * kScanTile;
+        const int t0 = tile * kTile;
         if (p.checkpoints != nullptr && l.live)
             for (int s = l.lane; s < S; s += kScanLanes)
                 if (mine(s)) p.checkpoints[((int64_t)l.row * p.tiles + tile) * S + s] = carry[s];
@@ -88,7 +88,7 @@ __global__ __launch_bounds__(kScanThreads, sizeof(E) == 2 && !FLAGS ? 4 : 3) voi
         if constexpr (FLAGS)
             for (int s = l.lane; s < padded; s += kScanLanes)
                 if (mine(s)) all_ok &= tame(carry[s], kTameState);
-        float skipped[kOwn], dt[kScanK], dtu[kScanK], cut[kScanK], y[kScanK] = {};
+        float skipped[kOwn], dt[K], dtu[K], cut[K], y[K] = {};
         Steps<kOwn, E> z;
         if (z_row != nullptr) z.load(z_row + t0, end - t0 - own);
         {
@@ -96,14 +96,14 @@ __global__ __launch_bounds__(kScanThreads, sizeof(E) == 2 && !FLAGS ? 4 : 3) voi
             next_u.widen(u);
             next_delta.widen(raw);
             make_steps<FLAGS>(p, flags, bias, t0 + own, end, end, u, raw, own_dt, own_dtu, own_cut);
-            if (tile + 1 < live_tiles) load_tile(t0 + kScanTile);
+            if (tile + 1 < live_tiles) load_tile(t0 + kTile);
 #pragma unroll
             for (int k = 0; k < kOwn; ++k) {
                 if constexpr (SPLIT > 1) {
                     steps[quad][part * kOwn + k][in_wave] = own_dt[k];
-                    steps[quad][kScanK + part * kOwn + k][in_wave] = own_dtu[k];
+                    steps[quad][K + part * kOwn + k][in_wave] = own_dtu[k];
                     if constexpr (FLAGS)
-                        steps[quad][2 * kScanK + part * kOwn + k][in_wave] = own_cut[k];
+                        steps[quad][2 * K + part * kOwn + k][in_wave] = own_cut[k];
                 } else {
                     dt[k] = own_dt[k];
                     dtu[k] = own_dtu[k];
@@ -115,43 +115,43 @@ __global__ __launch_bounds__(kScanThreads, sizeof(E) == 2 && !FLAGS ? 4 : 3) voi
         }
         float dt_sum = 0.f;
         bool starts = false;
-        for (int s0 = 0; s0 < S; s0 += kForwardStates) {
+        for (int s0 = 0; s0 < S; s0 += kScanStates) {
             stage(tiles[buffer][stage_c][stage_s], next_stage, l.lane);
             if constexpr (FLAGS) {
                 const bool ok = whole_wave(all_tame(next_stage));
                 if (in_wave == 0) stage_tame[buffer][wave] = ok ? 1u : 0u;
             }
-            if (s0 + kForwardStates < S)
-                load_stage(t0, s0 + kForwardStates);
+            if (s0 + kScanStates < S)
+                load_stage(t0, s0 + kScanStates);
             else if (tile + 1 < live_tiles)
-                load_stage(t0 + kScanTile, 0);
+                load_stage(t0 + kTile, 0);
             __syncthreads();
             if (s0 == 0) {
 #pragma unroll
-                for (int k = 0; k < kScanK; ++k) {
+                for (int k = 0; k < K; ++k) {
                     if constexpr (SPLIT > 1) {
                         dt[k] = steps[quad][k][in_wave];
-                        dtu[k] = steps[quad][kScanK + k][in_wave];
-                        if constexpr (FLAGS) cut[k] = steps[quad][2 * kScanK + k][in_wave];
+                        dtu[k] = steps[quad][K + k][in_wave];
+                        if constexpr (FLAGS) cut[k] = steps[quad][2 * K + k][in_wave];
                     }
                     dt_sum += dt[k];
                     if constexpr (FLAGS) starts |= cut[k] != 0.f;
                 }
                 if constexpr (FLAGS) all_ok = whole_wave(all_ok && steps_tame(dt, dtu));
             }
-            const TileRow *B_tile = tiles[buffer][0], *C_tile = tiles[buffer][1];
-            const int count = S - s0 < kForwardStates ? S - s0 : kForwardStates;
+            const TileRow<K> *B_tile = tiles[buffer][0], *C_tile = tiles[buffer][1];
+            const int count = S - s0 < kScanStates ? S - s0 : kScanStates;
             const auto scan_states = [&](auto careful) {
                 constexpr bool CUT = decltype(careful)::value;
                 for (int i = 2 * part; i < count; i += 2 * SPLIT) {
-                    float a[2][kScanK], b[2][kScanK], h[2], prod[2], enter[2];
+                    float a[2][K], b[2][K], h[2], prod[2], enter[2];
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         const float a2 = A2[s0 + i + j];
                         enter[j] = carry[s0 + i + j];
                         read_tile(B_tile[i + j], l.lane, b[j]);
 #pragma unroll
-                        for (int k = 0; k < kScanK; ++k) {
+                        for (int k = 0; k < K; ++k) {
                             a[j][k] = decay<FLAGS>(dt[k], cut[k], a2);
                             b[j][k] *= dtu[k];
                             h[j] = k == 0 ? b[j][0] : step_map<CUT>(a[j][k], b[j][k], h[j]);
@@ -164,10 +164,10 @@ __global__ __launch_bounds__(kScanThreads, sizeof(E) == 2 && !FLAGS ? 4 : 3) voi
                         const float after = step_map<CUT>(prod[j], h[j], enter[j]);
                         carry[s0 + i + j] = row_last<false>(after);
                         h[j] = row_shift<false>(after, enter[j]);
-                        float c[kScanK];
+                        float c[K];
                         read_tile(C_tile[i + j], l.lane, c);
 #pragma unroll
-                        for (int k = 0; k < kScanK; ++k) {
+                        for (int k = 0; k < K; ++k) {
                             h[j] = step_map<CUT>(a[j][k], b[j][k], h[j]);
                             y[k] = fmaf(c[k], h[j], y[k]);
                         }
@@ -191,7 +191,7 @@ __global__ __launch_bounds__(kScanThreads, sizeof(E) == 2 && !FLAGS ? 4 : 3) voi
         float out[kOwn];
         if constexpr (SPLIT > 1) {
 #pragma unroll
-            for (int k = 0; k < kScanK; ++k) sums[wave][k][in_wave] = y[k];
+            for (int k = 0; k < K; ++k) sums[wave][k][in_wave] = y[k];
             __syncthreads();
 #pragma unroll
             for (int k = 0; k < kOwn; ++k) {
@@ -219,7 +219,7 @@ __global__ __launch_bounds__(kScanThreads, sizeof(E) == 2 && !FLAGS ? 4 : 3) voi
         }
     }
     if (!l.live) return;
-    for (int t0 = live_tiles * kScanTile; t0 + own < p.T; t0 += kScanTile) {
+    for (int t0 = live_tiles * kTile; t0 + own < p.T; t0 += kTile) {
         const float zeros[kOwn] = {};
         store_steps<kOwn>(y_row + t0, p.T - t0 - own, zeros);
     }
@@ -231,6 +231,23 @@ __global__ __launch_bounds__(kScanThreads, sizeof(E) == 2 && !FLAGS ? 4 : 3) voi
 }
 
 // ------------------------------------------------------------------- host side
+// Steps of a lane: of 8, 4 and 2 the cheapest by the cost of the row's tiles, in
+// which 16 instructions for each step of 8 stand for what a tile costs beside
+// its steps.  Forward and backward with 2, 4 and 8 (256 channels, 16 states,
+// bf16): 2048 rows of 32 steps 538, 784 and 1387 us; 1024 of 64 507, 405 and
+// 728; 512 of 96 377, 382 and 372; 512 of 130 621, 569 and 696; 128 of 520 572,
+// 457 and 452.
+int steps_of(int64_t T) {
+    int best = 8;
+    int64_t least = INT64_MAX;
+    for (int K = 8; K >= 2; K /= 2) {
+        const int64_t tiles = (T + tile_of(K) - 1) / tile_of(K);
+        const int64_t cost = tiles * (16 + 8 * K);
+        if (cost < least) least = cost, best = K;
+    }
+    return best;
+}
+
 ScanParams scan_params(const rlca_scan_call &c, int rows) {
     ScanParams p = {};
     p.u = c.u;
@@ -266,7 +283,8 @@ ScanParams scan_params(const rlca_scan_call &c, int rows) {
     p.states = (uint32_t)c.states;
     p.blocks_per_group = (p.per_group + rows - 1) / rows;
     p.T = (int32_t)c.T;
-    p.tiles = (p.T + kScanTile - 1) / kScanTile;
+    const int tile = tile_of(steps_of(c.T));
+    p.tiles = (p.T + tile - 1) / tile;
     p.softplus = c.softplus;
     p.after_done = c.convention == RLCA_RESET_AFTER_DONE;
     return p;
@@ -285,21 +303,24 @@ static int split_of(const rlca_scan_call &c) {
     return waves <= 1536 && pairs >= 4 ? 4 : waves <= 3072 && pairs >= 2 ? 2 : 1;
 }
 
-template <typename E, int SPLIT>
+template <typename E, int SPLIT, int K>
 static const void *scan_kernel(bool flags) {
-    return flags ? (const void *)selective_scan<E, true, SPLIT>
-                 : (const void *)selective_scan<E, false, SPLIT>;
+    return flags ? (const void *)selective_scan<E, true, SPLIT, K>
+                 : (const void *)selective_scan<E, false, SPLIT, K>;
 }
 
 template <typename E>
-static const void *scan_kernel(bool flags, int split) {
-    return split == 4   ? scan_kernel<E, 4>(flags)
-           : split == 2 ? scan_kernel<E, 2>(flags)
-                        : scan_kernel<E, 1>(flags);
+static const void *scan_kernel(bool flags, int split, int steps) {
+    return steps == 2   ? scan_kernel<E, 1, 2>(flags)
+           : steps == 4 ? scan_kernel<E, 1, 4>(flags)
+           : split == 4 ? scan_kernel<E, 4, 8>(flags)
+           : split == 2 ? scan_kernel<E, 2, 8>(flags)
+                        : scan_kernel<E, 1, 8>(flags);
 }
 
 static int64_t checkpoint_values(const rlca_scan_call &c) {
-    return c.num_seqs * c.channels * ((c.T + kScanTile - 1) / kScanTile) * c.states;
+    const int tile = tile_of(steps_of(c.T));
+    return c.num_seqs * c.channels * ((c.T + tile - 1) / tile) * c.states;
 }
 
 rlca_status check_scan(const rlca_scan_call &c, bool backward, Arrays *a) {
@@ -373,11 +394,11 @@ rlca_status rlca_selective_scan(const rlca_scan_call *call, hipStream_t stream) 
     if (st == RLCA_OK) st = a.status();
     if (st != RLCA_OK) return st;
     if (c.num_seqs * c.channels == 0 || (c.T == 0 && c.final_state == nullptr)) return RLCA_OK;
-    const int split = split_of(c);
+    const int steps = steps_of(c.T), split = steps == 8 ? split_of(c) : 1;
     ScanParams p = scan_params(c, kScanRows / split);
-    const void *kernel = c.dtype == RLCA_F32    ? scan_kernel<float>(c.flags != nullptr, split)
-                         : c.dtype == RLCA_BF16 ? scan_kernel<__bf16>(c.flags != nullptr, split)
-                                                : scan_kernel<_Float16>(c.flags != nullptr, split);
+    const void *kernel = c.dtype == RLCA_F32    ? scan_kernel<float>(c.flags != nullptr, split, steps)
+                         : c.dtype == RLCA_BF16 ? scan_kernel<__bf16>(c.flags != nullptr, split, steps)
+                                                : scan_kernel<_Float16>(c.flags != nullptr, split, steps);
     return launch(kernel, dim3(p.num_seqs * p.groups * p.blocks_per_group), kScanThreads,
                   2 * (kScanRows / split) * padded_states(c.states) * 4, p, stream);
 }

@@ -4,8 +4,9 @@
 // For each channel and state,  h_t = a_t h_{t-1} + b_t  with a_t = exp(dt_t A)
 // and b_t = dt_t u_t B_t, is the forward affine recurrence of this library; a
 // wave scans it as the other kernels do.  A row of 16 lanes (one DPP row) owns
-// a channel and a tile of 128 steps, 8 consecutive steps a lane:
-//   * each lane folds its 8 maps serially into one; the product of its a's is
+// a channel and a tile of 16 K steps, K consecutive steps a lane (K = 8, fewer
+// for short rows):
+//   * each lane folds its K maps serially into one; the product of its a's is
 //     exp(A sum dt), one exponential;
 //   * four DPP row shifts scan the 16 lane maps;
 //   * the tile's incoming state is a carry per (channel, state) kept in LDS;
@@ -19,13 +20,17 @@
 namespace rlca {
 namespace seq {
 
-constexpr int kScanK = 8;                        // steps of a lane
-constexpr int kScanLanes = 16;                   // lanes of a row
-constexpr int kScanTile = kScanK * kScanLanes;   // 128 steps
-constexpr int kScanWaves = 4;                    // waves of a workgroup
+constexpr int kScanLanes = 16;  // lanes of a row
+constexpr int kScanWaves = 4;   // waves of a workgroup
 constexpr int kScanThreads = kScanWaves * kWave;
 constexpr int kScanRows = kScanThreads / kScanLanes;  // channels of a workgroup
-constexpr int kScanStates = 8;  // backward: states staged in LDS together
+constexpr int kScanStates = 8;  // states whose B and C are staged in LDS together
+
+// Steps of a lane, K, and of a tile.  A lane's cost for a tile and state is
+// about 13 instructions for the scan over lanes and 7 a step (forward), so long
+// rows take the most steps; rows that fill little of their last tile take
+// fewer (steps_of).
+constexpr int tile_of(int K) { return kScanLanes * K; }
 
 // States of a workgroup's LDS arrays: whole pairs, since the kernels take two
 // states at a time.
@@ -42,7 +47,7 @@ struct ScanParams {
     float *checkpoints;  // [num_seqs * channels][tiles][states]: states entering each tile
     void *grad_u, *grad_delta, *grad_z;
     float *grad_state;
-    float *bc_partials;  // [num_seqs][groups][blocks of a group][2][states][tiles * kScanTile]
+    float *bc_partials;  // [num_seqs][groups][blocks of a group][2][states][tiles * tile_of(K)]
     float *row_partials; // [num_seqs][channels][states + 2]: grad_A, grad_D, grad_delta_bias
     int64_t u_n, u_d, delta_n, delta_d, z_n, z_d, g_n, g_d;
     int64_t B_n, B_g, B_s, C_n, C_g, C_s;
@@ -157,29 +162,42 @@ __device__ __forceinline__ void wave_order() {
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 }
 
-// A tile of one state's B or C in LDS, fp32: a lane's 8 steps as two blocks of
+// A tile of one state's B or C in LDS, fp32: a lane's steps in blocks of up to
 // four, each lane's next to its neighbours', so that the 16-byte reads of 16
 // lanes cover all banks once.
-typedef float float4v __attribute__((ext_vector_type(4)));
+template <int N>
+using Floats = float __attribute__((ext_vector_type(N)));
+typedef Floats<4> float4v;
+
+template <int K>
 struct TileRow {
-    float4v half[2][kScanLanes];
+    static constexpr int kBlock = K < 4 ? K : 4;
+    Floats<kBlock> block[K / kBlock][kScanLanes];
 };
 
-__device__ __forceinline__ void read_tile(const TileRow &r, int lane, float (&v)[kScanK]) {
-    const float4v x = r.half[0][lane], y = r.half[1][lane];
+template <int K>
+__device__ __forceinline__ void read_tile(const TileRow<K> &r, int lane, float (&v)[K]) {
+    constexpr int N = TileRow<K>::kBlock;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = x[k], v[4 + k] = y[k];
+    for (int i = 0; i < K / N; ++i) {
+        const Floats<N> x = r.block[i][lane];
+#pragma unroll
+        for (int k = 0; k < N; ++k) v[i * N + k] = x[k];
+    }
 }
 
-template <typename E>
-__device__ __forceinline__ void stage(TileRow &to, const Steps<kScanK, E> &from, int lane) {
-    float v[kScanK];
+template <typename E, int K>
+__device__ __forceinline__ void stage(TileRow<K> &to, const Steps<K, E> &from, int lane) {
+    constexpr int N = TileRow<K>::kBlock;
+    float v[K];
     from.widen(v);
-    float4v x, y;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) x[k] = v[k], y[k] = v[4 + k];
-    to.half[0][lane] = x;
-    to.half[1][lane] = y;
+    for (int i = 0; i < K / N; ++i) {
+        Floats<N> x;
+#pragma unroll
+        for (int k = 0; k < N; ++k) x[k] = v[i * N + k];
+        to.block[i][lane] = x;
+    }
 }
 
 // K steps of a lane from step t: dt and dt u from raw = delta and u (0 past
@@ -234,7 +252,7 @@ __device__ __forceinline__ float decay(float dt, float cut, float A2) {
 
 // Tame values: too small for any state, gradient or product of the scans to
 // overflow within a tile.  With a in [0, 1] (dt >= 0 and A <= 0), dt u, B, C and
-// gy below 2^40 and entering values below 2^100, sums over 128 steps stay
+// gy below 2^40 and entering values below 2^100, sums over a tile's steps stay
 // below 2^101.  A NaN is not tame.
 constexpr float kTameStep = 0x1p40f, kTameState = 0x1p100f;
 __device__ __forceinline__ bool tame(float x, float limit) { return fabsf(x) < limit; }
@@ -250,10 +268,11 @@ __device__ __forceinline__ bool all_tame(const Steps<K, E> &s) {
 }
 
 // Whether a lane's steps are: dt not negative, dt and dt u small.
-__device__ __forceinline__ bool steps_tame(const float (&dt)[kScanK], const float (&dtu)[kScanK]) {
+template <int K>
+__device__ __forceinline__ bool steps_tame(const float (&dt)[K], const float (&dtu)[K]) {
     bool ok = true;
 #pragma unroll
-    for (int k = 0; k < kScanK; ++k)
+    for (int k = 0; k < K; ++k)
         ok &= dt[k] >= 0.f && tame(dt[k], kTameStep) && tame(dtu[k], kTameStep);
     return ok;
 }
@@ -262,6 +281,7 @@ __device__ __forceinline__ bool whole_wave(bool x) {
     return __builtin_amdgcn_ballot_w64(!x) == 0;
 }
 
+int steps_of(int64_t T);
 ScanParams scan_params(const rlca_scan_call &c, int rows);
 rlca_status check_scan(const rlca_scan_call &c, bool backward, Arrays *a);
 

@@ -15,8 +15,6 @@
 // gradient) meet in 12 lane-half swaps and 12 additions, after which each row
 // holds the sums of four of them.  The waves' sums meet in LDS, the
 // workgroups' in a workspace that bc_sums adds in order.
-#include <stdlib.h>
-
 #include "seq_scan.hpp"
 
 namespace rlca {
@@ -30,15 +28,17 @@ __device__ __forceinline__ void swap_add(float &x, float y, bool halves) {
     x = __builtin_bit_cast(float, (uint32_t)r[0]) + __builtin_bit_cast(float, (uint32_t)r[1]);
 }
 
-// v[0..15] of four rows -> row q's lanes hold the sums over rows of v[4q .. 4q+3].
-__device__ __forceinline__ float4v sum_rows(float (&v)[16]) {
+// 2K values of four rows -> row q's lanes hold the sums over rows of the values
+// from q K/2 on, K/2 of them.
+template <int K>
+__device__ __forceinline__ Floats<K / 2> sum_rows(float (&v)[2 * K]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) swap_add(v[i], v[8 + i], true);
+    for (int i = 0; i < K; ++i) swap_add(v[i], v[K + i], true);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) swap_add(v[i], v[4 + i], false);
-    float4v r;
+    for (int i = 0; i < K / 2; ++i) swap_add(v[i], v[K / 2 + i], false);
+    Floats<K / 2> r;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) r[i] = v[i];
+    for (int i = 0; i < K / 2; ++i) r[i] = v[i];
     return r;
 }
 
@@ -57,18 +57,18 @@ __device__ __forceinline__ void row_sum(float (&x)[2]) {
 }
 
 // A workgroup holds four sets of four channels, SPLIT waves to each.  Waves of
-// one set take every SPLIT-th pair of states, and prepare and finish 8 / SPLIT
+// one set take every SPLIT-th pair of states, and prepare and finish K / SPLIT
 // of a lane's steps, as in the forward scan.
-template <typename E, bool FLAGS, bool GATE, int SPLIT>
+template <typename E, bool FLAGS, bool GATE, int SPLIT, int K>
 __global__ __launch_bounds__(kScanThreads *SPLIT, 2) void selective_scan_backward(ScanParams p) {
     constexpr int kQuads = kScanWaves, kRows = kScanRows;
-    constexpr int kOwn = kScanK / SPLIT, kThreads = kScanThreads * SPLIT;
+    constexpr int kTile = tile_of(K), kOwn = K / SPLIT, kThreads = kScanThreads * SPLIT;
     constexpr int kBefore = FLAGS ? 4 : 3, kAfter = GATE ? 3 : 2;  // values a step that waves share
     extern __shared__ __attribute__((aligned(16))) char lds_bytes[];
-    __shared__ TileRow tiles[2][2][kScanStates];  // [buffer][B, C][state]
-    __shared__ float4v bc[kQuads][kScanStates][kWave];
-    __shared__ float before[SPLIT > 1 ? kQuads : 1][SPLIT > 1 ? kBefore * kScanK : 1][kWave];
-    __shared__ float after[SPLIT > 1 ? SPLIT * kQuads : 1][SPLIT > 1 ? kAfter * kScanK : 1][kWave];
+    __shared__ TileRow<K> tiles[2][2][kScanStates];  // [buffer][B, C][state]
+    __shared__ Floats<K / 2> bc[kQuads][kScanStates][kWave];
+    __shared__ float before[SPLIT > 1 ? kQuads : 1][SPLIT > 1 ? kBefore * K : 1][kWave];
+    __shared__ float after[SPLIT > 1 ? SPLIT * kQuads : 1][SPLIT > 1 ? kAfter * K : 1][kWave];
     __shared__ uint32_t stage_tame[2][kThreads / kWave];  // [buffer]: whether what a wave staged is
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int in_wave = threadIdx.x % kWave;
@@ -97,7 +97,7 @@ __global__ __launch_bounds__(kScanThreads *SPLIT, 2) void selective_scan_backwar
                            : p.grad_final[(int64_t)l.row * S + s];
             grad_A[s] = 0.f;
         }
-    const int own = l.lane * kScanK + part * kOwn;  // the lane's own steps in a tile
+    const int own = l.lane * K + part * kOwn;  // the lane's own steps in a tile
     const E *u_row = static_cast<const E *>(p.u) + l.n * p.u_n + l.d * p.u_d + own;
     const E *delta_row = static_cast<const E *>(p.delta) + l.n * p.delta_n + l.d * p.delta_d + own;
     const E *g_row = static_cast<const E *>(p.grad_y) + l.n * p.g_n + l.d * p.g_d + own;
@@ -108,7 +108,7 @@ __global__ __launch_bounds__(kScanThreads *SPLIT, 2) void selective_scan_backwar
     E *grad_u = static_cast<E *>(p.grad_u) + out_row;
     E *grad_delta = static_cast<E *>(p.grad_delta) + out_row;
     E *grad_z = GATE ? static_cast<E *>(p.grad_z) + out_row : nullptr;
-    float *partials = p.bc_partials + (int64_t)blockIdx.x * 2 * S * p.tiles * kScanTile;
+    float *partials = p.bc_partials + (int64_t)blockIdx.x * 2 * S * p.tiles * kTile;
     float totals[2] = {0.f, 0.f};  // of grad_D and grad_delta_bias
 
     // What a thread of the first four waves stages: 8 steps of one state of B
@@ -118,13 +118,13 @@ __global__ __launch_bounds__(kScanThreads *SPLIT, 2) void selective_scan_backwar
     const int64_t stage_stride = stage_c ? p.C_s : p.B_s;
     const E *stage_row = (stage_c ? static_cast<const E *>(p.C) + l.n * p.C_n + l.g * p.C_g
                                   : static_cast<const E *>(p.B) + l.n * p.B_n + l.g * p.B_g) +
-                         stage_s * stage_stride + l.lane * kScanK;
-    Steps<kScanK, E> next_stage;
+                         stage_s * stage_stride + l.lane * K;
+    Steps<K, E> next_stage;
     Steps<kOwn, E> u, delta, go, z, next_u, next_delta, next_go, next_z;
     const auto load_stage = [&](int t0, int s0) {
         if (stages)
             next_stage.load(stage_row + s0 * stage_stride + t0,
-                            s0 + stage_s < S ? row_steps - t0 - l.lane * kScanK : 0);
+                            s0 + stage_s < S ? row_steps - t0 - l.lane * K : 0);
     };
     const auto load_tile = [&](int t0) {
         next_u.load(u_row + t0, end - t0 - own);
@@ -134,8 +134,8 @@ __global__ __launch_bounds__(kScanThreads *SPLIT, 2) void selective_scan_backwar
     };
 
     // tiles past the row's steps are zeros, and their sums are not read
-    const int live_tiles = (row_steps + kScanTile - 1) / kScanTile;
-    for (int t0 = live_tiles * kScanTile; l.live && t0 + own < p.T; t0 += kScanTile) {
+    const int live_tiles = (row_steps + kTile - 1) / kTile;
+    for (int t0 = live_tiles * kTile; l.live && t0 + own < p.T; t0 += kTile) {
         const float zeros[kOwn] = {};
         const int n = p.T - t0 - own;
         store_steps<kOwn>(grad_u + t0, n, zeros);
@@ -149,12 +149,12 @@ __global__ __launch_bounds__(kScanThreads *SPLIT, 2) void selective_scan_backwar
     constexpr bool kReload = FLAGS && GATE;
     int buffer = 0;
     if (live_tiles > 0) {  // an empty row has no last tile
-        load_stage((live_tiles - 1) * kScanTile, 0);
-        if constexpr (kAhead) load_tile((live_tiles - 1) * kScanTile);
+        load_stage((live_tiles - 1) * kTile, 0);
+        if constexpr (kAhead) load_tile((live_tiles - 1) * kTile);
     }
 
     for (int tile = live_tiles - 1; tile >= 0; --tile) {
-        const int t0 = tile * kScanTile;
+        const int t0 = tile * kTile;
         bool all_ok = decays;  // of the lane's values in this tile: tame
         if constexpr (!kAhead) load_tile(t0);
         u = next_u;
@@ -171,9 +171,9 @@ __global__ __launch_bounds__(kScanThreads *SPLIT, 2) void selective_scan_backwar
                         all_ok &= tame(x, kTameState) && tame(carry[s], kTameState);
                 }
         }
-        if (kAhead && tile > 0) load_tile(t0 - kScanTile);
-        float dt[kScanK], dtu[kScanK], cut[kScanK], gy[kScanK];
-        float y[kScanK] = {}, grad_dt[kScanK] = {}, gB[kScanK] = {};
+        if (kAhead && tile > 0) load_tile(t0 - kTile);
+        float dt[K], dtu[K], cut[K], gy[K];
+        float y[K] = {}, grad_dt[K] = {}, gB[K] = {};
         {
             float v[kOwn], raw[kOwn], own_dt[kOwn], own_dtu[kOwn], own_cut[kOwn], own_gy[kOwn];
             u.widen(v);
@@ -191,9 +191,9 @@ __global__ __launch_bounds__(kScanThreads *SPLIT, 2) void selective_scan_backwar
                 if constexpr (SPLIT > 1) {
                     const int at = part * kOwn + k;
                     before[quad][at][in_wave] = own_dt[k];
-                    before[quad][kScanK + at][in_wave] = own_dtu[k];
-                    before[quad][2 * kScanK + at][in_wave] = own_gy[k];
-                    if constexpr (FLAGS) before[quad][3 * kScanK + at][in_wave] = own_cut[k];
+                    before[quad][K + at][in_wave] = own_dtu[k];
+                    before[quad][2 * K + at][in_wave] = own_gy[k];
+                    if constexpr (FLAGS) before[quad][3 * K + at][in_wave] = own_cut[k];
                 } else {
                     dt[k] = own_dt[k];
                     dtu[k] = own_dtu[k];
@@ -214,16 +214,16 @@ __global__ __launch_bounds__(kScanThreads *SPLIT, 2) void selective_scan_backwar
             if (s0 + kScanStates < S)
                 load_stage(t0, s0 + kScanStates);
             else if (tile > 0)
-                load_stage(t0 - kScanTile, 0);
+                load_stage(t0 - kTile, 0);
             __syncthreads();
             if (s0 == 0) {
 #pragma unroll
-                for (int k = 0; k < kScanK; ++k) {
+                for (int k = 0; k < K; ++k) {
                     if constexpr (SPLIT > 1) {
                         dt[k] = before[quad][k][in_wave];
-                        dtu[k] = before[quad][kScanK + k][in_wave];
-                        gy[k] = before[quad][2 * kScanK + k][in_wave];
-                        if constexpr (FLAGS) cut[k] = before[quad][3 * kScanK + k][in_wave];
+                        dtu[k] = before[quad][K + k][in_wave];
+                        gy[k] = before[quad][2 * K + k][in_wave];
+                        if constexpr (FLAGS) cut[k] = before[quad][3 * K + k][in_wave];
                     }
                     dt_sum += dt[k];
                     if constexpr (FLAGS) starts |= cut[k] != 0.f;
@@ -231,24 +231,24 @@ __global__ __launch_bounds__(kScanThreads *SPLIT, 2) void selective_scan_backwar
                 if constexpr (FLAGS) {
                     all_ok &= steps_tame(dt, dtu);
 #pragma unroll
-                    for (int k = 0; k < kScanK; ++k) all_ok &= tame(gy[k], kTameStep);
+                    for (int k = 0; k < K; ++k) all_ok &= tame(gy[k], kTameStep);
                     all_ok = whole_wave(all_ok);
                 }
             }
-            const TileRow *B_tile = tiles[buffer][0], *C_tile = tiles[buffer][1];
+            const TileRow<K> *B_tile = tiles[buffer][0], *C_tile = tiles[buffer][1];
             const auto scan_states = [&](auto careful) {
                 constexpr bool CUT = decltype(careful)::value;
                 for (int i = 2 * part; i < count; i += 2 * SPLIT) {
-                    float a[2][kScanK], w[2][kScanK], g[2], prod[2], dA[2];
+                    float a[2][K], w[2][K], g[2], prod[2], dA[2];
                     float h[2], prefix[2], enter[2];
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         const float a2 = A[s0 + i + j] * kLog2e;
                         enter[j] = enter_states[s0 + i + j];
-                        float b[kScanK];
+                        float b[K];
                         read_tile(B_tile[i + j], l.lane, b);
 #pragma unroll
-                        for (int k = 0; k < kScanK; ++k) {
+                        for (int k = 0; k < K; ++k) {
                             a[j][k] = decay<FLAGS>(dt[k], cut[k], a2);
                             const float x = b[k] * dtu[k];
                             h[j] = k == 0 ? x : step_map<CUT>(a[j][k], x, h[j]);
@@ -256,24 +256,24 @@ __global__ __launch_bounds__(kScanThreads *SPLIT, 2) void selective_scan_backwar
                         prefix[j] = prod[j] = lane_product<FLAGS>(dt_sum, starts, a2);
                     }
                     row_scan<CUT, false>(prefix, h);
-                    float v[2][16], r[2], c[2][kScanK];
+                    float v[2][2 * K], r[2], c[2][K];
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         h[j] = row_shift<false>(step_map<CUT>(prefix[j], h[j], enter[j]), enter[j]);
-                        float b[kScanK];
+                        float b[K];
                         read_tile(B_tile[i + j], l.lane, b);
                         read_tile(C_tile[i + j], l.lane, c[j]);
 #pragma unroll
-                        for (int k = 0; k < kScanK; ++k) {
+                        for (int k = 0; k < K; ++k) {
                             w[j][k] = product<CUT>(a[j][k], h[j]);
                             h[j] = fmaf(b[k], dtu[k], w[j][k]);
-                            v[j][8 + k] = gy[k] * h[j];
+                            v[j][K + k] = gy[k] * h[j];
                             if constexpr (GATE) y[k] = fmaf(c[j][k], h[j], y[k]);
                             c[j][k] *= gy[k];  // what y's gradient adds to g
                         }
-                        g[j] = c[j][kScanK - 1];
+                        g[j] = c[j][K - 1];
 #pragma unroll
-                        for (int k = kScanK - 2; k >= 0; --k)
+                        for (int k = K - 2; k >= 0; --k)
                             g[j] = step_map<CUT>(a[j][k + 1], c[j][k], g[j]);
                         r[j] = product<CUT>(a[j][0], g[j]);
                     }
@@ -283,13 +283,13 @@ __global__ __launch_bounds__(kScanThreads *SPLIT, 2) void selective_scan_backwar
                         const float right = carry[s0 + i + j], A_s = A[s0 + i + j];
                         r[j] = step_map<CUT>(prod[j], r[j], right);
                         carry[s0 + i + j] = row_last<true>(r[j]);
-                        g[j] = row_shift<true>(r[j], right);  // a_{t+8} g_{t+8}
-                        float b[kScanK];
+                        g[j] = row_shift<true>(r[j], right);  // a g of the step after the lane's
+                        float b[K];
                         read_tile(B_tile[i + j], l.lane, b);
                         dA[j] = 0.f;
 #pragma unroll
-                        for (int k = kScanK - 1; k >= 0; --k) {
-                            g[j] = k == kScanK - 1 ? c[j][k] + g[j]
+                        for (int k = K - 1; k >= 0; --k) {
+                            g[j] = k == K - 1 ? c[j][k] + g[j]
                                                    : step_map<CUT>(a[j][k + 1], c[j][k], g[j]);
                             v[j][k] = g[j] * dtu[k];
                             gB[k] = fmaf(g[j], b[k], gB[k]);
@@ -297,7 +297,7 @@ __global__ __launch_bounds__(kScanThreads *SPLIT, 2) void selective_scan_backwar
                             dA[j] = fmaf(q, dt[k], dA[j]);  // at a start w is 0, and dt put to 0
                             grad_dt[k] = fmaf(q, A_s, grad_dt[k]);
                         }
-                        bc[quad][i + j][in_wave] = sum_rows(v[j]);
+                        bc[quad][i + j][in_wave] = sum_rows<K>(v[j]);
                     }
                     row_sum(dA);
 #pragma unroll
@@ -320,24 +320,24 @@ __global__ __launch_bounds__(kScanThreads *SPLIT, 2) void selective_scan_backwar
             if constexpr (SPLIT > 1) {
                 if (s0 + kScanStates >= S) {  // the tile's last stage
 #pragma unroll
-                    for (int k = 0; k < kScanK; ++k) {
+                    for (int k = 0; k < K; ++k) {
                         after[wave][k][in_wave] = gB[k];
-                        after[wave][kScanK + k][in_wave] = grad_dt[k];
-                        if constexpr (GATE) after[wave][2 * kScanK + k][in_wave] = y[k];
+                        after[wave][K + k][in_wave] = grad_dt[k];
+                        if constexpr (GATE) after[wave][2 * K + k][in_wave] = y[k];
                     }
                 }
             }
             __syncthreads();
-            // lane x of a wave holds, for state i, four steps of grad_B (rows 0
-            // and 1) or grad_C (rows 2 and 3)
+            // lane x of a wave holds, for state i, half a lane's steps of grad_B
+            // (rows 0 and 1) or grad_C (rows 2 and 3)
             for (int j = threadIdx.x; j < count * kWave; j += kThreads) {
                 const int i = j / kWave, x = j % kWave, q = x / kScanLanes;
-                float4v sum = bc[0][i][x];
+                Floats<K / 2> sum = bc[0][i][x];
 #pragma unroll
                 for (int m = 1; m < kQuads; ++m) sum += bc[m][i][x];
-                float *to = partials + ((int64_t)(q >> 1) * S + s0 + i) * p.tiles * kScanTile + t0 +
-                            (x % kScanLanes) * kScanK + (q & 1) * 4;
-                *reinterpret_cast<float4v *>(to) = sum;
+                float *to = partials + ((int64_t)(q >> 1) * S + s0 + i) * p.tiles * kTile + t0 +
+                            (x % kScanLanes) * K + (q & 1) * (K / 2);
+                *reinterpret_cast<Floats<K / 2> *>(to) = sum;
             }
         }
         wave_order();
@@ -350,8 +350,8 @@ __global__ __launch_bounds__(kScanThreads *SPLIT, 2) void selective_scan_backwar
 #pragma unroll
                 for (int q = 0; q < SPLIT; ++q) {
                     sum_gB[k] += after[quad * SPLIT + q][at][in_wave];
-                    sum_dt[k] += after[quad * SPLIT + q][kScanK + at][in_wave];
-                    if constexpr (GATE) sum_y[k] += after[quad * SPLIT + q][2 * kScanK + at][in_wave];
+                    sum_dt[k] += after[quad * SPLIT + q][K + at][in_wave];
+                    if constexpr (GATE) sum_y[k] += after[quad * SPLIT + q][2 * K + at][in_wave];
                 }
             } else {
                 sum_gB[k] = gB[k];
@@ -455,7 +455,7 @@ struct BcSums {
     const int32_t *lengths;
     uint32_t blocks, states, groups, rows;  // rows: num_seqs * groups * 2 * states
     uint32_t lane_bits;
-    int32_t T, padded;  // padded: tiles * kScanTile
+    int32_t T, padded;  // padded: whole tiles
 };
 
 template <typename E>
@@ -556,36 +556,39 @@ static Ranges ranges_of(int64_t num_seqs) {
     return {(uint32_t)size, (uint32_t)((num_seqs + size - 1) / size)};
 }
 
-// Waves that share four channels: two where one would leave SIMDs with a
-// single wave (SPLITB_FIGURES).
+// Waves that share four channels: two where one would leave the SIMDs a single
+// wave each (with one and two, forward and backward, 16 states, bf16: 4096
+// channels of 4096 steps 567 and 544 us, 2048 of 2048 243 and 230, 8192 of
+// 2048 457 and 528).  Above 64 states two would need over 160 KB of LDS.
 static int split_of(const rlca_scan_call &c) {
-    const char *e = getenv("BSPLIT");
-    if (e) return atoi(e);
-    // (with more than 64 states two waves would need over 160 KB of LDS)
     return c.num_seqs * c.channels <= 4096 && c.states > 2 && c.states <= 64 ? 2 : 1;
 }
 
 static Workspace workspace_of(const rlca_scan_call &c) {
-    const int64_t tiles = (c.T + kScanTile - 1) / kScanTile;
+    const int tile = tile_of(steps_of(c.T));
+    const int64_t padded = (c.T + tile - 1) / tile * tile;
     const int64_t per_group = c.groups == 0 ? 0 : c.channels / c.groups;
     const int64_t blocks = c.num_seqs * c.groups * ((per_group + kScanRows - 1) / kScanRows);
-    return {(size_t)(blocks * 2 * c.states * tiles * kScanTile),
+    return {(size_t)(blocks * 2 * c.states * padded),
             (size_t)((c.num_seqs * c.channels * (c.states + 2) + 3) / 4 * 4),
             (size_t)(2 * ranges_of(c.num_seqs).count * c.channels * (c.states + 2))};
 }
 
-template <typename E, int SPLIT>
+template <typename E, int SPLIT, int K>
 static const void *backward_kernel(const rlca_scan_call &c) {
     const bool flags = c.flags != nullptr, gate = c.z != nullptr;
-    return flags ? (gate ? (const void *)selective_scan_backward<E, true, true, SPLIT>
-                         : (const void *)selective_scan_backward<E, true, false, SPLIT>)
-                 : (gate ? (const void *)selective_scan_backward<E, false, true, SPLIT>
-                         : (const void *)selective_scan_backward<E, false, false, SPLIT>);
+    return flags ? (gate ? (const void *)selective_scan_backward<E, true, true, SPLIT, K>
+                         : (const void *)selective_scan_backward<E, true, false, SPLIT, K>)
+                 : (gate ? (const void *)selective_scan_backward<E, false, true, SPLIT, K>
+                         : (const void *)selective_scan_backward<E, false, false, SPLIT, K>);
 }
 
 template <typename E>
-static const void *backward_kernel(const rlca_scan_call &c, int split) {
-    return split == 2 ? backward_kernel<E, 2>(c) : backward_kernel<E, 1>(c);
+static const void *backward_kernel(const rlca_scan_call &c, int split, int steps) {
+    return steps == 2   ? backward_kernel<E, 1, 2>(c)
+           : steps == 4 ? backward_kernel<E, 1, 4>(c)
+           : split == 2 ? backward_kernel<E, 2, 8>(c)
+                        : backward_kernel<E, 1, 8>(c);
 }
 
 }  // namespace seq
@@ -615,14 +618,14 @@ rlca_status rlca_selective_scan_backward(const rlca_scan_call *call, void *works
     if (st != RLCA_OK) return st;
     if (workspace_bytes < w.total() * 4) return RLCA_ERR_INVALID_SIZE;
     if (c.channels == 0) return RLCA_OK;
-    const int split = split_of(c);
+    const int steps = steps_of(c.T), split = steps == 8 ? split_of(c) : 1;
     ScanParams p = scan_params(c, kScanRows);
     p.bc_partials = static_cast<float *>(workspace);
     p.row_partials = p.bc_partials + w.bc;
     if (c.num_seqs != 0) {
-        const void *kernel = c.dtype == RLCA_F32    ? backward_kernel<float>(c, split)
-                             : c.dtype == RLCA_BF16 ? backward_kernel<__bf16>(c, split)
-                                                    : backward_kernel<_Float16>(c, split);
+        const void *kernel = c.dtype == RLCA_F32    ? backward_kernel<float>(c, split, steps)
+                             : c.dtype == RLCA_BF16 ? backward_kernel<__bf16>(c, split, steps)
+                                                    : backward_kernel<_Float16>(c, split, steps);
         st = launch(kernel, dim3(p.num_seqs * p.groups * p.blocks_per_group),
                     kScanThreads * split, 4 * kScanRows * padded_states(c.states) * 4, p, stream);
         if (st != RLCA_OK) return st;
@@ -637,7 +640,7 @@ rlca_status rlca_selective_scan_backward(const rlca_scan_call *call, void *works
             b.groups = p.groups;
             b.rows = p.num_seqs * p.groups * 2 * p.states;
             b.T = p.T;
-            b.padded = p.tiles * kScanTile;
+            b.padded = p.tiles * tile_of(steps);
             while ((4 << b.lane_bits) < p.T && (1 << b.lane_bits) < kScanThreads) ++b.lane_bits;
             const uint32_t across = (p.T + (4 << b.lane_bits) - 1) / (4 << b.lane_bits);
             const uint32_t at_once = kScanThreads >> b.lane_bits;

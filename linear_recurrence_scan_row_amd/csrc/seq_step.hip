@@ -4,8 +4,6 @@
 // Both are bound by the states' traffic: each is read and written once, and a
 // step's few products cost nothing beside that.  With one sequence the time is
 // a launch and one chain of dependent loads.
-#include <stdlib.h>
-
 #include "seq.hpp"
 
 namespace rlca {
@@ -179,11 +177,13 @@ __global__ __launch_bounds__(kStepThreads) void selective_step(ScanStepParams p)
 // ------------------------------------------------------------------- host side
 // Channels of a thread of the convolution's step, where that leaves
 // kWideThreads threads or more (one wave for each SIMD): the states' 6 bytes a
-// channel then move 16 at a time.
+// channel then move 16 at a time (512x8192 bf16: 21 us against 33; 1x2048 fp32
+// 3.7 against 3.0).
 constexpr int kWideChannels = 8;
 constexpr int64_t kWideThreads = 1 << 16;
 
-// Threads of the scan's step from which a lane takes two channels.
+// Threads of the scan's step from which a lane takes two channels (512x4096, 16
+// states, bf16: 70 us against 73 with one; 1x2048 3.7 against 4.9).
 constexpr uint64_t kTwoRowsThreads = 1 << 20;
 
 template <typename E>
@@ -246,8 +246,7 @@ rlca_status rlca_causal_conv_step(const rlca_conv_step_call *call, hipStream_t s
     p.out = c.out;
     p.x_n = c.x_stride_seq;
     p.places = c.places;
-    const char *we = getenv("WIDE");
-    const bool wide = N * ((D + kWideChannels - 1) / kWideChannels) >= (we ? atoll(we) : kWideThreads);
+    const bool wide = N * ((D + kWideChannels - 1) / kWideChannels) >= kWideThreads;
     const int64_t vec = wide ? kWideChannels : 1;
     p.num_seqs = (uint32_t)N;
     p.channels = (uint32_t)D;
@@ -315,8 +314,7 @@ rlca_status rlca_selective_step(const rlca_scan_step_call *call, hipStream_t str
     p.by_group = fast_div((uint32_t)(D / G));
     while ((4 << p.lane_bits) < S) ++p.lane_bits;  // at most 32 lanes (128 states)
     const uint32_t rows_per_block = kStepThreads >> p.lane_bits;
-    const char *re = getenv("ROWS2");
-    const int rows_per_lane = (uint64_t)p.rows << p.lane_bits >= (re ? (uint64_t)atoll(re) : kTwoRowsThreads) ? 2 : 1;
+    const int rows_per_lane = (uint64_t)p.rows << p.lane_bits >= kTwoRowsThreads ? 2 : 1;
     const void *kernel = c.dtype == RLCA_F32    ? step_kernel<float>(rows_per_lane)
                          : c.dtype == RLCA_BF16 ? step_kernel<__bf16>(rows_per_lane)
                                                 : step_kernel<_Float16>(rows_per_lane);

@@ -11,8 +11,14 @@ namespace seq {
 
 constexpr int kStepThreads = 256;
 
-// Sequence n's place in the pool, or -1 for an empty seat.
-__device__ __forceinline__ int64_t place_of(const int32_t *slots, uint32_t n, int64_t places) {
+// In both kernels blockIdx.x walks a sequence's channels and y the sequences, so
+// a slot is the same for a whole workgroup, and a thread takes its channels of
+// several sequences: their parameters are read once.
+
+// Sequence n's place in the pool, or -1 for an empty seat or none.
+__device__ __forceinline__ int64_t place_of(const int32_t *slots, uint32_t n, uint32_t num_seqs,
+                                            int64_t places) {
+    if (n >= num_seqs) return -1;
     if (slots == nullptr) return n;
     const int64_t s = slots[n];
     return s >= 0 && s < places ? s : -1;
@@ -27,57 +33,70 @@ struct ConvStepParams {
     const uint8_t *starts;
     void *out;
     int64_t x_n, places;
-    uint32_t num_seqs, channels, blocks;  // blocks: of VEC channels, in a sequence
+    uint32_t num_seqs, channels;
     int32_t silu;
-    FastDiv by_blocks;
+};
+
+// What a thread loads of one sequence.
+template <typename E, int W, int VEC>
+struct ConvStepLoads {
+    int64_t place;
+    Steps<VEC, E> state[W - 1], x;
+    __device__ __forceinline__ void load(const ConvStepParams &p, uint32_t n, uint32_t d, int left) {
+        place = place_of(p.slots, n, p.num_seqs, p.places);
+        if (place < 0) return;
+        const E *from = static_cast<const E *>(p.state) + (place * p.channels + d) * (W - 1);
+        const bool fresh = p.starts != nullptr && p.starts[n] != 0;
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j)
+            state[j].load(from + j * VEC, fresh ? 0 : left * (W - 1) - j * VEC);
+        x.load(static_cast<const E *>(p.x) + n * p.x_n + d, left);
+    }
 };
 
 // A thread takes VEC neighbouring channels: their states are VEC (W-1)
 // consecutive values, read and written in VEC-wide pieces.
 template <typename E, int W, int VEC>
 __global__ __launch_bounds__(kStepThreads) void causal_conv_step(ConvStepParams p) {
-    const uint32_t i = blockIdx.x * kStepThreads + threadIdx.x;
-    if (i >= p.num_seqs * p.blocks) return;
-    const uint32_t n = p.by_blocks.div(i), d = (i - n * p.blocks) * VEC;
-    const int left = (int)(p.channels - d);  // VEC or more: whole blocks
-    const int64_t place = place_of(p.slots, n, p.places);
-    E *out = static_cast<E *>(p.out) + (int64_t)n * p.channels + d;
-    float o[VEC] = {};
-    if (place >= 0) {
-        E *state = static_cast<E *>(p.state) + (place * p.channels + d) * (W - 1);
-        float v[W - 1][VEC], x[VEC], w[W][VEC], bias[VEC] = {};
+    const uint32_t d = (blockIdx.x * blockDim.x + threadIdx.x) * VEC;
+    if (d >= p.channels) return;
+    const int left = (int)(p.channels - d);  // VEC or more: a whole block
+    ConvStepLoads<E, W, VEC> next;
+    next.load(p, blockIdx.y, d, left);
+    float w[W][VEC], bias[VEC] = {};
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j)
-            load_steps<VEC>(state + j * VEC, left * (W - 1) - j * VEC, v[j]);
-        load_steps<VEC>(static_cast<const E *>(p.x) + n * p.x_n + d, left, x);
+    for (int j = 0; j < W; ++j)
+        load_steps<VEC>(p.weight + (int64_t)d * W + j * VEC, left * W - j * VEC, w[j]);
+    if (p.bias != nullptr) load_steps<VEC>(p.bias + d, left, bias);
+    for (uint32_t n = blockIdx.y; n < p.num_seqs; n += gridDim.y) {
+        const ConvStepLoads<E, W, VEC> now = next;
+        if (n + gridDim.y < p.num_seqs) next.load(p, n + gridDim.y, d, left);
+        float out[VEC] = {};
+        if (now.place >= 0) {
+            float old[W - 1][VEC], x[VEC], shifted[W - 1][VEC];
 #pragma unroll
-        for (int j = 0; j < W; ++j)
-            load_steps<VEC>(p.weight + (int64_t)d * W + j * VEC, left * W - j * VEC, w[j]);
-        if (p.bias != nullptr) load_steps<VEC>(p.bias + d, left, bias);
-        if (p.starts != nullptr && p.starts[n] != 0)
+            for (int j = 0; j < W - 1; ++j) now.state[j].widen(old[j]);
+            now.x.widen(x);
+#pragma unroll
+            for (int c = 0; c < VEC; ++c) {
+                float pre = bias[c];
+#pragma unroll
+                for (int k = 0; k < W; ++k) {
+                    // element k of channel c in runs of W - 1 (state) or W (weight)
+                    const int e = c * (W - 1) + k, q = c * W + k;
+                    const float tap = k == W - 1 ? x[c] : old[e / VEC][e % VEC];
+                    pre = fmaf(w[q / VEC][q % VEC], tap, pre);
+                    if (k > 0) shifted[(e - 1) / VEC][(e - 1) % VEC] = tap;
+                }
+                out[c] = p.silu != 0 ? silu(pre) : pre;
+            }
+            E *to = static_cast<E *>(p.state) + (now.place * p.channels + d) * (W - 1);
 #pragma unroll
             for (int j = 0; j < W - 1; ++j)
-#pragma unroll
-                for (int c = 0; c < VEC; ++c) v[j][c] = 0.f;
-        float next[W - 1][VEC];
-#pragma unroll
-        for (int c = 0; c < VEC; ++c) {
-            float pre = bias[c];
-#pragma unroll
-            for (int k = 0; k < W; ++k) {
-                // element k of channel c in a run of rows of W - 1 (state) or W (weight)
-                const int e = c * (W - 1) + k, q = c * W + k;
-                const float tap = k == W - 1 ? x[c] : v[e / VEC][e % VEC];
-                pre = fmaf(w[q / VEC][q % VEC], tap, pre);
-                if (k > 0) next[(e - 1) / VEC][(e - 1) % VEC] = tap;
-            }
-            o[c] = p.silu != 0 ? silu(pre) : pre;
+                store_steps<VEC>(to + j * VEC, left * (W - 1) - j * VEC, shifted[j]);
         }
-#pragma unroll
-        for (int j = 0; j < W - 1; ++j)
-            store_steps<VEC>(state + j * VEC, left * (W - 1) - j * VEC, next[j]);
+        store_steps<VEC>(static_cast<E *>(p.out) + (int64_t)n * p.channels + d, left, out);
     }
-    store_steps<VEC>(out, left, o);
 }
 
 // ------------------------------------------------------------------- the scan
@@ -89,115 +108,93 @@ struct ScanStepParams {
     const uint8_t *starts;
     void *y;
     int64_t u_n, delta_n, z_n, B_n, B_g, C_n, C_g, places;
-    uint32_t rows, channels, states;
+    uint32_t num_seqs, channels, states;
     uint32_t lane_bits;  // log2 of the lanes of a channel
     int32_t softplus;
-    FastDiv by_channels, by_group;
+    FastDiv by_group;
 };
 
-// One channel of a lane: where its values are, and those that every lane of
-// the channel needs.
+// What a lane loads of one sequence.
 template <typename E>
-struct StepRow {
-    bool in, live;  // a row of the call; one with a place in the pool
-    uint32_t row, d;
-    float u, raw, z;
-    float *state;
-    const E *B, *C;
-    bool fresh;
-    __device__ __forceinline__ void load(const ScanStepParams &p, uint64_t row64) {
-        in = row64 < p.rows;
-        live = false;
-        if (!in) return;
-        row = (uint32_t)row64;
-        const uint32_t n = p.by_channels.div(row);
-        d = row - n * p.channels;
-        const uint32_t g = p.by_group.div(d);
-        const int64_t place = place_of(p.slots, n, p.places);
-        live = place >= 0;
-        if (!live) return;
-        fresh = p.starts != nullptr && p.starts[n] != 0;
-        state = p.state + (place * p.channels + d) * (int)p.states;
-        B = static_cast<const E *>(p.B) + n * p.B_n + g * p.B_g;
-        C = static_cast<const E *>(p.C) + n * p.C_n + g * p.C_g;
-        u = (float)static_cast<const E *>(p.u)[n * p.u_n + d];
-        raw = (float)static_cast<const E *>(p.delta)[n * p.delta_n + d];
-        z = p.z == nullptr ? 0.f : (float)static_cast<const E *>(p.z)[n * p.z_n + d];
+struct StepLoads {
+    int64_t place;
+    Steps<4, float> h;
+    Steps<4, E> b, c;
+    E u, raw, z;
+    __device__ __forceinline__ void load(const ScanStepParams &p, uint32_t n, uint32_t d,
+                                         uint32_t g, int s, int S) {
+        place = place_of(p.slots, n, p.num_seqs, p.places);
+        if (place < 0) return;
+        const bool fresh = p.starts != nullptr && p.starts[n] != 0;
+        h.load(p.state + (place * p.channels + d) * S + s, fresh ? 0 : S - s);
+        u = static_cast<const E *>(p.u)[n * p.u_n + d];
+        raw = static_cast<const E *>(p.delta)[n * p.delta_n + d];
+        if (p.z != nullptr) z = static_cast<const E *>(p.z)[n * p.z_n + d];
+        b.load(static_cast<const E *>(p.B) + n * p.B_n + g * p.B_g + s, S - s);
+        c.load(static_cast<const E *>(p.C) + n * p.C_n + g * p.C_g + s, S - s);
     }
 };
 
 // 2^lane_bits lanes share a channel, each owning 4 consecutive states (with at
-// most 128 states, up to 32 lanes); y's sum meets in a butterfly over them.
-// ROWS channels of a lane are loaded together, which keeps enough bytes in
-// flight.  Lanes of a channel share every branch.
-template <typename E, int ROWS>
-__global__ __launch_bounds__(kStepThreads) void selective_step(ScanStepParams p) {
+// most 128 states, up to 32 lanes); y's sum meets in a butterfly over them.  A
+// workgroup walks the sequences blockIdx.y, blockIdx.y + gridDim.y, ... and
+// loads one while it computes the one before, so the parameters are read once
+// and the chain from a slot to its state is hidden.
+template <typename E>
+__global__ __launch_bounds__(kStepThreads, 8) void selective_step(ScanStepParams p) {
     const uint32_t lanes = 1u << p.lane_bits;
-    const uint32_t rows_per_block = kStepThreads >> p.lane_bits;
+    const uint32_t d = (blockIdx.x * kStepThreads + threadIdx.x) >> p.lane_bits;
+    if (d >= p.channels) return;  // a channel's lanes leave together
     const int S = (int)p.states, s = (int)(threadIdx.x & (lanes - 1)) * 4;
-    for (uint64_t row0 = (uint64_t)blockIdx.x * rows_per_block * ROWS + (threadIdx.x >> p.lane_bits);
-         row0 < p.rows; row0 += (uint64_t)gridDim.x * rows_per_block * ROWS) {
-        StepRow<E> r[ROWS];
-        float h[ROWS][4];
+    const uint32_t g = p.by_group.div(d);
+    StepLoads<E> next;
+    next.load(p, blockIdx.y, d, g, s, S);
+    float a[4];
+    load_steps<4>(p.A + (int64_t)d * S + s, S - s, a);
+    const float bias = p.delta_bias == nullptr ? 0.f : p.delta_bias[d];
+    const float skip = p.D == nullptr ? 0.f : p.D[d];
+    for (uint32_t n = blockIdx.y; n < p.num_seqs; n += gridDim.y) {
+        const StepLoads<E> now = next;
+        if (n + gridDim.y < p.num_seqs) next.load(p, n + gridDim.y, d, g, s, S);
+        float y = 0.f;
+        if (now.place >= 0) {
+            const float u = (float)now.u;
+            float dt = (float)now.raw + bias, h[4], in[4], out[4];
+            if (p.softplus != 0) dt = softplus(dt);
+            now.h.widen(h);
+            now.b.widen(in);
+            now.c.widen(out);
 #pragma unroll
-        for (int i = 0; i < ROWS; ++i) {
-            r[i].load(p, row0 + i * rows_per_block);
-            if (r[i].live) load_steps<4>(r[i].state + s, S - s, h[i]);
-        }
-#pragma unroll
-        for (int i = 0; i < ROWS; ++i) {
-            if (!r[i].in) continue;
-            float y = 0.f;
-            if (r[i].live) {
-                float a[4], b[4], c[4], dt = r[i].raw;
-                load_steps<4>(p.A + (int64_t)r[i].d * S + s, S - s, a);
-                load_steps<4>(r[i].B + s, S - s, b);
-                load_steps<4>(r[i].C + s, S - s, c);
-                if (p.delta_bias != nullptr) dt += p.delta_bias[r[i].d];
-                if (p.softplus != 0) dt = softplus(dt);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float old = r[i].fresh ? 0.f : h[i][k];
-                    h[i][k] = fmaf(exp2_fast(dt * a[k] * kLog2e), old, dt * r[i].u * b[k]);
-                    if (s + k < S) y = fmaf(c[k], h[i][k], y);
-                }
-                store_steps<4>(r[i].state + s, S - s, h[i]);
+            for (int k = 0; k < 4; ++k) {
+                h[k] = fmaf(exp2_fast(dt * a[k] * kLog2e), h[k], dt * u * in[k]);
+                if (s + k < S) y = fmaf(out[k], h[k], y);
             }
-            for (uint32_t m = 1; m < lanes; m <<= 1) y += __shfl_xor(y, (int)m);
-            if (s != 0) continue;
-            if (r[i].live) {
-                if (p.D != nullptr) y = fmaf(p.D[r[i].d], r[i].u, y);
-                if (p.z != nullptr) y *= silu(r[i].z);
-            }
-            static_cast<E *>(p.y)[r[i].row] = (E)y;
+            store_steps<4>(p.state + (now.place * p.channels + d) * S + s, S - s, h);
         }
+        for (uint32_t m = 1; m < lanes; m <<= 1) y += __shfl_xor(y, (int)m);
+        if (s != 0) continue;
+        if (now.place >= 0) {
+            y = fmaf(skip, (float)now.u, y);
+            if (p.z != nullptr) y *= silu((float)now.z);
+        }
+        static_cast<E *>(p.y)[(int64_t)n * p.channels + d] = (E)y;
     }
 }
 
 // ------------------------------------------------------------------- host side
-// Channels of a thread of the convolution's step, where that leaves
-// kWideThreads threads or more (one wave for each SIMD): the states' 6 bytes a
-// channel then move 16 at a time (512x8192 bf16: 21 us against 33; 1x2048 fp32
-// 3.7 against 3.0).
+// Workgroups of a launch, as far as there are sequences: what the chip holds at
+// once.  The scan's step, 512x4096, 16 states, bf16, states from HBM: 119, 91,
+// 70, 71 and 81 us with 512, 1024, 2048, 4096 and a workgroup for each sequence.
+constexpr uint32_t kStepBlocks = 2048;
+
+// The convolution's step: eight channels a thread, with a quarter of the
+// workgroups, from kWideThreads such threads on; the states' 6 bytes a channel
+// then move 16 at a time.  512x8192 bf16: 18 us against 23 with one channel;
+// 256x4096 fp32 14.1 against 12.6.
 constexpr int kWideChannels = 8;
-constexpr int64_t kWideThreads = 1 << 16;
-
-// Threads of the scan's step from which a lane takes two channels (512x4096, 16
-// states, bf16: 70 us against 73 with one; 1x2048 3.7 against 4.9).
-constexpr uint64_t kTwoRowsThreads = 1 << 20;
-
-template <typename E>
-static const void *step_kernel(int rows) {
-    return rows == 2 ? (const void *)selective_step<E, 2> : (const void *)selective_step<E, 1>;
-}
-
-static rlca_status check_step(int64_t num_seqs, int64_t channels, int64_t places,
-                              const int32_t *slots) {
-    if (!sizes_ok(num_seqs, channels, 1) || places < 0 || places > INT32_MAX ||
-        (slots == nullptr && places < num_seqs))
-        return RLCA_ERR_INVALID_SIZE;
-    return RLCA_OK;
-}
+constexpr int64_t kWideThreads = 1 << 18;
+constexpr uint32_t kWideBlocks = 512;
+constexpr uint32_t kStepGroups = 1u << 15;  // workgroups in y at most
 
 template <typename E, int VEC>
 static const void *conv_step_kernel(int width) {
@@ -207,8 +204,23 @@ static const void *conv_step_kernel(int width) {
 }
 
 template <typename E>
-static const void *conv_step_kernel(int width, bool wide) {
-    return wide ? conv_step_kernel<E, kWideChannels>(width) : conv_step_kernel<E, 1>(width);
+static const void *conv_step_kernel(int width, int vec) {
+    return vec == 1 ? conv_step_kernel<E, 1>(width) : conv_step_kernel<E, kWideChannels>(width);
+}
+
+// Workgroups in y: enough to fill the chip, each then walks several sequences.
+static uint32_t step_groups(int64_t num_seqs, uint32_t across, uint32_t blocks) {
+    const uint32_t most = (blocks + across - 1) / across;
+    const uint32_t all = (uint32_t)(num_seqs < kStepGroups ? num_seqs : kStepGroups);
+    return all < most ? all : most;
+}
+
+static rlca_status check_step(int64_t num_seqs, int64_t channels, int64_t places,
+                              const int32_t *slots) {
+    if (!sizes_ok(num_seqs, channels, 1) || places < 0 || places > INT32_MAX ||
+        (slots == nullptr && places < num_seqs))
+        return RLCA_ERR_INVALID_SIZE;
+    return RLCA_OK;
 }
 
 }  // namespace seq
@@ -246,18 +258,18 @@ rlca_status rlca_causal_conv_step(const rlca_conv_step_call *call, hipStream_t s
     p.out = c.out;
     p.x_n = c.x_stride_seq;
     p.places = c.places;
-    const bool wide = N * ((D + kWideChannels - 1) / kWideChannels) >= kWideThreads;
-    const int64_t vec = wide ? kWideChannels : 1;
     p.num_seqs = (uint32_t)N;
     p.channels = (uint32_t)D;
-    p.blocks = (uint32_t)((D + vec - 1) / vec);
     p.silu = c.silu;
-    p.by_blocks = fast_div(p.blocks);
-    const void *kernel = c.dtype == RLCA_F32    ? conv_step_kernel<float>(c.width, wide)
-                         : c.dtype == RLCA_BF16 ? conv_step_kernel<__bf16>(c.width, wide)
-                                                : conv_step_kernel<_Float16>(c.width, wide);
-    return launch(kernel, dim3((p.num_seqs * p.blocks + kStepThreads - 1) / kStepThreads),
-                  kStepThreads, 0, p, stream);
+    const int vec = N * ((D + kWideChannels - 1) / kWideChannels) >= kWideThreads ? kWideChannels : 1;
+    const uint32_t threads = (uint32_t)((D + vec - 1) / vec);
+    const uint32_t size = threads >= (uint32_t)kStepThreads ? kStepThreads : (threads + 63) / 64 * 64;
+    const uint32_t across = (threads + size - 1) / size;
+    const void *kernel = c.dtype == RLCA_F32    ? conv_step_kernel<float>(c.width, vec)
+                         : c.dtype == RLCA_BF16 ? conv_step_kernel<__bf16>(c.width, vec)
+                                                : conv_step_kernel<_Float16>(c.width, vec);
+    return launch(kernel, dim3(across, step_groups(N, across, vec == 1 ? kStepBlocks : kWideBlocks)),
+                  size, 0, p, stream);
 }
 
 rlca_status rlca_selective_step(const rlca_scan_step_call *call, hipStream_t stream) {
@@ -306,22 +318,18 @@ rlca_status rlca_selective_step(const rlca_scan_step_call *call, hipStream_t str
     p.C_n = c.C_stride_seq;
     p.C_g = c.C_stride_group;
     p.places = c.places;
-    p.rows = (uint32_t)(N * D);
+    p.num_seqs = (uint32_t)N;
     p.channels = (uint32_t)D;
     p.states = (uint32_t)S;
     p.softplus = c.softplus;
-    p.by_channels = fast_div(p.channels);
     p.by_group = fast_div((uint32_t)(D / G));
     while ((4 << p.lane_bits) < S) ++p.lane_bits;  // at most 32 lanes (128 states)
-    const uint32_t rows_per_block = kStepThreads >> p.lane_bits;
-    const int rows_per_lane = (uint64_t)p.rows << p.lane_bits >= kTwoRowsThreads ? 2 : 1;
-    const void *kernel = c.dtype == RLCA_F32    ? step_kernel<float>(rows_per_lane)
-                         : c.dtype == RLCA_BF16 ? step_kernel<__bf16>(rows_per_lane)
-                                                : step_kernel<_Float16>(rows_per_lane);
-    const uint64_t blocks =
-        ((uint64_t)p.rows + rows_per_block * rows_per_lane - 1) / (rows_per_block * rows_per_lane);
-    return launch(kernel, dim3((uint32_t)(blocks < (1u << 22) ? blocks : 1u << 22)), kStepThreads,
-                  0, p, stream);
+    const uint64_t threads = (uint64_t)D << p.lane_bits;
+    const uint32_t across = (uint32_t)((threads + kStepThreads - 1) / kStepThreads);
+    const void *kernel = c.dtype == RLCA_F32    ? (const void *)selective_step<float>
+                         : c.dtype == RLCA_BF16 ? (const void *)selective_step<__bf16>
+                                                : (const void *)selective_step<_Float16>;
+    return launch(kernel, dim3(across, step_groups(N, across, kStepBlocks)), kStepThreads, 0, p, stream);
 }
 
 }  // extern "C"

@@ -126,8 +126,9 @@ def test_conv_strided_views(gpu_device):
 @pytest.mark.parametrize("dtype", DTYPES, ids=NAMES)
 @pytest.mark.parametrize("W", [2, 3, 4])
 def test_conv_step(dtype, W, gpu_device):
+    # the last: eight channels a thread, workgroups that walk several sequences
     for N, D, slots in ((1, 1, False), (3, 7, False), (5, 64, True), (2, 300, True),
-                        (1, 2048, False), (300, 9, True)):
+                        (1, 2048, False), (300, 9, True), (520, 4099, True)):
         g = gen(10 + D)
         print(f"conv step {dtype} W={W} {N}x{D} slots={slots}", flush=True)
         places = N + 3
@@ -204,6 +205,24 @@ def test_scan(dtype, shape, which, gpu_device):
         assert len(given) == (9 if full else 5)
 
 
+@pytest.mark.parametrize("which", ["", "flags"], ids=lambda w: w or "plain")
+@pytest.mark.parametrize("dtype", DTYPES, ids=NAMES)
+def test_scan_many_channels(dtype, which, gpu_device):
+    """Enough channels that one wave takes four of them alone."""
+    N, ch, S, T, G = 4, 3100, 5, 140, 1
+    g = gen(31)
+    t = scan_inputs(g, N, ch, S, T, G, dtype, True)
+    go = normal(g, N, ch, T, dtype=dtype)
+    flags, _ = episodes(g, N, T, which)
+    want = ref.scan(**t, flags=flags, grad_y=go)
+    y, final, grads = run_scan(t, None, flags, None, 0, True, go)
+    check(y, want["y"], "y")
+    check(final, want["final"], "final state")
+    for name in grads._fields:
+        if getattr(grads, name) is not None:
+            check(getattr(grads, name), want[name], f"grad {name}")
+
+
 @pytest.mark.parametrize("dtype", DTYPES, ids=NAMES)
 def test_scan_extreme_steps(dtype, gpu_device):
     """Step sizes from e^-15 to 15 and decays from 1 (A = 0) to e^-300 a step."""
@@ -270,7 +289,7 @@ def test_scan_strided_views(gpu_device):
 def test_scan_step(dtype, gpu_device):
     for N, ch, S, G, slots in ((1, 1, 1, 1, False), (3, 6, 4, 2, False), (5, 33, 16, 1, True),
                                (2, 10, 7, 5, True), (1, 2048, 16, 1, False), (40, 8, 128, 2, True),
-                               (3, 5, 65, 1, True)):
+                               (3, 5, 65, 1, True), (70, 4100, 16, 2, True)):
         g = gen(20 + S)
         print(f"scan step {dtype} {N}x{ch}x{S} G={G} slots={slots}", flush=True)
         places = N + 2

@@ -120,33 +120,44 @@ __device__ __forceinline__ float softplus(float x) {
     return (x > 0.f ? x : 0.f) + (y == y ? l : y);  // a NaN stays one
 }
 
-// Bit k of the result: an episode starts at step t0 + k (k < K <= 8), from a
-// row of T flags.  AFTER_DONE: a flag at t - 1 makes t a start.  Eight flags are
-// one load, moved inside the row where they would begin before it or end past
-// it, and the bits moved back.
-template <int K>
-__device__ __forceinline__ uint32_t start_bits(const uint8_t *flags, int t0, int T, int after_done) {
-    const int first = t0 - after_done;
-    uint32_t bits = 0;
-    if (T >= 8) {
-        const int at = first < 0 ? 0 : first > T - 8 ? T - 8 : first;
-        uint64_t w;
-        __builtin_memcpy(&w, flags + at, 8);
-        // nonzero bytes -> their top bit -> one bit each, in order
-        w |= (w & 0x7f7f7f7f7f7f7f7full) + 0x7f7f7f7f7f7f7f7full;
-        w = (w >> 7) & 0x0101010101010101ull;
-        const uint64_t found = (w * 0x0102040810204080ull) >> 56;
-        const int d = at - first;  // -7 .. 7 where any of the flags lies in the row
-        bits = d >= 8 || d <= -8 ? 0u : d >= 0 ? (uint32_t)(found << d) : (uint32_t)(found >> -d);
-        bits &= (1u << K) - 1;
-    } else {
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const int t = first + k;
-            if (t >= 0 && t < T && flags[t] != 0) bits |= 1u << k;
+// Eight flags of a row of T from step `first` on, which may begin before the
+// row or end past it (those count as 0).  One load, moved inside the row where
+// necessary and its bits moved back; bits() is apart from load() so that the
+// load can be issued long before its use.
+struct FlagWindow {
+    uint64_t w;
+    int d;
+    __device__ __forceinline__ void load(const uint8_t *flags, int first, int T) {
+        if (T >= 8) {
+            const int at = first < 0 ? 0 : first > T - 8 ? T - 8 : first;
+            d = at - first;
+            __builtin_memcpy(&w, flags + at, 8);
+        } else {
+            w = 0;
+            d = 0;
+            for (int k = 0; k < 8; ++k)
+                if (first + k >= 0 && first + k < T) w |= (uint64_t)flags[first + k] << (8 * k);
         }
     }
-    return bits;
+    // Bit k: the flag at first + k is set (k < K).
+    template <int K>
+    __device__ __forceinline__ uint32_t bits() const {
+        // nonzero bytes -> their top bit -> one bit each, in order
+        uint64_t x = w | ((w & 0x7f7f7f7f7f7f7f7full) + 0x7f7f7f7f7f7f7f7full);
+        x = (x >> 7) & 0x0101010101010101ull;
+        const uint32_t found = (uint32_t)((x * 0x0102040810204080ull) >> 56);
+        const uint32_t at = d >= 8 || d <= -8 ? 0u : d >= 0 ? found << d : found >> -d;
+        return at & ((1u << K) - 1);
+    }
+};
+
+// Bit k of the result: an episode starts at step t0 + k (k < K <= 8), from a
+// row of T flags.  AFTER_DONE: a flag at t - 1 makes t a start.
+template <int K>
+__device__ __forceinline__ uint32_t start_bits(const uint8_t *flags, int t0, int T, int after_done) {
+    FlagWindow f;
+    f.load(flags, t0 - after_done, T);
+    return f.bits<K>();
 }
 
 __device__ __forceinline__ bool is_start(const uint8_t *flags, int t, int T, int after_done) {

@@ -7,6 +7,11 @@
 // inputs before them (and, backward, the steps after them, whose pre is formed
 // again here) are loads of lines that the neighbouring lanes read as well, so
 // lanes need nothing from each other and HBM delivers each line once.
+//
+// Next to the memory's time stand a step's 30 to 60 instructions.  So a
+// workgroup keeps its channels and walks tiles of several rows: weights and
+// addresses are formed once, one item is loaded while the one before is
+// computed, and the weights' gradients leave the registers once at the end.
 #include "seq.hpp"
 
 namespace rlca {
@@ -16,8 +21,6 @@ constexpr int kConvThreads = 256;
 constexpr int kConvK = 8;
 constexpr int kBack = 4;   // steps loaded before the block: W - 1 <= 3 are used
 constexpr int kAhead = 4;  // backward: steps loaded after it
-// at most so many workgroups in each grid dimension; they walk further ones
-constexpr uint32_t kConvMaxRowBlocks = 1u << 22, kConvMaxTiles = 1u << 15;
 
 struct ConvParams {
     const void *x, *grad_out;
@@ -27,36 +30,76 @@ struct ConvParams {
     const int32_t *lengths;
     void *out, *final_state;
     void *grad_x, *grad_state;
-    float *partials;  // [channels][num_seqs * tiles][W + 1]
+    float *partials;  // [channels][gridDim.y][W + 1]
     int64_t x_n, x_d, g_n, g_d;
-    uint32_t rows, channels;
-    int32_t T;
+    uint32_t num_seqs, channels, tiles;
     uint32_t lane_bits;  // log2 of the lanes of a row
-    uint32_t row_blocks, tiles;
+    int32_t T;
     int32_t silu, after_done;
-    FastDiv by_channels;
 };
 
-// Where a lane's block lies, and what its row's end and episode starts say of
-// it.
-struct ConvLane {
-    uint32_t row, n, d;
+// The tiles of all rows in order, every gridDim.y-th from blockIdx.y on.
+struct ConvItem {
+    uint32_t n, tile, step_n, step_tile;
+    __device__ __forceinline__ explicit ConvItem(const ConvParams &p)
+        : n(blockIdx.y / p.tiles), tile(blockIdx.y % p.tiles), step_n(gridDim.y / p.tiles),
+          step_tile(gridDim.y % p.tiles) {}
+    __device__ __forceinline__ void advance(const ConvParams &p) {
+        n += step_n;
+        tile += step_tile;
+        if (tile >= p.tiles) tile -= p.tiles, ++n;
+    }
+};
+
+// What a lane loads for a block of steps: the block, the steps before it (the
+// state's at the row's start) and, backward, the steps after it and the
+// output's gradient; and the flags that say where episodes start.
+template <typename E, int W, bool FLAGS, bool BACKWARD>
+struct ConvLoads {
     int t0, end;
-};
+    uint32_t n;
+    Steps<kConvK, E> x, g;
+    Steps<kBack, E> back;
+    Steps<kAhead, E> after, g_after;
+    FlagWindow flags, more_flags;
 
-__device__ __forceinline__ ConvLane conv_lane(const ConvParams &p, uint32_t row_block,
-                                              uint32_t tile) {
-    const uint32_t rows_per_block = kConvThreads >> p.lane_bits;
-    ConvLane l;
-    l.row = row_block * rows_per_block + (threadIdx.x >> p.lane_bits);
-    const uint32_t block = (tile << p.lane_bits) + (threadIdx.x & ((1u << p.lane_bits) - 1));
-    l.n = p.by_channels.div(l.row);
-    l.d = l.row - l.n * p.channels;
-    l.t0 = (int)(block * kConvK);
-    l.end = 0;
-    if (l.row < p.rows) l.end = row_end(p.lengths, l.n, p.T);
-    return l;
-}
+    __device__ __forceinline__ void load(const ConvParams &p, const ConvItem &item, uint32_t d,
+                                         uint32_t lane) {
+        n = item.n;
+        end = row_end(p.lengths, n, p.T);
+        t0 = (int)(((item.tile << p.lane_bits) + lane) * kConvK);
+        if (t0 >= end) return;
+        const E *row = static_cast<const E *>(p.x) + n * p.x_n + d * p.x_d + t0;
+        x.load(row, end - t0);
+        if (t0 > 0) {
+            back.load(row - kBack, kBack);
+        } else {
+            back.load(row, 0);
+            if (p.state != nullptr) {
+                const E *s = static_cast<const E *>(p.state) +
+                             ((int64_t)n * p.channels + d) * (W - 1);
+#pragma unroll
+                for (int i = 0; i < W - 1; ++i) back.b[kBack - (W - 1) + i] = s[i];
+            }
+        }
+        if constexpr (BACKWARD) {
+            const E *grad = static_cast<const E *>(p.grad_out) + n * p.g_n + d * p.g_d + t0;
+            g.load(grad, end - t0);
+            after.load(row + kConvK, end - t0 - kConvK);
+            g_after.load(grad + kConvK, end - t0 - kConvK);
+        }
+        if constexpr (FLAGS) {
+            const uint8_t *f = p.flags + (int64_t)n * p.T;
+            flags.load(f, t0 - 2 - p.after_done, p.T);
+            more_flags.load(f, t0 + 6 - p.after_done, p.T);
+        }
+    }
+    // bit i: an episode starts at step t0 - 2 + i
+    __device__ __forceinline__ uint32_t starts() const {
+        if constexpr (!FLAGS) return 0u;
+        return flags.template bits<8>() | more_flags.template bits<5>() << 8;
+    }
+};
 
 // Which taps stay within their step's episode.  `starts` bit i: an episode
 // starts at step t0 - 2 + i.  Tap j of step k reads across a start if one lies
@@ -89,9 +132,8 @@ __device__ __forceinline__ float tap(const float (&x)[N], const Episodes<W> &e, 
 
 // The state's input at time -1-q (q = 0 the newest), 0 without a state.
 template <int W, typename E>
-__device__ __forceinline__ float state_at(const void *state, uint32_t row, int q) {
-    return state == nullptr ? 0.f
-                            : (float)static_cast<const E *>(state)[(int64_t)row * (W - 1) + W - 2 - q];
+__device__ __forceinline__ float state_at(const void *state, int64_t row, int q) {
+    return state == nullptr ? 0.f : (float)static_cast<const E *>(state)[row * (W - 1) + W - 2 - q];
 }
 
 // Whether the input at time p is still seen by the step after the row's last:
@@ -106,195 +148,191 @@ __device__ __forceinline__ bool reaches_end(const uint8_t *flags, int p, int end
 
 template <typename E, int W, bool FLAGS>
 __global__ __launch_bounds__(kConvThreads) void causal_conv(ConvParams p) {
-    for (uint32_t rb = blockIdx.x; rb < p.row_blocks; rb += gridDim.x)
-        for (uint32_t tile = blockIdx.y; tile < p.tiles; tile += gridDim.y) {
-            const ConvLane l = conv_lane(p, rb, tile);
-            if (l.row >= p.rows) continue;
-            const E *x = static_cast<const E *>(p.x) + l.n * p.x_n + l.d * p.x_d;
-            const uint8_t *flags = FLAGS ? p.flags + (int64_t)l.n * p.T : nullptr;
-            if (l.t0 < p.T) {
-                float v[kBack + kConvK], o[kConvK] = {};
-                const int n = l.end - l.t0;
-                if (n > 0) {
-                    float back[kBack], cur[kConvK];
-                    load_steps<kConvK>(x + l.t0, n, cur);
-                    load_steps_before<kBack>(x + l.t0, l.t0, back);
-                    if (l.t0 == 0)
+    constexpr int K = kConvK;
+    const uint32_t lane = threadIdx.x & ((1u << p.lane_bits) - 1);
+    const uint32_t d = (blockIdx.x * blockDim.x + threadIdx.x) >> p.lane_bits;
+    if (d >= p.channels) return;
+    ConvItem item(p);
+    ConvLoads<E, W, FLAGS, false> next;
+    next.load(p, item, d, lane);  // gridDim.y is at most the number of items
+    float w[W];
 #pragma unroll
-                        for (int q = 0; q < W - 1; ++q)
-                            back[kBack - 1 - q] = state_at<W, E>(p.state, l.row, q);
-                    uint32_t starts = 0;
-                    if constexpr (FLAGS)
-                        starts = start_bits<8>(flags, l.t0 - 2, p.T, p.after_done) |
-                                 start_bits<2>(flags, l.t0 + 6, p.T, p.after_done) << 8;
-                    const Episodes<W> episodes(starts);
+    for (int j = 0; j < W; ++j) w[j] = p.weight[(int64_t)d * W + j];
+    const float bias = p.bias == nullptr ? 0.f : p.bias[d];
+    bool more = true;
+    while (more) {
+        const ConvLoads<E, W, FLAGS, false> now = next;
+        item.advance(p);
+        more = item.n < p.num_seqs;
+        if (more) next.load(p, item, d, lane);
+        const int64_t row = (int64_t)now.n * p.channels + d;
+        const int n = now.end - now.t0;
+        float o[K] = {};
+        if (n > 0) {
+            float v[kBack + K], back[kBack], cur[K];
+            now.back.widen(back);
+            now.x.widen(cur);
 #pragma unroll
-                    for (int k = 0; k < kBack; ++k) v[k] = back[k];
+            for (int k = 0; k < kBack; ++k) v[k] = back[k];
 #pragma unroll
-                    for (int k = 0; k < kConvK; ++k) v[kBack + k] = cur[k];
-                    float w[W];
+            for (int k = 0; k < K; ++k) v[kBack + k] = cur[k];
+            const Episodes<W> episodes(now.starts());
 #pragma unroll
-                    for (int j = 0; j < W; ++j) w[j] = p.weight[(int64_t)l.d * W + j];
-                    const float bias = p.bias == nullptr ? 0.f : p.bias[l.d];
+            for (int k = 0; k < K; ++k) {
+                float pre = bias;
 #pragma unroll
-                    for (int k = 0; k < kConvK; ++k) {
-                        float pre = bias;
-#pragma unroll
-                        for (int j = 0; j < W; ++j)
-                            pre = fmaf(w[W - 1 - j], tap<W, FLAGS>(v, episodes, k, j), pre);
-                        pre = p.silu != 0 ? silu(pre) : pre;
-                        o[k] = k < n ? pre : 0.f;
-                    }
-                }
-                store_steps<kConvK>(static_cast<E *>(p.out) + (int64_t)l.row * p.T + l.t0,
-                                    p.T - l.t0, o);
+                for (int j = 0; j < W; ++j)
+                    pre = fmaf(w[W - 1 - j], tap<W, FLAGS>(v, episodes, k, j), pre);
+                o[k] = p.silu != 0 ? silu(pre) : pre;
             }
-            if (p.final_state != nullptr && l.t0 == 0) {
-                E *f = static_cast<E *>(p.final_state) + (int64_t)l.row * (W - 1);
-                for (int i = 0; i < W - 1; ++i) {
-                    const int at = l.end - (W - 1) + i;
-                    float y = at >= 0 ? (float)x[at] : state_at<W, E>(p.state, l.row, -1 - at);
-                    if (FLAGS && !reaches_end(flags, at, l.end, p.T, p.after_done)) y = 0.f;
-                    f[i] = (E)y;
-                }
+            if (n < K)
+#pragma unroll
+                for (int k = 0; k < K; ++k) o[k] = k < n ? o[k] : 0.f;
+        }
+        if (now.t0 < p.T)
+            store_steps<K>(static_cast<E *>(p.out) + row * p.T + now.t0, p.T - now.t0, o);
+        if (p.final_state != nullptr && now.t0 == 0) {
+            const E *x = static_cast<const E *>(p.x) + now.n * p.x_n + d * p.x_d;
+            const uint8_t *flags = FLAGS ? p.flags + (int64_t)now.n * p.T : nullptr;
+            E *f = static_cast<E *>(p.final_state) + row * (W - 1);
+            for (int i = 0; i < W - 1; ++i) {
+                const int at = now.end - (W - 1) + i;
+                float y = at >= 0 ? (float)x[at] : state_at<W, E>(p.state, row, -1 - at);
+                if (FLAGS && !reaches_end(flags, at, now.end, p.T, p.after_done)) y = 0.f;
+                f[i] = (E)y;
             }
         }
+    }
 }
 
 // Backward:  dpre_t = grad_out_t silu'(pre_t),
 //   grad_x_t = sum_j weight[W-1-j] dpre_{t+j}   (taps within t's episode),
 //   grad_weight[k] = sum dpre_t x_{t-(W-1)+k},  grad_bias = sum dpre_t.
-// A lane forms pre for its 8 steps and the W-1 after them.  Its sums for the
-// weights meet the other lanes' of its row (at most one wave) and are written
-// as one partial per row and tile; conv_weight_sums adds those in order.
+// A lane forms pre for its K steps and the W-1 after them.  Its sums for the
+// weights meet the other lanes' of its row (at most one wave) at the end and
+// are written as one partial per workgroup; conv_weight_sums adds those in
+// order.
 template <typename E, int W, bool FLAGS>
 __global__ __launch_bounds__(kConvThreads) void causal_conv_backward(ConvParams p) {
-    constexpr int kSteps = kConvK + W - 1;  // pre of these
-    for (uint32_t rb = blockIdx.x; rb < p.row_blocks; rb += gridDim.x)
-        for (uint32_t tile = blockIdx.y; tile < p.tiles; tile += gridDim.y) {
-            const ConvLane l = conv_lane(p, rb, tile);
-            float dw[W] = {}, db = 0.f;
-            if (l.row < p.rows && l.t0 < p.T) {
-                const E *x = static_cast<const E *>(p.x) + l.n * p.x_n + l.d * p.x_d;
-                const E *g = static_cast<const E *>(p.grad_out) + l.n * p.g_n + l.d * p.g_d;
-                const uint8_t *flags = FLAGS ? p.flags + (int64_t)l.n * p.T : nullptr;
-                const int n = l.end - l.t0;
-                float dx[kConvK] = {};
-                if (n > 0) {
-                    float w[W];
+    constexpr int K = kConvK, kSteps = K + W - 1;  // pre of these
+    const uint32_t lane = threadIdx.x & ((1u << p.lane_bits) - 1);
+    const uint32_t d = (blockIdx.x * blockDim.x + threadIdx.x) >> p.lane_bits;
+    if (d >= p.channels) return;  // a row's lanes leave together
+    ConvItem item(p);
+    ConvLoads<E, W, FLAGS, true> next;
+    next.load(p, item, d, lane);  // gridDim.y is at most the number of items
+    float w[W], dw[W] = {}, db = 0.f;
 #pragma unroll
-                    for (int j = 0; j < W; ++j) w[j] = p.weight[(int64_t)l.d * W + j];
-                    const float bias = p.bias == nullptr ? 0.f : p.bias[l.d];
-                    float v[kBack + kConvK + kAhead], go[kConvK + kAhead];
-                    {
-                        float back[kBack], cur[kConvK], ahead[kAhead];
-                        float gcur[kConvK], gahead[kAhead];
-                        load_steps<kConvK>(x + l.t0, n, cur);
-                        load_steps<kConvK>(g + l.t0, n, gcur);
-                        load_steps_before<kBack>(x + l.t0, l.t0, back);
-                        load_steps<kAhead>(x + l.t0 + kConvK, n - kConvK, ahead);
-                        load_steps<kAhead>(g + l.t0 + kConvK, n - kConvK, gahead);
-                        if (l.t0 == 0)
+    for (int j = 0; j < W; ++j) w[j] = p.weight[(int64_t)d * W + j];
+    const float bias = p.bias == nullptr ? 0.f : p.bias[d];
+    bool more = true;
+    while (more) {
+        const ConvLoads<E, W, FLAGS, true> now = next;
+        item.advance(p);
+        more = item.n < p.num_seqs;
+        if (more) next.load(p, item, d, lane);
+        const int64_t row = (int64_t)now.n * p.channels + d;
+        const int t0 = now.t0, end = now.end, n = end - t0;
+        const uint8_t *flags = FLAGS ? p.flags + (int64_t)now.n * p.T : nullptr;
+        float dx[K] = {};
+        if (n > 0) {
+            float v[kBack + K + kAhead], go[K + kAhead];
+            {
+                float back[kBack], cur[K], after[kAhead], g[K], g_after[kAhead];
+                now.back.widen(back);
+                now.x.widen(cur);
+                now.after.widen(after);
+                now.g.widen(g);
+                now.g_after.widen(g_after);
 #pragma unroll
-                            for (int q = 0; q < W - 1; ++q)
-                                back[kBack - 1 - q] = state_at<W, E>(p.state, l.row, q);
+                for (int k = 0; k < kBack; ++k) v[k] = back[k];
 #pragma unroll
-                        for (int k = 0; k < kBack; ++k) v[k] = back[k];
+                for (int k = 0; k < K; ++k) v[kBack + k] = cur[k], go[k] = g[k];
 #pragma unroll
-                        for (int k = 0; k < kConvK; ++k) v[kBack + k] = cur[k], go[k] = gcur[k];
-#pragma unroll
-                        for (int k = 0; k < kAhead; ++k)
-                            v[kBack + kConvK + k] = ahead[k], go[kConvK + k] = gahead[k];
-                    }
-                    uint32_t starts = 0;  // bit i: step t0 - 2 + i
-                    if constexpr (FLAGS)
-                        starts = start_bits<8>(flags, l.t0 - 2, p.T, p.after_done) |
-                                 start_bits<5>(flags, l.t0 + 6, p.T, p.after_done) << 8;
-                    const Episodes<W> episodes(starts);
-                    float dpre[kSteps];
-#pragma unroll
-                    for (int k = 0; k < kSteps; ++k) {
-                        float pre = bias;
-#pragma unroll
-                        for (int j = 0; j < W; ++j)
-                            pre = fmaf(w[W - 1 - j], tap<W, FLAGS>(v, episodes, k, j), pre);
-                        const float slope = p.silu != 0 ? silu_slope(pre, sigmoid(pre)) : 1.f;
-                        dpre[k] = k < n ? go[k] * slope : 0.f;
-                    }
-#pragma unroll
-                    for (int k = 0; k < kConvK; ++k) {
-                        float s = 0.f;
-#pragma unroll
-                        for (int j = 0; j < W; ++j) {
-                            // step k is tap j of step k + j
-                            const float g = FLAGS && j > 0 ? episodes.keep(dpre[k + j], k + j, j)
-                                                           : dpre[k + j];
-                            s = fmaf(w[W - 1 - j], g, s);
-                        }
-                        dx[k] = k < n ? s : 0.f;
-                        db += dpre[k];
-#pragma unroll
-                        for (int j = 0; j < W; ++j)
-                            dw[W - 1 - j] = fmaf(dpre[k], tap<W, FLAGS>(v, episodes, k, j),
-                                                 dw[W - 1 - j]);
-                    }
-                    if (p.grad_state != nullptr && l.t0 == 0) {
-                        E *gs = static_cast<E *>(p.grad_state) + (int64_t)l.row * (W - 1);
-#pragma unroll
-                        for (int q = 0; q < W - 1; ++q) {  // the input at time q - (W-1)
-                            float s = 0.f;
-#pragma unroll
-                            for (int t = 0; t <= q; ++t) {  // tap t + (W-1) - q of step t
-                                const bool cut = FLAGS && (starts & (((1u << (t + 1)) - 1) << 2)) != 0;
-                                s = fmaf(w[q - t], cut ? 0.f : dpre[t], s);
-                            }
-                            const int i = q - l.end;  // its place in the final state
-                            if (p.grad_final != nullptr && i >= 0 &&
-                                !(FLAGS && !reaches_end(flags, q - (W - 1), l.end, p.T,
-                                                        p.after_done)))
-                                s += (float)static_cast<const E *>(
-                                    p.grad_final)[(int64_t)l.row * (W - 1) + i];
-                            gs[q] = (E)s;
-                        }
-                    }
-                    if (p.grad_final != nullptr && n - kConvK < W - 1) {
-                        const E *gf =
-                            static_cast<const E *>(p.grad_final) + (int64_t)l.row * (W - 1);
-#pragma unroll
-                        for (int k = 0; k < kConvK; ++k) {
-                            const int i = l.t0 + k - (l.end - (W - 1));
-                            if (i < 0 || i >= W - 1) continue;
-                            if (FLAGS &&
-                                !reaches_end(flags, l.t0 + k, l.end, p.T, p.after_done))
-                                continue;
-                            dx[k] += (float)gf[i];
-                        }
-                    }
-                }
-                store_steps<kConvK>(static_cast<E *>(p.grad_x) + (int64_t)l.row * p.T + l.t0,
-                                    p.T - l.t0, dx);
+                for (int k = 0; k < kAhead; ++k) v[kBack + K + k] = after[k], go[K + k] = g_after[k];
             }
-            if (l.row < p.rows && l.t0 == 0 && l.end == 0 && p.grad_state != nullptr)
-                for (int q = 0; q < W - 1; ++q) {  // an empty row hands its state on
-                    const int64_t at = (int64_t)l.row * (W - 1) + q;
-                    static_cast<E *>(p.grad_state)[at] =
-                        p.grad_final == nullptr ? (E)0.f : static_cast<const E *>(p.grad_final)[at];
-                }
-            // the row's lanes, in a fixed tree
-            for (uint32_t m = 1; m < (1u << p.lane_bits); m <<= 1) {
+            const uint32_t starts = now.starts();
+            const Episodes<W> episodes(starts);
+            float dpre[kSteps];
 #pragma unroll
-                for (int j = 0; j < W; ++j) dw[j] += __shfl_xor(dw[j], (int)m);
-                db += __shfl_xor(db, (int)m);
+            for (int k = 0; k < kSteps; ++k) {
+                float pre = bias;
+#pragma unroll
+                for (int j = 0; j < W; ++j)
+                    pre = fmaf(w[W - 1 - j], tap<W, FLAGS>(v, episodes, k, j), pre);
+                dpre[k] = p.silu != 0 ? go[k] * silu_slope(pre, sigmoid(pre)) : go[k];
             }
-            if (l.row < p.rows && (threadIdx.x & ((1u << p.lane_bits) - 1)) == 0) {
-                const uint64_t per_channel = (uint64_t)(p.rows / p.channels) * p.tiles;
-                float *o = p.partials +
-                           (l.d * per_channel + (uint64_t)l.n * p.tiles + tile) * (W + 1);
+            if (n < kSteps)  // past the end go is 0, but a slope may be anything
 #pragma unroll
-                for (int j = 0; j < W; ++j) o[j] = dw[j];
-                o[W] = db;
+                for (int k = 0; k < kSteps; ++k) dpre[k] = k < n ? dpre[k] : 0.f;
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                float s = 0.f;
+#pragma unroll
+                for (int j = 0; j < W; ++j) {
+                    // step k is tap j of step k + j
+                    const float g =
+                        FLAGS && j > 0 ? episodes.keep(dpre[k + j], k + j, j) : dpre[k + j];
+                    s = fmaf(w[W - 1 - j], g, s);
+                }
+                dx[k] = s;
+                db += dpre[k];
+#pragma unroll
+                for (int j = 0; j < W; ++j)
+                    dw[W - 1 - j] = fmaf(dpre[k], tap<W, FLAGS>(v, episodes, k, j), dw[W - 1 - j]);
+            }
+            if (n < K)
+#pragma unroll
+                for (int k = 0; k < K; ++k) dx[k] = k < n ? dx[k] : 0.f;
+            if (p.grad_state != nullptr && t0 == 0) {
+                E *gs = static_cast<E *>(p.grad_state) + row * (W - 1);
+#pragma unroll
+                for (int q = 0; q < W - 1; ++q) {  // the input at time q - (W-1)
+                    float s = 0.f;
+#pragma unroll
+                    for (int t = 0; t <= q; ++t) {  // tap t + (W-1) - q of step t
+                        const bool cut = FLAGS && (starts & (((1u << (t + 1)) - 1) << 2)) != 0;
+                        s = fmaf(w[q - t], cut ? 0.f : dpre[t], s);
+                    }
+                    const int i = q - end;  // its place in the final state
+                    if (p.grad_final != nullptr && i >= 0 &&
+                        !(FLAGS && !reaches_end(flags, q - (W - 1), end, p.T, p.after_done)))
+                        s += (float)static_cast<const E *>(p.grad_final)[row * (W - 1) + i];
+                    gs[q] = (E)s;
+                }
+            }
+            if (p.grad_final != nullptr && n - K < W - 1) {
+                const E *gf = static_cast<const E *>(p.grad_final) + row * (W - 1);
+#pragma unroll
+                for (int k = 0; k < K; ++k) {
+                    const int i = t0 + k - (end - (W - 1));
+                    if (i < 0 || i >= W - 1) continue;
+                    if (FLAGS && !reaches_end(flags, t0 + k, end, p.T, p.after_done)) continue;
+                    dx[k] += (float)gf[i];
+                }
+            }
+        } else if (t0 == 0 && p.grad_state != nullptr) {  // an empty row hands its state on
+            for (int q = 0; q < W - 1; ++q) {
+                const int64_t at = row * (W - 1) + q;
+                static_cast<E *>(p.grad_state)[at] =
+                    p.grad_final == nullptr ? (E)0.f : static_cast<const E *>(p.grad_final)[at];
             }
         }
+        if (t0 < p.T)
+            store_steps<K>(static_cast<E *>(p.grad_x) + row * p.T + t0, p.T - t0, dx);
+    }
+    // the row's lanes, in a fixed tree
+    for (uint32_t m = 1; m < (1u << p.lane_bits); m <<= 1) {
+#pragma unroll
+        for (int j = 0; j < W; ++j) dw[j] += __shfl_xor(dw[j], (int)m);
+        db += __shfl_xor(db, (int)m);
+    }
+    if (lane == 0) {
+        float *o = p.partials + ((int64_t)d * gridDim.y + blockIdx.y) * (W + 1);
+#pragma unroll
+        for (int j = 0; j < W; ++j) o[j] = dw[j];
+        o[W] = db;
+    }
 }
 
 // A workgroup per channel adds its partials in fp64, its waves' sums in order.
@@ -349,12 +387,34 @@ static uint32_t lane_bits_for(int64_t T, uint32_t most) {
     return bits;
 }
 
-static uint32_t tiles_of(int64_t T, uint32_t bits) {
-    const int64_t blocks = T <= 0 ? 1 : (T + kConvK - 1) / kConvK;
-    return (uint32_t)((blocks + (1ll << bits) - 1) >> bits);
+struct ConvShape {
+    uint32_t lane_bits, tiles, threads;
+    dim3 grid;
+    // a launch's threads in x (2^24 channels of long rows do not fit one)
+    bool fits() const { return (uint64_t)grid.x * threads < (1ull << 32); }
+};
+
+// A workgroup of at most 256 threads takes whole channels; about `blocks` of them
+// walk the rows' tiles, with one number of turns for all.
+static ConvShape conv_shape(const rlca_conv_call &c, uint32_t most_bits, uint32_t blocks) {
+    ConvShape s = {};
+    s.lane_bits = lane_bits_for(c.T, most_bits);
+    const int64_t row_blocks = c.T <= 0 ? 1 : (c.T + kConvK - 1) / kConvK;
+    s.tiles = (uint32_t)((row_blocks + (1ll << s.lane_bits) - 1) >> s.lane_bits);
+    const uint64_t lanes = (uint64_t)c.channels << s.lane_bits;
+    s.threads = lanes >= (uint64_t)kConvThreads ? kConvThreads
+                : lanes == 0                    ? 64
+                                                : (uint32_t)(lanes + 63) / 64 * 64;
+    const uint64_t across = (lanes + s.threads - 1) / s.threads;
+    const uint64_t items = (uint64_t)c.num_seqs * s.tiles;
+    uint64_t most = across == 0 ? 1 : (blocks + across - 1) / across;  // 0: no channels
+    if (most > 65535) most = 65535;
+    const uint64_t turns = (items + most - 1) / most;
+    s.grid = dim3((uint32_t)across, turns == 0 ? 0u : (uint32_t)((items + turns - 1) / turns));
+    return s;
 }
 
-static ConvParams conv_params(const rlca_conv_call &c, uint32_t most_bits) {
+static ConvParams conv_params(const rlca_conv_call &c, const ConvShape &s) {
     ConvParams p = {};
     p.x = c.x;
     p.grad_out = c.grad_out;
@@ -372,22 +432,14 @@ static ConvParams conv_params(const rlca_conv_call &c, uint32_t most_bits) {
     p.x_d = c.x_stride_channel;
     p.g_n = c.grad_stride_seq;
     p.g_d = c.grad_stride_channel;
-    p.rows = (uint32_t)(c.num_seqs * c.channels);
+    p.num_seqs = (uint32_t)c.num_seqs;
     p.channels = (uint32_t)c.channels;
+    p.tiles = s.tiles;
     p.T = (int32_t)c.T;
-    p.lane_bits = lane_bits_for(c.T, most_bits);
-    const uint32_t rows_per_block = kConvThreads >> p.lane_bits;
-    p.row_blocks = (uint32_t)(((uint64_t)p.rows + rows_per_block - 1) / rows_per_block);
-    p.tiles = tiles_of(c.T, p.lane_bits);
+    p.lane_bits = s.lane_bits;
     p.silu = c.silu;
     p.after_done = c.convention == RLCA_RESET_AFTER_DONE;
-    p.by_channels = fast_div(p.channels);
     return p;
-}
-
-static dim3 conv_grid(const ConvParams &p) {
-    return dim3(p.row_blocks < kConvMaxRowBlocks ? p.row_blocks : kConvMaxRowBlocks,
-                p.tiles < kConvMaxTiles ? p.tiles : kConvMaxTiles);
 }
 
 static rlca_status check_conv(const rlca_conv_call &c, bool backward, Arrays *a) {
@@ -442,7 +494,12 @@ static const void *conv_kernel(const rlca_conv_call &c, bool backward) {
                                   : conv_kernel<_Float16>(c.width, flags, backward);
 }
 
-constexpr uint32_t kForwardLaneBits = 8, kBackwardLaneBits = 6;
+// Lanes of a row and workgroups of the two launches.  Forward and backward,
+// fp32 with episode starts, 4096x64x128: 198, 193, 180, 177 and 181 us with
+// 1024 / 640, 2048 / 1280, 4096 / 2560, 8192 / 5120 workgroups and one for every
+// tile; bf16, 4x2048x2048: 48, 46, 48, 48 and 46.
+static ConvShape forward_shape(const rlca_conv_call &c) { return conv_shape(c, 8, 8192); }
+static ConvShape backward_shape(const rlca_conv_call &c) { return conv_shape(c, 6, 5120); }
 
 }  // namespace seq
 }  // namespace rlca
@@ -459,13 +516,14 @@ rlca_status rlca_causal_conv(const rlca_conv_call *call, hipStream_t stream) {
     if (st != RLCA_OK) return st;
     if (call->num_seqs * call->channels == 0 || (call->T == 0 && call->final_state == nullptr))
         return RLCA_OK;
-    ConvParams p = conv_params(*call, kForwardLaneBits);
-    return launch(conv_kernel(*call, false), conv_grid(p), kConvThreads, 0, p, stream);
+    const ConvShape shape = forward_shape(*call);
+    if (!shape.fits()) return RLCA_ERR_INVALID_SIZE;
+    ConvParams p = conv_params(*call, shape);
+    return launch(conv_kernel(*call, false), shape.grid, shape.threads, 0, p, stream);
 }
 
 static size_t conv_partials(const rlca_conv_call &c) {
-    return (size_t)c.num_seqs * c.channels *
-           tiles_of(c.T, lane_bits_for(c.T, kBackwardLaneBits)) * (c.width + 1) * 4;
+    return (size_t)c.channels * backward_shape(c).grid.y * (c.width + 1) * 4;
 }
 
 size_t rlca_causal_conv_backward_workspace_size(const rlca_conv_call *call) {
@@ -486,15 +544,16 @@ rlca_status rlca_causal_conv_backward(const rlca_conv_call *call, void *workspac
     if (st != RLCA_OK) return st;
     if (workspace_bytes < need) return RLCA_ERR_INVALID_SIZE;
     if (call->channels == 0) return RLCA_OK;
-    const uint32_t tiles = tiles_of(call->T, lane_bits_for(call->T, kBackwardLaneBits));
+    const ConvShape shape = backward_shape(*call);
+    if (!shape.fits()) return RLCA_ERR_INVALID_SIZE;
     if (call->num_seqs != 0) {
-        ConvParams p = conv_params(*call, kBackwardLaneBits);
+        ConvParams p = conv_params(*call, shape);
         p.partials = static_cast<float *>(workspace);
-        st = launch(conv_kernel(*call, true), conv_grid(p), kConvThreads, 0, p, stream);
+        st = launch(conv_kernel(*call, true), shape.grid, shape.threads, 0, p, stream);
         if (st != RLCA_OK) return st;
     }
     const float *partials = static_cast<const float *>(workspace);
-    uint64_t per_channel = (uint64_t)call->num_seqs * tiles;
+    uint64_t per_channel = call->num_seqs == 0 ? 0 : shape.grid.y;
     uint32_t channels = (uint32_t)call->channels;
     float *gw = call->grad_weight, *gb = call->grad_bias;
     void *args[] = {&partials, &per_channel, &channels, &gw, &gb};

@@ -4,8 +4,8 @@
 //
 // Bound by the vector units: each (step, state) takes one exponential and the
 // products of the fold, of the second pass over the maps and of y, against
-// one or two stored values per step.  A workgroup's 16 channels share the
-// tile's B and C, staged in LDS in fp32 and read there 16 bytes a lane.
+// one or two stored values per step.  A workgroup's channels share the tile's B
+// and C, staged in LDS in fp32 and read there 16 bytes a lane.
 #include "seq_scan.hpp"
 
 namespace rlca {
@@ -14,31 +14,32 @@ namespace seq {
 // B and C are staged in two buffers: the next stage's rows are loaded while one
 // is computed, and one barrier a stage suffices.
 //
-// SPLIT waves share four channels: each takes every SPLIT-th pair of states
-// over all the steps, and prepares and finishes K / SPLIT of a lane's steps.
+// SPLIT waves share the channels of one: each takes every SPLIT-th pair of states
+// over all the steps, and prepares and finishes 8 / SPLIT of a lane's steps.
 // They meet in LDS twice a tile, in dt and dt u before and in y's partial sums
 // after (split_of below says when that pays).
-template <typename E, bool FLAGS, int SPLIT, int K>
-__global__ __launch_bounds__(kScanThreads, sizeof(E) == 2 && !FLAGS ? 4 : 3) void selective_scan(ScanParams p) {
-    constexpr int kQuads = kScanWaves / SPLIT, kRows = 4 * kQuads, kOwn = K / SPLIT;
-    constexpr int kTile = tile_of(K);
+template <typename E, bool FLAGS, int SPLIT, int L>
+__global__ __launch_bounds__(kScanThreads, sizeof(E) == 2 && !FLAGS ? 4 : 3) void selective_scan(
+    ScanParams p) {
+    constexpr int K = kScanK, kSets = kScanWaves / SPLIT, kRows = rows_of(L) / SPLIT;
+    constexpr int kTile = tile_of(L), kStates = states_of(L), kOwn = K / SPLIT;
     extern __shared__ __attribute__((aligned(16))) char lds_bytes[];
-    __shared__ TileRow<K> tiles[2][2][kScanStates];  // [buffer][B, C][state]
-    __shared__ float steps[kQuads][SPLIT > 1 ? (FLAGS ? 3 : 2) * K : 1][kWave];
+    __shared__ TileRow<L> tiles[2][2][kStates];  // [buffer][B, C][state]
+    __shared__ float steps[kSets][SPLIT > 1 ? (FLAGS ? 3 : 2) * K : 1][kWave];
     __shared__ float sums[SPLIT > 1 ? kScanWaves : 1][SPLIT > 1 ? K : 1][kWave];
     __shared__ uint32_t stage_tame[2][kScanWaves];  // [buffer]: whether what a wave staged is
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int in_wave = threadIdx.x % kWave;
-    const int quad = wave / SPLIT, part = wave % SPLIT;
-    const ScanLane l = scan_lane(p, quad * 4 + in_wave / kScanLanes, kRows);
-    const int S = (int)p.states, padded = padded_states(S);
-    // [rows][padded]: the states entering the tile, and A log2(e)
-    float *carry = reinterpret_cast<float *>(lds_bytes) + l.local * padded;
-    float *A2 = carry + kRows * padded;
+    const int set = wave / SPLIT, part = wave % SPLIT;
+    const ScanLane l = scan_lane<L>(p, set * (kWave / L) + in_wave / L, kRows);
+    const int S = (int)p.states, padded = padded_states(S), pitch = pitch_of(S, L);
+    // [rows][pitch]: the states entering the tile, and A log2(e)
+    float *carry = reinterpret_cast<float *>(lds_bytes) + l.local * pitch;
+    float *A2 = carry + kRows * pitch;
     // a wave initialises and hands on the states that it computes
     const auto mine = [&](int s) { return SPLIT == 1 || (s / 2) % SPLIT == part; };
     bool decays = true;
-    for (int s = l.lane; s < padded; s += kScanLanes)
+    for (int s = l.lane; s < padded; s += L)
         if (mine(s)) {
             const float x = s >= S ? 0.f : p.A[(int64_t)l.d * S + s] * kLog2e;
             carry[s] = p.state == nullptr || s >= S ? 0.f : p.state[(int64_t)l.row * S + s];
@@ -56,18 +57,17 @@ __global__ __launch_bounds__(kScanThreads, sizeof(E) == 2 && !FLAGS ? 4 : 3) voi
     const float skip = p.D == nullptr ? 0.f : p.D[l.d];
     E *y_row = static_cast<E *>(p.y) + (int64_t)l.row * p.T + own;
 
-    // What a thread stages: 8 steps of one state, of B in the first two waves
-    // and of C in the others.
-    const int stage_c = wave / 2, stage_s = threadIdx.x / kScanLanes % kScanStates;
-    const int64_t stage_stride = stage_c ? p.C_s : p.B_s;
-    const E *stage_row = (stage_c ? static_cast<const E *>(p.C) + l.n * p.C_n + l.g * p.C_g
-                                  : static_cast<const E *>(p.B) + l.n * p.B_n + l.g * p.B_g) +
-                         stage_s * stage_stride + l.lane * K;
+    const Stager<L, kScanThreads> st(l.lane, wave);
+    const int64_t stage_stride = st.c ? p.C_s : p.B_s;
+    const E *stage_row = (st.c ? static_cast<const E *>(p.C) + l.n * p.C_n + l.g * p.C_g
+                               : static_cast<const E *>(p.B) + l.n * p.B_n + l.g * p.B_g) +
+                         st.s * stage_stride + st.lane * K;
     Steps<K, E> next_stage;
     Steps<kOwn, E> next_u, next_delta;
     const auto load_stage = [&](int t0, int s0) {
-        next_stage.load(stage_row + s0 * stage_stride + t0,
-                        s0 + stage_s < S ? end - t0 - l.lane * K : 0);
+        if (st.active)
+            next_stage.load(stage_row + s0 * stage_stride + t0,
+                            s0 + st.s < S ? end - t0 - st.lane * K : 0);
     };
     const auto load_tile = [&](int t0) {
         next_u.load(u_row + t0, end - t0 - own);
@@ -82,11 +82,11 @@ __global__ __launch_bounds__(kScanThreads, sizeof(E) == 2 && !FLAGS ? 4 : 3) voi
     for (int tile = 0; tile < live_tiles; ++tile) {
         const int t0 = tile * kTile;
         if (p.checkpoints != nullptr && l.live)
-            for (int s = l.lane; s < S; s += kScanLanes)
+            for (int s = l.lane; s < S; s += L)
                 if (mine(s)) p.checkpoints[((int64_t)l.row * p.tiles + tile) * S + s] = carry[s];
         bool all_ok = decays;  // of the lane's values in this tile: tame
         if constexpr (FLAGS)
-            for (int s = l.lane; s < padded; s += kScanLanes)
+            for (int s = l.lane; s < padded; s += L)
                 if (mine(s)) all_ok &= tame(carry[s], kTameState);
         float skipped[kOwn], dt[K], dtu[K], cut[K], y[K] = {};
         Steps<kOwn, E> z;
@@ -100,10 +100,10 @@ __global__ __launch_bounds__(kScanThreads, sizeof(E) == 2 && !FLAGS ? 4 : 3) voi
 #pragma unroll
             for (int k = 0; k < kOwn; ++k) {
                 if constexpr (SPLIT > 1) {
-                    steps[quad][part * kOwn + k][in_wave] = own_dt[k];
-                    steps[quad][K + part * kOwn + k][in_wave] = own_dtu[k];
+                    steps[set][part * kOwn + k][in_wave] = own_dt[k];
+                    steps[set][K + part * kOwn + k][in_wave] = own_dtu[k];
                     if constexpr (FLAGS)
-                        steps[quad][2 * K + part * kOwn + k][in_wave] = own_cut[k];
+                        steps[set][2 * K + part * kOwn + k][in_wave] = own_cut[k];
                 } else {
                     dt[k] = own_dt[k];
                     dtu[k] = own_dtu[k];
@@ -115,14 +115,14 @@ __global__ __launch_bounds__(kScanThreads, sizeof(E) == 2 && !FLAGS ? 4 : 3) voi
         }
         float dt_sum = 0.f;
         bool starts = false;
-        for (int s0 = 0; s0 < S; s0 += kScanStates) {
-            stage(tiles[buffer][stage_c][stage_s], next_stage, l.lane);
+        for (int s0 = 0; s0 < S; s0 += kStates) {
+            if (st.active) stage(tiles[buffer][st.c][st.s], next_stage, st.lane);
             if constexpr (FLAGS) {
-                const bool ok = whole_wave(all_tame(next_stage));
+                const bool ok = whole_wave(!st.active || all_tame(next_stage));
                 if (in_wave == 0) stage_tame[buffer][wave] = ok ? 1u : 0u;
             }
-            if (s0 + kScanStates < S)
-                load_stage(t0, s0 + kScanStates);
+            if (s0 + kStates < S)
+                load_stage(t0, s0 + kStates);
             else if (tile + 1 < live_tiles)
                 load_stage(t0 + kTile, 0);
             __syncthreads();
@@ -130,17 +130,17 @@ __global__ __launch_bounds__(kScanThreads, sizeof(E) == 2 && !FLAGS ? 4 : 3) voi
 #pragma unroll
                 for (int k = 0; k < K; ++k) {
                     if constexpr (SPLIT > 1) {
-                        dt[k] = steps[quad][k][in_wave];
-                        dtu[k] = steps[quad][K + k][in_wave];
-                        if constexpr (FLAGS) cut[k] = steps[quad][2 * K + k][in_wave];
+                        dt[k] = steps[set][k][in_wave];
+                        dtu[k] = steps[set][K + k][in_wave];
+                        if constexpr (FLAGS) cut[k] = steps[set][2 * K + k][in_wave];
                     }
                     dt_sum += dt[k];
                     if constexpr (FLAGS) starts |= cut[k] != 0.f;
                 }
                 if constexpr (FLAGS) all_ok = whole_wave(all_ok && steps_tame(dt, dtu));
             }
-            const TileRow<K> *B_tile = tiles[buffer][0], *C_tile = tiles[buffer][1];
-            const int count = S - s0 < kScanStates ? S - s0 : kScanStates;
+            const TileRow<L> *B_tile = tiles[buffer][0], *C_tile = tiles[buffer][1];
+            const int count = S - s0 < kStates ? S - s0 : kStates;
             const auto scan_states = [&](auto careful) {
                 constexpr bool CUT = decltype(careful)::value;
                 for (int i = 2 * part; i < count; i += 2 * SPLIT) {
@@ -154,16 +154,21 @@ __global__ __launch_bounds__(kScanThreads, sizeof(E) == 2 && !FLAGS ? 4 : 3) voi
                         for (int k = 0; k < K; ++k) {
                             a[j][k] = decay<FLAGS>(dt[k], cut[k], a2);
                             b[j][k] *= dtu[k];
-                            h[j] = k == 0 ? b[j][0] : step_map<CUT>(a[j][k], b[j][k], h[j]);
+                            if constexpr (L > 1)
+                                h[j] = k == 0 ? b[j][0] : step_map<CUT>(a[j][k], b[j][k], h[j]);
                         }
-                        prod[j] = lane_product<FLAGS>(dt_sum, starts, a2);
+                        if constexpr (L > 1) prod[j] = lane_product<FLAGS>(dt_sum, starts, a2);
                     }
-                    row_scan<CUT, false>(prod, h);
+                    if constexpr (L > 1) row_scan<CUT, false, L>(prod, h, l.lane);
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        const float after = step_map<CUT>(prod[j], h[j], enter[j]);
-                        carry[s0 + i + j] = row_last<false>(after);
-                        h[j] = row_shift<false>(after, enter[j]);
+                        if constexpr (L > 1) {
+                            const float after = step_map<CUT>(prod[j], h[j], enter[j]);
+                            carry[s0 + i + j] = row_last<false, L>(after);
+                            h[j] = row_shift<false, L>(after, enter[j], l.lane);
+                        } else {
+                            h[j] = enter[j];
+                        }
                         float c[K];
                         read_tile(C_tile[i + j], l.lane, c);
 #pragma unroll
@@ -171,6 +176,7 @@ __global__ __launch_bounds__(kScanThreads, sizeof(E) == 2 && !FLAGS ? 4 : 3) voi
                             h[j] = step_map<CUT>(a[j][k], b[j][k], h[j]);
                             y[k] = fmaf(c[k], h[j], y[k]);
                         }
+                        if constexpr (L == 1) carry[s0 + i + j] = h[j];
                     }
                 }
             };
@@ -198,7 +204,7 @@ __global__ __launch_bounds__(kScanThreads, sizeof(E) == 2 && !FLAGS ? 4 : 3) voi
                 out[k] = skipped[k];
 #pragma unroll
                 for (int q = 0; q < SPLIT; ++q)
-                    out[k] += sums[quad * SPLIT + q][part * kOwn + k][in_wave];
+                    out[k] += sums[set * SPLIT + q][part * kOwn + k][in_wave];
             }
         } else {
 #pragma unroll
@@ -225,25 +231,36 @@ __global__ __launch_bounds__(kScanThreads, sizeof(E) == 2 && !FLAGS ? 4 : 3) voi
     }
     if (p.final_state != nullptr) {
         const bool over = FLAGS && p.after_done != 0 && end > 0 && flags[end - 1] != 0;
-        for (int s = l.lane; s < S; s += kScanLanes)
+        for (int s = l.lane; s < S; s += L)
             if (mine(s)) p.final_state[(int64_t)l.row * S + s] = over ? 0.f : carry[s];
     }
 }
 
 // ------------------------------------------------------------------- host side
-// Steps of a lane: of 8, 4 and 2 the cheapest by the cost of the row's tiles, in
-// which 16 instructions for each step of 8 stand for what a tile costs beside
-// its steps.  Forward and backward with 2, 4 and 8 (256 channels, 16 states,
-// bf16): 2048 rows of 32 steps 538, 784 and 1387 us; 1024 of 64 507, 405 and
-// 728; 512 of 96 377, 382 and 372; 512 of 130 621, 569 and 696; 128 of 520 572,
-// 457 and 452.
-int steps_of(int64_t T) {
-    int best = 8;
-    int64_t least = INT64_MAX;
-    for (int K = 8; K >= 2; K /= 2) {
-        const int64_t tiles = (T + tile_of(K) - 1) / tile_of(K);
-        const int64_t cost = tiles * (16 + 8 * K);
-        if (cost < least) least = cost, best = K;
+// Lanes of a row: the cheapest of 16, 4 and 1 by the waves and the tiles of
+// each, a tile weighed by what it took beside 16 lanes' (1.1 for 4 lanes and
+// 16 states, 1.4 where more states leave fewer workgroups a CU, 1.85 for a lane
+// alone and 0.6 for its start), where fewer waves than SIMDs count as many.  LDS
+// limits the states of the two.  Forward and backward in us with 16, 4 and 1 (256
+// channels, bf16 and a gate, 16 states): 4096 rows of 3 steps 2776, 782 and
+// 412; 2048 of 32 1387, 386 and 565; 1024 of 64 726, 384 and 579; 512 of 130 693,
+// 489 and 628; 256 of 260 542, 452 and 595; 128 of 520 446, 424 and 1011; 512
+// of 64 with 64 states 1190 and 847; forward alone 16 rows of 30 (4096
+// channels) 49, 23 and 26.
+int lanes_of(const rlca_scan_call &c) {
+    const int64_t per_group = c.groups == 0 ? 0 : c.channels / c.groups;
+    int best = 16;
+    double least = INFINITY;
+    for (int L = 16; L >= 1; L /= 4) {
+        if ((L == 4 && c.states > 64) || (L == 1 && c.states > 16)) continue;
+        const int64_t blocks = (per_group + rows_of(L) - 1) / rows_of(L) * c.groups;
+        const double waves = (double)c.num_seqs * blocks * kScanWaves;
+        const int64_t tiles = (c.T + tile_of(L) - 1) / tile_of(L);
+        const double wave = L == 16  ? 1.0 * tiles
+                            : L == 4 ? (c.states > 16 ? 1.4 : 1.1) * tiles
+                                     : 0.6 + 1.85 * tiles;
+        const double cost = wave * (waves < 1024 ? 1024 : waves);
+        if (cost < least) least = cost, best = L;
     }
     return best;
 }
@@ -283,16 +300,16 @@ ScanParams scan_params(const rlca_scan_call &c, int rows) {
     p.states = (uint32_t)c.states;
     p.blocks_per_group = (p.per_group + rows - 1) / rows;
     p.T = (int32_t)c.T;
-    const int tile = tile_of(steps_of(c.T));
+    const int tile = tile_of(lanes_of(c));
     p.tiles = (p.T + tile - 1) / tile;
     p.softplus = c.softplus;
     p.after_done = c.convention == RLCA_RESET_AFTER_DONE;
     return p;
 }
 
-// Waves that share four channels: enough that the launch gives the 1024 SIMDs
-// several waves each, as long as every wave has a pair of states.  Measured
-// with 1, 2 and 4 (16 states, bf16): 1024 waves at one a quad (1x4096x4096)
+// Waves that share four channels (rows of 16 lanes): enough that the launch
+// gives the 1024 SIMDs several waves each, as long as every wave has a pair of
+// states.  Measured with 1, 2 and 4 (16 states, bf16): 1024 waves at one each (1x4096x4096)
 // 151, 131 and 127 us; 2304 (6x1536x2049, ragged) 112, 92 and 93; 4096
 // (8x2048x2048) 180, 194 and 216.
 constexpr int kFewestRows = 4;
@@ -300,26 +317,26 @@ constexpr int kFewestRows = 4;
 static int split_of(const rlca_scan_call &c) {
     const int64_t waves = c.num_seqs * c.channels / 4;
     const int pairs = padded_states(c.states) / 2;
-    return waves <= 1536 && pairs >= 4 ? 4 : waves <= 3072 && pairs >= 2 ? 2 : 1;
+    return waves <= 1536 && pairs >= 4 ? 4 : waves <= 3000 && pairs >= 2 ? 2 : 1;
 }
 
-template <typename E, int SPLIT, int K>
+template <typename E, int SPLIT, int L>
 static const void *scan_kernel(bool flags) {
-    return flags ? (const void *)selective_scan<E, true, SPLIT, K>
-                 : (const void *)selective_scan<E, false, SPLIT, K>;
+    return flags ? (const void *)selective_scan<E, true, SPLIT, L>
+                 : (const void *)selective_scan<E, false, SPLIT, L>;
 }
 
 template <typename E>
-static const void *scan_kernel(bool flags, int split, int steps) {
-    return steps == 2   ? scan_kernel<E, 1, 2>(flags)
-           : steps == 4 ? scan_kernel<E, 1, 4>(flags)
-           : split == 4 ? scan_kernel<E, 4, 8>(flags)
-           : split == 2 ? scan_kernel<E, 2, 8>(flags)
-                        : scan_kernel<E, 1, 8>(flags);
+static const void *scan_kernel(bool flags, int split, int lanes) {
+    return lanes == 1   ? scan_kernel<E, 1, 1>(flags)
+           : lanes == 4 ? scan_kernel<E, 1, 4>(flags)
+           : split == 4 ? scan_kernel<E, 4, 16>(flags)
+           : split == 2 ? scan_kernel<E, 2, 16>(flags)
+                        : scan_kernel<E, 1, 16>(flags);
 }
 
 static int64_t checkpoint_values(const rlca_scan_call &c) {
-    const int tile = tile_of(steps_of(c.T));
+    const int tile = tile_of(lanes_of(c));
     return c.num_seqs * c.channels * ((c.T + tile - 1) / tile) * c.states;
 }
 
@@ -394,13 +411,15 @@ rlca_status rlca_selective_scan(const rlca_scan_call *call, hipStream_t stream) 
     if (st == RLCA_OK) st = a.status();
     if (st != RLCA_OK) return st;
     if (c.num_seqs * c.channels == 0 || (c.T == 0 && c.final_state == nullptr)) return RLCA_OK;
-    const int steps = steps_of(c.T), split = steps == 8 ? split_of(c) : 1;
-    ScanParams p = scan_params(c, kScanRows / split);
-    const void *kernel = c.dtype == RLCA_F32    ? scan_kernel<float>(c.flags != nullptr, split, steps)
-                         : c.dtype == RLCA_BF16 ? scan_kernel<__bf16>(c.flags != nullptr, split, steps)
-                                                : scan_kernel<_Float16>(c.flags != nullptr, split, steps);
+    const int lanes = lanes_of(c), split = lanes == 16 ? split_of(c) : 1;
+    const int rows = rows_of(lanes) / split;
+    ScanParams p = scan_params(c, rows);
+    const bool flags = c.flags != nullptr;
+    const void *kernel = c.dtype == RLCA_F32    ? scan_kernel<float>(flags, split, lanes)
+                         : c.dtype == RLCA_BF16 ? scan_kernel<__bf16>(flags, split, lanes)
+                                                : scan_kernel<_Float16>(flags, split, lanes);
     return launch(kernel, dim3(p.num_seqs * p.groups * p.blocks_per_group), kScanThreads,
-                  2 * (kScanRows / split) * padded_states(c.states) * 4, p, stream);
+                  2 * rows * pitch_of(c.states, lanes) * 4, p, stream);
 }
 
 }  // extern "C"

@@ -3,16 +3,16 @@
 //
 // For each channel and state,  h_t = a_t h_{t-1} + b_t  with a_t = exp(dt_t A)
 // and b_t = dt_t u_t B_t, is the forward affine recurrence of this library; a
-// wave scans it as the other kernels do.  A row of 16 lanes (one DPP row) owns
-// a channel and a tile of 16 K steps, K consecutive steps a lane (K = 8, fewer
-// for short rows):
-//   * each lane folds its K maps serially into one; the product of its a's is
+// wave scans it as the other kernels do.  A row of L = 16, 4 or 1 lanes owns a
+// channel and a tile of 8 L steps, 8 consecutive steps a lane:
+//   * each lane folds its 8 maps serially into one; the product of its a's is
 //     exp(A sum dt), one exponential;
-//   * four DPP row shifts scan the 16 lane maps;
+//   * lane-crossing moves scan the L lane maps (four DPP row shifts for 16);
 //   * the tile's incoming state is a carry per (channel, state) kept in LDS;
 //   * each lane then applies its maps again from the state that enters it.
-// A wave holds 4 channels, so even one sequence of a thousand channels gives
-// every SIMD work, and a row of any length walks its tiles.
+// A lane alone (L = 1) applies them once, from the carry.  Fewer lanes a row
+// waste less of a short row and cost less a step, but make fewer waves:
+// lanes_of weighs the two.  A row of any length walks its tiles.
 #pragma once
 
 #include "seq.hpp"
@@ -20,21 +20,23 @@
 namespace rlca {
 namespace seq {
 
-constexpr int kScanLanes = 16;  // lanes of a row
-constexpr int kScanWaves = 4;   // waves of a workgroup
+constexpr int kScanK = 8;      // steps of a lane
+constexpr int kScanWaves = 4;  // waves of a workgroup
 constexpr int kScanThreads = kScanWaves * kWave;
-constexpr int kScanRows = kScanThreads / kScanLanes;  // channels of a workgroup
-constexpr int kScanStates = 8;  // states whose B and C are staged in LDS together
 
-// Steps of a lane, K, and of a tile.  A lane's cost for a tile and state is
-// about 13 instructions for the scan over lanes and 7 a step (forward), so long
-// rows take the most steps; rows that fill little of their last tile take
-// fewer (steps_of).
-constexpr int tile_of(int K) { return kScanLanes * K; }
+// Steps of a tile, channels of a workgroup, and states whose B and C are staged
+// in LDS together, by the lanes of a row.
+constexpr int tile_of(int L) { return kScanK * L; }
+constexpr int rows_of(int L) { return kScanThreads / L; }
+constexpr int states_of(int L) { return L == 16 ? 8 : 16; }
 
 // States of a workgroup's LDS arrays: whole pairs, since the kernels take two
-// states at a time.
+// states at a time.  A row's values are `pitch` apart from the next row's, so
+// that the rows of a wave fall into different banks.
 __host__ __device__ constexpr int padded_states(int S) { return (S + 1) & ~1; }
+__host__ __device__ constexpr int pitch_of(int S, int L) {
+    return padded_states(S) + (L == 16 ? 0 : 2);
+}
 
 struct ScanParams {
     const void *u, *delta, *B, *C, *z, *grad_y;
@@ -47,7 +49,7 @@ struct ScanParams {
     float *checkpoints;  // [num_seqs * channels][tiles][states]: states entering each tile
     void *grad_u, *grad_delta, *grad_z;
     float *grad_state;
-    float *bc_partials;  // [num_seqs][groups][blocks of a group][2][states][tiles * tile_of(K)]
+    float *bc_partials;  // [num_seqs][groups][blocks of a group][2][states][tiles * tile_of(L)]
     float *row_partials; // [num_seqs][channels][states + 2]: grad_A, grad_D, grad_delta_bias
     int64_t u_n, u_d, delta_n, delta_d, z_n, z_d, g_n, g_d;
     int64_t B_n, B_g, B_s, C_n, C_g, C_s;
@@ -66,13 +68,14 @@ struct ScanLane {
     bool live;
 };
 
+template <int L>
 __device__ __forceinline__ ScanLane scan_lane(const ScanParams &p, int local, uint32_t rows) {
     ScanLane l;
     const uint32_t b = blockIdx.x;
     const uint32_t ng = b / p.blocks_per_group;
     l.n = ng / p.groups;
     l.g = ng - l.n * p.groups;
-    l.lane = threadIdx.x & (kScanLanes - 1);
+    l.lane = threadIdx.x & (L - 1);
     l.local = local;
     const uint32_t c = (b - ng * p.blocks_per_group) * rows + local;
     l.live = c < p.per_group;
@@ -99,21 +102,50 @@ __device__ __forceinline__ float product(float a, float b) {
     return a * b;
 }
 
-// Inclusive scan of the row's 16 lane maps of two states, towards higher lanes
-// (row_shr) or, REVERSE, towards lower ones (row_shl).  Lanes whose source
-// lies outside the row keep their map.
+// The lane-crossing moves of a row: STEP lanes on in scan order (REVERSE: towards
+// lower lanes), its last lane to all.
+template <int L, bool REVERSE, int STEP>
+constexpr int shift_ctrl() {
+    if constexpr (L == 16) return (REVERSE ? 0x100 : 0x110) + STEP;  // row_shl, row_shr
+    // quad_perm: lane i takes lane i - STEP (i + STEP), itself where there is none
+    int c = 0;
+    for (int i = 0; i < 4; ++i) {
+        const int from = REVERSE ? i + STEP : i - STEP;
+        c |= (from < 0 || from > 3 ? i : from) << (2 * i);
+    }
+    return c;
+}
+
+// Inclusive scan of the row's lane maps of two states, towards higher lanes or,
+// REVERSE, towards lower ones.  Lanes whose source lies outside the row keep
+// their map.
 //
-// Without cuts a step is two instructions a state, an FMA and a product that
-// fetch their operand from the other lane themselves; the compiler would move
-// it to a register first, and fill that register before (8 instructions).  The
-// two states take turns, so that two instructions always lie between a write
-// and the lane-crossing read of it, as the hardware requires.
-template <bool CUT, bool REVERSE>
-__device__ __forceinline__ void row_scan(float (&a)[2], float (&h)[2]) {
-    if constexpr (CUT) {
-        constexpr int kShift = REVERSE ? 0x100 : 0x110;
-        const auto step = [&](auto ctrl) {
-            constexpr int kCtrl = decltype(ctrl)::value;
+// For 16 lanes without cuts a step is two instructions a state, an FMA and a
+// product that fetch their operand from the other lane themselves; the
+// compiler would move it to a register first, and fill that register before (8
+// instructions).  The two states take turns, so that two instructions always
+// lie between a write and the lane-crossing read of it, as the hardware
+// requires.
+template <bool CUT, bool REVERSE, int L>
+__device__ __forceinline__ void row_scan(float (&a)[2], float (&h)[2], int lane) {
+    if constexpr (L == 4) {
+        const auto step = [&](auto by) {
+            constexpr int kStep = decltype(by)::value;
+            constexpr int kCtrl = shift_ctrl<4, REVERSE, kStep>();
+            const bool has = REVERSE ? lane + kStep < 4 : lane >= kStep;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const float ph = dpp_move<kCtrl, 0xf>(h[j], h[j]);
+                const float pa = dpp_move<kCtrl, 0xf>(a[j], a[j]);
+                h[j] = has ? step_map<CUT>(a[j], h[j], ph) : h[j];
+                a[j] = has ? product<CUT>(a[j], pa) : a[j];
+            }
+        };
+        step(std::integral_constant<int, 1>{});
+        step(std::integral_constant<int, 2>{});
+    } else if constexpr (CUT) {
+        const auto step = [&](auto by) {
+            constexpr int kCtrl = shift_ctrl<16, REVERSE, decltype(by)::value>();
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const float ph = dpp_move<kCtrl, 0xf>(h[j], 0.f);
@@ -122,10 +154,10 @@ __device__ __forceinline__ void row_scan(float (&a)[2], float (&h)[2]) {
                 a[j] = product<CUT>(a[j], pa);
             }
         };
-        step(std::integral_constant<int, kShift + 1>{});
-        step(std::integral_constant<int, kShift + 2>{});
-        step(std::integral_constant<int, kShift + 4>{});
-        step(std::integral_constant<int, kShift + 8>{});
+        step(std::integral_constant<int, 1>{});
+        step(std::integral_constant<int, 2>{});
+        step(std::integral_constant<int, 4>{});
+        step(std::integral_constant<int, 8>{});
     } else {
 #define RLCA_STEP(SHIFT)                                                   \
     "v_fmac_f32_dpp %1, %1, %0 " SHIFT " row_mask:0xf bank_mask:0xf\n\t"   \
@@ -145,15 +177,18 @@ __device__ __forceinline__ void row_scan(float (&a)[2], float (&h)[2]) {
 }
 
 // The neighbouring lane's value in scan order; the row's first lane gets `x0`.
-template <bool REVERSE>
-__device__ __forceinline__ float row_shift(float x, float x0) {
-    return dpp_move<(REVERSE ? 0x101 : 0x111), 0xf>(x, x0);
+template <bool REVERSE, int L>
+__device__ __forceinline__ float row_shift(float x, float x0, int lane) {
+    if constexpr (L == 16) return dpp_move<shift_ctrl<16, REVERSE, 1>(), 0xf>(x, x0);
+    const float y = dpp_move<shift_ctrl<4, REVERSE, 1>(), 0xf>(x, x);
+    return lane == (REVERSE ? L - 1 : 0) ? x0 : y;
 }
 
 // The value of the row's last lane in scan order, in all its lanes.
-template <bool REVERSE>
+template <bool REVERSE, int L>
 __device__ __forceinline__ float row_last(float x) {
-    return dpp_move<(REVERSE ? 0x150 : 0x15f), 0xf>(x, x);
+    if constexpr (L == 16) return dpp_move<(REVERSE ? 0x150 : 0x15f), 0xf>(x, x);
+    return dpp_move<(REVERSE ? 0x00 : 0xff), 0xf>(x, x);
 }
 
 // Waves run their LDS accesses in order, so lanes of one wave hand values to
@@ -162,43 +197,46 @@ __device__ __forceinline__ void wave_order() {
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 }
 
-// A tile of one state's B or C in LDS, fp32: a lane's steps in blocks of up to
+// A tile of one state's B or C in LDS, fp32: a lane's steps as two blocks of
 // four, each lane's next to its neighbours', so that the 16-byte reads of 16
 // lanes cover all banks once.
-template <int N>
-using Floats = float __attribute__((ext_vector_type(N)));
-typedef Floats<4> float4v;
-
-template <int K>
+typedef float float4v __attribute__((ext_vector_type(4)));
+template <int L>
 struct TileRow {
-    static constexpr int kBlock = K < 4 ? K : 4;
-    Floats<kBlock> block[K / kBlock][kScanLanes];
+    float4v half[2][L];
 };
 
-template <int K>
-__device__ __forceinline__ void read_tile(const TileRow<K> &r, int lane, float (&v)[K]) {
-    constexpr int N = TileRow<K>::kBlock;
+template <int L>
+__device__ __forceinline__ void read_tile(const TileRow<L> &r, int lane, float (&v)[kScanK]) {
+    const float4v x = r.half[0][lane], y = r.half[1][lane];
 #pragma unroll
-    for (int i = 0; i < K / N; ++i) {
-        const Floats<N> x = r.block[i][lane];
-#pragma unroll
-        for (int k = 0; k < N; ++k) v[i * N + k] = x[k];
-    }
+    for (int k = 0; k < 4; ++k) v[k] = x[k], v[4 + k] = y[k];
 }
 
-template <typename E, int K>
-__device__ __forceinline__ void stage(TileRow<K> &to, const Steps<K, E> &from, int lane) {
-    constexpr int N = TileRow<K>::kBlock;
-    float v[K];
+template <typename E, int L>
+__device__ __forceinline__ void stage(TileRow<L> &to, const Steps<kScanK, E> &from, int lane) {
+    float v[kScanK];
     from.widen(v);
+    float4v x, y;
 #pragma unroll
-    for (int i = 0; i < K / N; ++i) {
-        Floats<N> x;
-#pragma unroll
-        for (int k = 0; k < N; ++k) x[k] = v[i * N + k];
-        to.block[i][lane] = x;
-    }
+    for (int k = 0; k < 4; ++k) x[k] = v[k], y[k] = v[4 + k];
+    to.half[0][lane] = x;
+    to.half[1][lane] = y;
 }
+
+// What a thread stages: 8 steps of one state, of B in the first kWaves waves and
+// of C in the next.
+template <int L, int THREADS>
+struct Stager {
+    static constexpr int kWaves = states_of(L) * L > kWave ? states_of(L) * L / kWave : 1;
+    int c, s, lane;
+    bool active;
+    __device__ __forceinline__ Stager(int lane_of_row, int wave)
+        : c(wave / kWaves % 2), s(wave % kWaves * (kWave / L) + threadIdx.x % kWave / L),
+          lane(lane_of_row),
+          active((2 * kWaves * kWave >= THREADS || wave < 2 * kWaves) &&
+                 (L > 1 || s < states_of(L))) {}
+};
 
 // K steps of a lane from step t: dt and dt u from raw = delta and u (0 past
 // `end`, where a step then changes nothing; raw becomes dt before softplus).
@@ -281,7 +319,7 @@ __device__ __forceinline__ bool whole_wave(bool x) {
     return __builtin_amdgcn_ballot_w64(!x) == 0;
 }
 
-int steps_of(int64_t T);
+int lanes_of(const rlca_scan_call &c);
 ScanParams scan_params(const rlca_scan_call &c, int rows);
 rlca_status check_scan(const rlca_scan_call &c, bool backward, Arrays *a);
 

@@ -5,15 +5,15 @@
 //   grad_C_t = sum_d gy_t h_t                    grad_B_t = sum_d g_t dt_t u_t
 //   grad_dt_t = sum_s g_t w_t A + u_t sum_s g_t B_t
 //   grad_u_t = dt_t sum_s g_t B_t + D gy_t       grad_A = sum_t g_t w_t dt_t
-// A workgroup walks its 16 channels' tiles from the last to the first.  The
+// A workgroup walks its channels' tiles from the last to the first.  The
 // state that enters a tile comes from the forward call's checkpoints, the
 // tile's states from one forward scan, and g from one reverse scan whose carry
 // r = a_t g_t passes to the tile before.
 //
-// grad_B and grad_C sum over the channels of a group.  Within a wave the four
-// rows hold four channels of the same steps: 16 values (8 steps of each
-// gradient) meet in 12 lane-half swaps and 12 additions, after which each row
-// holds the sums of four of them.  The waves' sums meet in LDS, the
+// grad_B and grad_C sum over the channels of a group.  Within a wave the rows
+// hold channels of the same steps: 16 values (8 steps of each gradient) meet in
+// 12 lane-half swaps and 12 additions, after which each 16 lanes hold four of
+// them, summed over rows of 16 lanes (sum_rows goes on for fewer).  The waves' sums meet in LDS, the
 // workgroups' in a workspace that bc_sums adds in order.
 #include "seq_scan.hpp"
 
@@ -28,66 +28,101 @@ __device__ __forceinline__ void swap_add(float &x, float y, bool halves) {
     x = __builtin_bit_cast(float, (uint32_t)r[0]) + __builtin_bit_cast(float, (uint32_t)r[1]);
 }
 
-// 2K values of four rows -> row q's lanes hold the sums over rows of the values
-// from q K/2 on, K/2 of them.
-template <int K>
-__device__ __forceinline__ Floats<K / 2> sum_rows(float (&v)[2 * K]) {
+// The sums over a wave's rows of 16 values a lane (8 steps of grad_B, then of
+// grad_C).  Halves of the wave, then its rows of 16 lanes, swap half of what
+// they hold: a lane of 16 keeps the four values from 4 (lane / 16) on.  Rows of
+// fewer lanes go on within the 16: a lane keeps value lane / 4 (of its place in
+// the row, L = 4), or all four lanes of a quad do (L = 1).
+template <int L>
+using RowSums = typename std::conditional<L == 16, float4v, float>::type;
+
+template <int L>
+__device__ __forceinline__ RowSums<L> sum_rows(float (&v)[16], int in_wave) {
 #pragma unroll
-    for (int i = 0; i < K; ++i) swap_add(v[i], v[K + i], true);
+    for (int i = 0; i < 8; ++i) swap_add(v[i], v[8 + i], true);
 #pragma unroll
-    for (int i = 0; i < K / 2; ++i) swap_add(v[i], v[K / 2 + i], false);
-    Floats<K / 2> r;
+    for (int i = 0; i < 4; ++i) swap_add(v[i], v[4 + i], false);
+    if constexpr (L == 16) {
+        float4v r;
 #pragma unroll
-    for (int i = 0; i < K / 2; ++i) r[i] = v[i];
-    return r;
+        for (int i = 0; i < 4; ++i) r[i] = v[i];
+        return r;
+    } else {
+        // lanes 8 apart: those with bit 3 keep the upper two values
+        const bool up8 = (in_wave & 8) != 0, up4 = (in_wave & 4) != 0;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float keep = up8 ? v[2 + i] : v[i], give = up8 ? v[i] : v[2 + i];
+            v[i] = keep + dpp_move<0x128, 0xf>(give, 0.f);  // row_ror:8
+        }
+        // lanes 4 apart: quads 0 and 2 take from the quad above, 1 and 3 from below
+        const float keep = up4 ? v[1] : v[0], give = up4 ? v[0] : v[1];
+        const float above = dpp_move<0x12c, 0xf>(give, 0.f);  // row_ror:12
+        const float below = dpp_move<0x124, 0xf>(give, 0.f);  // row_ror:4
+        float r = keep + (up4 ? below : above);
+        if constexpr (L == 1) {  // and the quad's four lanes
+            r += dpp_move<0xb1, 0xf>(r, 0.f);  // quad_perm 1, 0, 3, 2
+            r += dpp_move<0x4e, 0xf>(r, 0.f);  // quad_perm 2, 3, 0, 1
+        }
+        return r;
+    }
 }
 
-// Sums over a row's 16 lanes of two values, complete in lane 15.
+// Sums over a row's lanes of two values, complete in its last lane.
+template <int L>
 __device__ __forceinline__ void row_sum(float (&x)[2]) {
-    // the two take turns, and one idle instruction keeps the required two
-    // between a write and the lane-crossing read of it
+    if constexpr (L == 16) {
+        // the two take turns, and one idle instruction keeps the required two
+        // between a write and the lane-crossing read of it
 #define RLCA_STEP(SHIFT)                                                  \
     "v_add_f32_dpp %0, %0, %0 " SHIFT " row_mask:0xf bank_mask:0xf\n\t"   \
     "v_add_f32_dpp %1, %1, %1 " SHIFT " row_mask:0xf bank_mask:0xf\n\t"   \
     "s_nop 0\n\t"
-    asm("s_nop 1\n\t" RLCA_STEP("row_shr:1") RLCA_STEP("row_shr:2") RLCA_STEP("row_shr:4")
-            RLCA_STEP("row_shr:8")
-        : "+v"(x[0]), "+v"(x[1]));
+        asm("s_nop 1\n\t" RLCA_STEP("row_shr:1") RLCA_STEP("row_shr:2") RLCA_STEP("row_shr:4")
+                RLCA_STEP("row_shr:8")
+            : "+v"(x[0]), "+v"(x[1]));
 #undef RLCA_STEP
+    } else if constexpr (L == 4) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            x[j] += dpp_move<0xb1, 0xf>(x[j], 0.f);
+            x[j] += dpp_move<0x4e, 0xf>(x[j], 0.f);
+        }
+    }
 }
 
-// A workgroup holds four sets of four channels, SPLIT waves to each.  Waves of
-// one set take every SPLIT-th pair of states, and prepare and finish K / SPLIT
+// A workgroup holds four sets of 64 / L channels, SPLIT waves to each.  Waves of
+// one set take every SPLIT-th pair of states, and prepare and finish 8 / SPLIT
 // of a lane's steps, as in the forward scan.
-template <typename E, bool FLAGS, bool GATE, int SPLIT, int K>
+template <typename E, bool FLAGS, bool GATE, int SPLIT, int L>
 __global__ __launch_bounds__(kScanThreads *SPLIT, 2) void selective_scan_backward(ScanParams p) {
-    constexpr int kQuads = kScanWaves, kRows = kScanRows;
-    constexpr int kTile = tile_of(K), kOwn = K / SPLIT, kThreads = kScanThreads * SPLIT;
+    constexpr int K = kScanK, kSets = kScanWaves, kRows = rows_of(L), kStates = states_of(L);
+    constexpr int kTile = tile_of(L), kOwn = K / SPLIT, kThreads = kScanThreads * SPLIT;
     constexpr int kBefore = FLAGS ? 4 : 3, kAfter = GATE ? 3 : 2;  // values a step that waves share
     extern __shared__ __attribute__((aligned(16))) char lds_bytes[];
-    __shared__ TileRow<K> tiles[2][2][kScanStates];  // [buffer][B, C][state]
-    __shared__ Floats<K / 2> bc[kQuads][kScanStates][kWave];
-    __shared__ float before[SPLIT > 1 ? kQuads : 1][SPLIT > 1 ? kBefore * K : 1][kWave];
-    __shared__ float after[SPLIT > 1 ? SPLIT * kQuads : 1][SPLIT > 1 ? kAfter * K : 1][kWave];
+    __shared__ TileRow<L> tiles[2][2][kStates];  // [buffer][B, C][state]
+    __shared__ RowSums<L> bc[kSets][kStates][kWave];
+    __shared__ float before[SPLIT > 1 ? kSets : 1][SPLIT > 1 ? kBefore * K : 1][kWave];
+    __shared__ float after[SPLIT > 1 ? SPLIT * kSets : 1][SPLIT > 1 ? kAfter * K : 1][kWave];
     __shared__ uint32_t stage_tame[2][kThreads / kWave];  // [buffer]: whether what a wave staged is
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int in_wave = threadIdx.x % kWave;
-    const int quad = wave / SPLIT, part = wave % SPLIT;
-    const ScanLane l = scan_lane(p, quad * 4 + in_wave / kScanLanes, kRows);
-    const int S = (int)p.states, padded = padded_states(S);
-    // [rows][padded]: A, the gradient a_t g_t entering the tile from its right,
+    const int set = wave / SPLIT, part = wave % SPLIT;
+    const ScanLane l = scan_lane<L>(p, set * (kWave / L) + in_wave / L, kRows);
+    const int S = (int)p.states, padded = padded_states(S), pitch = pitch_of(S, L);
+    // [rows][pitch]: A, the gradient a_t g_t entering the tile from its right,
     // the states entering it from its left, and the sums of grad_A
-    float *A = reinterpret_cast<float *>(lds_bytes) + l.local * padded;
-    float *carry = A + kRows * padded;
-    float *enter_states = carry + kRows * padded;
-    float *grad_A = enter_states + kRows * padded;
+    float *A = reinterpret_cast<float *>(lds_bytes) + l.local * pitch;
+    float *carry = A + kRows * pitch;
+    float *enter_states = carry + kRows * pitch;
+    float *grad_A = enter_states + kRows * pitch;
     const auto mine = [&](int s) { return SPLIT == 1 || (s / 2) % SPLIT == part; };
     const int row_steps = row_end(p.lengths, l.n, p.T);
     const int end = l.live ? row_steps : 0;  // a clamped row computes on zeros
     const uint8_t *flags = FLAGS ? p.flags + (int64_t)l.n * p.T : nullptr;
     const bool over = FLAGS && p.after_done != 0 && end > 0 && flags[end - 1] != 0;
     bool decays = true;
-    for (int s = l.lane; s < padded; s += kScanLanes)
+    for (int s = l.lane; s < padded; s += L)
         if (mine(s)) {
             const float x = s >= S ? 0.f : p.A[(int64_t)l.d * S + s];
             A[s] = x;
@@ -111,20 +146,17 @@ __global__ __launch_bounds__(kScanThreads *SPLIT, 2) void selective_scan_backwar
     float *partials = p.bc_partials + (int64_t)blockIdx.x * 2 * S * p.tiles * kTile;
     float totals[2] = {0.f, 0.f};  // of grad_D and grad_delta_bias
 
-    // What a thread of the first four waves stages: 8 steps of one state of B
-    // (two waves) or C.
-    const int stage_c = wave / 2 % 2, stage_s = threadIdx.x / kScanLanes % kScanStates;
-    const bool stages = kThreads == 256 || wave < 4;
-    const int64_t stage_stride = stage_c ? p.C_s : p.B_s;
-    const E *stage_row = (stage_c ? static_cast<const E *>(p.C) + l.n * p.C_n + l.g * p.C_g
-                                  : static_cast<const E *>(p.B) + l.n * p.B_n + l.g * p.B_g) +
-                         stage_s * stage_stride + l.lane * K;
+    const Stager<L, kThreads> st(l.lane, wave);
+    const int64_t stage_stride = st.c ? p.C_s : p.B_s;
+    const E *stage_row = (st.c ? static_cast<const E *>(p.C) + l.n * p.C_n + l.g * p.C_g
+                               : static_cast<const E *>(p.B) + l.n * p.B_n + l.g * p.B_g) +
+                         st.s * stage_stride + st.lane * K;
     Steps<K, E> next_stage;
     Steps<kOwn, E> u, delta, go, z, next_u, next_delta, next_go, next_z;
     const auto load_stage = [&](int t0, int s0) {
-        if (stages)
+        if (st.active)
             next_stage.load(stage_row + s0 * stage_stride + t0,
-                            s0 + stage_s < S ? row_steps - t0 - l.lane * K : 0);
+                            s0 + st.s < S ? row_steps - t0 - st.lane * K : 0);
     };
     const auto load_tile = [&](int t0) {
         next_u.load(u_row + t0, end - t0 - own);
@@ -163,7 +195,7 @@ __global__ __launch_bounds__(kScanThreads *SPLIT, 2) void selective_scan_backwar
         if constexpr (GATE) z = next_z;
         {
             const float *from = p.checkpoints + ((int64_t)l.row * p.tiles + tile) * S;
-            for (int s = l.lane; s < padded; s += kScanLanes)
+            for (int s = l.lane; s < padded; s += L)
                 if (mine(s)) {
                     const float x = l.live && s < S ? from[s] : 0.f;
                     enter_states[s] = x;
@@ -190,10 +222,10 @@ __global__ __launch_bounds__(kScanThreads *SPLIT, 2) void selective_scan_backwar
             for (int k = 0; k < kOwn; ++k) {
                 if constexpr (SPLIT > 1) {
                     const int at = part * kOwn + k;
-                    before[quad][at][in_wave] = own_dt[k];
-                    before[quad][K + at][in_wave] = own_dtu[k];
-                    before[quad][2 * K + at][in_wave] = own_gy[k];
-                    if constexpr (FLAGS) before[quad][3 * K + at][in_wave] = own_cut[k];
+                    before[set][at][in_wave] = own_dt[k];
+                    before[set][K + at][in_wave] = own_dtu[k];
+                    before[set][2 * K + at][in_wave] = own_gy[k];
+                    if constexpr (FLAGS) before[set][3 * K + at][in_wave] = own_cut[k];
                 } else {
                     dt[k] = own_dt[k];
                     dtu[k] = own_dtu[k];
@@ -204,15 +236,15 @@ __global__ __launch_bounds__(kScanThreads *SPLIT, 2) void selective_scan_backwar
         }
         float dt_sum = 0.f;
         bool starts = false;
-        for (int s0 = 0; s0 < S; s0 += kScanStates) {
-            const int count = S - s0 < kScanStates ? S - s0 : kScanStates;
-            if (stages) stage(tiles[buffer][stage_c][stage_s], next_stage, l.lane);
+        for (int s0 = 0; s0 < S; s0 += kStates) {
+            const int count = S - s0 < kStates ? S - s0 : kStates;
+            if (st.active) stage(tiles[buffer][st.c][st.s], next_stage, st.lane);
             if constexpr (FLAGS) {
-                const bool ok = whole_wave(!stages || all_tame(next_stage));
+                const bool ok = whole_wave(!st.active || all_tame(next_stage));
                 if (in_wave == 0) stage_tame[buffer][wave] = ok ? 1u : 0u;
             }
-            if (s0 + kScanStates < S)
-                load_stage(t0, s0 + kScanStates);
+            if (s0 + kStates < S)
+                load_stage(t0, s0 + kStates);
             else if (tile > 0)
                 load_stage(t0 - kTile, 0);
             __syncthreads();
@@ -220,10 +252,10 @@ __global__ __launch_bounds__(kScanThreads *SPLIT, 2) void selective_scan_backwar
 #pragma unroll
                 for (int k = 0; k < K; ++k) {
                     if constexpr (SPLIT > 1) {
-                        dt[k] = before[quad][k][in_wave];
-                        dtu[k] = before[quad][K + k][in_wave];
-                        gy[k] = before[quad][2 * K + k][in_wave];
-                        if constexpr (FLAGS) cut[k] = before[quad][3 * K + k][in_wave];
+                        dt[k] = before[set][k][in_wave];
+                        dtu[k] = before[set][K + k][in_wave];
+                        gy[k] = before[set][2 * K + k][in_wave];
+                        if constexpr (FLAGS) cut[k] = before[set][3 * K + k][in_wave];
                     }
                     dt_sum += dt[k];
                     if constexpr (FLAGS) starts |= cut[k] != 0.f;
@@ -235,7 +267,7 @@ __global__ __launch_bounds__(kScanThreads *SPLIT, 2) void selective_scan_backwar
                     all_ok = whole_wave(all_ok);
                 }
             }
-            const TileRow<K> *B_tile = tiles[buffer][0], *C_tile = tiles[buffer][1];
+            const TileRow<L> *B_tile = tiles[buffer][0], *C_tile = tiles[buffer][1];
             const auto scan_states = [&](auto careful) {
                 constexpr bool CUT = decltype(careful)::value;
                 for (int i = 2 * part; i < count; i += 2 * SPLIT) {
@@ -246,20 +278,27 @@ __global__ __launch_bounds__(kScanThreads *SPLIT, 2) void selective_scan_backwar
                         const float a2 = A[s0 + i + j] * kLog2e;
                         enter[j] = enter_states[s0 + i + j];
                         float b[K];
-                        read_tile(B_tile[i + j], l.lane, b);
+                        if constexpr (L > 1) read_tile(B_tile[i + j], l.lane, b);
 #pragma unroll
                         for (int k = 0; k < K; ++k) {
                             a[j][k] = decay<FLAGS>(dt[k], cut[k], a2);
-                            const float x = b[k] * dtu[k];
-                            h[j] = k == 0 ? x : step_map<CUT>(a[j][k], x, h[j]);
+                            if constexpr (L > 1) {
+                                const float x = b[k] * dtu[k];
+                                h[j] = k == 0 ? x : step_map<CUT>(a[j][k], x, h[j]);
+                            }
                         }
-                        prefix[j] = prod[j] = lane_product<FLAGS>(dt_sum, starts, a2);
+                        if constexpr (L > 1)
+                            prefix[j] = prod[j] = lane_product<FLAGS>(dt_sum, starts, a2);
                     }
-                    row_scan<CUT, false>(prefix, h);
-                    float v[2][2 * K], r[2], c[2][K];
+                    if constexpr (L > 1) row_scan<CUT, false, L>(prefix, h, l.lane);
+                    float v[2][16], r[2], c[2][K];
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        h[j] = row_shift<false>(step_map<CUT>(prefix[j], h[j], enter[j]), enter[j]);
+                        if constexpr (L > 1)
+                            h[j] = row_shift<false, L>(step_map<CUT>(prefix[j], h[j], enter[j]),
+                                                       enter[j], l.lane);
+                        else
+                            h[j] = enter[j];
                         float b[K];
                         read_tile(B_tile[i + j], l.lane, b);
                         read_tile(C_tile[i + j], l.lane, c[j]);
@@ -267,42 +306,50 @@ __global__ __launch_bounds__(kScanThreads *SPLIT, 2) void selective_scan_backwar
                         for (int k = 0; k < K; ++k) {
                             w[j][k] = product<CUT>(a[j][k], h[j]);
                             h[j] = fmaf(b[k], dtu[k], w[j][k]);
-                            v[j][K + k] = gy[k] * h[j];
+                            v[j][8 + k] = gy[k] * h[j];
                             if constexpr (GATE) y[k] = fmaf(c[j][k], h[j], y[k]);
                             c[j][k] *= gy[k];  // what y's gradient adds to g
                         }
-                        g[j] = c[j][K - 1];
+                        if constexpr (L > 1) {
+                            g[j] = c[j][K - 1];
 #pragma unroll
-                        for (int k = K - 2; k >= 0; --k)
-                            g[j] = step_map<CUT>(a[j][k + 1], c[j][k], g[j]);
-                        r[j] = product<CUT>(a[j][0], g[j]);
+                            for (int k = K - 2; k >= 0; --k)
+                                g[j] = step_map<CUT>(a[j][k + 1], c[j][k], g[j]);
+                            r[j] = product<CUT>(a[j][0], g[j]);
+                        }
                     }
-                    row_scan<CUT, true>(prod, r);
+                    if constexpr (L > 1) row_scan<CUT, true, L>(prod, r, l.lane);
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         const float right = carry[s0 + i + j], A_s = A[s0 + i + j];
-                        r[j] = step_map<CUT>(prod[j], r[j], right);
-                        carry[s0 + i + j] = row_last<true>(r[j]);
-                        g[j] = row_shift<true>(r[j], right);  // a g of the step after the lane's
+                        if constexpr (L > 1) {
+                            r[j] = step_map<CUT>(prod[j], r[j], right);
+                            carry[s0 + i + j] = row_last<true, L>(r[j]);
+                            // a g of the step after the lane's
+                            g[j] = row_shift<true, L>(r[j], right, l.lane);
+                        } else {
+                            g[j] = right;
+                        }
                         float b[K];
                         read_tile(B_tile[i + j], l.lane, b);
                         dA[j] = 0.f;
 #pragma unroll
                         for (int k = K - 1; k >= 0; --k) {
                             g[j] = k == K - 1 ? c[j][k] + g[j]
-                                                   : step_map<CUT>(a[j][k + 1], c[j][k], g[j]);
+                                              : step_map<CUT>(a[j][k + 1], c[j][k], g[j]);
                             v[j][k] = g[j] * dtu[k];
                             gB[k] = fmaf(g[j], b[k], gB[k]);
                             const float q = g[j] * w[j][k];
                             dA[j] = fmaf(q, dt[k], dA[j]);  // at a start w is 0, and dt put to 0
                             grad_dt[k] = fmaf(q, A_s, grad_dt[k]);
                         }
-                        bc[quad][i + j][in_wave] = sum_rows<K>(v[j]);
+                        if constexpr (L == 1) carry[s0 + i + j] = product<CUT>(a[j][0], g[j]);
+                        bc[set][i + j][in_wave] = sum_rows<L>(v[j], in_wave);
                     }
-                    row_sum(dA);
+                    row_sum<L>(dA);
 #pragma unroll
                     for (int j = 0; j < 2; ++j)  // all lanes of the row write the same value
-                        grad_A[s0 + i + j] += row_last<false>(dA[j]);
+                        grad_A[s0 + i + j] += L == 16 ? row_last<false, L>(dA[j]) : dA[j];
                 }
             };
             if constexpr (FLAGS) {
@@ -318,7 +365,7 @@ __global__ __launch_bounds__(kScanThreads *SPLIT, 2) void selective_scan_backwar
             }
             buffer ^= 1;
             if constexpr (SPLIT > 1) {
-                if (s0 + kScanStates >= S) {  // the tile's last stage
+                if (s0 + kStates >= S) {  // the tile's last stage
 #pragma unroll
                     for (int k = 0; k < K; ++k) {
                         after[wave][k][in_wave] = gB[k];
@@ -328,16 +375,29 @@ __global__ __launch_bounds__(kScanThreads *SPLIT, 2) void selective_scan_backwar
                 }
             }
             __syncthreads();
-            // lane x of a wave holds, for state i, half a lane's steps of grad_B
-            // (rows 0 and 1) or grad_C (rows 2 and 3)
-            for (int j = threadIdx.x; j < count * kWave; j += kThreads) {
-                const int i = j / kWave, x = j % kWave, q = x / kScanLanes;
-                Floats<K / 2> sum = bc[0][i][x];
+            if constexpr (L == 16) {
+                // lane x of a wave holds, for state i, half a lane's steps of
+                // grad_B (rows 0 and 1) or grad_C (rows 2 and 3)
+                for (int j = threadIdx.x; j < count * kWave; j += kThreads) {
+                    const int i = j / kWave, x = j % kWave, q = x / 16;
+                    float4v sum = bc[0][i][x];
 #pragma unroll
-                for (int m = 1; m < kQuads; ++m) sum += bc[m][i][x];
-                float *to = partials + ((int64_t)(q >> 1) * S + s0 + i) * p.tiles * kTile + t0 +
-                            (x % kScanLanes) * K + (q & 1) * (K / 2);
-                *reinterpret_cast<Floats<K / 2> *>(to) = sum;
+                    for (int m = 1; m < kSets; ++m) sum += bc[m][i][x];
+                    float *to = partials + ((int64_t)(q >> 1) * S + s0 + i) * p.tiles * kTile + t0 +
+                                (x % 16) * K + (q & 1) * 4;
+                    *reinterpret_cast<float4v *>(to) = sum;
+                }
+            } else {
+                // lane x holds value x / 4 of its place in the row (L = 4), or
+                // of the row (L = 1)
+                for (int j = threadIdx.x; j < count * 2 * kTile; j += kThreads) {
+                    const int i = j / (2 * kTile), which = j / kTile % 2, t = j % kTile;
+                    const int x = (which * 8 + t % K) * 4 + t / K;
+                    float sum = bc[0][i][x];
+#pragma unroll
+                    for (int m = 1; m < kSets; ++m) sum += bc[m][i][x];
+                    partials[((int64_t)which * S + s0 + i) * p.tiles * kTile + t0 + t] = sum;
+                }
             }
         }
         wave_order();
@@ -349,9 +409,9 @@ __global__ __launch_bounds__(kScanThreads *SPLIT, 2) void selective_scan_backwar
                 const int at = part * kOwn + k;
 #pragma unroll
                 for (int q = 0; q < SPLIT; ++q) {
-                    sum_gB[k] += after[quad * SPLIT + q][at][in_wave];
-                    sum_dt[k] += after[quad * SPLIT + q][K + at][in_wave];
-                    if constexpr (GATE) sum_y[k] += after[quad * SPLIT + q][2 * K + at][in_wave];
+                    sum_gB[k] += after[set * SPLIT + q][at][in_wave];
+                    sum_dt[k] += after[set * SPLIT + q][K + at][in_wave];
+                    if constexpr (GATE) sum_y[k] += after[set * SPLIT + q][2 * K + at][in_wave];
                 }
             } else {
                 sum_gB[k] = gB[k];
@@ -418,29 +478,29 @@ __global__ __launch_bounds__(kScanThreads *SPLIT, 2) void selective_scan_backwar
             store_steps<kOwn>(grad_delta + t0, p.T - t, out_delta);
         }
     }
-    row_sum(totals);
+    row_sum<L>(totals);
     if constexpr (SPLIT > 1) {  // the parts' totals, in order
         __syncthreads();
-        if (l.lane == kScanLanes - 1)
+        if (l.lane == L - 1)
 #pragma unroll
             for (int q = 0; q < 2; ++q) after[wave][q][in_wave] = totals[q];
         __syncthreads();
-        if (l.lane == kScanLanes - 1)
+        if (l.lane == L - 1)
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
                 totals[q] = 0.f;
 #pragma unroll
-                for (int m = 0; m < SPLIT; ++m) totals[q] += after[quad * SPLIT + m][q][in_wave];
+                for (int m = 0; m < SPLIT; ++m) totals[q] += after[set * SPLIT + m][q][in_wave];
             }
     }
     if (!l.live) return;
     float *out = p.row_partials + (int64_t)l.row * (S + 2);
-    for (int s = l.lane; s < S; s += kScanLanes)
+    for (int s = l.lane; s < S; s += L)
         if (mine(s)) {
             out[s] = grad_A[s];
             if (p.grad_state != nullptr) p.grad_state[(int64_t)l.row * S + s] = carry[s];
         }
-    if (part == 0 && l.lane == kScanLanes - 1) {
+    if (part == 0 && l.lane == L - 1) {
         out[S] = totals[0];
         out[S + 1] = totals[1];
     }
@@ -565,30 +625,30 @@ static int split_of(const rlca_scan_call &c) {
 }
 
 static Workspace workspace_of(const rlca_scan_call &c) {
-    const int tile = tile_of(steps_of(c.T));
+    const int lanes = lanes_of(c), tile = tile_of(lanes);
     const int64_t padded = (c.T + tile - 1) / tile * tile;
     const int64_t per_group = c.groups == 0 ? 0 : c.channels / c.groups;
-    const int64_t blocks = c.num_seqs * c.groups * ((per_group + kScanRows - 1) / kScanRows);
+    const int64_t blocks = c.num_seqs * c.groups * ((per_group + rows_of(lanes) - 1) / rows_of(lanes));
     return {(size_t)(blocks * 2 * c.states * padded),
             (size_t)((c.num_seqs * c.channels * (c.states + 2) + 3) / 4 * 4),
             (size_t)(2 * ranges_of(c.num_seqs).count * c.channels * (c.states + 2))};
 }
 
-template <typename E, int SPLIT, int K>
+template <typename E, int SPLIT, int L>
 static const void *backward_kernel(const rlca_scan_call &c) {
     const bool flags = c.flags != nullptr, gate = c.z != nullptr;
-    return flags ? (gate ? (const void *)selective_scan_backward<E, true, true, SPLIT, K>
-                         : (const void *)selective_scan_backward<E, true, false, SPLIT, K>)
-                 : (gate ? (const void *)selective_scan_backward<E, false, true, SPLIT, K>
-                         : (const void *)selective_scan_backward<E, false, false, SPLIT, K>);
+    return flags ? (gate ? (const void *)selective_scan_backward<E, true, true, SPLIT, L>
+                         : (const void *)selective_scan_backward<E, true, false, SPLIT, L>)
+                 : (gate ? (const void *)selective_scan_backward<E, false, true, SPLIT, L>
+                         : (const void *)selective_scan_backward<E, false, false, SPLIT, L>);
 }
 
 template <typename E>
-static const void *backward_kernel(const rlca_scan_call &c, int split, int steps) {
-    return steps == 2   ? backward_kernel<E, 1, 2>(c)
-           : steps == 4 ? backward_kernel<E, 1, 4>(c)
-           : split == 2 ? backward_kernel<E, 2, 8>(c)
-                        : backward_kernel<E, 1, 8>(c);
+static const void *backward_kernel(const rlca_scan_call &c, int split, int lanes) {
+    return lanes == 1   ? backward_kernel<E, 1, 1>(c)
+           : lanes == 4 ? backward_kernel<E, 1, 4>(c)
+           : split == 2 ? backward_kernel<E, 2, 16>(c)
+                        : backward_kernel<E, 1, 16>(c);
 }
 
 }  // namespace seq
@@ -618,16 +678,17 @@ rlca_status rlca_selective_scan_backward(const rlca_scan_call *call, void *works
     if (st != RLCA_OK) return st;
     if (workspace_bytes < w.total() * 4) return RLCA_ERR_INVALID_SIZE;
     if (c.channels == 0) return RLCA_OK;
-    const int steps = steps_of(c.T), split = steps == 8 ? split_of(c) : 1;
-    ScanParams p = scan_params(c, kScanRows);
+    const int lanes = lanes_of(c), split = lanes == 16 ? split_of(c) : 1;
+    ScanParams p = scan_params(c, rows_of(lanes));
     p.bc_partials = static_cast<float *>(workspace);
     p.row_partials = p.bc_partials + w.bc;
     if (c.num_seqs != 0) {
-        const void *kernel = c.dtype == RLCA_F32    ? backward_kernel<float>(c, split, steps)
-                             : c.dtype == RLCA_BF16 ? backward_kernel<__bf16>(c, split, steps)
-                                                    : backward_kernel<_Float16>(c, split, steps);
+        const void *kernel = c.dtype == RLCA_F32    ? backward_kernel<float>(c, split, lanes)
+                             : c.dtype == RLCA_BF16 ? backward_kernel<__bf16>(c, split, lanes)
+                                                    : backward_kernel<_Float16>(c, split, lanes);
         st = launch(kernel, dim3(p.num_seqs * p.groups * p.blocks_per_group),
-                    kScanThreads * split, 4 * kScanRows * padded_states(c.states) * 4, p, stream);
+                    kScanThreads * split, 4 * rows_of(lanes) * pitch_of(c.states, lanes) * 4, p,
+                    stream);
         if (st != RLCA_OK) return st;
         if (p.T != 0) {
             BcSums b = {};
@@ -640,7 +701,7 @@ rlca_status rlca_selective_scan_backward(const rlca_scan_call *call, void *works
             b.groups = p.groups;
             b.rows = p.num_seqs * p.groups * 2 * p.states;
             b.T = p.T;
-            b.padded = p.tiles * tile_of(steps);
+            b.padded = p.tiles * tile_of(lanes);
             while ((4 << b.lane_bits) < p.T && (1 << b.lane_bits) < kScanThreads) ++b.lane_bits;
             const uint32_t across = (p.T + (4 << b.lane_bits) - 1) / (4 << b.lane_bits);
             const uint32_t at_once = kScanThreads >> b.lane_bits;

@@ -223,6 +223,30 @@ def test_scan_many_channels(dtype, which, gpu_device):
             check(getattr(grads, name), want[name], f"grad {name}")
 
 
+# Rows of few steps, enough of them that four lanes or one take a row, over several
+# tiles too; and rows of 16 lanes whose four channels one wave takes alone.
+MANY_ROWS = [(20, 1026, 5, 70, 1), (64, 210, 17, 20, 3), (90, 510, 4, 7, 1), (160, 510, 3, 13, 1),
+             (4, 3100, 5, 250, 1)]
+
+
+@pytest.mark.parametrize("which", ["", "flags lengths after"], ids=lambda w: w or "plain")
+@pytest.mark.parametrize("shape", MANY_ROWS, ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("dtype", DTYPES, ids=NAMES)
+def test_scan_many_rows(dtype, shape, which, gpu_device):
+    N, ch, S, T, G = shape
+    g = gen(32)
+    t = scan_inputs(g, N, ch, S, T, G, dtype, True)
+    s, gf, go = normal(g, N, ch, S), normal(g, N, ch, S), normal(g, N, ch, T, dtype=dtype)
+    flags, lengths = episodes(g, N, T, which)
+    kw = dict(flags=flags, lengths=lengths, convention=convention_of(which))
+    want = ref.scan(**t, state=s, grad_y=go, grad_final=gf, **kw)
+    y, final, grads = run_scan(t, s, flags, lengths, kw["convention"], True, go, gf)
+    check(y, want["y"], "y")
+    check(final, want["final"], "final state")
+    for name in grads._fields:
+        check(getattr(grads, name), want[name], f"grad {name}")
+
+
 @pytest.mark.parametrize("dtype", DTYPES, ids=NAMES)
 def test_scan_extreme_steps(dtype, gpu_device):
     """Step sizes from e^-15 to 15 and decays from 1 (A = 0) to e^-300 a step."""
@@ -397,6 +421,35 @@ def test_nothing_passes_an_episode_start(bad, gpu_device):
             assert torch.equal(a, b), k
         for k, v in ends.items():
             assert torch.equal(v, ends2[k]), k
+
+
+@pytest.mark.parametrize("shape", [(200, 510, 3, 13), (40, 1026, 5, 70)],
+                         ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_nothing_passes_an_episode_start_in_many_rows(bad, shape, gpu_device):
+    """Where one lane or four take a row: steps 5..9 are poisoned."""
+    N, ch, S, T = shape
+    g = gen(18)
+    t = scan_inputs(g, N, ch, S, T, 1, torch.float32, True)
+    go = normal(g, N, ch, T)
+    flags = torch.zeros(N, T, dtype=torch.uint8, device="cuda")
+    flags[1, 5] = flags[1, 10] = 1
+
+    def run(t, go):
+        y, final, points = rl.selective_scan(**t, flags=flags, with_state=True,
+                                             with_checkpoints=True)
+        gr = rl.selective_scan_backward(go, **t, checkpoints=points, flags=flags)
+        return {"y": y, "gu": gr.u, "gdelta": gr.delta, "gz": gr.z, "gB": gr.B, "gC": gr.C}, final
+
+    rows, final = run(t, go)
+    t2, go2 = {k: v.clone() for k, v in t.items()}, go.clone()
+    for v in (t2["u"], t2["delta"], t2["z"], t2["B"], t2["C"], go2):
+        v[1, ..., 5:10] = bad
+    rows2, final2 = run(t2, go2)
+    for k, v in rows.items():
+        v[1, ..., 5:10] = rows2[k][1, ..., 5:10] = 0
+        assert torch.equal(v, rows2[k]), k
+    assert torch.equal(final, final2)
 
 
 def test_nothing_enters_past_a_rows_length(gpu_device):

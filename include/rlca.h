@@ -568,9 +568,9 @@ rlca_status rlca_selective_step(const rlca_scan_step_call *call, hipStream_t str
  *   out = x * min(1, max_norm / (norm[0] + eps))
  * (and out = x where the norm is 0).  out may be data itself (in place, the
  * usual case) or another array that overlaps no array of the call.  With
- * max_norm = +infinity only the norm is computed, and out is not used.  A NaN gradient makes the norm and every scaled value NaN, as the
- * formula says; with an infinite one the scale is 0 and infinite values
- * become NaN.  max_norm >= 0, eps >= 0 and finite.  `tensors` is host memory,
+ * max_norm = +infinity only the norm is computed, and out is not used.  A NaN
+ * gradient makes the norm and every scaled value NaN, as the formula says; with
+ * an infinite one the scale is 0 and infinite values become NaN.  max_norm >= 0, eps >= 0 and finite.  `tensors` is host memory,
  * read before the function returns; tensors of count 0 are skipped, and with
  * nothing to sum the norm is 0.  The sums run in a fixed order: the norm is
  * reproducible bit for bit. */

@@ -35,16 +35,23 @@ import sys
 ROOT = os.path.dirname(os.path.abspath(__file__))
 
 
-def _kernel_sources():
+# Sources of the operators of a recurrent policy or model (their summaries:
+# profiles/*_sequence.md); the rest are the estimators'.
+_SEQUENCE_SOURCES = ("seq", "grad_clip")
+
+
+def _kernel_sources(sequence=False):
     csrc = sorted(glob.glob(os.path.join(ROOT, "linear_recurrence_scan_row_amd", "csrc", "*")))
-    return [os.path.relpath(p, ROOT) for p in csrc] + ["include/rlca.h"]
+    return [os.path.relpath(p, ROOT) for p in csrc
+            if os.path.basename(p).startswith(_SEQUENCE_SOURCES) == sequence] + ["include/rlca.h"]
 
 
-def source_digest() -> str:
-    """Digest of the kernel sources; stored with a counter summary so that a
-    summary taken on other code is not reported for this code."""
+def source_digest(sequence=False) -> str:
+    """Digest of the estimators' kernel sources (sequence: of the sequence
+    operators'); stored with a counter summary so that a summary taken on
+    other code is not reported for this code."""
     h = hashlib.sha256()
-    for rel in _kernel_sources():
+    for rel in _kernel_sources(sequence):
         with open(os.path.join(ROOT, rel), "rb") as f:
             h.update(f.read())
     return h.hexdigest()[:16]

@@ -8,10 +8,14 @@
 // again here) are loads of lines that the neighbouring lanes read as well, so
 // lanes need nothing from each other and HBM delivers each line once.
 //
-// Next to the memory's time stand a step's 30 to 60 instructions.  So a
-// workgroup keeps its channels and walks tiles of several rows: weights and
+// Next to the memory's time stand a step's vector instructions: 20 forward, 36
+// with episode starts, 86 backward with them.  So a workgroup keeps its channels and walks tiles of several rows: weights and
 // addresses are formed once, one item is loaded while the one before is
 // computed, and the weights' gradients leave the registers once at the end.
+//
+// Measured, inputs from HBM: forward 1x4096x8191 bf16 27.5 us (4.9 TB/s);
+// 4096x64x128 fp32 with episode starts 59 us forward (4.7 TB/s), 108 backward
+// (3.8 TB/s; the vector units are busy 70% of it) and 5 for the weights' sums.
 #include "seq.hpp"
 
 namespace rlca {

@@ -462,7 +462,11 @@ def selective_step(u, delta, A, B, C, state, D=None, z=None, delta_bias=None, sl
 # ---------------------------------------------------------------- the clipping
 def _clip_workspace(dev, stream):
     """A zero-filled workspace per (device, stream), shared with no other call
-    kind: the running total and the scale live in it between launches."""
+    kind: the running total and the scale live in it between launches.  A call
+    captured into a graph gets its own, which the graph fills and keeps: graphs
+    may be replayed on any stream, and nothing is filled while one is captured."""
+    if torch.cuda.is_current_stream_capturing():
+        return torch.zeros(CLIP_WORKSPACE_BYTES, dtype=torch.uint8, device=dev)
     key = (dev.index, stream, "clip")
     with _workspaces_lock:
         ws = _workspaces.get(key)

@@ -129,3 +129,29 @@ def test_refusals(gpu_device):
             rl.clip_grad_norm([t], **kw)
     with pytest.raises(rl.RlcaError):
         rl.clip_grad_norm([t, t], 1.0)
+
+
+def test_first_call_on_a_stream_is_captured(gpu_device):
+    """No eager call has made the stream's workspace: a captured call brings its
+    own, and eager calls on that stream before and between replays are right."""
+    g = torch.Generator(device="cuda").manual_seed(5)
+    new = [[normal(g, n) for n in (70_001, 5, 4096)] for _ in range(4)]
+    grads, outs = [t.clone() for t in new[0]], [torch.empty_like(t) for t in new[0]]
+    rl.clip_grad_norm(grads, 1.0, out=outs)  # on another stream, which loads the kernels
+    stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=stream):
+        norm = rl.clip_grad_norm(grads, 1.0, out=outs)
+    for values in new:
+        with torch.cuda.stream(stream):
+            eager_out = [torch.empty_like(t) for t in values]
+            eager = rl.clip_grad_norm(values, 1.0, out=eager_out)
+        stream.synchronize()
+        for t, v in zip(grads, values):
+            t.copy_(v)
+        graph.replay()
+        torch.cuda.synchronize()
+        want, scaled = ref.clip(values, 1.0, 1e-6)
+        assert eager.item() == pytest.approx(want, rel=1e-10, abs=0)
+        assert norm.item() == eager.item()
+        assert all(torch.equal(a, b) for a, b in zip(outs, eager_out))

@@ -423,7 +423,11 @@ rlca_status rlca_ppo_clip_loss(const float *advantages, const double *stats,
  * Sizes:    num_seqs * channels < 2^31 and T <= RLCA_MAX_T; a call with
  *           num_seqs, channels or T of 0 is a valid no-op where it has no
  *           state to hand on; with T = 0 the final state is the state, and
- *           the gradients of an empty sum are 0.
+ *           the gradients of an empty sum are 0.  A call whose launch would
+ *           hold 2^32 threads is refused as too large: the scan over rows
+ *           takes num_seqs * groups * ceil(channels / groups / 4) < 2^24, the
+ *           convolution over rows channels < 2^24 (more if rows are short),
+ *           the scan's step channels * states < 2^32.
  * Errors and memory: as stated at the top.  Workspaces need no
  *           initialisation, except rlca_clip_grad_norm's (as the fused
  *           consumers': zero-filled before its first use, and left so). */

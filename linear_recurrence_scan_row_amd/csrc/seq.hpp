@@ -55,21 +55,6 @@ struct Steps {
     }
 };
 
-// The K steps before p, of which the last n exist.
-template <int K, typename E>
-__device__ __forceinline__ void load_steps_before(const E *p, int n, float (&v)[K]) {
-    typedef E block __attribute__((ext_vector_type(K)));
-    if (n >= K) {
-        block b;
-        __builtin_memcpy(&b, p - K, sizeof b);
-#pragma unroll
-        for (int k = 0; k < K; ++k) v[k] = (float)b[k];
-    } else {
-#pragma unroll
-        for (int k = 0; k < K; ++k) v[k] = K - k <= n ? (float)p[k - K] : 0.f;
-    }
-}
-
 // One rounding, to nearest even, from fp32 to the storage type.
 template <int K, typename E>
 __device__ __forceinline__ void store_steps(E *p, int n, const float (&v)[K]) {

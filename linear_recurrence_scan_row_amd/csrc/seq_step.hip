@@ -284,6 +284,7 @@ rlca_status rlca_selective_step(const rlca_scan_step_call *call, hipStream_t str
     const size_t e = element_bytes(c.dtype);
     if (e == 0 || S < 1 || S > RLCA_MAX_STATES || G < 1 || D % G != 0)
         return RLCA_ERR_INVALID_VALUE;
+    if (D * S >= (int64_t)1 << 32) return RLCA_ERR_INVALID_SIZE;  // the launch's threads
     const int64_t params = N == 0 ? 0 : D;
     Arrays a;
     a.in(c.u, e, true, {{N, c.u_stride_seq}, {D, 1}});

@@ -322,3 +322,12 @@ def test_clip_aliasing(lib):
     many = [(a + 400 * i, a + 400 * i, 100, f32) for i in range(700)]
     many[3] = (many[600][0] + 8, many[600][0] + 8, 10, f32)
     assert clip(lib, many) == ALIAS
+
+
+def test_launches_of_too_many_threads(lib):
+    for backward in (False, True):
+        assert run(lib, scan_call(backward, num_seqs=1 << 24, channels=4, groups=1)) == SIZE
+    # forward, 2^8 lanes share a long row
+    assert run(lib, conv_call(num_seqs=1, channels=1 << 24, T=4096, x_stride_channel=0,
+                              out=1 << 45)) == SIZE
+    assert run(lib, scan_step_call(num_seqs=1, channels=1 << 25, groups=1, states=128)) == SIZE

@@ -78,7 +78,7 @@ struct ConvLoads {
         if (t0 > 0) {
             back.load(row - kBack, kBack);
         } else {
-            back.load(row, 0);
+            back.b = {};
             if (p.state != nullptr) {
                 const E *s = static_cast<const E *>(p.state) +
                              ((int64_t)n * p.channels + d) * (W - 1);
@@ -89,8 +89,13 @@ struct ConvLoads {
         if constexpr (BACKWARD) {
             const E *grad = static_cast<const E *>(p.grad_out) + n * p.g_n + d * p.g_d + t0;
             g.load(grad, end - t0);
-            after.load(row + kConvK, end - t0 - kConvK);
-            g_after.load(grad + kConvK, end - t0 - kConvK);
+            if (end - t0 > kConvK) {
+                after.load(row + kConvK, end - t0 - kConvK);
+                g_after.load(grad + kConvK, end - t0 - kConvK);
+            } else {  // a row's last lane, in nearly every wave: no step by step
+                after.b = {};
+                g_after.b = {};
+            }
         }
         if constexpr (FLAGS) {
             const uint8_t *f = p.flags + (int64_t)n * p.T;

@@ -89,20 +89,19 @@ __device__ __forceinline__ float silu_slope(float x, float sig) {
 
 // softplus(x) = log(1 + e^x) = max(x, 0) + log1p(e), e = exp(-|x|) in (0, 1].
 // A step size of 1e-3 is log1p(1e-3), where log(1 + e) alone would keep four
-// digits: with w the rounded 1 + e, log1p(e) = log(w) e / (w - 1), in which
-// the roundings of w in both factors cancel.  e's exponent is formed with the
-// low part of log2(e), so that its error does not grow with |x|.
+// digits: with w the rounded 1 + e, log1p(e) = log(w) + (e - (w - 1)) / w, and
+// the 1 / w is left out, since what it scales is at most half a step of w.  e's
+// exponent is formed with the low part of log2(e), so that its error does not
+// grow with |x|.  Relative error at most 6 x 2^-24.  -|x| ends at -200, where e
+// is 0: a step masked by -infinity or the lowest value has size 0, not NaN.
 __device__ __forceinline__ float softplus(float x) {
-    const float y = -fabsf(x);
+    const float y = fmaxf(-fabsf(x), -200.f);
     const float t = y * kLog2e;
     const float low = fmaf(y, kLog2e, -t) + y * kLog2eLow;
     const float e = exp2_fast(t) * fmaf(low, 0.6931471805599453f, 1.f);
     const float w = 1.f + e;
-    const float wm1 = w - 1.f;
-    const float l = wm1 == 0.f ? e
-                               : __builtin_amdgcn_logf(w) * 0.6931471805599453f * e *
-                                     __builtin_amdgcn_rcpf(wm1);
-    return (x > 0.f ? x : 0.f) + (y == y ? l : y);  // a NaN stays one
+    const float l = fmaf(__builtin_amdgcn_logf(w), 0.6931471805599453f, e - (w - 1.f));
+    return (x < 0.f ? 0.f : x) + l;  // a NaN stays one
 }
 
 // Eight flags of a row of T from step `first` on, which may begin before the

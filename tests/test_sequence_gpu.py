@@ -266,6 +266,37 @@ def test_scan_extreme_steps(dtype, gpu_device):
             check(getattr(grads, name), want[name], f"grad {name}")
 
 
+@pytest.mark.parametrize("dtype", DTYPES, ids=NAMES)
+@pytest.mark.parametrize("T", [5, 150])
+def test_masked_step_sizes(T, dtype, gpu_device):
+    """Steps whose delta is the type's lowest value, or -infinity, have size 0:
+    they change no state and pass finite gradients; a row may be all such steps."""
+    g = gen(41)
+    N, ch, S = 4, 18, 6
+    t = scan_inputs(g, N, ch, S, T, 1, dtype, True)
+    masked = torch.rand(N, 1, T, generator=g, device="cuda") < 0.4
+    masked[1], masked[2] = True, False
+    masked = masked.expand(N, ch, T)
+    t["delta"] = t["delta"].masked_fill(masked, torch.finfo(dtype).min)
+    s, gf, go = normal(g, N, ch, S), normal(g, N, ch, S), normal(g, N, ch, T, dtype=dtype)
+    want = ref.scan(**t, state=s, grad_y=go, grad_final=gf)
+    y, final, grads = run_scan(t, s, None, None, 0, True, go, gf)
+    check(y, want["y"], "y")
+    check(final, want["final"], "final state")
+    assert torch.equal(final[1], s[1])
+    for name in grads._fields:
+        check(getattr(grads, name), want[name], f"grad {name}")
+    inf = dict(t, delta=t["delta"].masked_fill(masked, -float("inf")))
+    y2, final2, grads2 = run_scan(inf, s, None, None, 0, True, go, gf)
+    assert torch.equal(y2, y) and torch.equal(final2, final)
+    assert all(torch.equal(a, b) for a, b in zip(grads2, grads))
+    pool = s.clone()
+    out = rl.selective_step(t["u"][..., 0].contiguous(), inf["delta"][..., 0].contiguous(),
+                            t["A"], t["B"][..., 0].contiguous(), t["C"][..., 0].contiguous(),
+                            pool, t["D"], t["z"][..., 0].contiguous(), t["delta_bias"])
+    assert torch.equal(pool[1], s[1]) and bool(out.isfinite().all())
+
+
 def test_scan_rows_continue(gpu_device):
     """A row in two calls, the state handed on, agrees with the row in one."""
     g = gen(4)

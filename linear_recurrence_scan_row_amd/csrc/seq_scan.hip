@@ -7,10 +7,10 @@
 // one or two stored values per step.  A workgroup's channels share the tile's B
 // and C, staged in LDS in fp32 and read there 16 bytes a lane.
 //
-// A (step, state) takes 10.4 vector instructions (87 M wave instructions for
+// A (step, state) takes 10.1 vector instructions (85 M wave instructions for
 // 8x2048 channels of 2048 steps and 16 states) of at least 6, one of which, the
 // exponential, issues at a quarter of the rate.  Measured there, bf16 with a
-// gate: 190 to 200 us, the vector units busy 81 to 83% of it (at 2.4 GHz); the
+// gate: 186 to 194 us, the vector units busy 81% of it (at 2.4 GHz); the
 // bytes alone would take 60.
 #include "seq_scan.hpp"
 

@@ -16,7 +16,7 @@
 // them, summed over rows of 16 lanes (sum_rows goes on for fewer).  The waves' sums meet in LDS, the
 // workgroups' in a workspace that bc_sums adds in order.
 //
-// A (step, state) takes 28.7 vector instructions, of about 22 in the formulas
+// A (step, state) takes 28.4 vector instructions, of about 22 in the formulas
 // above and the sums.  Measured for 8x2048 channels of 2048 steps and 16 states,
 // bf16 with a gate: 510 to 530 us, the vector units busy 81% of it at 2.4 GHz
 // (298 MB read and 471 written, 268 of them partial sums, would take 161), and

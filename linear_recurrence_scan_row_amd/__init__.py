@@ -7,7 +7,8 @@ of those calls, and the fused PPO consumers of the advantages (gae_stats,
 ppo_clip_loss), each HIP kernel launches behind the C ABI of include/rlca.h.
 For policies and models with a recurrent core: the short causal convolution and
 the selective state space scan over the same rows, with gradients and
-single-step forms, and gradient clipping by the global norm (sequence.py).
+single-step forms, and gradient clipping by the global norm (sequence.py);
+recurrent_policy.py trains a policy on all of them.
 Real-valued arrays may be float32, bfloat16 or float16 (fp32 arithmetic).
 PyTorch supplies device memory and the stream; the computation is entirely in
 librlca.so, which must be built (``python -m linear_recurrence_scan_row_amd.build``).

@@ -35,8 +35,8 @@ import sys
 ROOT = os.path.dirname(os.path.abspath(__file__))
 
 
-# Sources of the operators of a recurrent policy or model (their summaries:
-# profiles/*_sequence.md); the rest are the estimators'.
+# Sources of the operators of a recurrent policy or model, whose summary has a
+# digest of its own; the rest are the estimators'.
 _SEQUENCE_SOURCES = ("seq", "grad_clip")
 
 

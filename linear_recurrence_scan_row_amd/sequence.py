@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import struct
+import threading
 from array import array
 from typing import NamedTuple, Optional
 
@@ -460,20 +461,26 @@ def selective_step(u, delta, A, B, C, state, D=None, z=None, delta_bias=None, sl
 
 
 # ---------------------------------------------------------------- the clipping
+_clip_locks = {}  # by the key of the workspace
+
+
 def _clip_workspace(dev, stream):
     """A zero-filled workspace per (device, stream), shared with no other call
-    kind: the running total and the scale live in it between launches.  A call
-    captured into a graph gets its own, which the graph fills and keeps: graphs
-    may be replayed on any stream, and nothing is filled while one is captured."""
+    kind, and its lock: the running total and the scale live in it from a call's
+    first launch to its last, so a call holds the lock over all of them (threads
+    may share a stream).  A call captured into a graph gets its own, which the
+    graph fills and keeps: graphs may be replayed on any stream, and nothing is
+    filled while one is captured."""
     if torch.cuda.is_current_stream_capturing():
-        return torch.zeros(CLIP_WORKSPACE_BYTES, dtype=torch.uint8, device=dev)
+        return (torch.zeros(CLIP_WORKSPACE_BYTES, dtype=torch.uint8, device=dev),
+                threading.Lock())
     key = (dev.index, stream, "clip")
     with _workspaces_lock:
         ws = _workspaces.get(key)
         if ws is None:
             ws = torch.zeros(CLIP_WORKSPACE_BYTES, dtype=torch.uint8, device=dev)
-            _workspaces[key] = ws
-    return ws
+            _workspaces[key], _clip_locks[key] = ws, threading.Lock()
+        return ws, _clip_locks[key]
 
 
 def _dense(t):
@@ -527,8 +534,9 @@ def clip_grad_norm(grads, max_norm, eps=1e-6, out=None, norm=None):
     packed[3::4] = array("Q", codes)
     n = _out(norm, (1,), dev, torch.float64, name="norm")
     h = _current_stream(dev)
-    ws = _clip_workspace(dev, h)
-    _check(lib().rlca_clip_grad_norm(packed.buffer_info()[0], len(grads), max_norm, eps,
-                                     n.data_ptr(), ws.data_ptr(), ws.numel(), h),
-           "rlca_clip_grad_norm")
+    ws, lock = _clip_workspace(dev, h)
+    with lock:
+        status = lib().rlca_clip_grad_norm(packed.buffer_info()[0], len(grads), max_norm, eps,
+                                           n.data_ptr(), ws.data_ptr(), ws.numel(), h)
+    _check(status, "rlca_clip_grad_norm")
     return n

@@ -76,6 +76,16 @@ constexpr float kLog2eLow = 1.925963033500913e-08f;  // log2(e) - (float)log2(e)
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
+// h 2^x, where 2^x alone may leave float32's range: 0 stays 0, and what is in
+// range comes out.  2^x is split at x's whole part, towards 0, so that the
+// product with the rest (in [1, 2) for a growth, (1/2, 1] for a decay) rounds
+// as h 2^x does.  Beyond 2^300 every h but 0 is infinite, and below 2^-300 0.
+__device__ __forceinline__ float times_exp2(float h, float x) {
+    x = x > 300.f ? 300.f : x < -300.f ? -300.f : x;  // a NaN stays one
+    const float whole = truncf(x);
+    return ldexpf(h * exp2_fast(x - whole), (int)whole);
+}
+
 // 1 / (1 + exp(-x)); 0 and 1 at the infinities.
 __device__ __forceinline__ float sigmoid(float x) {
     return __builtin_amdgcn_rcpf(1.f + exp2_fast(-x * kLog2e));

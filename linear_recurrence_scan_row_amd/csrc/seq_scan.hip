@@ -24,50 +24,59 @@ namespace seq {
 // over all the steps, and prepares and finishes 8 / SPLIT of a lane's steps.
 // They meet in LDS twice a tile, in dt and dt u before and in y's partial sums
 // after (split_of below says when that pays).
-template <typename E, bool FLAGS, int SPLIT, int L>
-__global__ __launch_bounds__(kScanThreads, sizeof(E) == 2 && !FLAGS ? 4 : 3) void selective_scan(
-    ScanParams p) {
-    constexpr int K = kScanK, kSets = kScanWaves / SPLIT, kRows = rows_of(L) / SPLIT;
+//
+// There are two bodies: GROW false for workgroups whose states all decay, which leaves
+// with false, nothing written, where one may grow; GROW true has the serial steps too.
+// They share neither addresses nor arguments in registers.  (A mere choice in one
+// walk costs every decaying model 2 to 12%; the check costs rows of one tile up to 4%
+// and longer ones nothing.)  Steps without softplus take the second alone, 4 to 7%
+// slower than the first would be.
+template <typename E, bool FLAGS, int SPLIT, int L, bool GROW, int SETS, int VALUES, int WAVES,
+          int OUTS>
+__device__ __forceinline__ bool scan_rows(const ScanParams &p, uint32_t thread,
+                                          char *lds_bytes, TileRow<L> (&tiles)[2][2][states_of(L)],
+                                          float (&steps)[SETS][VALUES][kWave],
+                                          float (&sums)[WAVES][OUTS][kWave],
+                                          uint32_t (&steady_waves)[kScanWaves],
+                                          uint32_t (&stage_tame)[2][kScanWaves]) {
+    constexpr int K = kScanK, kRows = rows_of(L) / SPLIT;
     constexpr int kTile = tile_of(L), kStates = states_of(L), kOwn = K / SPLIT;
-    extern __shared__ __attribute__((aligned(16))) char lds_bytes[];
-    __shared__ TileRow<L> tiles[2][2][kStates];  // [buffer][B, C][state]
-    __shared__ float steps[kSets][SPLIT > 1 ? (FLAGS ? 3 : 2) * K : 1][kWave];
-    __shared__ float sums[SPLIT > 1 ? kScanWaves : 1][SPLIT > 1 ? K : 1][kWave];
-    __shared__ uint32_t stage_tame[2][kScanWaves];  // [buffer]: whether what a wave staged is
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const int in_wave = threadIdx.x % kWave;
+    const int wave = __builtin_amdgcn_readfirstlane(thread / kWave);
+    const int in_wave = thread % kWave;
     const int set = wave / SPLIT, part = wave % SPLIT;
-    const ScanLane l = scan_lane<L>(p, set * (kWave / L) + in_wave / L, kRows);
+    const ScanLane l = scan_lane<L>(p, thread, set * (kWave / L) + in_wave / L, kRows);
     const int S = (int)p.states, padded = padded_states(S), pitch = pitch_of(S, L);
     // [rows][pitch]: the states entering the tile, and A log2(e)
     float *carry = reinterpret_cast<float *>(lds_bytes) + l.local * pitch;
     float *A2 = carry + kRows * pitch;
     // a wave initialises and hands on the states that it computes
     const auto mine = [&](int s) { return SPLIT == 1 || (s / 2) % SPLIT == part; };
-    bool decays = true;
-    for (int s = l.lane; s < padded; s += L)
-        if (mine(s)) {
-            const float x = s >= S ? 0.f : p.A[(int64_t)l.d * S + s] * kLog2e;
-            carry[s] = p.state == nullptr || s >= S ? 0.f : p.state[(int64_t)l.row * S + s];
-            A2[s] = x;
-            if constexpr (FLAGS) decays &= x <= 0.f && tame(x, kTameStep);
-        }
     const int end = row_end(p.lengths, l.n, p.T);
     const int own = l.lane * K + part * kOwn;  // the lane's own steps in a tile
-    const E *u_row = static_cast<const E *>(p.u) + l.n * p.u_n + l.d * p.u_d + own;
-    const E *delta_row = static_cast<const E *>(p.delta) + l.n * p.delta_n + l.d * p.delta_d + own;
-    const E *z_row =
-        p.z == nullptr ? nullptr : static_cast<const E *>(p.z) + l.n * p.z_n + l.d * p.z_d + own;
     const uint8_t *flags = FLAGS ? p.flags + (int64_t)l.n * p.T : nullptr;
     const float bias = p.delta_bias == nullptr ? 0.f : p.delta_bias[l.d];
     const float skip = p.D == nullptr ? 0.f : p.D[l.d];
-    E *y_row = static_cast<E *>(p.y) + (int64_t)l.row * p.T + own;
-
-    const Stager<L, kScanThreads> st(l.lane, wave);
+    const Stager<L, kScanThreads> st(l.lane, wave, in_wave);
     const int64_t stage_stride = st.c ? p.C_s : p.B_s;
     const E *stage_row = (st.c ? static_cast<const E *>(p.C) + l.n * p.C_n + l.g * p.C_g
                                : static_cast<const E *>(p.B) + l.n * p.B_n + l.g * p.B_g) +
                          st.s * stage_stride + st.lane * K;
+    // The lane's steps of the tile at t0, in an input or y; where registers are
+    // short the address is formed there and then.
+    constexpr bool kLate = GROW || (FLAGS && L == 1);
+    const auto in_row = [&](const void *x, int64_t by_n, int64_t by_d, int t0) {
+        if constexpr (kLate)
+            return static_cast<const E *>(x) + (l.n * by_n + t0) + (here(l.d) * by_d + here(own));
+        return static_cast<const E *>(x) + l.n * by_n + l.d * by_d + own + t0;
+    };
+    const auto out_row = [&](void *out, int t0) {
+        if constexpr (kLate)
+            return static_cast<E *>(out) + t0 + ((int64_t)here(l.row) * p.T + here(own));
+        return static_cast<E *>(out) + (int64_t)l.row * p.T + own + t0;
+    };
+    // Past the row's steps y is 0.
+    const int live_tiles = (end + kTile - 1) / kTile;
+
     Steps<K, E> next_stage;
     Steps<kOwn, E> next_u, next_delta;
     const auto load_stage = [&](int t0, int s0) {
@@ -76,27 +85,43 @@ __global__ __launch_bounds__(kScanThreads, sizeof(E) == 2 && !FLAGS ? 4 : 3) voi
                             s0 + st.s < S ? end - t0 - st.lane * K : 0);
     };
     const auto load_tile = [&](int t0) {
-        next_u.load(u_row + t0, end - t0 - own);
-        next_delta.load(delta_row + t0, end - t0 - own);
+        next_u.load(in_row(p.u, p.u_n, p.u_d, t0), end - t0 - own);
+        next_delta.load(in_row(p.delta, p.delta_n, p.delta_d, t0), end - t0 - own);
     };
-    // Past the row's steps y is 0.
-    const int live_tiles = (end + kTile - 1) / kTile;
     int buffer = 0;
     load_stage(0, 0);
     load_tile(0);
+
+    bool tame_A = true;
+    Growth growth;
+    for (int s = l.lane; s < padded; s += L)
+        if (mine(s)) {
+            const float x = s >= S ? 0.f : p.A[(int64_t)l.d * S + s] * kLog2e;
+            carry[s] = p.state == nullptr || s >= S ? 0.f : p.state[(int64_t)l.row * S + s];
+            A2[s] = x;
+            growth.add(x);
+            if constexpr (FLAGS) tame_A &= tame(x, kTameStep);
+        }
+    if constexpr (GROW) {
+        growth.meet();
+    } else {
+        // no a above 1 in any tile
+        const bool steady = whole_wave(growth.up == 0.f);
+        if (!all_waves(steady, steady_waves, wave, in_wave)) return false;
+    }
 
     for (int tile = 0; tile < live_tiles; ++tile) {
         const int t0 = tile * kTile;
         if (p.checkpoints != nullptr && l.live)
             for (int s = l.lane; s < S; s += L)
                 if (mine(s)) p.checkpoints[((int64_t)l.row * p.tiles + tile) * S + s] = carry[s];
-        bool all_ok = decays;  // of the lane's values in this tile: tame
+        bool all_ok = tame_A;  // of the lane's values in this tile: tame
         if constexpr (FLAGS)
             for (int s = l.lane; s < padded; s += L)
                 if (mine(s)) all_ok &= tame(carry[s], kTameState);
         float skipped[kOwn], dt[K], dtu[K], cut[K], y[K] = {};
         Steps<kOwn, E> z;
-        if (z_row != nullptr) z.load(z_row + t0, end - t0 - own);
+        if (p.z != nullptr) z.load(in_row(p.z, p.z_n, p.z_d, t0), end - t0 - own);
         {
             float u[kOwn], raw[kOwn], own_dt[kOwn], own_dtu[kOwn], own_cut[kOwn];
             next_u.widen(u);
@@ -120,7 +145,7 @@ __global__ __launch_bounds__(kScanThreads, sizeof(E) == 2 && !FLAGS ? 4 : 3) voi
             }
         }
         float dt_sum = 0.f;
-        bool starts = false;
+        bool starts = false, serial = false;
         for (int s0 = 0; s0 < S; s0 += kStates) {
             if (st.active) stage(tiles[buffer][st.c][st.s], next_stage, st.lane);
             if constexpr (FLAGS) {
@@ -144,12 +169,13 @@ __global__ __launch_bounds__(kScanThreads, sizeof(E) == 2 && !FLAGS ? 4 : 3) voi
                     if constexpr (FLAGS) starts |= cut[k] != 0.f;
                 }
                 if constexpr (FLAGS) all_ok = whole_wave(all_ok && steps_tame(dt, dtu));
+                if constexpr (GROW) serial = growth.too_much<L>(dt);
             }
             const TileRow<L> *B_tile = tiles[buffer][0], *C_tile = tiles[buffer][1];
             const int count = S - s0 < kStates ? S - s0 : kStates;
-            const auto scan_states = [&](auto careful) {
+            const auto scan_states = [&](auto careful, int most) {
                 constexpr bool CUT = decltype(careful)::value;
-                for (int i = 2 * part; i < count; i += 2 * SPLIT) {
+                for (int i = 2 * part; i < most; i += 2 * SPLIT) {
                     float a[2][K], b[2][K], h[2], prod[2], enter[2];
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
@@ -186,16 +212,45 @@ __global__ __launch_bounds__(kScanThreads, sizeof(E) == 2 && !FLAGS ? 4 : 3) voi
                     }
                 }
             };
+            const auto scan_serially = [&](int most) {
+#pragma unroll 1
+                for (int i = 0; i < most; ++i) {
+                    if (!mine(s0 + i)) continue;
+                    const int at = s0 + i;
+                    const float a2 = A2[at];
+                    float v[K];
+                    read_tile(B_tile[i], l.lane, v);
+#pragma unroll
+                    for (int k = 0; k < K; ++k) v[k] *= dtu[k];
+                    float h = serial_enter<FLAGS, L>(dt, cut, v, a2, carry[at], l.lane);
+                    float c[K];
+                    read_tile(C_tile[i], l.lane, c);
+#pragma unroll
+                    for (int k = 0; k < K; ++k) {
+                        h = serial_pass<FLAGS>(dt[k], cut[k], a2, h) + v[k];
+                        y[k] = fmaf(c[k], h, y[k]);
+                    }
+                    if constexpr (L > 1)
+                        carry[at] = row_last<false, L>(h);
+                    else
+                        carry[at] = h;
+                }
+            };
+            bool plain = true;
             if constexpr (FLAGS) {
                 uint32_t staged = 1u;
 #pragma unroll
                 for (int w = 0; w < kScanWaves; ++w) staged &= stage_tame[buffer][w];
-                if (all_ok && __builtin_amdgcn_readfirstlane(staged) != 0u)
-                    scan_states(std::false_type{});
-                else
-                    scan_states(std::true_type{});
-            } else {
-                scan_states(std::false_type{});
+                plain = all_ok && __builtin_amdgcn_readfirstlane(staged) != 0u;
+            }
+            if constexpr (GROW) {  // loops in turn: fewer registers than a choice
+                plain = plain && !serial;
+                scan_serially(plain ? 0 : count);
+                scan_states(std::false_type{}, plain ? count : 0);
+            } else if (!FLAGS || plain) {
+                scan_states(std::false_type{}, count);
+            } else if constexpr (FLAGS) {
+                scan_states(std::true_type{}, count);
             }
             buffer ^= 1;
         }
@@ -218,7 +273,7 @@ __global__ __launch_bounds__(kScanThreads, sizeof(E) == 2 && !FLAGS ? 4 : 3) voi
         }
         const int t = t0 + own;
         if (l.live && t < p.T) {
-            if (z_row != nullptr) {
+            if (p.z != nullptr) {
                 float gate[kOwn];
                 z.widen(gate);
 #pragma unroll
@@ -227,19 +282,40 @@ __global__ __launch_bounds__(kScanThreads, sizeof(E) == 2 && !FLAGS ? 4 : 3) voi
             if (t + kOwn > end)  // few lanes
 #pragma unroll
                 for (int k = 0; k < kOwn; ++k) out[k] = t + k < end ? out[k] : 0.f;
-            store_steps<kOwn>(y_row + t0, p.T - t, out);
+            store_steps<kOwn>(out_row(p.y, t0), p.T - t, out);
         }
     }
-    if (!l.live) return;
+    if (!l.live) return true;
     for (int t0 = live_tiles * kTile; t0 + own < p.T; t0 += kTile) {
         const float zeros[kOwn] = {};
-        store_steps<kOwn>(y_row + t0, p.T - t0 - own, zeros);
+        store_steps<kOwn>(out_row(p.y, t0), p.T - t0 - own, zeros);
     }
     if (p.final_state != nullptr) {
         const bool over = FLAGS && p.after_done != 0 && end > 0 && flags[end - 1] != 0;
         for (int s = l.lane; s < S; s += L)
             if (mine(s)) p.final_state[(int64_t)l.row * S + s] = over ? 0.f : carry[s];
     }
+    return true;
+}
+
+// GIVEN: steps without softplus, which may be below 0.
+template <typename E, bool FLAGS, int SPLIT, int L, bool GIVEN>
+__global__ __launch_bounds__(kScanThreads, sizeof(E) == 2 && !FLAGS ? 4 : 3) void selective_scan(
+    ScanParams p) {
+    extern __shared__ __attribute__((aligned(16))) char lds_bytes[];
+    __shared__ TileRow<L> tiles[2][2][states_of(L)];  // [buffer][B, C][state]
+    __shared__ float steps[kScanWaves / SPLIT][SPLIT > 1 ? (FLAGS ? 3 : 2) * kScanK : 1][kWave];
+    __shared__ float sums[SPLIT > 1 ? kScanWaves : 1][SPLIT > 1 ? kScanK : 1][kWave];
+    __shared__ uint32_t steady_waves[kScanWaves];
+    __shared__ uint32_t stage_tame[2][kScanWaves];  // [buffer]: whether what a wave staged is
+    if constexpr (GIVEN)
+        scan_rows<E, FLAGS, SPLIT, L, true>(p, threadIdx.x, lds_bytes, tiles, steps, sums,
+                                            steady_waves, stage_tame);
+    else if (!scan_rows<E, FLAGS, SPLIT, L, false>(p, threadIdx.x, lds_bytes, tiles, steps, sums,
+                                                   steady_waves, stage_tame))
+        scan_rows<E, FLAGS, SPLIT, L, true>(arguments_again<ScanParams>(), here(threadIdx.x),
+                                            lds_bytes, tiles, steps, sums, steady_waves,
+                                            stage_tame);
 }
 
 // ------------------------------------------------------------------- host side
@@ -327,18 +403,21 @@ static int split_of(const rlca_scan_call &c) {
 }
 
 template <typename E, int SPLIT, int L>
-static const void *scan_kernel(bool flags) {
-    return flags ? (const void *)selective_scan<E, true, SPLIT, L>
-                 : (const void *)selective_scan<E, false, SPLIT, L>;
+static const void *scan_kernel(const rlca_scan_call &c) {
+    const bool flags = c.flags != nullptr, given = c.softplus == 0;
+    return flags ? (given ? (const void *)selective_scan<E, true, SPLIT, L, true>
+                          : (const void *)selective_scan<E, true, SPLIT, L, false>)
+                 : (given ? (const void *)selective_scan<E, false, SPLIT, L, true>
+                          : (const void *)selective_scan<E, false, SPLIT, L, false>);
 }
 
 template <typename E>
-static const void *scan_kernel(bool flags, int split, int lanes) {
-    return lanes == 1   ? scan_kernel<E, 1, 1>(flags)
-           : lanes == 4 ? scan_kernel<E, 1, 4>(flags)
-           : split == 4 ? scan_kernel<E, 4, 16>(flags)
-           : split == 2 ? scan_kernel<E, 2, 16>(flags)
-                        : scan_kernel<E, 1, 16>(flags);
+static const void *scan_kernel(const rlca_scan_call &c, int split, int lanes) {
+    return lanes == 1   ? scan_kernel<E, 1, 1>(c)
+           : lanes == 4 ? scan_kernel<E, 1, 4>(c)
+           : split == 4 ? scan_kernel<E, 4, 16>(c)
+           : split == 2 ? scan_kernel<E, 2, 16>(c)
+                        : scan_kernel<E, 1, 16>(c);
 }
 
 static int64_t checkpoint_values(const rlca_scan_call &c) {
@@ -420,10 +499,9 @@ rlca_status rlca_selective_scan(const rlca_scan_call *call, hipStream_t stream) 
     const int lanes = lanes_of(c), split = lanes == 16 ? split_of(c) : 1;
     const int rows = rows_of(lanes) / split;
     ScanParams p = scan_params(c, rows);
-    const bool flags = c.flags != nullptr;
-    const void *kernel = c.dtype == RLCA_F32    ? scan_kernel<float>(flags, split, lanes)
-                         : c.dtype == RLCA_BF16 ? scan_kernel<__bf16>(flags, split, lanes)
-                                                : scan_kernel<_Float16>(flags, split, lanes);
+    const void *kernel = c.dtype == RLCA_F32    ? scan_kernel<float>(c, split, lanes)
+                         : c.dtype == RLCA_BF16 ? scan_kernel<__bf16>(c, split, lanes)
+                                                : scan_kernel<_Float16>(c, split, lanes);
     return launch(kernel, dim3(p.num_seqs * p.groups * p.blocks_per_group), kScanThreads,
                   2 * rows * pitch_of(c.states, lanes) * 4, p, stream);
 }

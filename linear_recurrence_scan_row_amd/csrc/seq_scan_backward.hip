@@ -100,21 +100,24 @@ __device__ __forceinline__ void row_sum(float (&x)[2]) {
 // A workgroup holds four sets of 64 / L channels, SPLIT waves to each.  Waves of
 // one set take every SPLIT-th pair of states, and prepare and finish 8 / SPLIT
 // of a lane's steps, as in the forward scan.
-template <typename E, bool FLAGS, bool GATE, int SPLIT, int L>
-__global__ __launch_bounds__(kScanThreads *SPLIT, 2) void selective_scan_backward(ScanParams p) {
+//
+// Two bodies, as the forward scan's kernel has.
+template <typename E, bool FLAGS, bool GATE, int SPLIT, int L, bool GROW, int WAVES, int SETS,
+          int BEFORE, int PARTS, int AFTER>
+__device__ __forceinline__ bool scan_rows_back(const ScanParams &p, uint32_t thread,
+                                               char *lds_bytes,
+                                               TileRow<L> (&tiles)[2][2][states_of(L)],
+                                               RowSums<L> (&bc)[kScanWaves][states_of(L)][kWave],
+                                               float (&before)[SETS][BEFORE][kWave],
+                                               float (&after)[PARTS][AFTER][kWave],
+                                               uint32_t (&steady_waves)[WAVES],
+                                               uint32_t (&stage_tame)[2][WAVES]) {
     constexpr int K = kScanK, kSets = kScanWaves, kRows = rows_of(L), kStates = states_of(L);
     constexpr int kTile = tile_of(L), kOwn = K / SPLIT, kThreads = kScanThreads * SPLIT;
-    constexpr int kBefore = FLAGS ? 4 : 3, kAfter = GATE ? 3 : 2;  // values a step that waves share
-    extern __shared__ __attribute__((aligned(16))) char lds_bytes[];
-    __shared__ TileRow<L> tiles[2][2][kStates];  // [buffer][B, C][state]
-    __shared__ RowSums<L> bc[kSets][kStates][kWave];
-    __shared__ float before[SPLIT > 1 ? kSets : 1][SPLIT > 1 ? kBefore * K : 1][kWave];
-    __shared__ float after[SPLIT > 1 ? SPLIT * kSets : 1][SPLIT > 1 ? kAfter * K : 1][kWave];
-    __shared__ uint32_t stage_tame[2][kThreads / kWave];  // [buffer]: whether what a wave staged is
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const int in_wave = threadIdx.x % kWave;
+    const int wave = __builtin_amdgcn_readfirstlane(thread / kWave);
+    const int in_wave = thread % kWave;
     const int set = wave / SPLIT, part = wave % SPLIT;
-    const ScanLane l = scan_lane<L>(p, set * (kWave / L) + in_wave / L, kRows);
+    const ScanLane l = scan_lane<L>(p, thread, set * (kWave / L) + in_wave / L, kRows);
     const int S = (int)p.states, padded = padded_states(S), pitch = pitch_of(S, L);
     // [rows][pitch]: A, the gradient a_t g_t entering the tile from its right,
     // the states entering it from its left, and the sums of grad_A
@@ -127,36 +130,32 @@ __global__ __launch_bounds__(kScanThreads *SPLIT, 2) void selective_scan_backwar
     const int end = l.live ? row_steps : 0;  // a clamped row computes on zeros
     const uint8_t *flags = FLAGS ? p.flags + (int64_t)l.n * p.T : nullptr;
     const bool over = FLAGS && p.after_done != 0 && end > 0 && flags[end - 1] != 0;
-    bool decays = true;
-    for (int s = l.lane; s < padded; s += L)
-        if (mine(s)) {
-            const float x = s >= S ? 0.f : p.A[(int64_t)l.d * S + s];
-            A[s] = x;
-            if constexpr (FLAGS) decays &= x <= 0.f && tame(x, kTameStep);
-            carry[s] = p.grad_final == nullptr || over || !l.live || s >= S
-                           ? 0.f
-                           : p.grad_final[(int64_t)l.row * S + s];
-            grad_A[s] = 0.f;
-        }
     const int own = l.lane * K + part * kOwn;  // the lane's own steps in a tile
-    const E *u_row = static_cast<const E *>(p.u) + l.n * p.u_n + l.d * p.u_d + own;
-    const E *delta_row = static_cast<const E *>(p.delta) + l.n * p.delta_n + l.d * p.delta_d + own;
-    const E *g_row = static_cast<const E *>(p.grad_y) + l.n * p.g_n + l.d * p.g_d + own;
-    const E *z_row = GATE ? static_cast<const E *>(p.z) + l.n * p.z_n + l.d * p.z_d + own : nullptr;
+    // The lane's steps of the tile at t0, in an input or a gradient; where registers are
+    // short the address is formed there and then.
+    constexpr bool kLate = GROW || (GATE && (FLAGS || (L == 4 && sizeof(E) == 4)));
+    constexpr bool kLateOut = kLate || (GATE && L == 4);
+    const auto in_row = [&](const void *x, int64_t by_n, int64_t by_d, int t0) {
+        if constexpr (kLate)
+            return static_cast<const E *>(x) + (l.n * by_n + t0) + (here(l.d) * by_d + here(own));
+        return static_cast<const E *>(x) + l.n * by_n + l.d * by_d + own + t0;
+    };
+    const auto out_row = [&](void *out, int t0) {
+        if constexpr (kLateOut)
+            return static_cast<E *>(out) + t0 + ((int64_t)here(l.row) * p.T + here(own));
+        return static_cast<E *>(out) + (int64_t)l.row * p.T + own + t0;
+    };
     const float bias = p.delta_bias == nullptr ? 0.f : p.delta_bias[l.d];
     const float skip = p.D == nullptr ? 0.f : p.D[l.d];
-    const int64_t out_row = (int64_t)l.row * p.T + own;
-    E *grad_u = static_cast<E *>(p.grad_u) + out_row;
-    E *grad_delta = static_cast<E *>(p.grad_delta) + out_row;
-    E *grad_z = GATE ? static_cast<E *>(p.grad_z) + out_row : nullptr;
     float *partials = p.bc_partials + (int64_t)blockIdx.x * 2 * S * p.tiles * kTile;
     float totals[2] = {0.f, 0.f};  // of grad_D and grad_delta_bias
 
-    const Stager<L, kThreads> st(l.lane, wave);
+    const Stager<L, kThreads> st(l.lane, wave, in_wave);
     const int64_t stage_stride = st.c ? p.C_s : p.B_s;
     const E *stage_row = (st.c ? static_cast<const E *>(p.C) + l.n * p.C_n + l.g * p.C_g
                                : static_cast<const E *>(p.B) + l.n * p.B_n + l.g * p.B_g) +
                          st.s * stage_stride + st.lane * K;
+    const int live_tiles = (row_steps + kTile - 1) / kTile;
     Steps<K, E> next_stage;
     Steps<kOwn, E> u, delta, go, z, next_u, next_delta, next_go, next_z;
     const auto load_stage = [&](int t0, int s0) {
@@ -165,21 +164,12 @@ __global__ __launch_bounds__(kScanThreads *SPLIT, 2) void selective_scan_backwar
                             s0 + st.s < S ? row_steps - t0 - st.lane * K : 0);
     };
     const auto load_tile = [&](int t0) {
-        next_u.load(u_row + t0, end - t0 - own);
-        next_delta.load(delta_row + t0, end - t0 - own);
-        next_go.load(g_row + t0, end - t0 - own);
-        if constexpr (GATE) next_z.load(z_row + t0, end - t0 - own);
+        next_u.load(in_row(p.u, p.u_n, p.u_d, t0), end - t0 - own);
+        next_delta.load(in_row(p.delta, p.delta_n, p.delta_d, t0), end - t0 - own);
+        next_go.load(in_row(p.grad_y, p.g_n, p.g_d, t0), end - t0 - own);
+        if constexpr (GATE) next_z.load(in_row(p.z, p.z_n, p.z_d, t0), end - t0 - own);
     };
 
-    // tiles past the row's steps are zeros, and their sums are not read
-    const int live_tiles = (row_steps + kTile - 1) / kTile;
-    for (int t0 = live_tiles * kTile; l.live && t0 + own < p.T; t0 += kTile) {
-        const float zeros[kOwn] = {};
-        const int n = p.T - t0 - own;
-        store_steps<kOwn>(grad_u + t0, n, zeros);
-        store_steps<kOwn>(grad_delta + t0, n, zeros);
-        if constexpr (GATE) store_steps<kOwn>(grad_z + t0, n, zeros);
-    }
     // Each tile's rows are loaded a tile ahead, where registers allow it.
     constexpr bool kAhead = !GATE || ((sizeof(E) == 2 || SPLIT > 1) && !FLAGS);
     // With both episodes and a gate they are loaded again at a tile's end instead
@@ -191,9 +181,39 @@ __global__ __launch_bounds__(kScanThreads *SPLIT, 2) void selective_scan_backwar
         if constexpr (kAhead) load_tile((live_tiles - 1) * kTile);
     }
 
+    bool tame_A = true;
+    Growth growth;
+    for (int s = l.lane; s < padded; s += L)
+        if (mine(s)) {
+            const float x = s >= S ? 0.f : p.A[(int64_t)l.d * S + s];
+            A[s] = x;
+            growth.add(x * kLog2e);
+            if constexpr (FLAGS) tame_A &= tame(x, kTameStep);
+            carry[s] = p.grad_final == nullptr || over || !l.live || s >= S
+                           ? 0.f
+                           : p.grad_final[(int64_t)l.row * S + s];
+            grad_A[s] = 0.f;
+        }
+    if constexpr (GROW) {
+        growth.meet();
+    } else {
+        // no a above 1 in any tile
+        const bool steady = whole_wave(growth.up == 0.f);
+        if (!all_waves(steady, steady_waves, wave, in_wave)) return false;
+    }
+    // tiles past the row's steps are zeros, and their sums are not read
+    for (int t0 = live_tiles * kTile; l.live && t0 + own < p.T; t0 += kTile) {
+        const float zeros[kOwn] = {};
+        const int n = p.T - t0 - own;
+        store_steps<kOwn>(out_row(p.grad_u, t0), n, zeros);
+        store_steps<kOwn>(out_row(p.grad_delta, t0), n, zeros);
+        if constexpr (GATE) store_steps<kOwn>(out_row(p.grad_z, t0), n, zeros);
+    }
+
+
     for (int tile = live_tiles - 1; tile >= 0; --tile) {
         const int t0 = tile * kTile;
-        bool all_ok = decays;  // of the lane's values in this tile: tame
+        bool all_ok = tame_A;  // of the lane's values in this tile: tame
         if constexpr (!kAhead) load_tile(t0);
         u = next_u;
         delta = next_delta;
@@ -241,7 +261,7 @@ __global__ __launch_bounds__(kScanThreads *SPLIT, 2) void selective_scan_backwar
             }
         }
         float dt_sum = 0.f;
-        bool starts = false;
+        bool starts = false, serial = false;
         for (int s0 = 0; s0 < S; s0 += kStates) {
             const int count = S - s0 < kStates ? S - s0 : kStates;
             if (st.active) stage(tiles[buffer][st.c][st.s], next_stage, st.lane);
@@ -272,11 +292,12 @@ __global__ __launch_bounds__(kScanThreads *SPLIT, 2) void selective_scan_backwar
                     for (int k = 0; k < K; ++k) all_ok &= tame(gy[k], kTameStep);
                     all_ok = whole_wave(all_ok);
                 }
+                if constexpr (GROW) serial = growth.too_much<L>(dt);
             }
             const TileRow<L> *B_tile = tiles[buffer][0], *C_tile = tiles[buffer][1];
-            const auto scan_states = [&](auto careful) {
+            const auto scan_states = [&](auto careful, int most) {
                 constexpr bool CUT = decltype(careful)::value;
-                for (int i = 2 * part; i < count; i += 2 * SPLIT) {
+                for (int i = 2 * part; i < most; i += 2 * SPLIT) {
                     float a[2][K], w[2][K], g[2], prod[2], dA[2];
                     float h[2], prefix[2], enter[2];
 #pragma unroll
@@ -358,16 +379,63 @@ __global__ __launch_bounds__(kScanThreads *SPLIT, 2) void selective_scan_backwar
                         grad_A[s0 + i + j] += L == 16 ? row_last<false, L>(dA[j]) : dA[j];
                 }
             };
+            const auto scan_serially = [&](int most) {
+#pragma unroll 1
+                for (int i = 0; i < most; ++i) {
+                    if (!mine(s0 + i)) continue;
+                    const int at = s0 + i;
+                    const float A_s = A[at], a2 = A_s * kLog2e;
+                    float b[K], c[K], w[K], v[16];
+                    read_tile(B_tile[i], l.lane, b);
+#pragma unroll
+                    for (int k = 0; k < K; ++k) b[k] *= dtu[k];
+                    float h = serial_enter<FLAGS, L>(dt, cut, b, a2, enter_states[at], l.lane);
+                    read_tile(C_tile[i], l.lane, c);
+#pragma unroll
+                    for (int k = 0; k < K; ++k) {
+                        w[k] = serial_pass<FLAGS>(dt[k], cut[k], a2, h);
+                        h = b[k] + w[k];
+                        v[8 + k] = gy[k] * h;
+                        if constexpr (GATE) y[k] = fmaf(c[k], h, y[k]);
+                        c[k] *= gy[k];
+                    }
+                    float g = serial_enter_back<FLAGS, L>(dt, cut, c, a2, carry[at], l.lane);
+                    float dA[2] = {0.f, 0.f};
+                    read_tile(B_tile[i], l.lane, b);
+#pragma unroll
+                    for (int k = K - 1; k >= 0; --k) {
+                        g += c[k];
+                        v[k] = g * dtu[k];
+                        gB[k] = fmaf(g, b[k], gB[k]);
+                        const float q = g * w[k];
+                        dA[0] = fmaf(q, dt[k], dA[0]);
+                        grad_dt[k] = fmaf(q, A_s, grad_dt[k]);
+                        g = serial_pass<FLAGS>(dt[k], cut[k], a2, g);
+                    }
+                    bc[set][i][in_wave] = sum_rows<L>(v, in_wave);
+                    if constexpr (L > 1)
+                        carry[at] = row_last<true, L>(g);
+                    else
+                        carry[at] = g;
+                    row_sum<L>(dA);
+                    grad_A[at] += L == 16 ? row_last<false, L>(dA[0]) : dA[0];
+                }
+            };
+            bool plain = true;
             if constexpr (FLAGS) {
                 uint32_t staged = 1u;
 #pragma unroll
                 for (int w = 0; w < kThreads / kWave; ++w) staged &= stage_tame[buffer][w];
-                if (all_ok && __builtin_amdgcn_readfirstlane(staged) != 0u)
-                    scan_states(std::false_type{});
-                else
-                    scan_states(std::true_type{});
-            } else {
-                scan_states(std::false_type{});
+                plain = all_ok && __builtin_amdgcn_readfirstlane(staged) != 0u;
+            }
+            if constexpr (GROW) {  // loops in turn: fewer registers than a choice
+                plain = plain && !serial;
+                scan_serially(plain ? 0 : count);
+                scan_states(std::false_type{}, plain ? count : 0);
+            } else if (!FLAGS || plain) {
+                scan_states(std::false_type{}, count);
+            } else if constexpr (FLAGS) {
+                scan_states(std::true_type{}, count);
             }
             buffer ^= 1;
             if constexpr (SPLIT > 1) {
@@ -384,7 +452,7 @@ __global__ __launch_bounds__(kScanThreads *SPLIT, 2) void selective_scan_backwar
             if constexpr (L == 16) {
                 // lane x of a wave holds, for state i, half a lane's steps of
                 // grad_B (rows 0 and 1) or grad_C (rows 2 and 3)
-                for (int j = threadIdx.x; j < count * kWave; j += kThreads) {
+                for (int j = thread; j < count * kWave; j += kThreads) {
                     const int i = j / kWave, x = j % kWave, q = x / 16;
                     float4v sum = bc[0][i][x];
 #pragma unroll
@@ -396,7 +464,7 @@ __global__ __launch_bounds__(kScanThreads *SPLIT, 2) void selective_scan_backwar
             } else {
                 // lane x holds value x / 4 of its place in the row (L = 4), or
                 // of the row (L = 1)
-                for (int j = threadIdx.x; j < count * 2 * kTile; j += kThreads) {
+                for (int j = thread; j < count * 2 * kTile; j += kThreads) {
                     const int i = j / (2 * kTile), which = j / kTile % 2, t = j % kTile;
                     const int x = (which * 8 + t % K) * 4 + t / K;
                     float sum = bc[0][i][x];
@@ -451,7 +519,7 @@ __global__ __launch_bounds__(kScanThreads *SPLIT, 2) void selective_scan_backwar
                 if (t + kOwn > end)  // few lanes
 #pragma unroll
                     for (int k = 0; k < kOwn; ++k) out_z[k] = t + k < end ? out_z[k] : 0.f;
-                store_steps<kOwn>(grad_z + t0, p.T - t, out_z);
+                store_steps<kOwn>(out_row(p.grad_z, t0), p.T - t, out_z);
             }
 #pragma unroll
             for (int k = 0; k < kOwn; ++k) {
@@ -480,8 +548,8 @@ __global__ __launch_bounds__(kScanThreads *SPLIT, 2) void selective_scan_backwar
                 totals[0] = fmaf(own_gy[k], own_u[k], totals[0]);
                 totals[1] += out_delta[k];
             }
-            store_steps<kOwn>(grad_u + t0, p.T - t, out_u);
-            store_steps<kOwn>(grad_delta + t0, p.T - t, out_delta);
+            store_steps<kOwn>(out_row(p.grad_u, t0), p.T - t, out_u);
+            store_steps<kOwn>(out_row(p.grad_delta, t0), p.T - t, out_delta);
         }
     }
     row_sum<L>(totals);
@@ -499,7 +567,7 @@ __global__ __launch_bounds__(kScanThreads *SPLIT, 2) void selective_scan_backwar
                 for (int m = 0; m < SPLIT; ++m) totals[q] += after[set * SPLIT + m][q][in_wave];
             }
     }
-    if (!l.live) return;
+    if (!l.live) return true;
     float *out = p.row_partials + (int64_t)l.row * (S + 2);
     for (int s = l.lane; s < S; s += L)
         if (mine(s)) {
@@ -510,6 +578,29 @@ __global__ __launch_bounds__(kScanThreads *SPLIT, 2) void selective_scan_backwar
         out[S] = totals[0];
         out[S + 1] = totals[1];
     }
+    return true;
+}
+
+// GIVEN: steps without softplus, which may be below 0.
+template <typename E, bool FLAGS, bool GATE, int SPLIT, int L, bool GIVEN>
+__global__ __launch_bounds__(kScanThreads *SPLIT, 2) void selective_scan_backward(ScanParams p) {
+    extern __shared__ __attribute__((aligned(16))) char lds_bytes[];
+    constexpr int kWaves = kScanWaves * SPLIT;
+    constexpr int kBefore = FLAGS ? 4 : 3, kAfter = GATE ? 3 : 2;  // values a step that waves share
+    __shared__ TileRow<L> tiles[2][2][states_of(L)];  // [buffer][B, C][state]
+    __shared__ RowSums<L> bc[kScanWaves][states_of(L)][kWave];
+    __shared__ float before[SPLIT > 1 ? kScanWaves : 1][SPLIT > 1 ? kBefore * kScanK : 1][kWave];
+    __shared__ float after[SPLIT > 1 ? kWaves : 1][SPLIT > 1 ? kAfter * kScanK : 1][kWave];
+    __shared__ uint32_t steady_waves[kWaves];
+    __shared__ uint32_t stage_tame[2][kWaves];  // [buffer]: whether what a wave staged is
+    if constexpr (GIVEN)
+        scan_rows_back<E, FLAGS, GATE, SPLIT, L, true>(p, threadIdx.x, lds_bytes, tiles, bc, before,
+                                                       after, steady_waves, stage_tame);
+    else if (!scan_rows_back<E, FLAGS, GATE, SPLIT, L, false>(
+                 p, threadIdx.x, lds_bytes, tiles, bc, before, after, steady_waves, stage_tame))
+        scan_rows_back<E, FLAGS, GATE, SPLIT, L, true>(
+            arguments_again<ScanParams>(), here(threadIdx.x), lds_bytes, tiles, bc, before, after,
+            steady_waves, stage_tame);
 }
 
 // grad_B and grad_C: the sum of a group's workgroups, in order, 4 steps a lane.
@@ -640,13 +731,19 @@ static Workspace workspace_of(const rlca_scan_call &c) {
             (size_t)(2 * ranges_of(c.num_seqs).count * c.channels * (c.states + 2))};
 }
 
-template <typename E, int SPLIT, int L>
+template <typename E, int SPLIT, int L, bool GIVEN>
 static const void *backward_kernel(const rlca_scan_call &c) {
     const bool flags = c.flags != nullptr, gate = c.z != nullptr;
-    return flags ? (gate ? (const void *)selective_scan_backward<E, true, true, SPLIT, L>
-                         : (const void *)selective_scan_backward<E, true, false, SPLIT, L>)
-                 : (gate ? (const void *)selective_scan_backward<E, false, true, SPLIT, L>
-                         : (const void *)selective_scan_backward<E, false, false, SPLIT, L>);
+    return flags ? (gate ? (const void *)selective_scan_backward<E, true, true, SPLIT, L, GIVEN>
+                         : (const void *)selective_scan_backward<E, true, false, SPLIT, L, GIVEN>)
+                 : (gate ? (const void *)selective_scan_backward<E, false, true, SPLIT, L, GIVEN>
+                         : (const void *)selective_scan_backward<E, false, false, SPLIT, L, GIVEN>);
+}
+
+template <typename E, int SPLIT, int L>
+static const void *backward_kernel(const rlca_scan_call &c) {
+    return c.softplus == 0 ? backward_kernel<E, SPLIT, L, true>(c)
+                           : backward_kernel<E, SPLIT, L, false>(c);
 }
 
 template <typename E>

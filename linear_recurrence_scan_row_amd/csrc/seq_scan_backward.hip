@@ -79,13 +79,14 @@ template <int L>
 __device__ __forceinline__ void row_sum(float (&x)[2]) {
     if constexpr (L == 16) {
         // the two take turns, and one idle instruction keeps the required two
-        // between a write and the lane-crossing read of it
+        // between a write and the lane-crossing read of it; one more at the end
+        // does so for whatever reads the sums next, which the compiler does not know
 #define RLCA_STEP(SHIFT)                                                  \
     "v_add_f32_dpp %0, %0, %0 " SHIFT " row_mask:0xf bank_mask:0xf\n\t"   \
     "v_add_f32_dpp %1, %1, %1 " SHIFT " row_mask:0xf bank_mask:0xf\n\t"   \
     "s_nop 0\n\t"
         asm("s_nop 1\n\t" RLCA_STEP("row_shr:1") RLCA_STEP("row_shr:2") RLCA_STEP("row_shr:4")
-                RLCA_STEP("row_shr:8")
+                RLCA_STEP("row_shr:8") "s_nop 0"
             : "+v"(x[0]), "+v"(x[1]));
 #undef RLCA_STEP
     } else if constexpr (L == 4) {

@@ -63,7 +63,8 @@ template <typename E, int W, int VEC>
 __global__ __launch_bounds__(kStepThreads) void causal_conv_step(ConvStepParams p) {
     const uint32_t d = (blockIdx.x * blockDim.x + threadIdx.x) * VEC;
     if (d >= p.channels) return;
-    const int left = (int)(p.channels - d);  // VEC or more: a whole block
+    // the thread's channels: times the taps, the channels left would pass 32 bits
+    const int left = p.channels - d < (uint32_t)VEC ? (int)(p.channels - d) : VEC;
     ConvStepLoads<E, W, VEC> next;
     next.load(p, blockIdx.y, d, left);
     float w[W][VEC], bias[VEC] = {};

@@ -170,7 +170,9 @@ __global__ __launch_bounds__(kStepThreads, 8) void selective_step(ScanStepParams
             now.c.widen(out);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                h[k] = fmaf(exp2_fast(dt * a[k] * kLog2e), h[k], dt * u * in[k]);
+                const float x = dt * a[k] * kLog2e, b = dt * u * in[k];
+                // a growth beyond float32's range leaves a state of 0 at 0
+                h[k] = x < 100.f ? fmaf(exp2_fast(x), h[k], b) : times_exp2(h[k], x) + b;
                 if (s + k < S) y = fmaf(out[k], h[k], y);
             }
             store_steps<4>(p.state + (now.place * p.channels + d) * S + s, S - s, h);

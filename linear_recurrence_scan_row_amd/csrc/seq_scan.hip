@@ -184,12 +184,12 @@ __device__ __forceinline__ bool scan_rows(const ScanParams &p, uint32_t thread,
                         read_tile(B_tile[i + j], l.lane, b[j]);
 #pragma unroll
                         for (int k = 0; k < K; ++k) {
-                            a[j][k] = decay<FLAGS>(dt[k], cut[k], a2);
+                            a[j][k] = decay<FLAGS, CUT>(dt[k], cut[k], a2);
                             b[j][k] *= dtu[k];
                             if constexpr (L > 1)
                                 h[j] = k == 0 ? b[j][0] : step_map<CUT>(a[j][k], b[j][k], h[j]);
                         }
-                        if constexpr (L > 1) prod[j] = lane_product<FLAGS>(dt_sum, starts, a2);
+                        if constexpr (L > 1) prod[j] = lane_product<FLAGS, CUT>(dt_sum, starts, a2);
                     }
                     if constexpr (L > 1) row_scan<CUT, false, L>(prod, h, l.lane);
 #pragma unroll

@@ -89,7 +89,7 @@ __device__ __forceinline__ ScanLane scan_lane(const ScanParams &p, uint32_t thre
 
 // How a wave computes a tile's states:
 //   * plain: fused steps and the lane scan;
-//   * with cuts: the same, with every 0 of a selected (rows with episode starts
+//   * with cuts: the same, with every start selected (rows with episode starts
 //     whose values are not all tame);
 //   * serially, where states may grow (A above 0, or steps below 0 without
 //     softplus).  The product of a tile's a's may be infinite there while the states
@@ -124,21 +124,30 @@ __device__ __forceinline__ Params arguments_again() {
 }
 
 // One map: a later run's (a, h) after an earlier run's (pa, ph).  CUT: the
-// runs may hold episode starts, where a is 0 and whatever lies before, a NaN
-// or infinity too, must not pass, so the product is selected away (as in
-// apply_map and compose of scan_core.hpp).  Otherwise a plain fused step, which
-// is enough for rows with starts too while all values are tame (below): 0
-// times a finite number is 0.  For finite values both give the same bits.
+// runs may hold episode starts, where whatever lies before, a NaN or infinity too,
+// must not pass, so the product is selected away.  A start's a is -0; an a that has
+// underflowed is 0 and starts nothing: 0 times a NaN stays one.  Otherwise a plain
+// fused step, which is enough for rows with starts too while all values are tame
+// (below): 0 times a finite number is 0.  For finite values both give the same bits.
+__device__ __forceinline__ bool is_cut(float a) { return as_bits(a) == as_bits(-0.f); }
+
 template <bool CUT>
 __device__ __forceinline__ float step_map(float a, float b, float h) {
-    if constexpr (CUT) return a == 0.f ? b : fmaf(a, h, b);
+    if constexpr (CUT) return is_cut(a) ? b : fmaf(a, h, b);
     return fmaf(a, h, b);
 }
 
+// What passes of a state or gradient, and the product of two runs' a's.
 template <bool CUT>
-__device__ __forceinline__ float product(float a, float b) {
-    if constexpr (CUT) return a == 0.f ? 0.f : a * b;
-    return a * b;
+__device__ __forceinline__ float pass(float a, float h) {
+    if constexpr (CUT) return is_cut(a) ? 0.f : a * h;
+    return a * h;
+}
+
+template <bool CUT>
+__device__ __forceinline__ float product(float a, float pa) {
+    if constexpr (CUT) return is_cut(a) || is_cut(pa) ? -0.f : a * pa;
+    return a * pa;
 }
 
 // The lane-crossing moves of a row: STEP lanes on in scan order (REVERSE: towards
@@ -406,18 +415,20 @@ __device__ __forceinline__ void make_steps(const ScanParams &p, const uint8_t *f
     }
 }
 
-// The product of a lane's a's for one state: exp(A sum dt), or 0 where an
-// episode starts in the lane, whatever the steps before the start hold.
-template <bool FLAGS>
+// The product of a lane's a's for one state: exp(A sum dt), or a start's 0 (-0 with
+// CUT) where an episode starts in the lane, whatever the steps before the start hold.
+template <bool FLAGS, bool CUT>
 __device__ __forceinline__ float lane_product(float dt_sum, bool starts, float A2) {
     const float a = exp2_fast(dt_sum * A2);
-    return FLAGS && starts ? 0.f : a;
+    return FLAGS && starts ? (CUT ? -0.f : 0.f) : a;
 }
 
-// a_k of a lane's steps for one state, A2 = A log2(e).
-template <bool FLAGS>
+// a_k of a lane's steps for one state, A2 = A log2(e); at a start 0, or -0 with CUT
+// (cut's sign).
+template <bool FLAGS, bool CUT>
 __device__ __forceinline__ float decay(float dt, float cut, float A2) {
-    return exp2_fast(FLAGS ? fmaf(dt, A2, cut) : dt * A2);
+    const float a = exp2_fast(FLAGS ? fmaf(dt, A2, cut) : dt * A2);
+    return CUT ? from_bits<float>(as_bits(a) | (as_bits(cut) & (int)0x80000000)) : a;
 }
 
 // Tame values: too small for any state, gradient or product of the scans to

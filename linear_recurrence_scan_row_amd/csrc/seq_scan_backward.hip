@@ -309,14 +309,14 @@ __device__ __forceinline__ bool scan_rows_back(const ScanParams &p, uint32_t thr
                         if constexpr (L > 1) read_tile(B_tile[i + j], l.lane, b);
 #pragma unroll
                         for (int k = 0; k < K; ++k) {
-                            a[j][k] = decay<FLAGS>(dt[k], cut[k], a2);
+                            a[j][k] = decay<FLAGS, CUT>(dt[k], cut[k], a2);
                             if constexpr (L > 1) {
                                 const float x = b[k] * dtu[k];
                                 h[j] = k == 0 ? x : step_map<CUT>(a[j][k], x, h[j]);
                             }
                         }
                         if constexpr (L > 1)
-                            prefix[j] = prod[j] = lane_product<FLAGS>(dt_sum, starts, a2);
+                            prefix[j] = prod[j] = lane_product<FLAGS, CUT>(dt_sum, starts, a2);
                     }
                     if constexpr (L > 1) row_scan<CUT, false, L>(prefix, h, l.lane);
                     float v[2][16], r[2], c[2][K];
@@ -332,7 +332,7 @@ __device__ __forceinline__ bool scan_rows_back(const ScanParams &p, uint32_t thr
                         read_tile(C_tile[i + j], l.lane, c[j]);
 #pragma unroll
                         for (int k = 0; k < K; ++k) {
-                            w[j][k] = product<CUT>(a[j][k], h[j]);
+                            w[j][k] = pass<CUT>(a[j][k], h[j]);
                             h[j] = fmaf(b[k], dtu[k], w[j][k]);
                             v[j][8 + k] = gy[k] * h[j];
                             if constexpr (GATE) y[k] = fmaf(c[j][k], h[j], y[k]);
@@ -343,7 +343,7 @@ __device__ __forceinline__ bool scan_rows_back(const ScanParams &p, uint32_t thr
 #pragma unroll
                             for (int k = K - 2; k >= 0; --k)
                                 g[j] = step_map<CUT>(a[j][k + 1], c[j][k], g[j]);
-                            r[j] = product<CUT>(a[j][0], g[j]);
+                            r[j] = pass<CUT>(a[j][0], g[j]);
                         }
                     }
                     if constexpr (L > 1) row_scan<CUT, true, L>(prod, r, l.lane);
@@ -371,7 +371,7 @@ __device__ __forceinline__ bool scan_rows_back(const ScanParams &p, uint32_t thr
                             dA[j] = fmaf(q, dt[k], dA[j]);  // at a start w is 0, and dt put to 0
                             grad_dt[k] = fmaf(q, A_s, grad_dt[k]);
                         }
-                        if constexpr (L == 1) carry[s0 + i + j] = product<CUT>(a[j][0], g[j]);
+                        if constexpr (L == 1) carry[s0 + i + j] = pass<CUT>(a[j][0], g[j]);
                         bc[set][i + j][in_wave] = sum_rows<L>(v[j], in_wave);
                     }
                     row_sum<L>(dA);

@@ -423,7 +423,9 @@ rlca_status rlca_ppo_clip_loss(const float *advantages, const double *stats,
  * Sizes:    num_seqs * channels < 2^31 and T <= RLCA_MAX_T; a call with
  *           num_seqs, channels or T of 0 is a valid no-op where it has no
  *           state to hand on; with T = 0 the final state is the state, and
- *           the gradients of an empty sum are 0.  A call whose launch would
+ *           the gradients of an empty sum are 0.  With channels = 0 nothing is
+ *           launched or written: grad_B and grad_C, sums over no channels, are
+ *           the caller's to clear.  A call whose launch would
  *           hold 2^32 threads is refused as too large: the scan over rows
  *           takes num_seqs * groups * ceil(channels / groups / 4) < 2^24, the
  *           convolution over rows channels < 2^24 (more if rows are short),

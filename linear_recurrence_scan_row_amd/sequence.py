@@ -413,10 +413,16 @@ def selective_scan_backward(grad_y, u, delta, A, B, C, checkpoints, D=None, z=No
     n = lib().rlca_selective_scan_checkpoints_size(_pack_scan(*fields, *(0,) * 16)) // 4
     c = _dense_in("checkpoints", checkpoints, (n,), torch.float32, dev)
     f32 = torch.float32
+
+    def shared():
+        # without channels the library writes nothing: sums of no terms
+        if channels == 0:
+            return torch.zeros(N, G, S, T, dtype=dtype, device=dev)
+        return _new(None, (N, G, S, T), dtype, dev)
+
     grads = ScanGrads(
         u=_new(None, shape, dtype, dev), delta=_new(None, shape, dtype, dev),
-        A=_new(None, (channels, S), f32, dev), B=_new(None, (N, G, S, T), dtype, dev),
-        C=_new(None, (N, G, S, T), dtype, dev),
+        A=_new(None, (channels, S), f32, dev), B=shared(), C=shared(),
         D=None if D is None else _new(None, (channels,), f32, dev),
         z=None if z is None else _new(None, shape, dtype, dev),
         delta_bias=None if delta_bias is None else _new(None, (channels,), f32, dev),

@@ -133,21 +133,35 @@ __global__ __launch_bounds__(kThreads) void grad_norm(Launch l) {
     });
 }
 
+// A value times the scale, which is rounded to fp32 once.  Where fp32 would hold it
+// with fewer digits, or as 0 (a norm of 1e38 and more times max_norm: large gradients
+// that come out in range all the same), the product is taken in fp64.
+struct Scale {
+    double exact;
+    float rounded;
+    __device__ __forceinline__ explicit Scale(double s) : exact(s), rounded((float)s) {}
+    __device__ __forceinline__ bool wide() const { return exact > 0.0 && exact < 0x1p-126; }
+};
+
 template <typename E>
-__device__ __forceinline__ void scale_chunk(const Tensor &t, uint32_t chunk, float scale) {
+__device__ __forceinline__ void scale_chunk(const Tensor &t, uint32_t chunk, const Scale &scale) {
     for_blocks<E>(t, chunk, [&](float(&v)[Blocks<E>::kElems], uint64_t at, int n) {
+        if (scale.wide())
 #pragma unroll
-        for (int k = 0; k < Blocks<E>::kElems; ++k) v[k] *= scale;
+            for (int k = 0; k < Blocks<E>::kElems; ++k) v[k] = (float)((double)v[k] * scale.exact);
+        else
+#pragma unroll
+            for (int k = 0; k < Blocks<E>::kElems; ++k) v[k] *= scale.rounded;
         seq::store_steps<Blocks<E>::kElems>(static_cast<E *>(t.out) + at, n, v);
     });
 }
 
 __global__ __launch_bounds__(kThreads) void grad_scale(Launch l) {
-    const float scale = (float)load_coherent(&l.head->scale);
+    const Scale scale(load_coherent(&l.head->scale));
     for (uint32_t i = blockIdx.x; i < l.chunks; i += gridDim.x) {
         const uint32_t c = l.chunks - 1 - i;
         const Tensor &t = l.tensors[tensor_of(l, c)];
-        if (scale == 1.f && t.out == t.data) continue;  // nothing changes
+        if (scale.rounded == 1.f && t.out == t.data) continue;  // nothing changes
         const uint32_t chunk = c - t.first_chunk;
         if (t.dtype == RLCA_F32)
             scale_chunk<float>(t, chunk, scale);

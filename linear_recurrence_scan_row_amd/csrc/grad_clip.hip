@@ -10,8 +10,6 @@
 // The tensors' addresses travel as kernel arguments, so nothing is copied to the
 // device; one launch takes up to kMaxTensors tensors as a list of chunks of
 // kChunk elements, so many small tensors fill the chip like one large one.
-#include <stdlib.h>
-
 #include <algorithm>
 
 #include "kernels.hpp"
@@ -175,59 +173,87 @@ __global__ __launch_bounds__(kThreads) void grad_scale(Launch l) {
 // ------------------------------------------------------------------- host side
 struct Range {
     uintptr_t begin, end;
+    uint32_t id;  // of the call's ranges, for an order among equal addresses
     bool written;
+    bool operator<(const Range &o) const {
+        return begin != o.begin ? begin < o.begin : id < o.id;
+    }
 };
 
-// No written range may overlap another range: one pass over them in order.
-static bool disjoint(Range *r, size_t n) {
-    std::sort(r, r + n, [](const Range &a, const Range &b) { return a.begin < b.begin; });
-    uintptr_t any = 0, written = 0;  // the ends of the ranges so far
-    for (size_t i = 0; i < n; ++i) {
-        if (r[i].begin < (r[i].written ? any : written)) return false;
-        any = std::max(any, r[i].end);
-        if (r[i].written) written = std::max(written, r[i].end);
+// The call's ranges in order of their addresses, kAtOnce at a time: the smallest of
+// those after the last batch's, kept in a heap on the stack (each batch goes over all
+// ranges again, and the host allocates nothing).
+class Ordered {
+  public:
+    // Whether the sweep so far has met an overlap of a written range.
+    bool overlap() const { return overlap_; }
+    // Offers one of the call's ranges to the batch.
+    void offer(const Range &r) {
+        if (started_ && !(last_ < r)) return;
+        if (count_ < kAtOnce) {
+            batch_[count_++] = r;
+            if (count_ == kAtOnce) std::make_heap(batch_, batch_ + kAtOnce);
+        } else if (r < batch_[0]) {
+            std::pop_heap(batch_, batch_ + kAtOnce);
+            batch_[kAtOnce - 1] = r;
+            std::push_heap(batch_, batch_ + kAtOnce);
+        }
     }
-    return true;
-}
+    // Sweeps the batch; false: it was the last.
+    bool sweep() {
+        std::sort(batch_, batch_ + count_);
+        for (size_t i = 0; i < count_; ++i) {
+            const Range &r = batch_[i];
+            if (r.begin < (r.written ? any_ : written_)) overlap_ = true;
+            any_ = std::max(any_, r.end);
+            if (r.written) written_ = std::max(written_, r.end);
+        }
+        const bool more = count_ == kAtOnce;
+        if (more) last_ = batch_[kAtOnce - 1];
+        started_ = true;
+        count_ = 0;
+        return more;
+    }
+
+  private:
+    static constexpr size_t kAtOnce = 2048;  // 48 KB
+    Range batch_[kAtOnce];
+    size_t count_ = 0;
+    Range last_ = {};
+    bool started_ = false, overlap_ = false;
+    uintptr_t any_ = 0, written_ = 0;  // the ends of the ranges so far
+};
 
 static rlca_status check_tensors(const rlca_grad_tensor *tensors, int64_t n, bool scaled,
                                  double *norm, void *workspace) {
-    constexpr int64_t kOnStack = 256;
-    Range local[2 * kOnStack + 2], *ranges = local;
-    if (n > kOnStack) {
-        ranges = static_cast<Range *>(malloc((2 * (size_t)n + 2) * sizeof(Range)));
-        if (ranges == nullptr) return RLCA_ERR_INVALID_SIZE;
-    }
-    size_t count = 0;
-    rlca_status st = RLCA_OK;
-    for (int64_t i = 0; i < n && st == RLCA_OK; ++i) {
+    for (int64_t i = 0; i < n; ++i) {
         const rlca_grad_tensor &t = tensors[i];
         const size_t e = seq::element_bytes(t.dtype);
-        if (t.count < 0 || t.count >= (int64_t)1 << 43)
-            st = RLCA_ERR_INVALID_SIZE;
-        else if (e == 0)
-            st = RLCA_ERR_INVALID_VALUE;
-        else if (t.count == 0)
-            continue;
-        else if (t.data == nullptr || (scaled && t.out == nullptr))
-            st = RLCA_ERR_NULL_POINTER;
-        else if ((uintptr_t)t.data % e != 0 || (scaled && (uintptr_t)t.out % e != 0))
-            st = RLCA_ERR_MISALIGNED;
-        else {
-            const size_t bytes = (size_t)t.count * e;
+        if (t.count < 0 || t.count >= (int64_t)1 << 43) return RLCA_ERR_INVALID_SIZE;
+        if (e == 0) return RLCA_ERR_INVALID_VALUE;
+        if (t.count == 0) continue;
+        if (t.data == nullptr || (scaled && t.out == nullptr)) return RLCA_ERR_NULL_POINTER;
+        if ((uintptr_t)t.data % e != 0 || (scaled && (uintptr_t)t.out % e != 0))
+            return RLCA_ERR_MISALIGNED;
+    }
+    // no written range may overlap another range
+    Ordered ranges;
+    const uint32_t ends = 2 * (uint32_t)n;
+    do {
+        for (int64_t i = 0; i < n; ++i) {
+            const rlca_grad_tensor &t = tensors[i];
+            if (t.count == 0) continue;
+            const size_t bytes = (size_t)t.count * seq::element_bytes(t.dtype);
             const uintptr_t data = (uintptr_t)t.data, out = (uintptr_t)t.out;
-            ranges[count++] = {data, data + bytes, scaled && out == data};
-            if (scaled && out != data) ranges[count++] = {out, out + bytes, true};
+            ranges.offer({data, data + bytes, 2 * (uint32_t)i, scaled && out == data});
+            if (scaled && out != data)
+                ranges.offer({out, out + bytes, 2 * (uint32_t)i + 1, true});
         }
-    }
-    if (st == RLCA_OK) {
-        ranges[count++] = {(uintptr_t)norm, (uintptr_t)norm + 8, true};
-        ranges[count++] = {(uintptr_t)workspace, (uintptr_t)workspace + RLCA_CLIP_WORKSPACE_BYTES,
-                           true};
-        if (!disjoint(ranges, count)) st = RLCA_ERR_ALIASING;
-    }
-    if (ranges != local) free(ranges);
-    return st;
+        ranges.offer({(uintptr_t)norm, (uintptr_t)norm + 8, ends, true});
+        ranges.offer({(uintptr_t)workspace, (uintptr_t)workspace + RLCA_CLIP_WORKSPACE_BYTES,
+                      ends + 1, true});
+    } while (ranges.sweep() && !ranges.overlap());
+    return ranges.overlap() ? RLCA_ERR_ALIASING : RLCA_OK;
 }
 
 // Fills `l` with a launch's worth of the tensors in [*begin, *end), from the

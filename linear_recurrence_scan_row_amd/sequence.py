@@ -499,18 +499,24 @@ def clip_grad_norm(grads, max_norm, eps=1e-6, out=None, norm=None):
     """Scale gradients to a global 2-norm of at most max_norm: every tensor
     times min(1, max_norm / (norm + eps)), in place or, with `out` (a list of
     tensors like `grads`), into those.  The tensors (float32, bfloat16 or
-    float16, mixed freely, dense in memory) count as one vector.  Returns the
-    norm before the scaling, a float64 tensor [1] on the device; nothing
-    synchronizes.  max_norm = inf computes the norm only."""
-    grads = list(grads)
+    float16, mixed freely, dense in memory) count as one vector; None, the
+    gradient of a parameter that has none, is left out.  Returns the norm before
+    the scaling, a float64 tensor [1] on the device; nothing synchronizes.
+    max_norm = inf computes the norm only."""
+    given = list(grads)
+    outs = None if out is None else list(out)
+    if outs is not None and len(outs) != len(given):
+        raise ValueError(f"out has {len(outs)} tensors, expected {len(given)}")
+    grads = [g for g in given if g is not None]
+    if outs is not None and len(grads) != len(given):
+        if any((g is None) != (o is None) for g, o in zip(given, outs)):
+            raise ValueError("out must be None where grads is, and only there")
+        outs = [o for o in outs if o is not None]
     if not grads:
         raise ValueError("grads is empty")
     dev = grads[0].device
     if dev.type != "cuda":
         raise ValueError("inputs must be GPU tensors")
-    outs = grads if out is None else list(out)
-    if len(outs) != len(grads):
-        raise ValueError(f"out has {len(outs)} tensors, expected {len(grads)}")
     # Properties of all tensors at once, the checks over those lists; a loop
     # names the tensor that fails one.
     tensor = torch.Tensor
@@ -524,7 +530,7 @@ def clip_grad_norm(grads, max_norm, eps=1e-6, out=None, norm=None):
             if g.device != dev or not _dense(g):
                 raise ValueError(f"grads[{i}] must be dense in memory and on {dev}")
     targets = addresses
-    if out is not None:
+    if outs is not None:
         targets = list(map(tensor.data_ptr, outs))
         if any(i != dev.index for i in map(tensor.get_device, outs)) \
                 or [o.dtype for o in outs] != dtypes \

@@ -19,6 +19,7 @@ from __future__ import annotations
 import argparse
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import (causal_conv, causal_conv_backward, causal_conv_step, clip_grad_norm, gae_stats,
                ppo_clip_loss, selective_scan, selective_scan_backward, selective_step)
@@ -31,10 +32,11 @@ class _Conv(torch.autograd.Function):
         return causal_conv(x, weight, bias, state=state, flags=flags)[0]
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad):
         x, weight, bias, state, flags = ctx.saved_tensors
         g = causal_conv_backward(grad.contiguous(), x, weight, bias, state=state, flags=flags)
-        return g.x, g.weight, g.bias, None, None
+        return g.x, g.weight, g.bias, g.state, None
 
 
 class _Scan(torch.autograd.Function):
@@ -46,10 +48,12 @@ class _Scan(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad):
+        B, C = ctx.saved_tensors[3:5]
         g = selective_scan_backward(grad.contiguous(), *ctx.saved_tensors)
-        return (g.u, g.delta, g.A, g.B.squeeze(1), g.C.squeeze(1), g.D, g.z, g.delta_bias, None,
-                None)
+        return (g.u, g.delta, g.A, g.B.view(B.shape), g.C.view(C.shape), g.D, g.z, g.delta_bias,
+                g.state, None)
 
 
 class RecurrentPolicy(torch.nn.Module):

@@ -8,6 +8,7 @@ and workspace allocation through torch, and the current HIP stream.
 from __future__ import annotations
 
 import ctypes
+import math
 import struct
 import threading
 from array import array
@@ -221,6 +222,16 @@ def _grouped(name, t, N, S, last, dtype, dev):
     return _view(name, t, (N, t.shape[1], S, *last), dtype, dev)
 
 
+# Tells autograd that tensors (a sequence) were written: a backward pass that has
+# saved one refuses to use it.  Torch's own, without the public function's wrapper.
+_written = getattr(torch._C, "_increment_version", torch.autograd.graph.increment_version)
+
+
+def _written_outputs(*tensors):
+    """As _written, for outputs that the caller may have brought."""
+    _written([t for t in tensors if t is not None])
+
+
 def _scratch(nbytes, dev):
     """A workspace that needs no initialisation; torch's allocator keeps it
     alive on the current stream."""
@@ -269,6 +280,8 @@ def causal_conv(x, weight, bias=None, state=None, flags=None, convention=RESET_O
         f = _new(final_state, (shape[0], shape[1], W - 1), dtype, dev, "final_state")
     call = _pack_conv(*fields, o.data_ptr(), _ptr(f), 0, 0, 0, 0, 0, 0, 0, 0)
     _check(lib().rlca_causal_conv(call, _current_stream(dev)), "rlca_causal_conv")
+    if out is not None or final_state is not None:
+        _written_outputs(out, final_state)
     return o, f
 
 
@@ -322,6 +335,7 @@ def causal_conv_step(x, weight, bias, state, slots=None, flags=None, silu=True, 
     call = _pack_conv_step(N, D, places, W, 1 if silu else 0, REAL_DTYPES[dtype], x.data_ptr(),
                            x.stride(0), w, b, s, i, f, o.data_ptr())
     _check(lib().rlca_causal_conv_step(call, _current_stream(dev)), "rlca_causal_conv_step")
+    _written((state,) if out is None else (state, out))
     return o
 
 
@@ -394,6 +408,8 @@ def selective_scan(u, delta, A, B, C, D=None, z=None, delta_bias=None, state=Non
         c = _new(None, (n // 4,), torch.float32, dev)
     call = _pack_scan(*fields, o.data_ptr(), _ptr(f), _ptr(c), *(0,) * 13)
     _check(lib().rlca_selective_scan(call, _current_stream(dev)), "rlca_selective_scan")
+    if y is not None or final_state is not None:
+        _written_outputs(y, final_state)
     return o, f, c
 
 
@@ -463,6 +479,7 @@ def selective_step(u, delta, A, B, C, state, D=None, z=None, delta_bias=None, sl
                            B.data_ptr(), C.data_ptr(), B.stride(0), B.stride(1), C.stride(0),
                            C.stride(1), d, bias, *gate, s, i, f, o.data_ptr())
     _check(lib().rlca_selective_step(call, _current_stream(dev)), "rlca_selective_step")
+    _written((state,) if y is None else (state, y))
     return o
 
 
@@ -523,7 +540,7 @@ def clip_grad_norm(grads, max_norm, eps=1e-6, out=None, norm=None):
     dtypes = [g.dtype for g in grads]
     codes = list(map(REAL_DTYPES.get, dtypes))
     addresses = list(map(tensor.data_ptr, grads))
-    if None in codes or any(i != dev.index for i in map(tensor.get_device, grads)) \
+    if None in codes or set(map(tensor.get_device, grads)) != {dev.index} \
             or not (all(map(tensor.is_contiguous, grads)) or all(map(_dense, grads))):
         for i, g in enumerate(grads):
             _real_dtype(f"grads[{i}]", g)
@@ -532,7 +549,7 @@ def clip_grad_norm(grads, max_norm, eps=1e-6, out=None, norm=None):
     targets = addresses
     if outs is not None:
         targets = list(map(tensor.data_ptr, outs))
-        if any(i != dev.index for i in map(tensor.get_device, outs)) \
+        if set(map(tensor.get_device, outs)) != {dev.index} \
                 or [o.dtype for o in outs] != dtypes \
                 or [o.shape for o in outs] != [g.shape for g in grads] \
                 or list(map(tensor.stride, outs)) != list(map(tensor.stride, grads)):
@@ -551,4 +568,8 @@ def clip_grad_norm(grads, max_norm, eps=1e-6, out=None, norm=None):
         status = lib().rlca_clip_grad_norm(packed.buffer_info()[0], len(grads), max_norm, eps,
                                            n.data_ptr(), ws.data_ptr(), ws.numel(), h)
     _check(status, "rlca_clip_grad_norm")
+    if not math.isinf(max_norm):
+        _written(grads if outs is None else outs)
+    if norm is not None:
+        _written((norm,))
     return n

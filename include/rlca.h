@@ -476,7 +476,10 @@ rlca_status rlca_causal_conv_backward(const rlca_conv_call *call, void *workspac
  *   dt_t = softplus(delta_t + delta_bias), or delta_t + delta_bias with softplus == 0
  *   h_t  = exp(dt_t A) h_{t-1} + dt_t u_t B_t        (h: [states]; h_{t-1} = 0 at a start)
  *   y_t  = (sum_s C_t[s] h_t[s] + D u_t) * silu(z_t)   (the gate only where z is given)
- * B and C are shared by the channels / groups consecutive channels of a group. */
+ * B and C are shared by the channels / groups consecutive channels of a group.
+ * States may grow (A above 0, or dt below 0 without softplus): they are what the
+ * recurrence gives step by step, however large the product of many decays, and
+ * strongly growing rows take up to three times as long. */
 #define RLCA_MAX_STATES 128
 
 typedef struct {

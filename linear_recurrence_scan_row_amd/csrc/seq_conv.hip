@@ -9,13 +9,13 @@
 // lanes need nothing from each other and HBM delivers each line once.
 //
 // Next to the memory's time stand a step's vector instructions: 20 forward, 36
-// with episode starts, 86 backward with them.  So a workgroup keeps its channels and walks tiles of several rows: weights and
-// addresses are formed once, one item is loaded while the one before is
+// with episode starts, 86 backward with them.  So a workgroup keeps its channels
+// and walks tiles of several rows: weights and addresses are formed once, one item is loaded while the one before is
 // computed, and the weights' gradients leave the registers once at the end.
 //
-// Measured, inputs from HBM: forward 1x4096x8191 bf16 27.5 us (4.9 TB/s);
-// 4096x64x128 fp32 with episode starts 59 us forward (4.7 TB/s), 108 backward
-// (3.8 TB/s; the vector units are busy 70% of it) and 5 for the weights' sums.
+// Measured, hundreds of calls in a row: forward 1x4096x8191 bf16 29 us (4.8 TB/s);
+// 4096x64x128 fp32 with episode starts 57 us forward (4.8 TB/s), 102 backward
+// (4.1 TB/s; the vector units are busy 74% of it) and 5 for the weights' sums.
 #include "seq.hpp"
 
 namespace rlca {
@@ -504,9 +504,9 @@ static const void *conv_kernel(const rlca_conv_call &c, bool backward) {
 }
 
 // Lanes of a row and workgroups of the two launches.  Forward and backward,
-// fp32 with episode starts, 4096x64x128: 198, 193, 180, 177 and 181 us with
+// fp32 with episode starts, 4096x64x128: 171, 166, 155, 151 and 156 us with
 // 1024 / 640, 2048 / 1280, 4096 / 2560, 8192 / 5120 workgroups and one for every
-// tile; bf16, 4x2048x2048: 48, 46, 48, 48 and 46.
+// tile; bf16, 4x2048x2048: 42, 41, 44, 42 and 43.
 static ConvShape forward_shape(const rlca_conv_call &c) { return conv_shape(c, 8, 8192); }
 static ConvShape backward_shape(const rlca_conv_call &c) { return conv_shape(c, 6, 5120); }
 

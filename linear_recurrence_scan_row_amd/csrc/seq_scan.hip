@@ -10,8 +10,9 @@
 // A (step, state) takes 10.1 vector instructions (85 M wave instructions for
 // 8x2048 channels of 2048 steps and 16 states) of at least 6, one of which, the
 // exponential, issues at a quarter of the rate.  Measured there, bf16 with a
-// gate: 186 to 194 us, the vector units busy 81% of it (at 2.4 GHz); the
-// bytes alone would take 60.
+// gate: 169 us (hundreds of calls in a row; 185 to 200 in the first tens after
+// idle, at a lower clock), the vector units busy 93% of it at 2.4 GHz; the bytes
+// alone would take 60.
 #include "seq_scan.hpp"
 
 namespace rlca {
@@ -324,11 +325,11 @@ __global__ __launch_bounds__(kScanThreads, sizeof(E) == 2 && !FLAGS ? 4 : 3) voi
 // 16 states, 1.4 where more states leave fewer workgroups a CU, 1.85 for a lane
 // alone and 0.6 for its start), where fewer waves than SIMDs count as many.  LDS
 // limits the states of the two.  Forward and backward in us with 16, 4 and 1 (256
-// channels, bf16 and a gate, 16 states): 4096 rows of 3 steps 2776, 782 and
-// 412; 2048 of 32 1387, 386 and 565; 1024 of 64 726, 384 and 579; 512 of 130 693,
-// 489 and 628; 256 of 260 542, 452 and 595; 128 of 520 446, 424 and 1011; 512
-// of 64 with 64 states 1190 and 847; forward alone 16 rows of 30 (4096
-// channels) 49, 23 and 26.
+// channels, bf16 and a gate, 16 states): 4096 rows of 3 steps 2759, 746 and
+// 407; 2048 of 32 1359, 381 and 550; 1024 of 64 711, 371 and 572; 512 of 130 693,
+// 469 and 628; 256 of 260 530, 428 and 586; 128 of 520 437, 423 and 1004; 512
+// of 64 with 64 states 1175 and 806; forward alone 16 rows of 30 (4096
+// channels) 45, 18 and 24.
 int lanes_of(const rlca_scan_call &c) {
     const int64_t per_group = c.groups == 0 ? 0 : c.channels / c.groups;
     int best = 16;
@@ -391,9 +392,15 @@ ScanParams scan_params(const rlca_scan_call &c, int rows) {
 
 // Waves that share four channels (rows of 16 lanes): enough that the launch
 // gives the 1024 SIMDs several waves each, as long as every wave has a pair of
-// states.  Measured with 1, 2 and 4 (16 states, bf16): 1024 waves at one each (1x4096x4096)
-// 151, 131 and 127 us; 2304 (6x1536x2049, ragged) 112, 92 and 93; 4096
-// (8x2048x2048) 180, 194 and 216.
+// states.  In us with 1, 2 and 4 (bf16, a gate, 16 states; by the waves at one each):
+//   4096 steps   128 waves 143, 97, 62; 384 141, 98, 74; 1024 151, 127, 113
+//   2048 steps   1280 95, 78, 75; 1536 95, 79, 83; 1792 99, 98, 95; 2048 101, 99, 106;
+//                2560 133, 126, 133; 2816 134, 141, 144; 4096 167, 180, 202
+//   1024 steps   3072 67, 71, 79; 3328 84, 80, 85; 4096 87, 93, 104
+//   300 steps    1024 17.2, 15.5, 15.6; 2048 22.5, 22.4, 25.4; 4096 36, 38, 45
+//   1024 steps and 64 states   1024 111, 92, 85; 2048 156, 150, 153; 3072 215, 212, 218
+// The crossings lie near 1500 and between 2560 and 3328 waves, where the sides differ
+// by 6% at most; they depend on neither the steps nor the states by more than that.
 constexpr int kFewestRows = 4;
 
 static int split_of(const rlca_scan_call &c) {

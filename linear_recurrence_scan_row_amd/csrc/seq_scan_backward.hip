@@ -13,14 +13,14 @@
 // grad_B and grad_C sum over the channels of a group.  Within a wave the rows
 // hold channels of the same steps: 16 values (8 steps of each gradient) meet in
 // 12 lane-half swaps and 12 additions, after which each 16 lanes hold four of
-// them, summed over rows of 16 lanes (sum_rows goes on for fewer).  The waves' sums meet in LDS, the
-// workgroups' in a workspace that bc_sums adds in order.
+// them, summed over rows of 16 lanes (sum_rows goes on for fewer).  The waves' sums
+// meet in LDS, the workgroups' in a workspace that bc_sums adds in order.
 //
 // A (step, state) takes 28.4 vector instructions, of about 22 in the formulas
 // above and the sums.  Measured for 8x2048 channels of 2048 steps and 16 states,
-// bf16 with a gate: 510 to 530 us, the vector units busy 81% of it at 2.4 GHz
-// (298 MB read and 471 written, 268 of them partial sums, would take 161), and
-// 55 for bc_sums (4.9 TB/s).
+// bf16 with a gate: 479 us (hundreds of calls in a row), the vector units busy 90%
+// of it at 2.4 GHz (298 MB read and 471 written, 268 of them partial sums, would
+// take 161), and 54 for bc_sums (5.0 TB/s).
 #include "seq_scan.hpp"
 
 namespace rlca {
@@ -715,9 +715,9 @@ static Ranges ranges_of(int64_t num_seqs) {
 }
 
 // Waves that share four channels: two where one would leave the SIMDs a single
-// wave each (with one and two, forward and backward, 16 states, bf16: 4096
-// channels of 4096 steps 567 and 544 us, 2048 of 2048 243 and 230, 8192 of
-// 2048 457 and 528).  Above 64 states two would need over 160 KB of LDS.
+// wave each (with one and two, forward and backward, 16 states, bf16: 1024
+// channels of 4096 steps 405 and 375 us, 4096 of 4096 502 and 480, 2048 of 2048 223
+// and 208, 4x1024 of 2048 244 and 230; 5120 354 and 414, 8192 430 and 492).  Above 64 states two would need over 160 KB of LDS.
 static int split_of(const rlca_scan_call &c) {
     return c.num_seqs * c.channels <= 4096 && c.states > 2 && c.states <= 64 ? 2 : 1;
 }

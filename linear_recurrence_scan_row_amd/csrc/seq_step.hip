@@ -5,8 +5,8 @@
 // step's few products cost nothing beside that.  With one sequence the time is
 // a launch and one chain of dependent loads.  Measured: convolution 512x8192
 // bf16 16 us (4.2 TB/s), scan 512x4096 with 16 states 66 us with the states
-// from HBM (4.3 TB/s) and 47 when half of them lie in the last-level cache; one
-// sequence of 2048 channels 2.8 and 3.5 us.
+// from HBM (4.3 TB/s) and 49 when half of them lie in the last-level cache; one
+// sequence of 2048 channels 2.6 and 3.5 us.
 #include "seq.hpp"
 
 namespace rlca {
@@ -189,14 +189,14 @@ __global__ __launch_bounds__(kStepThreads, 8) void selective_step(ScanStepParams
 
 // ------------------------------------------------------------------- host side
 // Workgroups of a launch, as far as there are sequences: what the chip holds at
-// once.  The scan's step, 512x4096, 16 states, bf16, states from HBM: 119, 91,
-// 70, 71 and 81 us with 512, 1024, 2048, 4096 and a workgroup for each sequence.
+// once.  The scan's step, 512x4096, 16 states, bf16, states from HBM: 130, 90,
+// 67, 66 and 73 us with 512, 1024, 2048, 4096 and a workgroup for each sequence.
 constexpr uint32_t kStepBlocks = 2048;
 
 // The convolution's step: eight channels a thread, with a quarter of the
 // workgroups, from kWideThreads such threads on; the states' 6 bytes a channel
-// then move 16 at a time.  512x8192 bf16: 18 us against 23 with one channel;
-// 256x4096 fp32 14.1 against 12.6.
+// then move 16 at a time.  512x8192 bf16: 15.8 us against 17.9 with one channel,
+// 512x4096 10.7 against 10.4; 256x4096 fp32 12.3 against 8.8.
 constexpr int kWideChannels = 8;
 constexpr int64_t kWideThreads = 1 << 18;
 constexpr uint32_t kWideBlocks = 512;

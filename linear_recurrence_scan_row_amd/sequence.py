@@ -3,7 +3,10 @@ causal convolution, the selective scan, their single-step forms and gradients,
 and the clipping of gradients by their global norm.
 
 Argument marshalling only, as in rlca.py: shape / dtype / device checks, output
-and workspace allocation through torch, and the current HIP stream.
+and workspace allocation through torch, and the current HIP stream.  The calls
+build no autograd graph: results carry none, whatever the inputs require, and the
+gradients are calls of their own (recurrent_policy.py wraps them for autograd).
+What a call writes into a tensor of the caller's counts as a change in place.
 """
 from __future__ import annotations
 

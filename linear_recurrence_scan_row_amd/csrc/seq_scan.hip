@@ -396,9 +396,9 @@ ScanParams scan_params(const rlca_scan_call &c, int rows) {
 //   4096 steps   128 waves 143, 97, 62; 384 141, 98, 74; 1024 151, 127, 113
 //   2048 steps   1280 95, 78, 75; 1536 95, 79, 83; 1792 99, 98, 95; 2048 101, 99, 106;
 //                2560 133, 126, 133; 2816 134, 141, 144; 4096 167, 180, 202
-//   1024 steps   3072 67, 71, 79; 3328 84, 80, 85; 4096 87, 93, 104
+//   1024 steps   3328 84, 80, 85; 4096 87, 93, 104
 //   300 steps    1024 17.2, 15.5, 15.6; 2048 22.5, 22.4, 25.4; 4096 36, 38, 45
-//   1024 steps and 64 states   1024 111, 92, 85; 2048 156, 150, 153; 3072 215, 212, 218
+//   1024 steps and 64 states   1024 111, 92, 85; 2048 156, 150, 153
 // The crossings lie near 1500 and between 2560 and 3328 waves, where the sides differ
 // by 6% at most; they depend on neither the steps nor the states by more than that.
 constexpr int kFewestRows = 4;

@@ -50,7 +50,8 @@ def check(instructions, last=None):
     return bad, since
 
 
-def test_the_checker():
+def test_reads_that_come_too_soon():
+    """What `check` finds, and what it lets pass."""
     assert check(["v_add_f32 v1, v2, v3", "v_mov_b32_dpp v4, v1 row_shr:1"])[0]
     assert check(["v_add_f32 v1, v2, v3", "s_nop 0", "v_mov_b32_dpp v4, v1 row_shr:1"])[0]
     assert not check(["v_add_f32 v1, v2, v3", "s_nop 1", "v_mov_b32_dpp v4, v1 row_shr:1"])[0]

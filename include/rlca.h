@@ -595,6 +595,172 @@ rlca_status rlca_clip_grad_norm(const rlca_grad_tensor *tensors, int64_t num_ten
                                 double max_norm, double eps, double *norm, void *workspace,
                                 size_t workspace_bytes, hipStream_t stream);
 
+/* ------------------------------------------- operators of a block and of a search
+ * What stands around the recurrences in a residual stack of blocks, and in
+ * generating with it, over the same rows and pools: the gated linear recurrence
+ * with its gradients and its single step, the root-mean-square norm with the
+ * residual's addition, and a beam search's selection and reordering of states.
+ * Layout, types, episodes, lengths, sizes, errors and memory are as above.
+ *
+ * The gated recurrence: one state a channel, whose decay and input are gated
+ * step by step,
+ *   r_t = sigmoid(decay_gate_t + decay_bias),  i_t = sigmoid(input_gate_t + input_bias),
+ *   L_t = scale softplus(decay) r_t,  a_t = exp(-L_t),
+ *   h_t = a_t h_{t-1} + sqrt(1 - a_t^2) i_t x_t      (h_{t-1} = 0 at a start);
+ * out_t is h_t, rounded once.  A state decays at every step and cannot grow; a_t is
+ * float32, so steps with L_t below 1e-7 do not decay.  The checkpoints (nullable)
+ * are the states that the backward call starts from.  scale is within 1e-30 ..
+ * 1e30, channels below 2^25.  The workspaces need no initialisation; the forward
+ * call's may be of size 0. */
+typedef struct {
+    int64_t num_seqs, channels, T;
+    int32_t dtype;      /* of x, the gates, out and their gradients */
+    int32_t convention; /* rlca_reset_convention, for flags */
+    double scale;
+    const void *x, *input_gate, *decay_gate; /* [num_seqs, channels, T] */
+    int64_t x_stride_seq, x_stride_channel;
+    int64_t input_stride_seq, input_stride_channel;
+    int64_t decay_stride_seq, decay_stride_channel;
+    const float *decay;                   /* [channels] */
+    const float *input_bias, *decay_bias; /* [channels], nullable (=> 0) */
+    const float *state;                   /* [num_seqs, channels], nullable (=> 0) */
+    const uint8_t *flags;                 /* [num_seqs, T], nullable */
+    const int32_t *lengths;               /* [num_seqs], nullable */
+    /* rlca_gated_recurrence */
+    void *out;          /* [num_seqs, channels, T] */
+    float *final_state; /* [num_seqs, channels], nullable */
+    float *checkpoints; /* rlca_gated_recurrence_checkpoints_size bytes, nullable */
+    /* rlca_gated_recurrence_backward (reads checkpoints) */
+    const void *grad_out; /* [num_seqs, channels, T] */
+    int64_t grad_stride_seq, grad_stride_channel;
+    const float *grad_final_state; /* [num_seqs, channels], nullable (=> 0) */
+    void *grad_x, *grad_input_gate, *grad_decay_gate; /* [num_seqs, channels, T] */
+    float *grad_decay;                                /* [channels] */
+    float *grad_input_bias, *grad_decay_bias;         /* [channels], nullable */
+    float *grad_state;                                /* [num_seqs, channels], nullable */
+} rlca_gated_call;
+
+size_t rlca_gated_recurrence_checkpoints_size(const rlca_gated_call *call);
+size_t rlca_gated_recurrence_workspace_size(const rlca_gated_call *call);
+rlca_status rlca_gated_recurrence(const rlca_gated_call *call, void *workspace,
+                                  size_t workspace_bytes, hipStream_t stream);
+
+/* The gradients of the call whose inputs and checkpoints `call` holds.  Nothing is
+ * accumulated into what the outputs held before, and all sums run in a fixed order
+ * (reproducible bit for bit). */
+size_t rlca_gated_recurrence_backward_workspace_size(const rlca_gated_call *call);
+rlca_status rlca_gated_recurrence_backward(const rlca_gated_call *call, void *workspace,
+                                           size_t workspace_bytes, hipStream_t stream);
+
+/* One step for each of `num_seqs` sequences, with a pool of states, slots and starts
+ * as for rlca_selective_step. */
+typedef struct {
+    int64_t num_seqs, channels, places;
+    int32_t dtype;
+    double scale;
+    const void *x, *input_gate, *decay_gate; /* [num_seqs, channels] */
+    int64_t x_stride_seq, input_stride_seq, decay_stride_seq;
+    const float *decay, *input_bias, *decay_bias;
+    float *state; /* [places, channels], in and out */
+    const int32_t *slots;
+    const uint8_t *starts;
+    void *out; /* [num_seqs, channels] */
+} rlca_gated_step_call;
+
+rlca_status rlca_gated_step(const rlca_gated_step_call *call, hipStream_t stream);
+
+/* The root-mean-square norm over the channels of each step, after a residual's
+ * addition:
+ *   s = x + residual (rounded to the storage type; s = x without a residual),
+ *   y = s / sqrt(mean over channels of s^2 + eps) * weight.
+ * s is the residual stream that goes on, and it is normed as it is stored.  The
+ * output is y in the storage type, or in 8 bits (OCP e4m3) with one float32 scale a
+ * step, for an 8-bit matrix product: scale = max(max over channels of |y| / 448,
+ * 2^-120), out8 = y / scale rounded to nearest even.  Squares and sums are float32,
+ * and are scaled down where they would overflow.  Steps past a row's length get
+ * output, sum, scale and gradient 0.  T = 1 with x_stride_channel = 1 (and the
+ * residual's and gradients' too) is the norm of dense rows of channels: a generated
+ * token's, or any [tokens, channels] array's.  eps >= 0 and finite. */
+typedef struct {
+    int64_t num_seqs, channels, T;
+    int32_t dtype;
+    double eps;
+    const void *x; /* [num_seqs, channels, T] */
+    int64_t x_stride_seq, x_stride_channel;
+    const void *residual; /* [num_seqs, channels, T], nullable */
+    int64_t residual_stride_seq, residual_stride_channel;
+    const float *weight;    /* [channels], nullable (=> 1) */
+    const int32_t *lengths; /* [num_seqs], nullable */
+    /* rlca_rms_norm */
+    void *out;    /* [num_seqs, channels, T]; NULL where out8 is wanted */
+    uint8_t *out8; /* [num_seqs, channels, T]; NULL where out is */
+    float *scale; /* [num_seqs, T]; required iff out8 */
+    void *sum;    /* [num_seqs, channels, T]; required iff residual */
+    /* rlca_rms_norm_backward: x is what was normed (s), residual is not used */
+    const void *grad_out; /* [num_seqs, channels, T] */
+    int64_t grad_stride_seq, grad_stride_channel;
+    const void *grad_sum; /* [num_seqs, channels, T], nullable: added to grad_x */
+    int64_t grad_sum_stride_seq, grad_sum_stride_channel;
+    void *grad_x;       /* [num_seqs, channels, T]: the gradient of s, so of x and residual */
+    float *grad_weight; /* [channels], nullable */
+} rlca_norm_call;
+
+size_t rlca_rms_norm_workspace_size(const rlca_norm_call *call);
+rlca_status rlca_rms_norm(const rlca_norm_call *call, void *workspace, size_t workspace_bytes,
+                          hipStream_t stream);
+size_t rlca_rms_norm_backward_workspace_size(const rlca_norm_call *call);
+rlca_status rlca_rms_norm_backward(const rlca_norm_call *call, void *workspace,
+                                   size_t workspace_bytes, hipStream_t stream);
+
+/* A beam search's selection.  For each of num_searches searches, over all `beams`
+ * beams and `vocab` tokens, the `picks` candidates with the highest
+ *   total = score_b + (logit_bv - log sum_v exp(logit_bv)),
+ * best first, equal ones by beam and then token (the lower first).  Sums are formed
+ * so that totals are good to 2^-40 or so before the one rounding to float32, and
+ * they are compared before it.  A beam that is finished has one candidate, pad_token
+ * at its own score; its other totals are -infinity.  So are all totals of a beam
+ * whose score is -infinity (an unused one: its logits do not count, whatever they
+ * hold) and those of logits of -infinity (tokens that are not allowed; all of them
+ * may be).  A logit of NaN or +infinity makes all totals of its beam NaN, as a NaN
+ * score does, and NaN ranks first.  beams and picks are 1 .. RLCA_MAX_BEAMS, picks at
+ * most beams * vocab, beams * vocab < 2^31. */
+#define RLCA_MAX_BEAMS 64
+
+typedef struct {
+    int64_t num_searches, beams, vocab;
+    int32_t picks, dtype, pad_token;
+    const void *logits; /* [num_searches, beams, vocab] */
+    int64_t logits_stride_search, logits_stride_beam;
+    const float *scores;     /* [num_searches, beams] */
+    const uint8_t *finished; /* [num_searches, beams], nullable */
+    float *out_scores;       /* [num_searches, picks] */
+    int32_t *out_tokens, *out_parents; /* [num_searches, picks] */
+} rlca_beam_call;
+
+size_t rlca_beam_select_workspace_size(const rlca_beam_call *call);
+rlca_status rlca_beam_select(const rlca_beam_call *call, void *workspace, size_t workspace_bytes,
+                             hipStream_t stream);
+
+/* The beams' states after a selection, in any number of pools [places, ...] of
+ * place_bytes a place.  Beam k of a search goes on from the state of its beam
+ * parents[k]: the first child of a parent keeps the parent's place, and each other
+ * one gets the place of a beam without children (both in order), to which the state
+ * is copied in every pool.  new_slots is where each beam's state is then; no other
+ * place is written.  Slots as for the single steps: those of one call must differ,
+ * and one outside 0..places-1 holds no state (nothing is copied from or to it).  A
+ * parent outside 0..beams-1 makes an unused beam, which gets a free place and no
+ * state.  `pools` is host memory, read before the function returns; beams <=
+ * RLCA_MAX_BEAMS. */
+typedef struct {
+    void *data;
+    int64_t place_bytes;
+} rlca_state_pool;
+
+rlca_status rlca_beam_reorder(const rlca_state_pool *pools, int64_t num_pools,
+                              int64_t num_searches, int64_t beams, int64_t places,
+                              const int32_t *slots, const int32_t *parents, int32_t *new_slots,
+                              hipStream_t stream);
+
 /* Static description of a status code (never NULL). */
 const char *rlca_status_string(rlca_status status);
 

@@ -44,3 +44,9 @@ from .sequence import (  # noqa: F401
     selective_scan_backward,
     selective_step,
 )
+from .blocks import (  # noqa: F401
+    GatedGrads,
+    gated_recurrence,
+    gated_recurrence_backward,
+    gated_step,
+)

@@ -1,0 +1,927 @@
+// gated.hip -- the gated linear recurrence over rows of T steps, its gradients,
+// and its single step:
+//   r = sigmoid(decay_gate + decay_bias),  i = sigmoid(input_gate + input_bias),
+//   L = scale softplus(decay) r,  a = exp(-L),
+//   h_t = a_t h_{t-1} + sqrt(1 - a_t^2) i_t x_t.
+//
+// The affine recurrence of this library, one state a channel.  A row of 16, 4 or
+// 1 lanes owns a channel and a tile of 8 steps a lane: each lane folds its 8 maps
+// into one, lane-crossing moves scan the maps, and each lane applies its own steps
+// again from the state that enters it.  A wave owns 4, 16 or 64 neighbouring
+// channels and walks tiles and then sequences, the next tile's loads issued before
+// this one is computed.  Where there are few rows a row is cut into chunks: one
+// launch leaves each chunk's map, the second starts each chunk from the maps
+// before it.
+#include "seq_scan.hpp"
+
+namespace rlca {
+namespace seq {
+
+constexpr int kGateK = 8;        // steps of a lane
+constexpr int kGateThreads = 256;
+constexpr int kGateWaves = kGateThreads / kWave;
+constexpr int gate_tile(int L) { return kGateK * L; }
+
+struct GateParams {
+    const void *x, *input_gate, *decay_gate, *grad_out;
+    const float *decay, *input_bias, *decay_bias;
+    const float *state, *grad_final;
+    const uint8_t *flags;
+    const int32_t *lengths;
+    void *out;
+    float *final_state;
+    float *checkpoints;  // [num_seqs][channels][tiles]: states entering each tile
+    void *grad_x, *grad_input, *grad_decay;
+    float *grad_state;
+    float *maps;      // [num_seqs][chunks][2][channels]: each chunk's map
+    float *partials;  // [walkers][3][channels]: sums for decay, decay_bias, input_bias
+    int64_t x_n, x_d, ig_n, ig_d, dg_n, dg_d, g_n, g_d;
+    uint32_t num_seqs, channels;
+    uint32_t groups;      // waves that share a sequence's channels
+    uint32_t walkers;     // waves that share a group's sequences and chunks
+    uint32_t units;       // num_seqs * chunks
+    uint32_t chunks, chunk_tiles;
+    int32_t T, tiles;
+    int32_t after_done;
+    float scale;
+    FastDiv by_chunks;
+};
+
+// --------------------------------------------------------------- the arithmetic
+// scale softplus(decay), and what a step's L = slow r may be at most: below, L a^2
+// and its like are 0 where a is, not infinity times 0.
+__device__ __forceinline__ float slow_of(float scale, float decay) {
+    const float s = scale * softplus(decay);
+    return s > 1e30f ? 1e30f : s;  // a NaN stays one
+}
+
+// A step's a = exp(-L) and 1 - a^2 = (1 - a)(1 + a).  Near L = 0 the difference 1 - a
+// would lose digits, so up to 1/2 it is L times the polynomial that interpolates
+// (1 - exp(-L)) / L there at 6 Chebyshev points (error 1.5e-9), and a is 1 minus it;
+// from there on a is the exponential, and the difference of at least 0.39 loses none.
+// SMALL: no L of the wave is above 1/2.
+template <bool SMALL>
+__device__ __forceinline__ void decay_of(float L, float &a, float &rest) {
+    float d = fmaf(L, -0.0011234042f, 0.0081896136f);
+    d = fmaf(L, d, -0.041630073f);
+    d = fmaf(L, d, 0.16666242f);
+    d = fmaf(L, d, -0.49999982f);
+    d = fmaf(L, d, 1.f);
+    d *= L;
+    a = 1.f - d;
+    if constexpr (!SMALL) {
+        const float e = exp2_fast(-L * kLog2e);
+        a = L > 0.5f ? e : a;
+        d = L > 0.5f ? 1.f - e : d;
+    }
+    rest = fmaf(d, a, d);
+}
+
+// Inclusive scan of the lane maps of a row of L lanes, towards higher lanes or,
+// REVERSE, towards lower ones; lanes whose source is outside the row keep theirs.
+// CUT as for step_map: an episode start's a is -0.
+template <bool CUT, bool REVERSE, int L>
+__device__ __forceinline__ void lanes_scan(float &a, float &h, int lane) {
+    if constexpr (L == 4) {
+        const auto step = [&](auto by) {
+            constexpr int kStep = decltype(by)::value;
+            constexpr int kCtrl = shift_ctrl<4, REVERSE, kStep>();
+            const bool has = REVERSE ? lane + kStep < 4 : lane >= kStep;
+            const float ph = dpp_move<kCtrl, 0xf>(h, h), pa = dpp_move<kCtrl, 0xf>(a, a);
+            h = has ? step_map<CUT>(a, h, ph) : h;
+            a = has ? product<CUT>(a, pa) : a;
+        };
+        step(std::integral_constant<int, 1>{});
+        step(std::integral_constant<int, 2>{});
+    } else if constexpr (L == 16) {
+        const auto step = [&](auto by) {
+            constexpr int kCtrl = shift_ctrl<16, REVERSE, decltype(by)::value>();
+            const float ph = dpp_move<kCtrl, 0xf>(h, 0.f), pa = dpp_move<kCtrl, 0xf>(a, 1.f);
+            h = step_map<CUT>(a, h, ph);
+            a = product<CUT>(a, pa);
+        };
+        step(std::integral_constant<int, 1>{});
+        step(std::integral_constant<int, 2>{});
+        step(std::integral_constant<int, 4>{});
+        step(std::integral_constant<int, 8>{});
+    }
+}
+
+// What enters each lane of a row from the lane before it, and the row's whole map
+// applied to `enter`: the value that leaves the row.
+template <bool CUT, bool REVERSE, int L>
+__device__ __forceinline__ float enter_lanes(float a, float h, float enter, int lane, float &leave) {
+    if constexpr (L == 1) {
+        leave = step_map<CUT>(a, h, enter);
+        return enter;
+    } else {
+        lanes_scan<CUT, REVERSE, L>(a, h, lane);
+        const float after = step_map<CUT>(a, h, enter);
+        leave = row_last<REVERSE, L>(after);
+        return row_shift<REVERSE, L>(after, enter, lane);
+    }
+}
+
+// ------------------------------------------------------------------- the walk
+// Where a wave stands: a unit (a sequence's chunk) and a tile of it.
+struct Place {
+    uint32_t unit, n, chunk;
+    int tile, end;  // end: the sequence's steps that count
+    __device__ __forceinline__ void set_unit(const GateParams &p, uint32_t u) {
+        unit = u;
+        if (u >= p.units) return;
+        n = p.chunks == 1 ? u : p.by_chunks.div(u);
+        chunk = u - n * p.chunks;
+        end = row_end(p.lengths, n, p.T);
+    }
+    __device__ __forceinline__ int first(const GateParams &p) const {
+        return (int)(chunk * p.chunk_tiles);
+    }
+    __device__ __forceinline__ int past(const GateParams &p) const {
+        const int x = (int)((chunk + 1) * p.chunk_tiles);
+        return x < p.tiles ? x : p.tiles;
+    }
+};
+
+// The wave's channels: lane `lane` of the row of channel d.
+struct GateLane {
+    uint32_t d;
+    int lane;
+    bool live;
+    float slow, input_bias, decay_bias;
+    template <int L>
+    __device__ __forceinline__ static GateLane of(const GateParams &p, uint32_t group) {
+        GateLane l;
+        const int in_wave = threadIdx.x % kWave;
+        l.lane = in_wave & (L - 1);
+        const uint32_t d = group * (kWave / L) + in_wave / L;
+        l.live = d < p.channels;
+        l.d = l.live ? d : p.channels - 1;
+        l.slow = slow_of(p.scale, p.decay[l.d]);
+        l.input_bias = p.input_bias == nullptr ? 0.f : p.input_bias[l.d];
+        l.decay_bias = p.decay_bias == nullptr ? 0.f : p.decay_bias[l.d];
+        return l;
+    }
+};
+
+// A lane's episode starts in its steps from t on, as bits; none from `end` on.
+__device__ __forceinline__ uint32_t gate_starts(const GateParams &p, uint32_t n, int t, int end) {
+    uint32_t s = start_bits<kGateK>(p.flags + (int64_t)n * p.T, t, p.T, p.after_done);
+    if (t + kGateK > end) s &= t < end ? (1u << (end - t)) - 1 : 0u;
+    return s;
+}
+
+// A lane's 8 steps: the gates, and the maps (a, b) of the recurrence.
+struct GateSteps {
+    float x[kGateK], i[kGateK], r[kGateK], a[kGateK], rest[kGateK];
+    template <typename E>
+    __device__ __forceinline__ void make(const GateLane &l, const Steps<kGateK, E> &xs,
+                                         const Steps<kGateK, E> &igs, const Steps<kGateK, E> &dgs) {
+        xs.widen(x);
+        igs.widen(i);
+        dgs.widen(r);
+        bool small = true;
+#pragma unroll
+        for (int k = 0; k < kGateK; ++k) {
+            i[k] = sigmoid(i[k] + l.input_bias);
+            r[k] = sigmoid(r[k] + l.decay_bias);
+            small &= l.slow * r[k] <= 0.5f;
+        }
+        if (whole_wave(small)) {
+#pragma unroll
+            for (int k = 0; k < kGateK; ++k) decay_of<true>(l.slow * r[k], a[k], rest[k]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < kGateK; ++k) decay_of<false>(l.slow * r[k], a[k], rest[k]);
+        }
+    }
+};
+
+// The state that enters a chunk: the row's state through the maps of the chunks
+// before it.  (REVERSE: the gradient that enters from the chunks after it.)
+template <bool REVERSE>
+__device__ __forceinline__ float enter_chunk(const GateParams &p, uint32_t n, uint32_t chunk,
+                                             uint32_t d, float x) {
+    const float *m = p.maps + (int64_t)n * p.chunks * 2 * p.channels + d;
+    const int count = REVERSE ? (int)(p.chunks - 1 - chunk) : (int)chunk;
+#pragma unroll 4
+    for (int j = 0; j < count; ++j) {
+        const int64_t c = REVERSE ? (int64_t)p.chunks - 1 - j : j;
+        const float *at = m + c * 2 * p.channels;
+        x = step_map<true>(at[0], at[p.channels], x);
+    }
+    return x;
+}
+
+// ------------------------------------------------------------------- forward
+// MAPS: leave each chunk's map only.
+template <typename E, bool FLAGS, int L, bool MAPS>
+__global__ __launch_bounds__(kGateThreads) void gated_rows(GateParams p) {
+    constexpr int K = kGateK, kTile = gate_tile(L);
+    const uint32_t wave = blockIdx.x * kGateWaves +
+                          __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const uint32_t walker = wave / p.groups, group = wave - walker * p.groups;
+    if (walker >= p.walkers) return;
+    const GateLane l = GateLane::of<L>(p, group);
+    const int own = l.lane * K;
+
+    struct Loads {
+        Steps<K, E> x, ig, dg;
+    } next;
+    const auto load = [&](const Place &at) {
+        const int t = at.tile * kTile + own, left = at.end - t;
+        next.x.load(static_cast<const E *>(p.x) + at.n * p.x_n + l.d * p.x_d + t, left);
+        next.ig.load(static_cast<const E *>(p.input_gate) + at.n * p.ig_n + l.d * p.ig_d + t, left);
+        next.dg.load(static_cast<const E *>(p.decay_gate) + at.n * p.dg_n + l.d * p.dg_d + t, left);
+    };
+    // The last chunk's map is not needed.
+    const auto wanted = [&](const Place &at) { return !MAPS || at.chunk + 1 < p.chunks; };
+    Place at;
+    at.set_unit(p, walker);
+    while (at.unit < p.units && !wanted(at)) at.set_unit(p, at.unit + p.walkers);
+    if (at.unit >= p.units) return;
+    at.tile = at.first(p);
+    load(at);
+    float carry = 0.f, map = 1.f;
+    bool fresh = true;
+    while (true) {
+        const int64_t row = (int64_t)at.n * p.channels + l.d;
+        const int t0 = at.tile * kTile, t = t0 + own;
+        if (fresh) {
+            if constexpr (MAPS) {
+                carry = 0.f;
+                map = 1.f;
+            } else {
+                carry = p.state == nullptr ? 0.f : p.state[row];
+                if (p.chunks > 1) carry = enter_chunk<false>(p, at.n, at.chunk, l.d, carry);
+            }
+        }
+        const Loads now = next;
+        uint32_t starts = 0;
+        if constexpr (FLAGS) starts = gate_starts(p, at.n, t, at.end);
+        // the place after this one, and its loads
+        Place ahead = at;
+        const bool last = at.tile + 1 == at.past(p);
+        if (last) {
+            do ahead.set_unit(p, ahead.unit + p.walkers);
+            while (ahead.unit < p.units && !wanted(ahead));
+            ahead.tile = ahead.unit < p.units ? ahead.first(p) : 0;
+        } else {
+            ++ahead.tile;
+        }
+        if (ahead.unit < p.units) load(ahead);
+
+        GateSteps s;
+        s.make(l, now.x, now.ig, now.dg);
+        float b[K], h[K];
+#pragma unroll
+        for (int k = 0; k < K; ++k) b[k] = __builtin_amdgcn_sqrtf(s.rest[k]) * (s.i[k] * s.x[k]);
+        if (t0 + kTile > at.end)
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                if (t + k >= at.end) s.a[k] = 1.f, b[k] = 0.f;
+        float a = 1.f, fold = 0.f;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            if (FLAGS && (starts >> k & 1)) fold = 0.f;
+            fold = fmaf(s.a[k], fold, b[k]);
+            a *= s.a[k];
+        }
+        if (FLAGS && starts != 0) a = -0.f;
+        if (!MAPS && p.checkpoints != nullptr && l.live && l.lane == 0)
+            p.checkpoints[row * p.tiles + at.tile] = carry;
+        float leave;
+        const float in = enter_lanes<FLAGS, false, L>(a, fold, carry, l.lane, leave);
+        carry = leave;
+        if constexpr (MAPS) {
+            // the tile's product of a's, from the row's lanes
+            float whole = a;
+            if constexpr (L > 1) {
+                float unused = 0.f;
+                lanes_scan<FLAGS, false, L>(whole, unused, l.lane);
+                whole = row_last<false, L>(whole);
+            }
+            map = product<FLAGS>(whole, map);
+            if (last && l.live && l.lane == 0) {
+                float *m = p.maps + ((int64_t)at.n * p.chunks + at.chunk) * 2 * p.channels + l.d;
+                m[0] = map;
+                m[p.channels] = carry;
+            }
+        } else {
+            float x = in;
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                if (FLAGS && (starts >> k & 1)) x = 0.f;
+                x = fmaf(s.a[k], x, b[k]);
+                h[k] = x;
+            }
+            if (t0 + kTile > at.end)
+#pragma unroll
+                for (int k = 0; k < K; ++k)
+                    if (t + k >= at.end) h[k] = 0.f;
+            if (l.live) store_steps<K>(static_cast<E *>(p.out) + row * p.T + t, p.T - t, h);
+            if (last && at.chunk + 1 == p.chunks && p.final_state != nullptr && l.live &&
+                l.lane == 0) {
+                const bool over = FLAGS && p.after_done && at.end > 0 &&
+                                  p.flags[(int64_t)at.n * p.T + at.end - 1] != 0;
+                p.final_state[row] = over ? 0.f : carry;
+            }
+        }
+        if (ahead.unit >= p.units) return;
+        fresh = last;
+        at = ahead;
+    }
+}
+
+// ------------------------------------------------------------------- backward
+// With lambda_t = grad_t + a_{t+1} lambda_{t+1} the gradient of h_t, beta = sqrt(1 - a^2)
+// and inv = 1 / beta:
+//   grad_x = lambda beta i,   grad_input_gate = grad_x x (1 - i),
+//   e = dL/d(log decay's rate) = lambda L a (a inv i x - h_{t-1}),
+//   grad_decay_gate = e (1 - r),  grad_decay = sum e sigmoid(decay) / softplus(decay).
+// The states are computed again, from the state that entered the tile.  What passes a
+// step to the left is a_t lambda_t, so a lane's map is r -> a_k (grad_k + r) over its
+// steps from the last.
+template <typename E, bool FLAGS, int L, bool MAPS>
+__global__ __launch_bounds__(kGateThreads) void gated_rows_backward(GateParams p) {
+    constexpr int K = kGateK, kTile = gate_tile(L);
+    const uint32_t wave = blockIdx.x * kGateWaves +
+                          __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const uint32_t walker = wave / p.groups, group = wave - walker * p.groups;
+    if (walker >= p.walkers) return;
+    const GateLane l = GateLane::of<L>(p, group);
+    const int own = l.lane * K;
+
+    struct Loads {
+        Steps<K, E> x, ig, dg, g;
+        float enter;
+    } next;
+    const auto load = [&](const Place &at) {
+        const int t = at.tile * kTile + own, left = at.end - t;
+        next.dg.load(static_cast<const E *>(p.decay_gate) + at.n * p.dg_n + l.d * p.dg_d + t, left);
+        next.g.load(static_cast<const E *>(p.grad_out) + at.n * p.g_n + l.d * p.g_d + t, left);
+        if constexpr (!MAPS) {
+            next.x.load(static_cast<const E *>(p.x) + at.n * p.x_n + l.d * p.x_d + t, left);
+            next.ig.load(static_cast<const E *>(p.input_gate) + at.n * p.ig_n + l.d * p.ig_d + t,
+                         left);
+            next.enter = p.checkpoints[((int64_t)at.n * p.channels + l.d) * p.tiles + at.tile];
+        }
+    };
+    // The first chunk's map is not needed.
+    const auto wanted = [&](const Place &at) { return !MAPS || at.chunk > 0; };
+    float sum_decay = 0.f, sum_rate = 0.f, sum_input = 0.f;
+    Place at;
+    at.set_unit(p, walker);
+    while (at.unit < p.units && !wanted(at)) at.set_unit(p, at.unit + p.walkers);
+    if (MAPS && at.unit >= p.units) return;
+    if (at.unit < p.units) {
+        at.tile = at.past(p) - 1;
+        load(at);
+    }
+    float carry = 0.f, map = 1.f;
+    bool fresh = true;
+    while (at.unit < p.units) {
+        const int64_t row = (int64_t)at.n * p.channels + l.d;
+        const int t0 = at.tile * kTile, t = t0 + own;
+        if (fresh) {
+            carry = 0.f;
+            map = 1.f;
+            if constexpr (!MAPS) {
+                const bool over = FLAGS && p.after_done && at.end > 0 &&
+                                  p.flags[(int64_t)at.n * p.T + at.end - 1] != 0;
+                if (p.grad_final != nullptr && !over) carry = p.grad_final[row];
+                if (p.chunks > 1) carry = enter_chunk<true>(p, at.n, at.chunk, l.d, carry);
+            }
+        }
+        const Loads now = next;
+        uint32_t starts = 0;
+        if constexpr (FLAGS) starts = gate_starts(p, at.n, t, at.end);
+        Place ahead = at;
+        const bool last = at.tile == at.first(p);
+        if (last) {
+            do ahead.set_unit(p, ahead.unit + p.walkers);
+            while (ahead.unit < p.units && !wanted(ahead));
+            ahead.tile = ahead.unit < p.units ? ahead.past(p) - 1 : 0;
+        } else {
+            --ahead.tile;
+        }
+        if (ahead.unit < p.units) load(ahead);
+
+        float g[K];
+        now.g.widen(g);
+        GateSteps s;
+        if constexpr (MAPS)
+            s.make(l, now.dg, now.dg, now.dg);
+        else
+            s.make(l, now.x, now.ig, now.dg);
+        const bool partial = t0 + kTile > at.end;
+        if (partial)
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                if (t + k >= at.end) s.a[k] = 1.f;
+        float a = 1.f;
+#pragma unroll
+        for (int k = 0; k < K; ++k) a *= s.a[k];
+        if (FLAGS && starts != 0) a = -0.f;
+        float back = 0.f;
+#pragma unroll
+        for (int k = K - 1; k >= 0; --k) {
+            back = s.a[k] * (g[k] + back);
+            if (FLAGS && (starts >> k & 1)) back = 0.f;
+        }
+        float leave;
+        float pass = enter_lanes<FLAGS, true, L>(a, back, carry, l.lane, leave);
+        carry = leave;
+        if constexpr (MAPS) {
+            float whole = a;
+            if constexpr (L > 1) {
+                float unused = 0.f;
+                lanes_scan<FLAGS, true, L>(whole, unused, l.lane);
+                whole = row_last<true, L>(whole);
+            }
+            map = product<FLAGS>(whole, map);
+            if (last && l.live && l.lane == 0) {
+                float *m = p.maps + ((int64_t)at.n * p.chunks + at.chunk) * 2 * p.channels + l.d;
+                m[0] = map;
+                m[p.channels] = carry;
+            }
+        } else {
+            float beta[K], inv[K], before[K];
+            float fold = 0.f;
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                inv[k] = __builtin_amdgcn_rsqf(s.rest[k] < 1.2e-38f ? 1.2e-38f : s.rest[k]);
+                beta[k] = s.rest[k] * inv[k];
+                if (partial && t + k >= at.end) beta[k] = 0.f;
+                if (FLAGS && (starts >> k & 1)) fold = 0.f;
+                fold = fmaf(s.a[k], fold, beta[k] * (s.i[k] * s.x[k]));
+            }
+            float unused, h = enter_lanes<FLAGS, false, L>(a, fold, now.enter, l.lane, unused);
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                if (FLAGS && (starts >> k & 1)) h = 0.f;
+                before[k] = h;
+                h = fmaf(s.a[k], h, beta[k] * (s.i[k] * s.x[k]));
+            }
+            float gx[K], gi[K], gr[K];
+#pragma unroll
+            for (int k = K - 1; k >= 0; --k) {
+                float lambda = g[k] + pass;
+                pass = s.a[k] * lambda;
+                if (FLAGS && (starts >> k & 1)) pass = 0.f;
+                if (partial && t + k >= at.end) lambda = 0.f;
+                const float gain = s.a[k] * inv[k] * (s.i[k] * s.x[k]);
+                const float e = lambda * (l.slow * s.r[k] * s.a[k] * (gain - before[k]));
+                gx[k] = lambda * beta[k] * s.i[k];
+                gi[k] = gx[k] * s.x[k] * (1.f - s.i[k]);
+                gr[k] = e * (1.f - s.r[k]);
+                if (partial && t + k >= at.end) {
+                    gx[k] = gi[k] = gr[k] = 0.f;
+                } else {
+                    sum_decay += e;
+                    sum_rate += gr[k];
+                    sum_input += gi[k];
+                }
+            }
+            if (l.live) {
+                store_steps<K>(static_cast<E *>(p.grad_x) + row * p.T + t, p.T - t, gx);
+                store_steps<K>(static_cast<E *>(p.grad_input) + row * p.T + t, p.T - t, gi);
+                store_steps<K>(static_cast<E *>(p.grad_decay) + row * p.T + t, p.T - t, gr);
+            }
+            if (last && at.chunk == 0 && p.grad_state != nullptr && l.live && l.lane == 0)
+                p.grad_state[row] = carry;
+        }
+        fresh = last;
+        at = ahead;
+    }
+    if constexpr (!MAPS) {
+#pragma unroll
+        for (int m = 1; m < L; m <<= 1) {
+            sum_decay += __shfl_xor(sum_decay, m);
+            sum_rate += __shfl_xor(sum_rate, m);
+            sum_input += __shfl_xor(sum_input, m);
+        }
+        if (l.live && l.lane == 0) {
+            float *to = p.partials + (int64_t)walker * 3 * p.channels + l.d;
+            to[0] = sum_decay;
+            to[p.channels] = sum_rate;
+            to[2 * (int64_t)p.channels] = sum_input;
+        }
+    }
+}
+
+// The walkers' sums in order: a workgroup takes 64 of the 3 * channels columns, its
+// 16 waves every 16th walker each.
+struct GateSums {
+    const float *partials, *decay;
+    float *grad_decay, *grad_rate, *grad_input;
+    uint32_t walkers, channels;
+    float scale;
+};
+constexpr int kGateSumWaves = 16;
+
+__global__ __launch_bounds__(kGateSumWaves *kWave) void gated_sums(GateSums p) {
+    __shared__ float sums[kGateSumWaves][kWave];
+    const uint32_t wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
+    const uint64_t columns = 3 * (uint64_t)p.channels, c = (uint64_t)blockIdx.x * kWave + lane;
+    float sum = 0.f;
+    if (c < columns)
+#pragma unroll 8
+        for (uint32_t w = wave; w < p.walkers; w += kGateSumWaves) sum += p.partials[w * columns + c];
+    sums[wave][lane] = sum;
+    __syncthreads();
+    if (wave != 0 || c >= columns) return;
+    for (int w = 1; w < kGateSumWaves; ++w) sum += sums[w][lane];
+    if (c < p.channels) {
+        // dL/d(decay): the rate's derivative over the rate, 1 where both underflow
+        const float x = p.decay[c];
+        p.grad_decay[c] = sum * (x < -16.f ? 1.f : sigmoid(x) / softplus(x));
+    } else if (c < 2 * (uint64_t)p.channels) {
+        if (p.grad_rate != nullptr) p.grad_rate[c - p.channels] = sum;
+    } else if (p.grad_input != nullptr) {
+        p.grad_input[c - 2 * (uint64_t)p.channels] = sum;
+    }
+}
+
+// ------------------------------------------------------------------ single steps
+struct GateStepParams {
+    const void *x, *input_gate, *decay_gate;
+    const float *decay, *input_bias, *decay_bias;
+    float *state;
+    const int32_t *slots;
+    const uint8_t *starts;
+    void *out;
+    int64_t x_n, ig_n, dg_n, places;
+    uint32_t num_seqs, channels;
+    float scale;
+};
+
+constexpr int kGateStepThreads = 256;
+
+__device__ __forceinline__ int64_t gate_place(const GateStepParams &p, uint32_t n) {
+    if (n >= p.num_seqs) return -1;
+    if (p.slots == nullptr) return n;
+    const int64_t s = p.slots[n];
+    return s >= 0 && s < p.places ? s : -1;
+}
+
+// A thread takes VEC neighbouring channels of the sequences blockIdx.y, blockIdx.y +
+// gridDim.y, ..., the next one's loads issued before one is computed.
+template <typename E, int VEC>
+__global__ __launch_bounds__(kGateStepThreads) void gated_step(GateStepParams p) {
+    const uint32_t d = (blockIdx.x * blockDim.x + threadIdx.x) * VEC;
+    if (d >= p.channels) return;
+    const int left = p.channels - d < (uint32_t)VEC ? (int)(p.channels - d) : VEC;
+    struct Loads {
+        int64_t place;
+        Steps<VEC, E> x, ig, dg;
+        Steps<VEC, float> h;
+    } next;
+    const auto load = [&](uint32_t n) {
+        next.place = gate_place(p, n);
+        if (next.place < 0) return;
+        next.x.load(static_cast<const E *>(p.x) + n * p.x_n + d, left);
+        next.ig.load(static_cast<const E *>(p.input_gate) + n * p.ig_n + d, left);
+        next.dg.load(static_cast<const E *>(p.decay_gate) + n * p.dg_n + d, left);
+        next.h.load(p.state + next.place * p.channels + d,
+                    p.starts != nullptr && p.starts[n] != 0 ? 0 : left);
+    };
+    load(blockIdx.y);
+    float slow[VEC], ib[VEC] = {}, db[VEC] = {};
+    load_steps<VEC>(p.decay + d, left, slow);
+    if (p.input_bias != nullptr) load_steps<VEC>(p.input_bias + d, left, ib);
+    if (p.decay_bias != nullptr) load_steps<VEC>(p.decay_bias + d, left, db);
+#pragma unroll
+    for (int c = 0; c < VEC; ++c) slow[c] = slow_of(p.scale, slow[c]);
+    for (uint32_t n = blockIdx.y; n < p.num_seqs; n += gridDim.y) {
+        const Loads now = next;
+        if (n + gridDim.y < p.num_seqs) load(n + gridDim.y);
+        float out[VEC] = {};
+        if (now.place >= 0) {
+            float x[VEC], ig[VEC], dg[VEC], h[VEC];
+            now.x.widen(x);
+            now.ig.widen(ig);
+            now.dg.widen(dg);
+            now.h.widen(h);
+#pragma unroll
+            for (int c = 0; c < VEC; ++c) {
+                float a, rest;
+                decay_of<false>(slow[c] * sigmoid(dg[c] + db[c]), a, rest);
+                const float in = __builtin_amdgcn_sqrtf(rest) * (sigmoid(ig[c] + ib[c]) * x[c]);
+                out[c] = fmaf(a, h[c], in);
+            }
+            store_steps<VEC>(p.state + now.place * p.channels + d, left, out);
+        }
+        store_steps<VEC>(static_cast<E *>(p.out) + (int64_t)n * p.channels + d, left, out);
+    }
+}
+
+// ------------------------------------------------------------------- host side
+// Lanes of a row: rows of up to 8 steps take one, up to 32 four.
+static int gate_lanes(int64_t T) { return T <= gate_tile(1) ? 1 : T <= gate_tile(4) ? 4 : 16; }
+
+// Waves that a launch wants; below half of them rows are cut into chunks of at
+// least kFewestTiles tiles, at most kMostChunks.
+constexpr int64_t kGateWanted = 4096;
+constexpr int64_t kFewestTiles = 4;
+constexpr int64_t kMostChunks = 64;
+
+struct GatePlan {
+    int L;
+    int64_t tiles, groups, chunks, chunk_tiles, units, walkers;
+};
+
+static GatePlan gate_plan(const rlca_gated_call &c) {
+    GatePlan g = {};
+    g.L = gate_lanes(c.T);
+    g.tiles = (c.T + gate_tile(g.L) - 1) / gate_tile(g.L);
+    g.groups = (c.channels + kWave / g.L - 1) / (kWave / g.L);
+    g.chunks = 1;
+    const int64_t waves = g.groups * c.num_seqs;
+    if (waves > 0 && waves <= kGateWanted / 2 && g.tiles >= 2 * kFewestTiles) {
+        int64_t want = kGateWanted / waves;
+        if (want > g.tiles / kFewestTiles) want = g.tiles / kFewestTiles;
+        if (want > kMostChunks) want = kMostChunks;
+        g.chunks = want;
+    }
+    g.chunk_tiles = g.chunks == 0 ? 0 : (g.tiles + g.chunks - 1) / g.chunks;
+    if (g.chunk_tiles > 0) g.chunks = (g.tiles + g.chunk_tiles - 1) / g.chunk_tiles;
+    g.units = c.num_seqs * g.chunks;
+    g.walkers = g.groups == 0 ? 0 : (kGateWanted + g.groups - 1) / g.groups;
+    if (g.walkers > g.units) g.walkers = g.units;
+    return g;
+}
+
+static GateParams gate_params(const rlca_gated_call &c, const GatePlan &g) {
+    GateParams p = {};
+    p.x = c.x, p.input_gate = c.input_gate, p.decay_gate = c.decay_gate;
+    p.grad_out = c.grad_out;
+    p.decay = c.decay, p.input_bias = c.input_bias, p.decay_bias = c.decay_bias;
+    p.state = c.state, p.grad_final = c.grad_final_state;
+    p.flags = c.flags, p.lengths = c.lengths;
+    p.out = c.out, p.final_state = c.final_state, p.checkpoints = c.checkpoints;
+    p.grad_x = c.grad_x, p.grad_input = c.grad_input_gate, p.grad_decay = c.grad_decay_gate;
+    p.grad_state = c.grad_state;
+    p.x_n = c.x_stride_seq, p.x_d = c.x_stride_channel;
+    p.ig_n = c.input_stride_seq, p.ig_d = c.input_stride_channel;
+    p.dg_n = c.decay_stride_seq, p.dg_d = c.decay_stride_channel;
+    p.g_n = c.grad_stride_seq, p.g_d = c.grad_stride_channel;
+    p.num_seqs = (uint32_t)c.num_seqs;
+    p.channels = (uint32_t)c.channels;
+    p.groups = (uint32_t)g.groups;
+    p.walkers = (uint32_t)g.walkers;
+    p.units = (uint32_t)g.units;
+    p.chunks = (uint32_t)g.chunks;
+    p.chunk_tiles = (uint32_t)g.chunk_tiles;
+    p.T = (int32_t)c.T;
+    p.tiles = (int32_t)g.tiles;
+    p.after_done = c.convention == RLCA_RESET_AFTER_DONE;
+    p.scale = (float)c.scale;
+    p.by_chunks = fast_div((uint32_t)g.chunks);
+    return p;
+}
+
+template <typename E, bool MAPS, int L>
+static const void *gate_kernel(bool backward, bool flags) {
+    if (backward)
+        return flags ? (const void *)gated_rows_backward<E, true, L, MAPS>
+                     : (const void *)gated_rows_backward<E, false, L, MAPS>;
+    return flags ? (const void *)gated_rows<E, true, L, MAPS>
+                 : (const void *)gated_rows<E, false, L, MAPS>;
+}
+
+// Chunks exist for rows of 16 lanes only.
+template <typename E>
+static const void *gate_kernel(bool backward, bool flags, int L, bool maps) {
+    return maps      ? gate_kernel<E, true, 16>(backward, flags)
+           : L == 16 ? gate_kernel<E, false, 16>(backward, flags)
+           : L == 4  ? gate_kernel<E, false, 4>(backward, flags)
+                     : gate_kernel<E, false, 1>(backward, flags);
+}
+
+static rlca_status gate_launch(const rlca_gated_call &c, const GatePlan &g, GateParams &p,
+                               bool backward, bool maps, hipStream_t stream) {
+    const bool flags = c.flags != nullptr;
+    const void *kernel = c.dtype == RLCA_F32    ? gate_kernel<float>(backward, flags, g.L, maps)
+                         : c.dtype == RLCA_BF16 ? gate_kernel<__bf16>(backward, flags, g.L, maps)
+                                                : gate_kernel<_Float16>(backward, flags, g.L, maps);
+    const uint64_t waves = (uint64_t)g.groups * g.walkers;
+    return launch(kernel, dim3((uint32_t)((waves + kGateWaves - 1) / kGateWaves)), kGateThreads, 0,
+                  p, stream);
+}
+
+static size_t gate_maps_bytes(const rlca_gated_call &c, const GatePlan &g) {
+    return g.chunks > 1 ? (size_t)c.num_seqs * g.chunks * 2 * c.channels * sizeof(float) : 0;
+}
+
+static size_t gate_checkpoints_bytes(const rlca_gated_call &c, const GatePlan &g) {
+    return (size_t)c.num_seqs * c.channels * g.tiles * sizeof(float);
+}
+
+// The launch's threads stay below 2^32, and so do the units.
+static bool gate_sizes_ok(const rlca_gated_call &c) {
+    return sizes_ok(c.num_seqs, c.channels, c.T) && c.channels < (int64_t)1 << 25;
+}
+
+static bool gate_values_ok(int dtype, double scale) {
+    // scale > 0 in float32, so that the decay's gradient has a rate to be relative to
+    return element_bytes(dtype) != 0 && scale >= 1e-30 && scale <= 1e30;
+}
+
+static rlca_status check_gated(const rlca_gated_call &c, bool backward, Arrays &a) {
+    if (!gate_sizes_ok(c)) return RLCA_ERR_INVALID_SIZE;
+    if (!gate_values_ok(c.dtype, c.scale) ||
+        (c.convention != RLCA_RESET_ON_START && c.convention != RLCA_RESET_AFTER_DONE))
+        return RLCA_ERR_INVALID_VALUE;
+    const int64_t N = c.num_seqs, D = c.channels, T = c.T;
+    const size_t e = element_bytes(c.dtype);
+    const int64_t params = N == 0 ? 0 : D;
+    a.in(c.x, e, true, {{N, c.x_stride_seq}, {D, c.x_stride_channel}, {T, 1}});
+    a.in(c.input_gate, e, true, {{N, c.input_stride_seq}, {D, c.input_stride_channel}, {T, 1}});
+    a.in(c.decay_gate, e, true, {{N, c.decay_stride_seq}, {D, c.decay_stride_channel}, {T, 1}});
+    a.in(c.decay, 4, true, {{backward ? D : params, 1}});
+    a.in(c.input_bias, 4, false, {{params, 1}});
+    a.in(c.decay_bias, 4, false, {{params, 1}});
+    a.in(c.state, 4, false, {{N, D}, {D, 1}});
+    a.in(c.flags, 1, false, {{N, T}, {T, 1}});
+    a.in(c.lengths, 4, false, {{N, 1}});
+    return RLCA_OK;
+}
+
+// What the walks' sums become; with no walkers the gradients of empty sums, 0.
+static rlca_status launch_gate_sums(const rlca_gated_call &c, const float *partials,
+                                    uint32_t walkers, hipStream_t stream) {
+    GateSums p = {};
+    p.partials = partials;
+    p.decay = c.decay;
+    p.grad_decay = c.grad_decay;
+    p.grad_rate = c.grad_decay_bias;
+    p.grad_input = c.grad_input_bias;
+    p.walkers = walkers;
+    p.channels = (uint32_t)c.channels;
+    const uint64_t columns = 3 * (uint64_t)c.channels;
+    return launch((const void *)gated_sums, dim3((uint32_t)((columns + kWave - 1) / kWave)),
+                  kGateSumWaves * kWave, 0, p, stream);
+}
+
+// T = 0: the state goes on as it is (to: final_state or grad_state).
+struct CopyParams {
+    const float *from;
+    float *to;
+    uint64_t count;
+};
+
+__global__ __launch_bounds__(256) void gated_copy_state(CopyParams p) {
+    for (uint64_t i = blockIdx.x * 256ull + threadIdx.x; i < p.count; i += gridDim.x * 256ull)
+        p.to[i] = p.from == nullptr ? 0.f : p.from[i];
+}
+
+static rlca_status copy_state(const float *from, float *to, int64_t count, hipStream_t stream) {
+    if (to == nullptr || count == 0) return RLCA_OK;
+    CopyParams p = {from, to, (uint64_t)count};
+    const int64_t blocks = (count + 255) / 256;
+    return launch((const void *)gated_copy_state, dim3((uint32_t)(blocks < 4096 ? blocks : 4096)), 256, 0,
+                  p, stream);
+}
+
+}  // namespace seq
+}  // namespace rlca
+
+using namespace rlca::seq;
+
+extern "C" {
+
+size_t rlca_gated_recurrence_checkpoints_size(const rlca_gated_call *call) {
+    if (call == nullptr || !gate_sizes_ok(*call)) return 0;
+    return gate_checkpoints_bytes(*call, gate_plan(*call));
+}
+
+size_t rlca_gated_recurrence_workspace_size(const rlca_gated_call *call) {
+    if (call == nullptr || !gate_sizes_ok(*call)) return 0;
+    return gate_maps_bytes(*call, gate_plan(*call));
+}
+
+size_t rlca_gated_recurrence_backward_workspace_size(const rlca_gated_call *call) {
+    if (call == nullptr || !gate_sizes_ok(*call)) return 0;
+    const GatePlan g = gate_plan(*call);
+    return gate_maps_bytes(*call, g) + (size_t)g.walkers * 3 * call->channels * sizeof(float);
+}
+
+rlca_status rlca_gated_recurrence(const rlca_gated_call *call, void *workspace,
+                                  size_t workspace_bytes, hipStream_t stream) {
+    if (call == nullptr) return RLCA_ERR_NULL_POINTER;
+    const rlca_gated_call &c = *call;
+    Arrays a;
+    rlca_status st = check_gated(c, false, a);
+    if (st != RLCA_OK) return st;
+    const GatePlan g = gate_plan(c);
+    const int64_t N = c.num_seqs, D = c.channels, T = c.T;
+    const size_t need = gate_maps_bytes(c, g);
+    a.out(c.out, element_bytes(c.dtype), true, {{N, D * T}, {D, T}, {T, 1}});
+    a.out(c.final_state, 4, false, {{N, D}, {D, 1}});
+    a.out(c.checkpoints, 4, false, {{(int64_t)(gate_checkpoints_bytes(c, g) / 4), 1}});
+    a.out(workspace, 4, need != 0, {{(int64_t)(need / 4), 1}});
+    if ((st = a.status()) != RLCA_OK) return st;
+    if (workspace_bytes < need) return RLCA_ERR_INVALID_SIZE;
+    if (N * D == 0) return RLCA_OK;
+    if (T == 0) return copy_state(c.state, c.final_state, N * D, stream);
+    GateParams p = gate_params(c, g);
+    p.maps = static_cast<float *>(workspace);
+    if (g.chunks > 1 && (st = gate_launch(c, g, p, false, true, stream)) != RLCA_OK) return st;
+    return gate_launch(c, g, p, false, false, stream);
+}
+
+rlca_status rlca_gated_recurrence_backward(const rlca_gated_call *call, void *workspace,
+                                           size_t workspace_bytes, hipStream_t stream) {
+    if (call == nullptr) return RLCA_ERR_NULL_POINTER;
+    const rlca_gated_call &c = *call;
+    Arrays a;
+    rlca_status st = check_gated(c, true, a);
+    if (st != RLCA_OK) return st;
+    const GatePlan g = gate_plan(c);
+    const int64_t N = c.num_seqs, D = c.channels, T = c.T;
+    const size_t e = element_bytes(c.dtype), maps = gate_maps_bytes(c, g);
+    const size_t need = maps + (size_t)g.walkers * 3 * D * sizeof(float);
+    a.in(c.grad_out, e, true, {{N, c.grad_stride_seq}, {D, c.grad_stride_channel}, {T, 1}});
+    a.in(c.grad_final_state, 4, false, {{N, D}, {D, 1}});
+    a.in(c.checkpoints, 4, true, {{(int64_t)(gate_checkpoints_bytes(c, g) / 4), 1}});
+    a.out(c.grad_x, e, true, {{N, D * T}, {D, T}, {T, 1}});
+    a.out(c.grad_input_gate, e, true, {{N, D * T}, {D, T}, {T, 1}});
+    a.out(c.grad_decay_gate, e, true, {{N, D * T}, {D, T}, {T, 1}});
+    a.out(c.grad_decay, 4, true, {{D, 1}});
+    a.out(c.grad_input_bias, 4, false, {{D, 1}});
+    a.out(c.grad_decay_bias, 4, false, {{D, 1}});
+    a.out(c.grad_state, 4, false, {{N, D}, {D, 1}});
+    a.out(workspace, 4, need != 0, {{(int64_t)(need / 4), 1}});
+    if ((st = a.status()) != RLCA_OK) return st;
+    if (workspace_bytes < need) return RLCA_ERR_INVALID_SIZE;
+    if (D == 0) return RLCA_OK;
+    GateParams p = gate_params(c, g);
+    p.maps = static_cast<float *>(workspace);
+    p.partials = p.maps + maps / sizeof(float);
+    uint32_t walkers = 0;
+    if (N > 0 && T == 0) {
+        if ((st = copy_state(c.grad_final_state, c.grad_state, N * D, stream)) != RLCA_OK) return st;
+    } else if (N > 0) {
+        walkers = p.walkers;
+        if (g.chunks > 1 && (st = gate_launch(c, g, p, true, true, stream)) != RLCA_OK) return st;
+        if ((st = gate_launch(c, g, p, true, false, stream)) != RLCA_OK) return st;
+    }
+    return launch_gate_sums(c, p.partials, walkers, stream);
+}
+
+rlca_status rlca_gated_step(const rlca_gated_step_call *call, hipStream_t stream) {
+    if (call == nullptr) return RLCA_ERR_NULL_POINTER;
+    const rlca_gated_step_call &c = *call;
+    const int64_t N = c.num_seqs, D = c.channels;
+    if (!sizes_ok(N, D, 1) || c.places < 0 || c.places > INT32_MAX ||
+        (c.slots == nullptr && c.places < N))
+        return RLCA_ERR_INVALID_SIZE;
+    if (!gate_values_ok(c.dtype, c.scale)) return RLCA_ERR_INVALID_VALUE;
+    const size_t e = element_bytes(c.dtype);
+    const int64_t params = N == 0 ? 0 : D;
+    Arrays a;
+    a.in(c.x, e, true, {{N, c.x_stride_seq}, {D, 1}});
+    a.in(c.input_gate, e, true, {{N, c.input_stride_seq}, {D, 1}});
+    a.in(c.decay_gate, e, true, {{N, c.decay_stride_seq}, {D, 1}});
+    a.in(c.decay, 4, true, {{params, 1}});
+    a.in(c.input_bias, 4, false, {{params, 1}});
+    a.in(c.decay_bias, 4, false, {{params, 1}});
+    a.in(c.slots, 4, false, {{N, 1}});
+    a.in(c.starts, 1, false, {{N, 1}});
+    a.out(c.state, 4, N != 0, {{c.places, D}, {D, 1}});
+    a.out(c.out, e, true, {{N, D}, {D, 1}});
+    const rlca_status st = a.status();
+    if (st != RLCA_OK || N * D == 0) return st;
+    GateStepParams p = {};
+    p.x = c.x, p.input_gate = c.input_gate, p.decay_gate = c.decay_gate;
+    p.decay = c.decay, p.input_bias = c.input_bias, p.decay_bias = c.decay_bias;
+    p.state = c.state;
+    p.slots = c.slots;
+    p.starts = c.starts;
+    p.out = c.out;
+    p.x_n = c.x_stride_seq, p.ig_n = c.input_stride_seq, p.dg_n = c.decay_stride_seq;
+    p.places = c.places;
+    p.num_seqs = (uint32_t)N;
+    p.channels = (uint32_t)D;
+    p.scale = (float)c.scale;
+    constexpr int kVec = 4;
+    const bool wide = N * D >= (int64_t)1 << 18;
+    const int vec = wide ? kVec : 1;
+    const uint32_t threads = (uint32_t)((D + vec - 1) / vec);
+    const uint32_t size =
+        threads >= (uint32_t)kGateStepThreads ? kGateStepThreads : (threads + 63) / 64 * 64;
+    const uint32_t across = (threads + size - 1) / size;
+    const uint32_t most = (2048 + across - 1) / across;
+    const int64_t all = N < 32768 ? N : 32768;
+    const void *kernel =
+        c.dtype == RLCA_F32    ? (wide ? (const void *)gated_step<float, kVec>
+                                       : (const void *)gated_step<float, 1>)
+        : c.dtype == RLCA_BF16 ? (wide ? (const void *)gated_step<__bf16, kVec>
+                                       : (const void *)gated_step<__bf16, 1>)
+                               : (wide ? (const void *)gated_step<_Float16, kVec>
+                                       : (const void *)gated_step<_Float16, 1>);
+    return launch(kernel, dim3(across, all < most ? (uint32_t)all : most), size, 0, p, stream);
+}
+
+}  // extern "C"

@@ -680,7 +680,7 @@ rlca_status rlca_gated_step(const rlca_gated_step_call *call, hipStream_t stream
  * and are scaled down where they would overflow.  Steps past a row's length get
  * output, sum, scale and gradient 0.  T = 1 with x_stride_channel = 1 (and the
  * residual's and gradients' too) is the norm of dense rows of channels: a generated
- * token's, or any [tokens, channels] array's.  eps >= 0 and finite. */
+ * token's, or any [tokens, channels] array's.  eps is within 1e-30 .. 1e30. */
 typedef struct {
     int64_t num_seqs, channels, T;
     int32_t dtype;
@@ -705,9 +705,10 @@ typedef struct {
     float *grad_weight; /* [channels], nullable */
 } rlca_norm_call;
 
-size_t rlca_rms_norm_workspace_size(const rlca_norm_call *call);
-rlca_status rlca_rms_norm(const rlca_norm_call *call, void *workspace, size_t workspace_bytes,
-                          hipStream_t stream);
+rlca_status rlca_rms_norm(const rlca_norm_call *call, hipStream_t stream);
+
+/* The gradients: the workspace needs no initialisation, and all sums run in a fixed
+ * order (reproducible bit for bit). */
 size_t rlca_rms_norm_backward_workspace_size(const rlca_norm_call *call);
 rlca_status rlca_rms_norm_backward(const rlca_norm_call *call, void *workspace,
                                    size_t workspace_bytes, hipStream_t stream);

@@ -46,7 +46,11 @@ from .sequence import (  # noqa: F401
 )
 from .blocks import (  # noqa: F401
     GatedGrads,
+    NormGrads,
     gated_recurrence,
     gated_recurrence_backward,
     gated_step,
+    rms_norm,
+    rms_norm_8bit,
+    rms_norm_backward,
 )

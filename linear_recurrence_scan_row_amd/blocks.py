@@ -58,15 +58,32 @@ class GatedStepCall(ctypes.Structure):
     ]
 
 
+class NormCall(ctypes.Structure):
+    """rlca_norm_call of include/rlca.h."""
+
+    _fields_ = [
+        ("num_seqs", _i64), ("channels", _i64), ("T", _i64), ("dtype", _i32), ("eps", _f64),
+        ("x", _p), ("x_stride_seq", _i64), ("x_stride_channel", _i64), ("residual", _p),
+        ("residual_stride_seq", _i64), ("residual_stride_channel", _i64), ("weight", _p),
+        ("lengths", _p), ("out", _p), ("out8", _p), ("scale", _p), ("sum", _p), ("grad_out", _p),
+        ("grad_stride_seq", _i64), ("grad_stride_channel", _i64), ("grad_sum", _p),
+        ("grad_sum_stride_seq", _i64), ("grad_sum_stride_channel", _i64), ("grad_x", _p),
+        ("grad_weight", _p),
+    ]
+
+
 SIGNATURES.update({
     "rlca_gated_recurrence": [_p, _p, _sz, _p],
     "rlca_gated_recurrence_backward": [_p, _p, _sz, _p],
     "rlca_gated_step": [_p, _p],
+    "rlca_rms_norm": [_p, _p],
+    "rlca_rms_norm_backward": [_p, _p, _sz, _p],
 })
 SIZE_QUERIES.update({
     "rlca_gated_recurrence_checkpoints_size": [_p],
     "rlca_gated_recurrence_workspace_size": [_p],
     "rlca_gated_recurrence_backward_workspace_size": [_p],
+    "rlca_rms_norm_backward_workspace_size": [_p],
 })
 
 
@@ -76,7 +93,8 @@ def _packer(cls):
     return struct.Struct("@" + "".join(codes[kind] for _, kind in cls._fields_)).pack
 
 
-_pack_gated, _pack_gated_step = _packer(GatedCall), _packer(GatedStepCall)
+_pack_gated, _pack_gated_step, _pack_norm = (
+    _packer(cls) for cls in (GatedCall, GatedStepCall, NormCall))
 
 
 def _run(name, dev, *args):
@@ -218,3 +236,91 @@ def gated_step(x, input_gate, decay_gate, decay, state, input_bias=None, decay_b
     _run("rlca_gated_step", dev, call)
     _written((state,) if out is None else (state, out))
     return o
+
+
+# -------------------------------------------------------------------- the norm
+class NormGrads(NamedTuple):
+    """Gradients of rms_norm's inputs: of the normed sum (so of x and residual
+    alike) and of the weight, None where there is none."""
+
+    x: torch.Tensor
+    weight: Optional[torch.Tensor]
+
+
+def _rows(name, t, shape, dtype, dev):
+    """An array of the norm: its address and the strides of sequences and
+    channels.  [num_seqs, channels] stands for [num_seqs, channels, 1]."""
+    if t is None:
+        return 0, 0, 0
+    t = _view(name, t, shape, dtype, dev)
+    return t.data_ptr(), t.stride(0), t.stride(1)
+
+
+def _norm_inputs(x, weight, eps, lengths):
+    """The record's fields before x and after the residual, and x's shape."""
+    if x is None or x.dim() not in (2, 3):
+        raise ValueError("x is [num_seqs, channels, T] or [num_seqs, channels]")
+    shape, dev, dtype = _activations("x", x, x.dim())
+    N, D = shape[:2]
+    T = shape[2] if len(shape) == 3 else 1
+    head = (N, D, T, REAL_DTYPES[dtype], float(eps))
+    tail = (_dense_in("weight", weight, (D,), torch.float32, dev),
+            _dense_in("lengths", lengths, (N,), torch.int32, dev))
+    return head, tail, shape, dev, dtype
+
+
+def _norm(x, weight, residual, eps, lengths, total, out, scale, bits8):
+    head, tail, shape, dev, dtype = _norm_inputs(x, weight, eps, lengths)
+    o = _new(out, shape, torch.float8_e4m3fn if bits8 else dtype, dev)
+    sc = _new(scale, (shape[0], *shape[2:]), torch.float32, dev, "scale") if bits8 else None
+    s = None
+    if residual is not None:
+        s = _new(total, shape, dtype, dev, "total")
+    elif total is not None:
+        raise ValueError("total is given without a residual")
+    call = _pack_norm(*head, *_rows("x", x, shape, dtype, dev),
+                      *_rows("residual", residual, shape, dtype, dev), *tail,
+                      0 if bits8 else o.data_ptr(), o.data_ptr() if bits8 else 0, _ptr(sc),
+                      _ptr(s), *(0,) * 8)
+    _run("rlca_rms_norm", dev, call)
+    if out is not None or total is not None or scale is not None:
+        _written_outputs(out, total, scale)
+    return o, sc, s
+
+
+def rms_norm(x, weight=None, residual=None, eps=1e-6, lengths=None, total=None, out=None):
+    """Root-mean-square norm over the channels of each step, after the residual's
+    addition: s = x + residual (as it is stored), s / sqrt(mean(s^2) + eps) * weight.
+
+    x and residual [num_seqs, channels, T] (float32, bfloat16 or float16; time
+    contiguous, other strides free), or [num_seqs, channels] for single steps (any
+    [tokens, channels] array); weight [channels] float32; lengths [num_seqs] int32.
+    Returns (out, s), s None without a residual; rms_norm_backward takes s."""
+    o, _, s = _norm(x, weight, residual, eps, lengths, total, out, None, False)
+    return o, s
+
+
+def rms_norm_8bit(x, weight=None, residual=None, eps=1e-6, lengths=None, total=None, out=None,
+                  scale=None):
+    """rms_norm with its output in 8 bits for a matrix product: (out, scale, s), out
+    float8_e4m3fn like x, scale [num_seqs, T] (or [num_seqs]) float32, the largest
+    magnitude of a step's channels / 448, so that out * scale is the norm."""
+    return _norm(x, weight, residual, eps, lengths, total, out, scale, True)
+
+
+def rms_norm_backward(grad_out, x, weight=None, eps=1e-6, grad_sum=None, lengths=None):
+    """Gradients of rms_norm from its output's gradient: x is what was normed (s, or
+    x where there was no residual), grad_sum the gradient that reaches s itself
+    further on, added to that of the norm.  Returns NormGrads."""
+    head, tail, shape, dev, dtype = _norm_inputs(x, weight, eps, lengths)
+    if grad_out is None:
+        raise ValueError("grad_out is required")
+    grads = NormGrads(x=_new(None, shape, dtype, dev),
+                      weight=None if weight is None else _new(None, shape[1:2], torch.float32, dev))
+    call = _pack_norm(*head, *_rows("x", x, shape, dtype, dev), 0, 0, 0, *tail, 0, 0, 0, 0,
+                      *_rows("grad_out", grad_out, shape, dtype, dev),
+                      *_rows("grad_sum", grad_sum, shape, dtype, dev), grads.x.data_ptr(),
+                      _ptr(grads.weight))
+    ws = _scratch(lib().rlca_rms_norm_backward_workspace_size(call), dev)
+    _run("rlca_rms_norm_backward", dev, call, ws.data_ptr(), ws.numel())
+    return grads

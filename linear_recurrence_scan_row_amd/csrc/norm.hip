@@ -1,0 +1,979 @@
+// norm.hip -- the root-mean-square norm over the channels of each step, with the
+// residual's addition before it, its output in the storage type or in 8 bits with
+// a scale a step, and its gradients:
+//   s = x + residual,  r = 1 / sqrt(mean s^2 + eps),  y = s r weight;
+//   grad_s = r (g w - s r mean(g w s r)) + grad_sum,  grad_weight = sum of g s r.
+//
+// Bound by memory: each value is read once and written once, so what a step's sums
+// are formed of stays in registers until they are known.  Time is contiguous in the
+// rows and the sums run over channels: a workgroup takes a few steps of a
+// sequence, a thread 16 bytes of a channel's steps in `R` channels; where there are
+// more channels than that, the rest are read again (from the caches).  Dense rows of
+// channels (T = 1) take a wave or a workgroup a row.
+#include "seq.hpp"
+
+namespace rlca {
+namespace norm {
+
+using seq::FastDiv;
+using seq::Steps;
+
+struct NormParams {
+    const void *x, *residual, *grad_out, *grad_sum;
+    const float *weight;
+    const int32_t *lengths;
+    void *out, *sum, *grad_x;
+    uint8_t *out8;
+    float *scale;
+    float *partials;  // [workgroups or waves][channels]: sums for grad_weight
+    int64_t x_n, x_d, r_n, r_d, g_n, g_d, s_n, s_d;
+    uint32_t num_seqs, channels;
+    int32_t T;
+    uint32_t tiles;       // of a sequence
+    uint32_t work;        // tiles, or rows, of the call
+    float eps, per_channel;  // 1 / channels
+    FastDiv by_tiles;
+};
+
+// x, without the compiler's knowledge that it is: addresses formed from it are formed
+// where they stand, not kept in registers from an earlier pass over the channels.
+__device__ __forceinline__ uint32_t here(uint32_t x) {
+    asm volatile("" : "+v"(x));
+    return x;
+}
+
+// The same for a block: what was widened for the sums is widened again, not kept.
+template <int K, typename E>
+__device__ __forceinline__ void here(Steps<K, E> &b) {
+    typedef uint32_t words __attribute__((ext_vector_type(sizeof(b.b) / 4)));
+    words w = __builtin_bit_cast(words, b.b);
+    asm volatile("" : "+v"(w));
+    b.b = __builtin_bit_cast(decltype(b.b), w);
+}
+
+// Squares of values from 2^50 on may overflow a sum of float32, so where a thread's
+// sum reaches 2^100 the workgroup forms its sums again, from values times 2^-80 in the
+// steps whose sums do.  (fp16 values end at 2^16.)  `factor` is 2^-80 or 1; r below
+// includes it.
+constexpr float kMuch = 0x1p100f, kDown = 0x1p-80f;
+template <typename E>
+constexpr bool overflows() {
+    return !std::is_same<E, _Float16>::value;
+}
+
+constexpr float kMostE4m3 = 448.f, kLeastScale = 0x1p-120f;
+
+// The largest magnitude, a NaN above all: float32 bits without the sign, as integers.
+__device__ __forceinline__ uint32_t magnitude(float x) {
+    return __builtin_bit_cast(uint32_t, x) & 0x7fffffffu;
+}
+__device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return a > b ? a : b; }
+
+// r, from the sum of squares of values times factor; and a step's scale.
+__device__ __forceinline__ float rsqrt_of(const NormParams &p, float sum, float factor) {
+    return factor * __builtin_amdgcn_rsqf(fmaf(sum, p.per_channel, p.eps * factor * factor));
+}
+__device__ __forceinline__ float scale_of(uint32_t most, float r) {
+    const float s = __builtin_bit_cast(float, most) * r / kMostE4m3;
+    return s < kLeastScale ? kLeastScale : s;  // a NaN stays one
+}
+// What s and the weight are multiplied by for the 8-bit value: 448 / max|s weight|, since
+// r is in both (each rounding left out is a value less that falls on the other side of
+// a border); r / scale at the least scale; NaN where the scale is.
+__device__ __forceinline__ float gain_of(uint32_t most, float factor, float r, float scale) {
+    float g = scale == kLeastScale ? r / kLeastScale
+                                   : kMostE4m3 / __builtin_bit_cast(float, most) * factor;
+    g = g > 3.4e38f ? 3.4e38f : g;  // 0 times it is 0
+    return scale != scale ? scale : g;
+}
+
+// K values in e4m3, rounded to nearest even.  Those of one step are at most 448 up to
+// the rounding of their products, which rounds to 448.
+template <int K>
+__device__ __forceinline__ void store_e4m3(uint8_t *to, int n, const float (&v)[K]) {
+    static_assert(K % 4 == 0, "whole words");
+    uint32_t w[K / 4];
+#pragma unroll
+    for (int j = 0; j < K / 4; ++j) {
+        int q = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * j], v[4 * j + 1], 0, false);
+        q = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * j + 2], v[4 * j + 3], q, true);
+        w[j] = (uint32_t)q;
+    }
+    if (n >= K) {
+        __builtin_memcpy(to, w, K);
+    } else {
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            if (k < n) to[k] = (uint8_t)(w[k / 4] >> (8 * (k % 4)));
+    }
+}
+
+template <int K, typename E>
+__device__ __forceinline__ void clear(Steps<K, E> &b) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) b.b[k] = (E)0.f;
+}
+
+// x + residual as it is stored.
+template <int K, typename E>
+__device__ __forceinline__ void add_residual(Steps<K, E> &b, const Steps<K, E> &r) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) b.b[k] = (E)((float)b.b[k] + (float)r.b[k]);
+}
+
+template <int K, typename E>
+__device__ __forceinline__ void store_block(E *p, int n, const Steps<K, E> &b) {
+    if (n >= K) {
+        __builtin_memcpy(p, &b.b, sizeof b.b);
+    } else {
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            if (k < n) p[k] = b.b[k];
+    }
+}
+
+// ------------------------------------------------------------- rows over time
+// Where a workgroup works: LT threads side by side take VEC = 16 / sizeof(E) steps
+// each, and THREADS / LT channels at a time.
+template <typename E, int THREADS, int LT>
+struct Tile {
+    static constexpr int VEC = 16 / sizeof(E), STEPS = LT * VEC, ACROSS = THREADS / LT,
+                         WAVES = THREADS / kWave;
+    uint32_t n, first;  // the sequence and the thread's first channel
+    int column, t, left, room;  // first step in the tile, in the row; steps that count, that exist
+    __device__ __forceinline__ void set(const NormParams &p, uint32_t tile) {
+        n = p.by_tiles.div(tile);
+        column = (int)(threadIdx.x % LT) * VEC;
+        t = (int)(tile - n * p.tiles) * STEPS + column;
+        first = here(threadIdx.x / LT);
+        left = seq::row_end(p.lengths, n, p.T) - t;
+        room = p.T - t;
+    }
+};
+
+// Sums over the channels of a tile's steps: s over a wave's lanes of one column, then
+// over the waves through LDS.
+template <int VEC, int LT>
+__device__ __forceinline__ void wave_sums(float (&s)[VEC]) {
+#pragma unroll
+    for (int m = LT; m < kWave; m <<= 1)
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) s[k] += __shfl_xor(s[k], m);
+}
+
+template <int VEC, int LT>
+__device__ __forceinline__ void wave_most(uint32_t (&s)[VEC]) {
+#pragma unroll
+    for (int m = LT; m < kWave; m <<= 1)
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) s[k] = larger(s[k], (uint32_t)__shfl_xor((int)s[k], m));
+}
+
+// Any lane of the workgroup: one word a wave in LDS, written before a barrier.
+__device__ __forceinline__ void tell(uint32_t *words, bool x) {
+    const bool any = __builtin_amdgcn_ballot_w64(x) != 0;
+    if (threadIdx.x % kWave == 0) words[threadIdx.x / kWave] = any ? 1u : 0u;
+}
+template <int WAVES>
+__device__ __forceinline__ bool told(const uint32_t *words) {
+    uint32_t any = 0;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) any |= words[w];
+    return __builtin_amdgcn_readfirstlane(any) != 0;
+}
+
+template <typename E, int THREADS, int LT, int R, bool Q8>
+__global__ __launch_bounds__(THREADS) void rms_norm_rows(NormParams p) {
+    typedef Tile<E, THREADS, LT> Mine;
+    constexpr int VEC = Mine::VEC, ACROSS = Mine::ACROSS, WAVES = Mine::WAVES;
+    __shared__ __attribute__((aligned(16))) float sums[WAVES][Mine::STEPS];
+    __shared__ __attribute__((aligned(16))) uint32_t mosts[Q8 ? WAVES : 1][Mine::STEPS];
+    __shared__ uint32_t large[WAVES];
+    Mine at;
+    at.set(p, blockIdx.x);
+    const E *x = static_cast<const E *>(p.x) + at.n * p.x_n + at.t;
+    const E *res = p.residual == nullptr
+                       ? nullptr
+                       : static_cast<const E *>(p.residual) + at.n * p.r_n + at.t;
+    const int64_t to = (int64_t)at.n * p.channels * p.T + at.t;
+    E *sum_out = static_cast<E *>(p.sum) + to;
+
+    // one channel's steps, and their sum stored where there is a residual
+    const auto fetch = [&](uint32_t d, Steps<VEC, E> &b) {
+        b.load(x + d * p.x_d, at.left);
+        if (res != nullptr) {
+            Steps<VEC, E> r;
+            r.load(res + d * p.r_d, at.left);
+            add_residual(b, r);
+            store_block(sum_out + (int64_t)d * p.T, at.room, b);
+        }
+    };
+    // the same again
+    const auto again = [&](uint32_t d, Steps<VEC, E> &b) {
+        b.load(x + d * p.x_d, at.left);
+        if (res != nullptr) {
+            Steps<VEC, E> r;
+            r.load(res + d * p.r_d, at.left);
+            add_residual(b, r);
+        }
+    };
+    const auto weight = [&](uint32_t d) { return p.weight == nullptr ? 1.f : p.weight[d]; };
+
+    Steps<VEC, E> kept[R];
+    float s[VEC] = {};
+    uint32_t most[VEC] = {};
+    float factor[VEC];
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) factor[k] = 1.f;
+    const auto add = [&](const Steps<VEC, E> &b, uint32_t d, bool scaled) {
+        float v[VEC];
+        b.widen(v);
+        const float w = Q8 ? weight(d) : 0.f;
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) {
+            if (scaled) v[k] *= factor[k];
+            s[k] = fmaf(v[k], v[k], s[k]);
+            if constexpr (Q8) most[k] = larger(most[k], magnitude(v[k] * w));
+        }
+    };
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+        const uint32_t d = at.first + j * ACROSS;
+        if (d < p.channels)
+            fetch(d, kept[j]);
+        else
+            clear(kept[j]);
+    }
+    const uint32_t wave = threadIdx.x / kWave;
+    const auto meet = [&] {
+        wave_sums<VEC, LT>(s);
+        if constexpr (Q8) wave_most<VEC, LT>(most);
+        if (threadIdx.x % kWave < LT)
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) {
+                sums[wave][at.column + k] = s[k];
+                if constexpr (Q8) mosts[wave][at.column + k] = most[k];
+            }
+    };
+    const auto all = [&] {
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) s[k] = 0.f, most[k] = 0;
+#pragma unroll 2
+        for (int w = 0; w < WAVES; ++w)
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) {
+                s[k] += sums[w][at.column + k];
+                if constexpr (Q8) most[k] = larger(most[k], mosts[w][at.column + k]);
+            }
+    };
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+        const uint32_t d = at.first + j * ACROSS;
+        if (d < p.channels) add(kept[j], d, false);
+    }
+    for (uint32_t d = at.first + R * ACROSS; d < p.channels; d += ACROSS) {
+        Steps<VEC, E> b;
+        fetch(d, b);
+        add(b, d, false);
+    }
+    if constexpr (overflows<E>()) {
+        bool much = false;
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) much |= s[k] >= kMuch;
+        tell(large, much);
+    }
+    meet();
+    __syncthreads();
+    all();
+    at.first = here(at.first);
+    if (overflows<E>() && told<WAVES>(large)) {
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) {
+            factor[k] = s[k] >= kMuch ? kDown : 1.f;
+            s[k] = 0.f, most[k] = 0;
+        }
+        // read again, so that this costs the usual case no registers
+#pragma unroll 1
+        for (uint32_t d = at.first; d < p.channels; d += ACROSS) {
+            Steps<VEC, E> b;
+            again(d, b);
+            add(b, d, true);
+        }
+        meet();
+        __syncthreads();
+        all();
+    }
+    float r[VEC], scale[VEC];
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) {
+        r[k] = rsqrt_of(p, s[k], factor[k]);
+        if constexpr (Q8) {
+            // `most` has the factor too
+            scale[k] = scale_of(most[k], r[k] / factor[k]);
+            r[k] = gain_of(most[k], factor[k], r[k], scale[k]);
+        }
+    }
+    if constexpr (Q8)
+        if (threadIdx.x < LT)
+#pragma unroll
+            for (int k = 0; k < VEC; ++k)
+                if (k < at.room)
+                    p.scale[(int64_t)at.n * p.T + at.t + k] = k < at.left ? scale[k] : 0.f;
+    at.first = here(at.first);
+#pragma unroll
+    for (int j = 0; j < R; ++j) here(kept[j]);
+    const auto finish = [&](const Steps<VEC, E> &b, uint32_t d) {
+        float v[VEC];
+        b.widen(v);
+        const float w = weight(d);
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) {
+            v[k] = v[k] * r[k] * w;
+            if (k >= at.left) v[k] = 0.f;
+        }
+        if constexpr (Q8)
+            store_e4m3<VEC>(p.out8 + to + (int64_t)d * p.T, at.room, v);
+        else
+            seq::store_steps<VEC>(static_cast<E *>(p.out) + to + (int64_t)d * p.T, at.room, v);
+    };
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+        const uint32_t d = at.first + j * ACROSS;
+        if (d < p.channels) finish(kept[j], d);
+    }
+    for (uint32_t d = at.first + R * ACROSS; d < p.channels; d += ACROSS) {
+        Steps<VEC, E> b;
+        again(d, b);
+        finish(b, d);
+    }
+}
+
+// The gradients: a workgroup walks tiles and keeps its channels' sums for
+// grad_weight, in registers for the channels that it keeps, in its own part of the
+// partial sums for the others.
+template <typename E, int THREADS, int LT, int R>
+__global__ __launch_bounds__(THREADS) void rms_norm_rows_backward(NormParams p) {
+    typedef Tile<E, THREADS, LT> Mine;
+    constexpr int VEC = Mine::VEC, ACROSS = Mine::ACROSS, WAVES = Mine::WAVES;
+    __shared__ __attribute__((aligned(16))) float sums[2][WAVES][Mine::STEPS];
+    __shared__ uint32_t large[WAVES];
+    const auto weight = [&](uint32_t d) { return p.weight == nullptr ? 1.f : p.weight[d]; };
+    float *partial = p.partials + (int64_t)blockIdx.x * p.channels;
+    float grad_weight[R] = {};
+    bool begun = false;
+    for (uint32_t tile = blockIdx.x; tile < p.work; tile += gridDim.x) {
+        Mine at;
+        at.set(p, tile);
+        const E *x = static_cast<const E *>(p.x) + at.n * p.x_n + at.t;
+        const E *go = static_cast<const E *>(p.grad_out) + at.n * p.g_n + at.t;
+        const E *gs = p.grad_sum == nullptr
+                          ? nullptr
+                          : static_cast<const E *>(p.grad_sum) + at.n * p.s_n + at.t;
+        E *to = static_cast<E *>(p.grad_x) + (int64_t)at.n * p.channels * p.T + at.t;
+        Steps<VEC, E> xs[R], gos[R];
+        float s[VEC] = {}, c[VEC] = {}, factor[VEC];
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) factor[k] = 1.f;
+        const auto add = [&](const Steps<VEC, E> &xb, const Steps<VEC, E> &gb, uint32_t d,
+                             bool scaled) {
+            float v[VEC], g[VEC];
+            xb.widen(v);
+            gb.widen(g);
+            const float w = weight(d);
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) {
+                if (scaled) v[k] *= factor[k];
+                s[k] = fmaf(v[k], v[k], s[k]);
+                c[k] = fmaf(v[k], g[k] * w, c[k]);
+            }
+        };
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+            const uint32_t d = at.first + j * ACROSS;
+            if (d < p.channels) {
+                xs[j].load(x + d * p.x_d, at.left);
+                gos[j].load(go + d * p.g_d, at.left);
+            } else {
+                clear(xs[j]);
+                clear(gos[j]);
+            }
+        }
+        const uint32_t wave = threadIdx.x / kWave;
+        const auto meet = [&] {
+            wave_sums<VEC, LT>(s);
+            wave_sums<VEC, LT>(c);
+            if (threadIdx.x % kWave < LT)
+#pragma unroll
+                for (int k = 0; k < VEC; ++k) {
+                    sums[0][wave][at.column + k] = s[k];
+                    sums[1][wave][at.column + k] = c[k];
+                }
+        };
+        const auto all = [&] {
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) s[k] = c[k] = 0.f;
+#pragma unroll 2
+            for (int w = 0; w < WAVES; ++w)
+#pragma unroll
+                for (int k = 0; k < VEC; ++k) {
+                    s[k] += sums[0][w][at.column + k];
+                    c[k] += sums[1][w][at.column + k];
+                }
+        };
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+            const uint32_t d = at.first + j * ACROSS;
+            if (d < p.channels) add(xs[j], gos[j], d, false);
+        }
+        for (uint32_t d = at.first + R * ACROSS; d < p.channels; d += ACROSS) {
+            Steps<VEC, E> xb, gb;
+            xb.load(x + d * p.x_d, at.left);
+            gb.load(go + d * p.g_d, at.left);
+            add(xb, gb, d, false);
+        }
+        __syncthreads();  // the sums of the tile before have been read
+        if constexpr (overflows<E>()) {
+            bool much = false;
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) much |= s[k] >= kMuch;
+            tell(large, much);
+        }
+        meet();
+        __syncthreads();
+        all();
+        at.first = here(at.first);
+        if (overflows<E>() && told<WAVES>(large)) {
+            __syncthreads();
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) {
+                factor[k] = s[k] >= kMuch ? kDown : 1.f;
+                s[k] = c[k] = 0.f;
+            }
+            // read again, so that this costs the usual case no registers
+#pragma unroll 1
+            for (uint32_t d = at.first; d < p.channels; d += ACROSS) {
+                Steps<VEC, E> xb, gb;
+                xb.load(x + d * p.x_d, at.left);
+                gb.load(go + d * p.g_d, at.left);
+                add(xb, gb, d, true);
+            }
+            meet();
+            __syncthreads();
+            all();
+        }
+        float r[VEC];
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) {
+            r[k] = rsqrt_of(p, s[k], factor[k]);
+            c[k] = c[k] * (r[k] / factor[k]) * p.per_channel;  // mean(g w s r)
+        }
+        at.first = here(at.first);
+#pragma unroll
+        for (int j = 0; j < R; ++j) here(xs[j]), here(gos[j]);
+        const auto finish = [&](const Steps<VEC, E> &xb, const Steps<VEC, E> &gb, uint32_t d) {
+            float v[VEC], g[VEC], more[VEC] = {}, total = 0.f;
+            xb.widen(v);
+            gb.widen(g);
+            if (gs != nullptr) seq::load_steps<VEC>(gs + d * p.s_d, at.left, more);
+            const float w = weight(d);
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) {
+                const float xh = v[k] * r[k];
+                const bool counts = k < at.left;
+                total += counts ? g[k] * xh : 0.f;
+                v[k] = counts ? fmaf(r[k], fmaf(g[k], w, -xh * c[k]), more[k]) : 0.f;
+            }
+            seq::store_steps<VEC>(to + (int64_t)d * p.T, at.room, v);
+            return total;
+        };
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+            const uint32_t d = at.first + j * ACROSS;
+            if (d < p.channels) grad_weight[j] += finish(xs[j], gos[j], d);
+        }
+        for (uint32_t d = at.first + R * ACROSS; d < p.channels; d += ACROSS) {
+            Steps<VEC, E> xb, gb;
+            xb.load(x + d * p.x_d, at.left);
+            gb.load(go + d * p.g_d, at.left);
+            float total = finish(xb, gb, d);
+#pragma unroll
+            for (int m = 1; m < LT; m <<= 1) total += __shfl_xor(total, m);
+            if (threadIdx.x % LT == 0) partial[d] = begun ? partial[d] + total : total;
+        }
+        begun = true;
+    }
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+        const uint32_t d = threadIdx.x / LT + j * ACROSS;
+        float total = grad_weight[j];
+#pragma unroll
+        for (int m = 1; m < LT; m <<= 1) total += __shfl_xor(total, m);
+        if (threadIdx.x % LT == 0 && d < p.channels) partial[d] = total;
+    }
+}
+
+// ------------------------------------------------------------- rows of channels
+// WAVES waves of a workgroup take a row: thread i the blocks i, i + 64 WAVES, ... of
+// VEC channels.
+constexpr int kRowThreads = 256;
+
+template <int WAVES>
+__device__ __forceinline__ void row_sums(float &a, float &b, uint32_t &most, float (&lds)[2][4],
+                                         uint32_t (&lds_most)[4]) {
+#pragma unroll
+    for (int m = 1; m < kWave; m <<= 1) {
+        a += __shfl_xor(a, m);
+        b += __shfl_xor(b, m);
+        most = larger(most, (uint32_t)__shfl_xor((int)most, m));
+    }
+    if constexpr (WAVES > 1) {
+        const uint32_t wave = threadIdx.x / kWave;
+        __syncthreads();  // what stood there has been read
+        if (threadIdx.x % kWave == 0) lds[0][wave] = a, lds[1][wave] = b, lds_most[wave] = most;
+        __syncthreads();
+        a = b = 0.f;
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) {
+            a += lds[0][w];
+            b += lds[1][w];
+            most = larger(most, lds_most[w]);
+        }
+    }
+}
+
+template <typename E, int WAVES, int R, bool Q8>
+__global__ __launch_bounds__(kRowThreads) void rms_norm_dense(NormParams p) {
+    constexpr int VEC = 16 / sizeof(E), ROWS = kRowThreads / kWave / WAVES;
+    constexpr uint32_t ACROSS = WAVES * kWave;
+    __shared__ float lds[2][4];
+    __shared__ uint32_t lds_most[4];
+    const uint32_t n = blockIdx.x * ROWS + threadIdx.x / ACROSS;
+    if (n >= p.work) return;  // whole waves, and whole workgroups where waves meet
+    const bool counts = seq::row_end(p.lengths, n, 1) > 0;
+    const int D = counts ? (int)p.channels : 0;
+    const E *x = static_cast<const E *>(p.x) + n * p.x_n;
+    const E *res =
+        p.residual == nullptr ? nullptr : static_cast<const E *>(p.residual) + n * p.r_n;
+    const int64_t to = (int64_t)n * p.channels;
+    const uint32_t blocks = (p.channels + VEC - 1) / VEC, first = threadIdx.x % ACROSS;
+    const auto fetch = [&](uint32_t i, Steps<VEC, E> &b, bool store) {
+        b.load(x + (int64_t)i * VEC, D - (int)i * VEC);
+        if (res != nullptr) {
+            Steps<VEC, E> r;
+            r.load(res + (int64_t)i * VEC, D - (int)i * VEC);
+            add_residual(b, r);
+            if (store)
+                store_block(static_cast<E *>(p.sum) + to + (int64_t)i * VEC,
+                            (int)p.channels - (int)i * VEC, b);
+        }
+    };
+    const auto weights = [&](uint32_t i, float(&w)[VEC]) {
+        if (p.weight != nullptr) {
+            seq::load_steps<VEC>(p.weight + (int64_t)i * VEC, (int)p.channels - (int)i * VEC, w);
+        } else {
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) w[k] = 1.f;
+        }
+    };
+    Steps<VEC, E> kept[R];
+    float s = 0.f, unused = 0.f;
+    uint32_t most = 0;
+    const auto add = [&](const Steps<VEC, E> &b, uint32_t i, float factor) {
+        float v[VEC], w[VEC];
+        b.widen(v);
+        if constexpr (Q8) weights(i, w);
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) {
+            v[k] *= factor;
+            s = fmaf(v[k], v[k], s);
+            if constexpr (Q8) most = larger(most, magnitude(v[k] * w[k]));
+        }
+    };
+#pragma unroll
+    for (int j = 0; j < R; ++j)
+        if (first + j * ACROSS < blocks) fetch(first + j * ACROSS, kept[j], true);
+#pragma unroll
+    for (int j = 0; j < R; ++j)
+        if (first + j * ACROSS < blocks) add(kept[j], first + j * ACROSS, 1.f);
+    for (uint32_t i = first + R * ACROSS; i < blocks; i += ACROSS) {
+        Steps<VEC, E> b;
+        fetch(i, b, true);
+        add(b, i, 1.f);
+    }
+    row_sums<WAVES>(s, unused, most, lds, lds_most);
+    float factor = 1.f;
+    if (overflows<E>() && s >= kMuch) {  // the same in all of a row's threads
+        factor = kDown;
+        s = 0.f;
+        most = 0;
+#pragma unroll
+        for (int j = 0; j < R; ++j)
+            if (first + j * ACROSS < blocks) add(kept[j], first + j * ACROSS, factor);
+        for (uint32_t i = first + R * ACROSS; i < blocks; i += ACROSS) {
+            Steps<VEC, E> b;
+            fetch(i, b, false);
+            add(b, i, factor);
+        }
+        row_sums<WAVES>(s, unused, most, lds, lds_most);
+    }
+    float r = rsqrt_of(p, s, factor);
+    if constexpr (Q8) {
+        const float scale = scale_of(most, r / factor);
+        if (first == 0) p.scale[n] = counts ? scale : 0.f;
+        r = gain_of(most, factor, r, scale);
+    }
+    const auto finish = [&](const Steps<VEC, E> &b, uint32_t i) {
+        float v[VEC], w[VEC];
+        b.widen(v);
+        weights(i, w);
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) v[k] = counts ? v[k] * r * w[k] : 0.f;
+        const int room = (int)p.channels - (int)i * VEC;
+        if constexpr (Q8)
+            store_e4m3<VEC>(p.out8 + to + (int64_t)i * VEC, room, v);
+        else
+            seq::store_steps<VEC>(static_cast<E *>(p.out) + to + (int64_t)i * VEC, room, v);
+    };
+#pragma unroll
+    for (int j = 0; j < R; ++j)
+        if (first + j * ACROSS < blocks) finish(kept[j], first + j * ACROSS);
+    for (uint32_t i = first + R * ACROSS; i < blocks; i += ACROSS) {
+        Steps<VEC, E> b;
+        fetch(i, b, false);
+        finish(b, i);
+    }
+}
+
+// The gradients: a wave, or a workgroup, walks rows.
+template <typename E, int WAVES, int R>
+__global__ __launch_bounds__(kRowThreads) void rms_norm_dense_backward(NormParams p) {
+    constexpr int VEC = 16 / sizeof(E), ROWS = kRowThreads / kWave / WAVES;
+    constexpr uint32_t ACROSS = WAVES * kWave;
+    __shared__ float lds[2][4];
+    __shared__ uint32_t lds_most[4];
+    const uint32_t walker = blockIdx.x * ROWS + threadIdx.x / ACROSS, walkers = gridDim.x * ROWS;
+    const uint32_t blocks = (p.channels + VEC - 1) / VEC, first = threadIdx.x % ACROSS;
+    float *partial = p.partials + (int64_t)walker * p.channels;
+    float grad_weight[R][VEC] = {};
+    const auto weights = [&](uint32_t i, float(&w)[VEC]) {
+        if (p.weight != nullptr) {
+            seq::load_steps<VEC>(p.weight + (int64_t)i * VEC, (int)p.channels - (int)i * VEC, w);
+        } else {
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) w[k] = 1.f;
+        }
+    };
+    bool begun = false;
+    for (uint32_t n = walker; n < p.work; n += walkers) {
+        const bool counts = seq::row_end(p.lengths, n, 1) > 0;
+        const int D = counts ? (int)p.channels : 0;
+        const E *x = static_cast<const E *>(p.x) + n * p.x_n;
+        const E *go = static_cast<const E *>(p.grad_out) + n * p.g_n;
+        const E *gs =
+            p.grad_sum == nullptr ? nullptr : static_cast<const E *>(p.grad_sum) + n * p.s_n;
+        E *to = static_cast<E *>(p.grad_x) + (int64_t)n * p.channels;
+        Steps<VEC, E> xs[R], gos[R];
+        float s = 0.f, c = 0.f;
+        uint32_t unused = 0;
+        const auto fetch = [&](uint32_t i, Steps<VEC, E> &xb, Steps<VEC, E> &gb) {
+            xb.load(x + (int64_t)i * VEC, D - (int)i * VEC);
+            gb.load(go + (int64_t)i * VEC, D - (int)i * VEC);
+        };
+        const auto add = [&](const Steps<VEC, E> &xb, const Steps<VEC, E> &gb, uint32_t i,
+                             float factor) {
+            float v[VEC], g[VEC], w[VEC];
+            xb.widen(v);
+            gb.widen(g);
+            weights(i, w);
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) {
+                v[k] *= factor;
+                s = fmaf(v[k], v[k], s);
+                c = fmaf(v[k], g[k] * w[k], c);
+            }
+        };
+        const auto all_channels = [&](float factor) {
+#pragma unroll
+            for (int j = 0; j < R; ++j)
+                if (first + j * ACROSS < blocks) add(xs[j], gos[j], first + j * ACROSS, factor);
+            for (uint32_t i = first + R * ACROSS; i < blocks; i += ACROSS) {
+                Steps<VEC, E> xb, gb;
+                fetch(i, xb, gb);
+                add(xb, gb, i, factor);
+            }
+            row_sums<WAVES>(s, c, unused, lds, lds_most);
+        };
+#pragma unroll
+        for (int j = 0; j < R; ++j)
+            if (first + j * ACROSS < blocks) fetch(first + j * ACROSS, xs[j], gos[j]);
+        all_channels(1.f);
+        float factor = 1.f;
+        if (overflows<E>() && s >= kMuch) {
+            factor = kDown;
+            s = c = 0.f;
+            all_channels(factor);
+        }
+        const float r = rsqrt_of(p, s, factor);
+        c = c * (r / factor) * p.per_channel;
+        const auto finish = [&](const Steps<VEC, E> &xb, const Steps<VEC, E> &gb, uint32_t i,
+                                float(&total)[VEC]) {
+            float v[VEC], g[VEC], w[VEC], more[VEC] = {};
+            xb.widen(v);
+            gb.widen(g);
+            weights(i, w);
+            if (gs != nullptr)
+                seq::load_steps<VEC>(gs + (int64_t)i * VEC, D - (int)i * VEC, more);
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) {
+                const float xh = v[k] * r;
+                total[k] += counts ? g[k] * xh : 0.f;
+                v[k] = counts ? fmaf(r, fmaf(g[k], w[k], -xh * c), more[k]) : 0.f;
+            }
+            seq::store_steps<VEC>(to + (int64_t)i * VEC, (int)p.channels - (int)i * VEC, v);
+        };
+#pragma unroll
+        for (int j = 0; j < R; ++j)
+            if (first + j * ACROSS < blocks)
+                finish(xs[j], gos[j], first + j * ACROSS, grad_weight[j]);
+        for (uint32_t i = first + R * ACROSS; i < blocks; i += ACROSS) {
+            Steps<VEC, E> xb, gb;
+            fetch(i, xb, gb);
+            float total[VEC] = {};
+            const int room = (int)p.channels - (int)i * VEC;
+            if (begun) seq::load_steps<VEC>(partial + (int64_t)i * VEC, room, total);
+            finish(xb, gb, i, total);
+            seq::store_steps<VEC>(partial + (int64_t)i * VEC, room, total);
+        }
+        begun = true;
+    }
+#pragma unroll
+    for (int j = 0; j < R; ++j)
+        if (first + j * ACROSS < blocks) {
+            const int64_t d = (int64_t)(first + j * ACROSS) * VEC;
+            seq::store_steps<VEC>(partial + d, (int)(p.channels - d), grad_weight[j]);
+        }
+}
+
+// The walkers' sums in order: a workgroup takes 64 channels, its 16 waves every 16th
+// walker each.
+struct SumParams {
+    const float *partials;
+    float *out;
+    uint32_t walkers, channels;
+};
+constexpr int kSumWaves = 16;
+
+__global__ __launch_bounds__(kSumWaves *kWave) void rms_norm_sums(SumParams p) {
+    __shared__ float sums[kSumWaves][kWave];
+    const uint32_t wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
+    const uint32_t d = blockIdx.x * kWave + lane;
+    float sum = 0.f;
+    if (d < p.channels)
+#pragma unroll 8
+        for (uint32_t w = wave; w < p.walkers; w += kSumWaves)
+            sum += p.partials[(int64_t)w * p.channels + d];
+    sums[wave][lane] = sum;
+    __syncthreads();
+    if (wave != 0 || d >= p.channels) return;
+    for (int w = 1; w < kSumWaves; ++w) sum += sums[w][lane];
+    p.out[d] = sum;
+}
+
+// ------------------------------------------------------------------- host side
+// How a call is launched.  Tiles: 64 bytes of a channel's steps side by side (128
+// with fewer channels, 16 where there are too few tiles for the chip).
+struct Shape {
+    bool dense;
+    int threads, lanes;  // time rows: THREADS and LT
+    int waves;           // dense rows: WAVES
+    int64_t tiles, work, groups;
+};
+
+constexpr int64_t kBackwardGroups = 512;  // workgroups that walk in the backward call
+
+static Shape shape_of(const rlca_norm_call &c, bool backward) {
+    Shape s = {};
+    const int64_t N = c.num_seqs, D = c.channels, T = c.T;
+    const int vec = (int)(16 / seq::element_bytes(c.dtype));
+    const auto row = [&](const void *p, int64_t stride) {
+        return p == nullptr || stride == 1 || D <= 1;
+    };
+    s.dense = T == 1 && row(c.x, c.x_stride_channel) &&
+              (backward ? row(c.grad_out, c.grad_stride_channel) &&
+                              row(c.grad_sum, c.grad_sum_stride_channel)
+                        : row(c.residual, c.residual_stride_channel));
+    if (s.dense) {
+        s.waves = D <= 4 * kWave * vec ? 1 : 4;
+        s.work = N;
+        const int64_t rows = 4 / s.waves;
+        s.groups = (N + rows - 1) / rows;
+        if (backward && s.groups > kBackwardGroups) s.groups = kBackwardGroups;
+        return s;
+    }
+    const auto tiles = [&](int lanes) { return (T + lanes * vec - 1) / (lanes * vec); };
+    if (D <= 128) {
+        s.threads = 256, s.lanes = 8;
+    } else {
+        s.threads = backward ? 512 : 1024;
+        s.lanes = N * tiles(4) < 256 ? 1 : D <= 1024 ? 8 : 4;
+    }
+    s.tiles = tiles(s.lanes);
+    s.work = N * s.tiles;
+    s.groups = backward && s.work > kBackwardGroups ? kBackwardGroups : s.work;
+    return s;
+}
+
+template <typename E, bool Q8>
+static const void *forward_kernel(const Shape &s) {
+    if (s.dense)
+        return s.waves == 1 ? (const void *)rms_norm_dense<E, 1, 4, Q8>
+                            : (const void *)rms_norm_dense<E, 4, 4, Q8>;
+    return s.threads == 256  ? (const void *)rms_norm_rows<E, 256, 8, 4, Q8>
+           : s.lanes == 8    ? (const void *)rms_norm_rows<E, 1024, 8, 8, Q8>
+           : s.lanes == 4    ? (const void *)rms_norm_rows<E, 1024, 4, 8, Q8>
+                             : (const void *)rms_norm_rows<E, 1024, 1, 8, Q8>;
+}
+
+template <typename E>
+static const void *backward_kernel(const Shape &s) {
+    if (s.dense)
+        return s.waves == 1 ? (const void *)rms_norm_dense_backward<E, 1, 4>
+                            : (const void *)rms_norm_dense_backward<E, 4, 4>;
+    return s.threads == 256  ? (const void *)rms_norm_rows_backward<E, 256, 8, 4>
+           : s.lanes == 8    ? (const void *)rms_norm_rows_backward<E, 512, 8, 16>
+           : s.lanes == 4    ? (const void *)rms_norm_rows_backward<E, 512, 4, 16>
+                             : (const void *)rms_norm_rows_backward<E, 512, 1, 8>;
+}
+
+// Workgroups are numbered in 32 bits, and their threads too.
+static bool sizes_fit(const rlca_norm_call &c, bool backward) {
+    if (!seq::sizes_ok(c.num_seqs, c.channels, c.T) || seq::element_bytes(c.dtype) == 0) return false;
+    const Shape s = shape_of(c, backward);
+    const int64_t threads = s.dense ? kRowThreads : s.threads;
+    return s.work < (int64_t)1 << 31 && s.groups * threads < (int64_t)1 << 32;
+}
+
+static size_t workspace_bytes_of(const rlca_norm_call &c) {
+    const Shape s = shape_of(c, true);
+    const int64_t walkers = s.dense ? s.groups * (4 / s.waves) : s.groups;
+    return (size_t)walkers * c.channels * sizeof(float);
+}
+
+static NormParams params_of(const rlca_norm_call &c, const Shape &s) {
+    NormParams p = {};
+    p.x = c.x, p.residual = c.residual, p.grad_out = c.grad_out, p.grad_sum = c.grad_sum;
+    p.weight = c.weight;
+    p.lengths = c.lengths;
+    p.out = c.out, p.sum = c.sum, p.grad_x = c.grad_x;
+    p.out8 = c.out8, p.scale = c.scale;
+    p.x_n = c.x_stride_seq, p.x_d = c.x_stride_channel;
+    p.r_n = c.residual_stride_seq, p.r_d = c.residual_stride_channel;
+    p.g_n = c.grad_stride_seq, p.g_d = c.grad_stride_channel;
+    p.s_n = c.grad_sum_stride_seq, p.s_d = c.grad_sum_stride_channel;
+    p.num_seqs = (uint32_t)c.num_seqs;
+    p.channels = (uint32_t)c.channels;
+    p.T = (int32_t)c.T;
+    p.tiles = (uint32_t)(s.dense ? 1 : s.tiles);
+    p.work = (uint32_t)s.work;
+    p.eps = (float)c.eps;
+    p.per_channel = (float)(1.0 / (double)c.channels);
+    p.by_tiles = seq::fast_div(p.tiles);
+    return p;
+}
+
+static rlca_status check_norm(const rlca_norm_call &c, bool backward, seq::Arrays &a) {
+    if (!seq::sizes_ok(c.num_seqs, c.channels, c.T)) return RLCA_ERR_INVALID_SIZE;
+    const size_t e = seq::element_bytes(c.dtype);
+    if (e == 0 || !(c.eps >= 1e-30 && c.eps <= 1e30)) return RLCA_ERR_INVALID_VALUE;
+    if (!sizes_fit(c, backward)) return RLCA_ERR_INVALID_SIZE;
+    const int64_t N = c.num_seqs, D = c.channels, T = c.T;
+    a.in(c.x, e, true, {{N, c.x_stride_seq}, {D, c.x_stride_channel}, {T, 1}});
+    a.in(c.weight, 4, false, {{N * T == 0 ? 0 : D, 1}});
+    a.in(c.lengths, 4, false, {{N, 1}});
+    return RLCA_OK;
+}
+
+}  // namespace norm
+}  // namespace rlca
+
+using namespace rlca::norm;
+using rlca::kWave;
+using rlca::seq::Arrays;
+using rlca::seq::element_bytes;
+using rlca::seq::launch;
+
+extern "C" {
+
+size_t rlca_rms_norm_backward_workspace_size(const rlca_norm_call *call) {
+    if (call == nullptr || !sizes_fit(*call, true)) return 0;
+    return workspace_bytes_of(*call);
+}
+
+rlca_status rlca_rms_norm(const rlca_norm_call *call, hipStream_t stream) {
+    if (call == nullptr) return RLCA_ERR_NULL_POINTER;
+    const rlca_norm_call &c = *call;
+    Arrays a;
+    rlca_status st = check_norm(c, false, a);
+    if (st != RLCA_OK) return st;
+    const int64_t N = c.num_seqs, D = c.channels, T = c.T;
+    const size_t e = element_bytes(c.dtype);
+    if (N * D != 0 && T != 0 && (c.out == nullptr) == (c.out8 == nullptr))
+        return c.out == nullptr ? RLCA_ERR_NULL_POINTER : RLCA_ERR_INVALID_VALUE;
+    a.in(c.residual, e, false,
+         {{N, c.residual_stride_seq}, {D, c.residual_stride_channel}, {T, 1}});
+    a.out(c.out, e, false, {{N, D * T}, {D, T}, {T, 1}});
+    a.out(c.out8, 1, false, {{N, D * T}, {D, T}, {T, 1}});
+    a.out(c.scale, 4, c.out8 != nullptr, {{D == 0 ? 0 : N, T}, {T, 1}});
+    a.out(c.sum, e, c.residual != nullptr, {{N, D * T}, {D, T}, {T, 1}});
+    if ((st = a.status()) != RLCA_OK || N * D == 0 || T == 0) return st;
+    const Shape s = shape_of(c, false);
+    NormParams p = params_of(c, s);
+    const bool q8 = c.out8 != nullptr;
+    const void *kernel =
+        c.dtype == RLCA_F32    ? (q8 ? forward_kernel<float, true>(s) : forward_kernel<float, false>(s))
+        : c.dtype == RLCA_BF16 ? (q8 ? forward_kernel<__bf16, true>(s)
+                                     : forward_kernel<__bf16, false>(s))
+                               : (q8 ? forward_kernel<_Float16, true>(s)
+                                     : forward_kernel<_Float16, false>(s));
+    return launch(kernel, dim3((uint32_t)s.groups), s.dense ? kRowThreads : s.threads, 0, p, stream);
+}
+
+rlca_status rlca_rms_norm_backward(const rlca_norm_call *call, void *workspace,
+                                   size_t workspace_bytes, hipStream_t stream) {
+    if (call == nullptr) return RLCA_ERR_NULL_POINTER;
+    const rlca_norm_call &c = *call;
+    Arrays a;
+    rlca_status st = check_norm(c, true, a);
+    if (st != RLCA_OK) return st;
+    const int64_t N = c.num_seqs, D = c.channels, T = c.T;
+    const size_t e = element_bytes(c.dtype), need = workspace_bytes_of(c);
+    a.in(c.grad_out, e, true, {{N, c.grad_stride_seq}, {D, c.grad_stride_channel}, {T, 1}});
+    a.in(c.grad_sum, e, false,
+         {{N, c.grad_sum_stride_seq}, {D, c.grad_sum_stride_channel}, {T, 1}});
+    a.out(c.grad_x, e, true, {{N, D * T}, {D, T}, {T, 1}});
+    a.out(c.grad_weight, 4, false, {{D, 1}});
+    a.out(workspace, 4, need != 0, {{(int64_t)(need / 4), 1}});
+    if ((st = a.status()) != RLCA_OK) return st;
+    if (workspace_bytes < need) return RLCA_ERR_INVALID_SIZE;
+    if (D == 0) return RLCA_OK;
+    uint32_t walkers = 0;
+    if (N * T != 0) {
+        const Shape s = shape_of(c, true);
+        NormParams p = params_of(c, s);
+        p.partials = static_cast<float *>(workspace);
+        walkers = (uint32_t)(s.dense ? s.groups * (4 / s.waves) : s.groups);
+        const void *kernel = c.dtype == RLCA_F32    ? backward_kernel<float>(s)
+                             : c.dtype == RLCA_BF16 ? backward_kernel<__bf16>(s)
+                                                    : backward_kernel<_Float16>(s);
+        st = launch(kernel, dim3((uint32_t)s.groups), s.dense ? kRowThreads : s.threads, 0, p,
+                    stream);
+        if (st != RLCA_OK) return st;
+    }
+    if (c.grad_weight == nullptr) return RLCA_OK;
+    SumParams sum = {static_cast<const float *>(workspace), c.grad_weight, walkers, (uint32_t)D};
+    return launch((const void *)rms_norm_sums, dim3((uint32_t)((D + kWave - 1) / kWave)),
+                  kSumWaves * kWave, 0, sum, stream);
+}
+
+}  // extern "C"

@@ -126,3 +126,62 @@ def gated(x, input_gate, decay_gate, decay, input_bias=None, decay_bias=None, sc
     s, s_e = total(rate_g, rate_m, rate_e)
     res["decay"] = (s * ratio, s_e * ratio + 24 * U * (s * ratio).abs())
     return res
+
+
+EPS = 1e-6
+
+
+def rms_norm(x, weight=None, residual=None, eps=EPS, lengths=None, grad_out=None, grad_sum=None):
+    """Over dimension 1 of [N, D, T] or [N, D].  The counts: a sum over D channels D / 32
+    + 16 (a thread's serial part, and the lanes and waves that meet), its root's
+    reciprocal half of that and 4; each further product or sum 1; a sum over
+    sequences and steps one for each."""
+    dims = x.dim()
+    dtype = x.dtype
+    total = x if residual is None else x + residual  # one rounding, as it is stored
+    s = d64(total)
+    if dims == 2:
+        s = s.unsqueeze(2)
+    N, D, T = s.shape
+    inside = (torch.arange(T)[None] < ends_of(lengths, N, T)[:, None])[:, None].expand(N, D, T)
+    s = torch.where(inside, s, 0.0)
+    w = torch.ones(D, dtype=torch.float64) if weight is None else d64(weight)
+    w = w[:, None]
+    n = D / 32 + 16
+    r = 1 / torch.sqrt((s * s).mean(1, keepdim=True) + eps)
+    er = n / 2 * U + 4 * U
+    xh = s * r
+    y = torch.where(inside, xh * w, 0.0)
+    y_e = y.abs() * (er + 3 * U)
+
+    def back(v, e):
+        return (v, e) if dims == 3 else (v.squeeze(2), e.squeeze(2))
+
+    most = y.abs().amax(1) if D > 0 else torch.zeros(N, T, dtype=torch.float64)
+    scale = torch.where(inside[:, 0] if D > 0 else torch.zeros(N, T, dtype=torch.bool),
+                        torch.clamp(most / 448, min=2.0 ** -120), 0.0)
+    scale_e = scale * (er + 5 * U)
+    # one rounding to e4m3: half of its step, 2^-4 of the value or 2^-10 below the
+    # smallest normal one
+    q_e = y_e + (y.abs() + y_e) * 2.0 ** -4 + 2.0 ** -10 * (scale + scale_e)[:, None]
+    res = {"out": back(y, y_e), "sum": back(s, torch.zeros_like(s)),
+           "dequantized": back(y, q_e),
+           "scale": (scale, scale_e) if dims == 3 else (scale[:, 0], scale_e[:, 0])}
+    if grad_out is None:
+        return res
+    g = d64(grad_out).reshape(N, D, T)
+    g = torch.where(inside, g, 0.0)
+    gw = g * w
+    c, c_m = (gw * xh).mean(1, keepdim=True), (gw * xh).abs().mean(1, keepdim=True)
+    c_e = c_m * (er + (n + 4) * U)
+    gx = r * (gw - xh * c)
+    gx_e = r * (gw.abs() * (er + 3 * U) + xh.abs() * (c.abs() * (2 * er + 4 * U) + c_e))
+    if grad_sum is not None:
+        gs = torch.where(inside, d64(grad_sum).reshape(N, D, T), 0.0)
+        gx = gx + gs
+        gx_e = gx_e + U * gs.abs()
+    gx, gx_e = torch.where(inside, gx, 0.0), torch.where(inside, gx_e, 0.0)
+    res["x"] = back(gx, gx_e)
+    terms = (g * xh).abs().sum((0, 2))
+    res["weight"] = ((g * xh).sum((0, 2)), terms * (er + 2 * U + N * T * U))
+    return res

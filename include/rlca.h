@@ -716,15 +716,16 @@ rlca_status rlca_rms_norm_backward(const rlca_norm_call *call, void *workspace,
 /* A beam search's selection.  For each of num_searches searches, over all `beams`
  * beams and `vocab` tokens, the `picks` candidates with the highest
  *   total = score_b + (logit_bv - log sum_v exp(logit_bv)),
- * best first, equal ones by beam and then token (the lower first).  Sums are formed
- * so that totals are good to 2^-40 or so before the one rounding to float32, and
- * they are compared before it.  A beam that is finished has one candidate, pad_token
+ * best first, equal ones by beam and then token (the lower first).  Exponentials are
+ * float32, their sums over a beam and the totals float64: totals are good to 1e-6,
+ * and they are compared before the one rounding to float32.  A beam that is finished has one candidate, pad_token
  * at its own score; its other totals are -infinity.  So are all totals of a beam
  * whose score is -infinity (an unused one: its logits do not count, whatever they
  * hold) and those of logits of -infinity (tokens that are not allowed; all of them
- * may be).  A logit of NaN or +infinity makes all totals of its beam NaN, as a NaN
- * score does, and NaN ranks first.  beams and picks are 1 .. RLCA_MAX_BEAMS, picks at
- * most beams * vocab, beams * vocab < 2^31. */
+ * may be).  A NaN or +infinity among a beam's logits, or as its score, makes its
+ * totals NaN, and NaN ranks first.  beams and picks are 1 .. RLCA_MAX_BEAMS, picks at
+ * most beams * vocab, beams * vocab < 2^31, and num_searches * beams *
+ * ceil(vocab / 8192) < 2^24. */
 #define RLCA_MAX_BEAMS 64
 
 typedef struct {

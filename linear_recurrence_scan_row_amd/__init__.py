@@ -45,8 +45,11 @@ from .sequence import (  # noqa: F401
     selective_step,
 )
 from .blocks import (  # noqa: F401
+    BeamChoice,
     GatedGrads,
     NormGrads,
+    beam_reorder,
+    beam_select,
     gated_recurrence,
     gated_recurrence_backward,
     gated_step,

@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import struct
+from array import array
 from typing import NamedTuple, Optional
 
 import torch
@@ -23,6 +24,8 @@ from .sequence import (
     _activations, _dense_in, _flags_in, _new, _new_step, _ptr, _scratch, _view, _written,
     _written_outputs,
 )
+
+MAX_BEAMS = 64
 
 _i32 = ctypes.c_int32
 _i64 = ctypes.c_int64
@@ -72,18 +75,38 @@ class NormCall(ctypes.Structure):
     ]
 
 
+class BeamCall(ctypes.Structure):
+    """rlca_beam_call of include/rlca.h."""
+
+    _fields_ = [
+        ("num_searches", _i64), ("beams", _i64), ("vocab", _i64), ("picks", _i32),
+        ("dtype", _i32), ("pad_token", _i32), ("logits", _p), ("logits_stride_search", _i64),
+        ("logits_stride_beam", _i64), ("scores", _p), ("finished", _p), ("out_scores", _p),
+        ("out_tokens", _p), ("out_parents", _p),
+    ]
+
+
+class StatePool(ctypes.Structure):
+    """rlca_state_pool of include/rlca.h."""
+
+    _fields_ = [("data", _p), ("place_bytes", _i64)]
+
+
 SIGNATURES.update({
     "rlca_gated_recurrence": [_p, _p, _sz, _p],
     "rlca_gated_recurrence_backward": [_p, _p, _sz, _p],
     "rlca_gated_step": [_p, _p],
     "rlca_rms_norm": [_p, _p],
     "rlca_rms_norm_backward": [_p, _p, _sz, _p],
+    "rlca_beam_select": [_p, _p, _sz, _p],
+    "rlca_beam_reorder": [_p, _i64, _i64, _i64, _i64, _p, _p, _p, _p],
 })
 SIZE_QUERIES.update({
     "rlca_gated_recurrence_checkpoints_size": [_p],
     "rlca_gated_recurrence_workspace_size": [_p],
     "rlca_gated_recurrence_backward_workspace_size": [_p],
     "rlca_rms_norm_backward_workspace_size": [_p],
+    "rlca_beam_select_workspace_size": [_p],
 })
 
 
@@ -93,8 +116,8 @@ def _packer(cls):
     return struct.Struct("@" + "".join(codes[kind] for _, kind in cls._fields_)).pack
 
 
-_pack_gated, _pack_gated_step, _pack_norm = (
-    _packer(cls) for cls in (GatedCall, GatedStepCall, NormCall))
+_pack_gated, _pack_gated_step, _pack_norm, _pack_beam = (
+    _packer(cls) for cls in (GatedCall, GatedStepCall, NormCall, BeamCall))
 
 
 def _run(name, dev, *args):
@@ -324,3 +347,90 @@ def rms_norm_backward(grad_out, x, weight=None, eps=1e-6, grad_sum=None, lengths
     ws = _scratch(lib().rlca_rms_norm_backward_workspace_size(call), dev)
     _run("rlca_rms_norm_backward", dev, call, ws.data_ptr(), ws.numel())
     return grads
+
+
+# ----------------------------------------------------------------- beam search
+class BeamChoice(NamedTuple):
+    """A selection, best first, [num_searches, picks]: total log probabilities
+    (float32), tokens and the beams that they continue (int32)."""
+
+    scores: torch.Tensor
+    tokens: torch.Tensor
+    parents: torch.Tensor
+
+
+def beam_select(logits, scores, picks=None, finished=None, pad_token=0):
+    """The best continuations of each search, over all its beams and the vocabulary:
+    the `picks` (default: one a beam) highest of score + log_softmax(logits), equal
+    ones by the lower beam, then the lower token.
+
+    logits [num_searches, beams, vocab] (float32, bfloat16 or float16; contiguous in
+    its last dimension), scores [num_searches, beams] float32 the beams' totals so
+    far (-infinity for a beam that is not in use).  finished [num_searches, beams]
+    marks beams that go on with pad_token alone, at their own score.  Returns
+    BeamChoice."""
+    shape = logits.shape
+    if len(shape) != 3:
+        raise ValueError("logits is [num_searches, beams, vocab]")
+    if not logits.is_cuda:
+        raise ValueError("inputs must be GPU tensors")
+    dtype, dev = logits.dtype, logits.device
+    if dtype not in REAL_DTYPES:
+        raise TypeError(f"logits must be float32, bfloat16 or float16, got {dtype}")
+    logits = _view("logits", logits, shape, dtype, dev)
+    N, K, V = shape
+    if not 1 <= K <= MAX_BEAMS:
+        raise ValueError(f"{K} beams, expected 1 to {MAX_BEAMS}")
+    P = K if picks is None else int(picks)
+    if not 1 <= P <= min(MAX_BEAMS, K * V):
+        raise ValueError(f"{P} picks, expected 1 to {min(MAX_BEAMS, K * V)}")
+    if scores is None:
+        raise ValueError("scores is required")
+    head = (N, K, V, P, REAL_DTYPES[dtype], int(pad_token), logits.data_ptr(), logits.stride(0),
+            logits.stride(1), _dense_in("scores", scores, (N, K), torch.float32, dev),
+            0 if finished is None else _flags_in(finished, (N, K), dev))
+    # one allocation: the scores' bits and the whole numbers are of one size
+    out = torch.empty((3, N, P), dtype=torch.int32, device=dev)
+    choice = BeamChoice(out[0].view(torch.float32), out[1], out[2])
+    call = _pack_beam(*head, *(t.data_ptr() for t in choice))
+    ws = _scratch(lib().rlca_beam_select_workspace_size(call), dev)
+    _run("rlca_beam_select", dev, call, ws.data_ptr(), ws.numel())
+    return choice
+
+
+def beam_reorder(pools, slots, parents, out=None):
+    """The beams' states after a selection, in place in every pool: beam k of a search
+    goes on from the state of its beam parents[k].
+
+    pools is a list of tensors [places, ...] of any types, dense (as the single-step
+    calls keep them); slots [num_searches, beams] int32 each beam's place in them,
+    all different (one out of range holds no state); parents [num_searches, beams]
+    int32.  A parent's first child keeps its place, the others' states are copied to
+    places of beams without children.  Returns the new slots."""
+    pools = list(pools)
+    if slots is None or slots.dim() != 2:
+        raise ValueError("slots is [num_searches, beams]")
+    if not slots.is_cuda:
+        raise ValueError("inputs must be GPU tensors")
+    N, K = slots.shape
+    dev = slots.device
+    if not 1 <= K <= MAX_BEAMS:
+        raise ValueError(f"{K} beams, expected 1 to {MAX_BEAMS}")
+    s = _dense_in("slots", slots, (N, K), torch.int32, dev)
+    if parents is None:
+        raise ValueError("parents is required")
+    f = _dense_in("parents", parents, (N, K), torch.int32, dev)
+    places = pools[0].shape[0] if pools and pools[0].dim() > 0 else 0
+    packed = array("q", [0]) * (2 * len(pools))
+    for i, t in enumerate(pools):
+        if t.dim() == 0 or t.shape[0] != places:
+            raise ValueError(f"pools[{i}] has shape {tuple(t.shape)}, expected {places} places")
+        if t.get_device() != dev.index or not t.is_contiguous():
+            raise ValueError(f"pools[{i}] must be contiguous and on {dev}")
+        packed[2 * i] = t.data_ptr()
+        packed[2 * i + 1] = t[0].numel() * t.element_size() if places > 0 else 0
+    o = _new(out, (N, K), torch.int32, dev)
+    _run("rlca_beam_reorder", dev, packed.buffer_info()[0], len(pools), N, K, places, s, f,
+         o.data_ptr())
+    _written(pools if out is None else [*pools, out])
+    return o

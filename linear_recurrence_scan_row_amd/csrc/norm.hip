@@ -61,6 +61,10 @@ constexpr bool overflows() {
     return !std::is_same<E, _Float16>::value;
 }
 
+constexpr int kBatch = 2;  // channels whose loads are issued together
+template <int N>
+using Count = std::integral_constant<int, N>;
+
 constexpr float kMostE4m3 = 448.f, kLeastScale = 0x1p-120f;
 
 // The largest magnitude, a NaN above all: float32 bits without the sign, as integers.
@@ -133,6 +137,14 @@ __device__ __forceinline__ void store_block(E *p, int n, const Steps<K, E> &b) {
 }
 
 // ------------------------------------------------------------- rows over time
+// The tile of workgroup i of n: workgroups go to the 8 XCDs in turn, and tiles side by
+// side share cache lines where a row is not aligned or a tile is narrower than a line,
+// so each XCD gets a run of tiles.
+__device__ __forceinline__ uint32_t near(uint32_t i, uint32_t n) {
+    const uint32_t run = n / 8;
+    return i < 8 * run ? i % 8 * run + i / 8 : i;
+}
+
 // Where a workgroup works: LT threads side by side take VEC = 16 / sizeof(E) steps
 // each, and THREADS / LT channels at a time.
 template <typename E, int THREADS, int LT>
@@ -141,7 +153,8 @@ struct Tile {
                          WAVES = THREADS / kWave;
     uint32_t n, first;  // the sequence and the thread's first channel
     int column, t, left, room;  // first step in the tile, in the row; steps that count, that exist
-    __device__ __forceinline__ void set(const NormParams &p, uint32_t tile) {
+    __device__ __forceinline__ void set(const NormParams &p, uint32_t i) {
+        const uint32_t tile = near(i, p.work);
         n = p.by_tiles.div(tile);
         column = (int)(threadIdx.x % LT) * VEC;
         t = (int)(tile - n * p.tiles) * STEPS + column;
@@ -198,24 +211,27 @@ __global__ __launch_bounds__(THREADS) void rms_norm_rows(NormParams p) {
     const int64_t to = (int64_t)at.n * p.channels * p.T + at.t;
     E *sum_out = static_cast<E *>(p.sum) + to;
 
-    // one channel's steps, and their sum stored where there is a residual
-    const auto fetch = [&](uint32_t d, Steps<VEC, E> &b) {
-        b.load(x + d * p.x_d, at.left);
-        if (res != nullptr) {
-            Steps<VEC, E> r;
-            r.load(res + d * p.r_d, at.left);
-            add_residual(b, r);
-            store_block(sum_out + (int64_t)d * p.T, at.room, b);
-        }
-    };
-    // the same again
-    const auto again = [&](uint32_t d, Steps<VEC, E> &b) {
-        b.load(x + d * p.x_d, at.left);
-        if (res != nullptr) {
-            Steps<VEC, E> r;
-            r.load(res + d * p.r_d, at.left);
-            add_residual(b, r);
-        }
+    // kBatch channels' steps, every load issued before the first value is used; their
+    // sums are stored the first time
+    const auto fetch_batch = [&](uint32_t d, auto *b, auto count, bool store) {
+        constexpr int N = decltype(count)::value;
+#pragma unroll
+        for (int u = 0; u < N; ++u)
+            if (d + u * ACROSS < p.channels)
+                b[u].load(x + (d + u * ACROSS) * p.x_d, at.left);
+            else
+                clear(b[u]);
+        if (res == nullptr) return;
+        Steps<VEC, E> r[N];
+#pragma unroll
+        for (int u = 0; u < N; ++u)
+            if (d + u * ACROSS < p.channels) r[u].load(res + (d + u * ACROSS) * p.r_d, at.left);
+#pragma unroll
+        for (int u = 0; u < N; ++u)
+            if (d + u * ACROSS < p.channels) {
+                add_residual(b[u], r[u]);
+                if (store) store_block(sum_out + (int64_t)(d + u * ACROSS) * p.T, at.room, b[u]);
+            }
     };
     const auto weight = [&](uint32_t d) { return p.weight == nullptr ? 1.f : p.weight[d]; };
 
@@ -237,13 +253,8 @@ __global__ __launch_bounds__(THREADS) void rms_norm_rows(NormParams p) {
         }
     };
 #pragma unroll
-    for (int j = 0; j < R; ++j) {
-        const uint32_t d = at.first + j * ACROSS;
-        if (d < p.channels)
-            fetch(d, kept[j]);
-        else
-            clear(kept[j]);
-    }
+    for (int j = 0; j < R; j += kBatch)
+        fetch_batch(at.first + j * ACROSS, kept + j, Count<kBatch>{}, true);
     const uint32_t wave = threadIdx.x / kWave;
     const auto meet = [&] {
         wave_sums<VEC, LT>(s);
@@ -271,10 +282,12 @@ __global__ __launch_bounds__(THREADS) void rms_norm_rows(NormParams p) {
         const uint32_t d = at.first + j * ACROSS;
         if (d < p.channels) add(kept[j], d, false);
     }
-    for (uint32_t d = at.first + R * ACROSS; d < p.channels; d += ACROSS) {
-        Steps<VEC, E> b;
-        fetch(d, b);
-        add(b, d, false);
+    for (uint32_t d = at.first + R * ACROSS; d < p.channels; d += kBatch * ACROSS) {
+        Steps<VEC, E> b[kBatch];
+        fetch_batch(d, b, Count<kBatch>{}, true);
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u)
+            if (d + u * ACROSS < p.channels) add(b[u], d + u * ACROSS, false);
     }
     if constexpr (overflows<E>()) {
         bool much = false;
@@ -296,9 +309,9 @@ __global__ __launch_bounds__(THREADS) void rms_norm_rows(NormParams p) {
         // read again, so that this costs the usual case no registers
 #pragma unroll 1
         for (uint32_t d = at.first; d < p.channels; d += ACROSS) {
-            Steps<VEC, E> b;
-            again(d, b);
-            add(b, d, true);
+            Steps<VEC, E> b[1];
+            fetch_batch(d, b, Count<1>{}, false);
+            add(b[0], d, true);
         }
         meet();
         __syncthreads();
@@ -342,10 +355,12 @@ __global__ __launch_bounds__(THREADS) void rms_norm_rows(NormParams p) {
         const uint32_t d = at.first + j * ACROSS;
         if (d < p.channels) finish(kept[j], d);
     }
-    for (uint32_t d = at.first + R * ACROSS; d < p.channels; d += ACROSS) {
-        Steps<VEC, E> b;
-        again(d, b);
-        finish(b, d);
+    for (uint32_t d = at.first + R * ACROSS; d < p.channels; d += kBatch * ACROSS) {
+        Steps<VEC, E> b[kBatch];
+        fetch_batch(d, b, Count<kBatch>{}, false);
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u)
+            if (d + u * ACROSS < p.channels) finish(b[u], d + u * ACROSS);
     }
 }
 
@@ -356,11 +371,13 @@ template <typename E, int THREADS, int LT, int R>
 __global__ __launch_bounds__(THREADS) void rms_norm_rows_backward(NormParams p) {
     typedef Tile<E, THREADS, LT> Mine;
     constexpr int VEC = Mine::VEC, ACROSS = Mine::ACROSS, WAVES = Mine::WAVES;
+    static_assert(R % kBatch == 0, "whole batches");
     __shared__ __attribute__((aligned(16))) float sums[2][WAVES][Mine::STEPS];
     __shared__ uint32_t large[WAVES];
     const auto weight = [&](uint32_t d) { return p.weight == nullptr ? 1.f : p.weight[d]; };
     float *partial = p.partials + (int64_t)blockIdx.x * p.channels;
-    float grad_weight[R] = {};
+    constexpr int kKept = R > 0 ? R : 1;
+    float grad_weight[kKept] = {};
     bool begun = false;
     for (uint32_t tile = blockIdx.x; tile < p.work; tile += gridDim.x) {
         Mine at;
@@ -371,7 +388,7 @@ __global__ __launch_bounds__(THREADS) void rms_norm_rows_backward(NormParams p) 
                           ? nullptr
                           : static_cast<const E *>(p.grad_sum) + at.n * p.s_n + at.t;
         E *to = static_cast<E *>(p.grad_x) + (int64_t)at.n * p.channels * p.T + at.t;
-        Steps<VEC, E> xs[R], gos[R];
+        Steps<VEC, E> xs[kKept], gos[kKept];
         float s[VEC] = {}, c[VEC] = {}, factor[VEC];
 #pragma unroll
         for (int k = 0; k < VEC; ++k) factor[k] = 1.f;
@@ -388,17 +405,30 @@ __global__ __launch_bounds__(THREADS) void rms_norm_rows_backward(NormParams p) 
                 c[k] = fmaf(v[k], g[k] * w, c[k]);
             }
         };
+        const auto fetch_batch = [&](uint32_t d, auto &xb, auto &gb) {
+            constexpr int N = sizeof(xb) / sizeof(xb[0]);
 #pragma unroll
-        for (int j = 0; j < R; ++j) {
-            const uint32_t d = at.first + j * ACROSS;
-            if (d < p.channels) {
-                xs[j].load(x + d * p.x_d, at.left);
-                gos[j].load(go + d * p.g_d, at.left);
-            } else {
-                clear(xs[j]);
-                clear(gos[j]);
+            for (int u = 0; u < N; ++u) {
+                const uint32_t e = d + u * ACROSS;
+                if (e < p.channels) {
+                    xb[u].load(x + e * p.x_d, at.left);
+                    gb[u].load(go + e * p.g_d, at.left);
+                } else {
+                    clear(xb[u]);
+                    clear(gb[u]);
+                }
             }
-        }
+        };
+        const auto fetch_more = [&](uint32_t d, auto &more) {
+            constexpr int N = sizeof(more) / sizeof(more[0]);
+#pragma unroll
+            for (int u = 0; u < N; ++u)
+                if (gs != nullptr && d + u * ACROSS < p.channels)
+                    more[u].load(gs + (d + u * ACROSS) * p.s_d, at.left);
+                else
+                    clear(more[u]);
+        };
+        if constexpr (R > 0) fetch_batch(at.first, xs, gos);
         const uint32_t wave = threadIdx.x / kWave;
         const auto meet = [&] {
             wave_sums<VEC, LT>(s);
@@ -426,11 +456,12 @@ __global__ __launch_bounds__(THREADS) void rms_norm_rows_backward(NormParams p) 
             const uint32_t d = at.first + j * ACROSS;
             if (d < p.channels) add(xs[j], gos[j], d, false);
         }
-        for (uint32_t d = at.first + R * ACROSS; d < p.channels; d += ACROSS) {
-            Steps<VEC, E> xb, gb;
-            xb.load(x + d * p.x_d, at.left);
-            gb.load(go + d * p.g_d, at.left);
-            add(xb, gb, d, false);
+        for (uint32_t d = at.first + R * ACROSS; d < p.channels; d += kBatch * ACROSS) {
+            Steps<VEC, E> xb[kBatch], gb[kBatch];
+            fetch_batch(d, xb, gb);
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u)
+                if (d + u * ACROSS < p.channels) add(xb[u], gb[u], d + u * ACROSS, false);
         }
         __syncthreads();  // the sums of the tile before have been read
         if constexpr (overflows<E>()) {
@@ -471,11 +502,12 @@ __global__ __launch_bounds__(THREADS) void rms_norm_rows_backward(NormParams p) 
         at.first = here(at.first);
 #pragma unroll
         for (int j = 0; j < R; ++j) here(xs[j]), here(gos[j]);
-        const auto finish = [&](const Steps<VEC, E> &xb, const Steps<VEC, E> &gb, uint32_t d) {
-            float v[VEC], g[VEC], more[VEC] = {}, total = 0.f;
+        const auto finish = [&](const Steps<VEC, E> &xb, const Steps<VEC, E> &gb,
+                                const Steps<VEC, E> &mb, uint32_t d) {
+            float v[VEC], g[VEC], more[VEC], total = 0.f;
             xb.widen(v);
             gb.widen(g);
-            if (gs != nullptr) seq::load_steps<VEC>(gs + d * p.s_d, at.left, more);
+            mb.widen(more);
             const float w = weight(d);
 #pragma unroll
             for (int k = 0; k < VEC; ++k) {
@@ -488,18 +520,28 @@ __global__ __launch_bounds__(THREADS) void rms_norm_rows_backward(NormParams p) 
             return total;
         };
 #pragma unroll
-        for (int j = 0; j < R; ++j) {
-            const uint32_t d = at.first + j * ACROSS;
-            if (d < p.channels) grad_weight[j] += finish(xs[j], gos[j], d);
-        }
-        for (uint32_t d = at.first + R * ACROSS; d < p.channels; d += ACROSS) {
-            Steps<VEC, E> xb, gb;
-            xb.load(x + d * p.x_d, at.left);
-            gb.load(go + d * p.g_d, at.left);
-            float total = finish(xb, gb, d);
+        for (int j = 0; j < R; j += kBatch) {
+            Steps<VEC, E> more[kBatch];
+            fetch_more(at.first + j * ACROSS, more);
 #pragma unroll
-            for (int m = 1; m < LT; m <<= 1) total += __shfl_xor(total, m);
-            if (threadIdx.x % LT == 0) partial[d] = begun ? partial[d] + total : total;
+            for (int u = 0; u < kBatch; ++u) {
+                const uint32_t d = at.first + (j + u) * ACROSS;
+                if (d < p.channels) grad_weight[j + u] += finish(xs[j + u], gos[j + u], more[u], d);
+            }
+        }
+        for (uint32_t d = at.first + R * ACROSS; d < p.channels; d += kBatch * ACROSS) {
+            Steps<VEC, E> xb[kBatch], gb[kBatch], more[kBatch];
+            fetch_batch(d, xb, gb);
+            fetch_more(d, more);
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                const uint32_t e = d + u * ACROSS;
+                if (e >= p.channels) continue;
+                float total = finish(xb[u], gb[u], more[u], e);
+#pragma unroll
+                for (int m = 1; m < LT; m <<= 1) total += __shfl_xor(total, m);
+                if (threadIdx.x % LT == 0) partial[e] = begun ? partial[e] + total : total;
+            }
         }
         begun = true;
     }
@@ -781,8 +823,7 @@ __global__ __launch_bounds__(kSumWaves *kWave) void rms_norm_sums(SumParams p) {
 }
 
 // ------------------------------------------------------------------- host side
-// How a call is launched.  Tiles: 64 bytes of a channel's steps side by side (128
-// with fewer channels, 16 where there are too few tiles for the chip).
+// How a call is launched.
 struct Shape {
     bool dense;
     int threads, lanes;  // time rows: THREADS and LT
@@ -812,12 +853,12 @@ static Shape shape_of(const rlca_norm_call &c, bool backward) {
         return s;
     }
     const auto tiles = [&](int lanes) { return (T + lanes * vec - 1) / (lanes * vec); };
-    if (D <= 128) {
-        s.threads = 256, s.lanes = 8;
-    } else {
-        s.threads = backward ? 512 : 1024;
-        s.lanes = N * tiles(4) < 256 ? 1 : D <= 1024 ? 8 : 4;
-    }
+    // 128 bytes of a channel's steps side by side, a whole cache line (64 bytes: 78 us
+    // against 58 forward and 101 against 80 backward for 8x2048 channels of 2048 steps,
+    // bf16 with residual).  64 with more channels than registers hold then (4096 of 1024
+    // steps: 70 against 94, and 99 against 115).  16 where there are too few tiles.
+    s.lanes = N * tiles(8) < 128 ? 1 : D <= 2048 ? 8 : 4;
+    s.threads = s.lanes != 8 || D > 512 ? 1024 : D > 128 ? 512 : 256;
     s.tiles = tiles(s.lanes);
     s.work = N * s.tiles;
     s.groups = backward && s.work > kBackwardGroups ? kBackwardGroups : s.work;
@@ -829,21 +870,26 @@ static const void *forward_kernel(const Shape &s) {
     if (s.dense)
         return s.waves == 1 ? (const void *)rms_norm_dense<E, 1, 4, Q8>
                             : (const void *)rms_norm_dense<E, 4, 4, Q8>;
-    return s.threads == 256  ? (const void *)rms_norm_rows<E, 256, 8, 4, Q8>
-           : s.lanes == 8    ? (const void *)rms_norm_rows<E, 1024, 8, 8, Q8>
-           : s.lanes == 4    ? (const void *)rms_norm_rows<E, 1024, 4, 8, Q8>
-                             : (const void *)rms_norm_rows<E, 1024, 1, 8, Q8>;
+    return s.threads == 256 ? (const void *)rms_norm_rows<E, 256, 8, 4, Q8>
+           : s.threads == 512 ? (const void *)rms_norm_rows<E, 512, 8, 8, Q8>
+           : s.lanes == 8     ? (const void *)rms_norm_rows<E, 1024, 8, Q8 ? 14 : 16, Q8>
+           : s.lanes == 4     ? (const void *)rms_norm_rows<E, 1024, 4, Q8 ? 14 : 16, Q8>
+                              : (const void *)rms_norm_rows<E, 1024, 1, 4, Q8>;
 }
 
+// Both arrays of the backward call do not fit the registers from 1024 channels on; few
+// are kept there, since what is read again matters less than waves to hide it (2048
+// channels: 2 blocks a thread 80 us, 8 86, 16 and half the threads 87).
 template <typename E>
 static const void *backward_kernel(const Shape &s) {
     if (s.dense)
         return s.waves == 1 ? (const void *)rms_norm_dense_backward<E, 1, 4>
                             : (const void *)rms_norm_dense_backward<E, 4, 4>;
-    return s.threads == 256  ? (const void *)rms_norm_rows_backward<E, 256, 8, 4>
-           : s.lanes == 8    ? (const void *)rms_norm_rows_backward<E, 512, 8, 16>
-           : s.lanes == 4    ? (const void *)rms_norm_rows_backward<E, 512, 4, 16>
-                             : (const void *)rms_norm_rows_backward<E, 512, 1, 8>;
+    return s.threads == 256 ? (const void *)rms_norm_rows_backward<E, 256, 8, 4>
+           : s.threads == 512 ? (const void *)rms_norm_rows_backward<E, 512, 8, 8>
+           : s.lanes == 8     ? (const void *)rms_norm_rows_backward<E, 1024, 8, 2>
+           : s.lanes == 4     ? (const void *)rms_norm_rows_backward<E, 1024, 4, 2>
+                              : (const void *)rms_norm_rows_backward<E, 1024, 1, 2>;
 }
 
 // Workgroups are numbered in 32 bits, and their threads too.

@@ -872,8 +872,8 @@ static const void *forward_kernel(const Shape &s) {
                             : (const void *)rms_norm_dense<E, 4, 4, Q8>;
     return s.threads == 256 ? (const void *)rms_norm_rows<E, 256, 8, 4, Q8>
            : s.threads == 512 ? (const void *)rms_norm_rows<E, 512, 8, 8, Q8>
-           : s.lanes == 8     ? (const void *)rms_norm_rows<E, 1024, 8, Q8 ? 14 : 16, Q8>
-           : s.lanes == 4     ? (const void *)rms_norm_rows<E, 1024, 4, Q8 ? 14 : 16, Q8>
+           : s.lanes == 8     ? (const void *)rms_norm_rows<E, 1024, 8, Q8 ? 12 : 16, Q8>
+           : s.lanes == 4     ? (const void *)rms_norm_rows<E, 1024, 4, Q8 ? 12 : 16, Q8>
                               : (const void *)rms_norm_rows<E, 1024, 1, 4, Q8>;
 }
 

@@ -1,17 +1,18 @@
-// gated.hip -- the gated linear recurrence over rows of T steps, its gradients,
+// seq_gated.hip -- the gated linear recurrence over rows of T steps, its gradients,
 // and its single step:
 //   r = sigmoid(decay_gate + decay_bias),  i = sigmoid(input_gate + input_bias),
 //   L = scale softplus(decay) r,  a = exp(-L),
 //   h_t = a_t h_{t-1} + sqrt(1 - a_t^2) i_t x_t.
 //
-// The affine recurrence of this library, one state a channel.  A row of 16, 4 or
+// The affine recurrence of this library, one state a channel.  A row of 64, 16, 4 or
 // 1 lanes owns a channel and a tile of 8 steps a lane: each lane folds its 8 maps
 // into one, lane-crossing moves scan the maps, and each lane applies its own steps
-// again from the state that enters it.  A wave owns 4, 16 or 64 neighbouring
+// again from the state that enters it.  A wave owns 1, 4, 16 or 64 neighbouring
 // channels and walks tiles and then sequences, the next tile's loads issued before
-// this one is computed.  Where there are few rows a row is cut into chunks: one
-// launch leaves each chunk's map, the second starts each chunk from the maps
-// before it.
+// this one is computed.  Where there are few rows, the waves of a workgroup share a
+// row, tile after tile, and hand their maps to each other through LDS; where there are
+// very few, a row is cut into chunks: one launch leaves each chunk's map, the second
+// starts each chunk from the maps before it.
 #include "seq_scan.hpp"
 
 namespace rlca {
@@ -34,11 +35,11 @@ struct GateParams {
     void *grad_x, *grad_input, *grad_decay;
     float *grad_state;
     float *maps;      // [num_seqs][chunks][2][channels]: each chunk's map
-    float *partials;  // [walkers][3][channels]: sums for decay, decay_bias, input_bias
+    float *partials;  // [walkers * WAVES][3][channels]: sums for decay, decay_bias, input_bias
     int64_t x_n, x_d, ig_n, ig_d, dg_n, dg_d, g_n, g_d;
     uint32_t num_seqs, channels;
     uint32_t groups;      // waves that share a sequence's channels
-    uint32_t walkers;     // waves that share a group's sequences and chunks
+    uint32_t walkers;     // waves (or workgroups) that share a group's sequences and chunks
     uint32_t units;       // num_seqs * chunks
     uint32_t chunks, chunk_tiles;
     int32_t T, tiles;
@@ -59,17 +60,25 @@ __device__ __forceinline__ float slow_of(float scale, float decay) {
 // would lose digits, so up to 1/2 it is L times the polynomial that interpolates
 // (1 - exp(-L)) / L there at 6 Chebyshev points (error 1.5e-9), and a is 1 minus it;
 // from there on a is the exponential, and the difference of at least 0.39 loses none.
-// SMALL: no L of the wave is above 1/2.
-template <bool SMALL>
+// SLOW: no L of the wave's channels is above 1/8, where 4 points do (error 3.2e-8).
+constexpr float kSlow = 0.125f;
+template <bool SLOW>
 __device__ __forceinline__ void decay_of(float L, float &a, float &rest) {
-    float d = fmaf(L, -0.0011234042f, 0.0081896136f);
-    d = fmaf(L, d, -0.041630073f);
-    d = fmaf(L, d, 0.16666242f);
-    d = fmaf(L, d, -0.49999982f);
-    d = fmaf(L, d, 1.f);
+    float d;
+    if constexpr (SLOW) {
+        d = fmaf(L, -0.039641775f, 0.16650987f);
+        d = fmaf(L, d, -0.4999961f);
+        d = fmaf(L, d, 1.f);
+    } else {
+        d = fmaf(L, -0.0011234042f, 0.0081896136f);
+        d = fmaf(L, d, -0.041630073f);
+        d = fmaf(L, d, 0.16666242f);
+        d = fmaf(L, d, -0.49999982f);
+        d = fmaf(L, d, 1.f);
+    }
     d *= L;
     a = 1.f - d;
-    if constexpr (!SMALL) {
+    if constexpr (!SLOW) {
         const float e = exp2_fast(-L * kLog2e);
         a = L > 0.5f ? e : a;
         d = L > 0.5f ? 1.f - e : d;
@@ -80,6 +89,15 @@ __device__ __forceinline__ void decay_of(float L, float &a, float &rest) {
 // Inclusive scan of the lane maps of a row of L lanes, towards higher lanes or,
 // REVERSE, towards lower ones; lanes whose source is outside the row keep theirs.
 // CUT as for step_map: an episode start's a is -0.
+//
+// Without cuts a step of 16 lanes is two instructions, an FMA and a product that fetch
+// their operand from the other lane themselves, and a wait: the hardware wants two
+// instructions between a write and the lane-crossing read of it.
+#define RLCA_GATE_STEP(MOVE, ROWS)                                    \
+    "v_fmac_f32_dpp %1, %1, %0 " MOVE " row_mask:" ROWS " bank_mask:0xf\n\t" \
+    "v_mul_f32_dpp %0, %0, %0 " MOVE " row_mask:" ROWS " bank_mask:0xf\n\t"  \
+    "s_nop 1\n\t"
+
 template <bool CUT, bool REVERSE, int L>
 __device__ __forceinline__ void lanes_scan(float &a, float &h, int lane) {
     if constexpr (L == 4) {
@@ -93,37 +111,99 @@ __device__ __forceinline__ void lanes_scan(float &a, float &h, int lane) {
         };
         step(std::integral_constant<int, 1>{});
         step(std::integral_constant<int, 2>{});
-    } else if constexpr (L == 16) {
-        const auto step = [&](auto by) {
-            constexpr int kCtrl = shift_ctrl<16, REVERSE, decltype(by)::value>();
-            const float ph = dpp_move<kCtrl, 0xf>(h, 0.f), pa = dpp_move<kCtrl, 0xf>(a, 1.f);
+    } else if constexpr (L >= 16) {
+        const auto step = [&](auto ctrl, auto rows) {
+            constexpr int kCtrl = decltype(ctrl)::value, kRows = decltype(rows)::value;
+            const float ph = dpp_move<kCtrl, kRows>(h, 0.f), pa = dpp_move<kCtrl, kRows>(a, 1.f);
             h = step_map<CUT>(a, h, ph);
             a = product<CUT>(a, pa);
         };
-        step(std::integral_constant<int, 1>{});
-        step(std::integral_constant<int, 2>{});
-        step(std::integral_constant<int, 4>{});
-        step(std::integral_constant<int, 8>{});
+        if constexpr (CUT) {
+            const std::integral_constant<int, 0xf> all;
+            step(std::integral_constant<int, shift_ctrl<16, REVERSE, 1>()>{}, all);
+            step(std::integral_constant<int, shift_ctrl<16, REVERSE, 2>()>{}, all);
+            step(std::integral_constant<int, shift_ctrl<16, REVERSE, 4>()>{}, all);
+            step(std::integral_constant<int, shift_ctrl<16, REVERSE, 8>()>{}, all);
+        } else if constexpr (REVERSE) {
+            asm("s_nop 1\n\t" RLCA_GATE_STEP("row_shl:1", "0xf") RLCA_GATE_STEP("row_shl:2", "0xf")
+                    RLCA_GATE_STEP("row_shl:4", "0xf") RLCA_GATE_STEP("row_shl:8", "0xf")
+                : "+v"(a), "+v"(h));
+        } else {
+            asm("s_nop 1\n\t" RLCA_GATE_STEP("row_shr:1", "0xf") RLCA_GATE_STEP("row_shr:2", "0xf")
+                    RLCA_GATE_STEP("row_shr:4", "0xf") RLCA_GATE_STEP("row_shr:8", "0xf")
+                : "+v"(a), "+v"(h));
+        }
+        if constexpr (L == 64 && !REVERSE) {
+            // the runs of 16 lanes: the last lane of the first and third to the next run,
+            // then the last lane of the second to both others
+            if constexpr (CUT) {
+                step(std::integral_constant<int, 0x142>{}, std::integral_constant<int, 0xa>{});
+                step(std::integral_constant<int, 0x143>{}, std::integral_constant<int, 0xc>{});
+            } else {
+                asm("s_nop 1\n\t" RLCA_GATE_STEP("row_bcast:15", "0xa")
+                        RLCA_GATE_STEP("row_bcast:31", "0xc")
+                    : "+v"(a), "+v"(h));
+            }
+        } else if constexpr (L == 64) {
+            // the maps of the runs after each run, from the first lanes of those
+            float na = read_lane(a, 48), nh = read_lane(h, 48);
+            const int run = lane / 16;
+            float ra = run == 2 ? na : 1.f, rh = run == 2 ? nh : 0.f;
+#pragma unroll
+            for (int at = 2; at > 0; --at) {
+                const float pa = read_lane(a, 16 * at), ph = read_lane(h, 16 * at);
+                nh = step_map<CUT>(pa, ph, nh);
+                na = product<CUT>(pa, na);
+                ra = run == at - 1 ? na : ra;
+                rh = run == at - 1 ? nh : rh;
+            }
+            h = step_map<CUT>(a, h, rh);
+            a = product<CUT>(a, ra);
+        }
     }
 }
+#undef RLCA_GATE_STEP
 
-// What enters each lane of a row from the lane before it, and the row's whole map
-// applied to `enter`: the value that leaves the row.
-template <bool CUT, bool REVERSE, int L>
-__device__ __forceinline__ float enter_lanes(float a, float h, float enter, int lane, float &leave) {
-    if constexpr (L == 1) {
-        leave = step_map<CUT>(a, h, enter);
-        return enter;
-    } else {
-        lanes_scan<CUT, REVERSE, L>(a, h, lane);
-        const float after = step_map<CUT>(a, h, enter);
-        leave = row_last<REVERSE, L>(after);
-        return row_shift<REVERSE, L>(after, enter, lane);
+// The value of the row's last lane in scan order, in all its lanes.
+template <bool REVERSE, int L>
+__device__ __forceinline__ float last_lane(float x) {
+    if constexpr (L == 64) return read_lane(x, REVERSE ? 0 : 63);
+    if constexpr (L == 1) return x;
+    return row_last<REVERSE, L>(x);
+}
+
+// The lane's scanned map applied to what enters the row, moved on by one lane: what
+// enters each lane.
+template <bool REVERSE, int L>
+__device__ __forceinline__ float next_lane(float after, float enter, int lane) {
+    if constexpr (L == 64) return dpp_move<(REVERSE ? 0x130 : 0x138), 0xf>(after, enter);
+    if constexpr (L == 1) return enter;
+    return row_shift<REVERSE, L>(after, enter, lane);
+}
+
+// What enters a wave's tile, from the maps of the WAVES waves whose tiles lie side by
+// side (REVERSE: from the last to the first), and what leaves them all.  The slots of
+// LDS alternate, so one barrier a tile is enough.
+template <bool CUT, bool REVERSE, int WAVES>
+__device__ __forceinline__ float enter_wave(float a, float h, float (&lds)[2][WAVES][2], int &parity,
+                                            int wave, float &carry) {
+    if (threadIdx.x % kWave == 0) lds[parity][wave][0] = a, lds[parity][wave][1] = h;
+    __syncthreads();
+    float x = carry, enter = carry;
+#pragma unroll
+    for (int i = 0; i < WAVES; ++i) {
+        const int w = REVERSE ? WAVES - 1 - i : i;
+        if (w == wave) enter = x;
+        x = step_map<CUT>(lds[parity][w][0], lds[parity][w][1], x);
     }
+    parity ^= 1;
+    carry = x;
+    return enter;
 }
 
 // ------------------------------------------------------------------- the walk
-// Where a wave stands: a unit (a sequence's chunk) and a tile of it.
+// Where a workgroup (or a wave, where they work apart) stands: a unit, which is a
+// sequence's chunk, and a tile of it, or as many tiles side by side as waves share it.
 struct Place {
     uint32_t unit, n, chunk;
     int tile, end;  // end: the sequence's steps that count
@@ -137,9 +217,11 @@ struct Place {
     __device__ __forceinline__ int first(const GateParams &p) const {
         return (int)(chunk * p.chunk_tiles);
     }
-    __device__ __forceinline__ int past(const GateParams &p) const {
-        const int x = (int)((chunk + 1) * p.chunk_tiles);
-        return x < p.tiles ? x : p.tiles;
+    // the last tile of the unit, of those that begin a step of the walk
+    __device__ __forceinline__ int last(const GateParams &p, int waves) const {
+        const int past = (int)((chunk + 1) * p.chunk_tiles);
+        const int tiles = (past < p.tiles ? past : p.tiles) - first(p);
+        return first(p) + (tiles - 1) / waves * waves;
     }
 };
 
@@ -147,8 +229,9 @@ struct Place {
 struct GateLane {
     uint32_t d;
     int lane;
-    bool live;
-    float slow, input_bias, decay_bias;
+    bool live, slow_only;  // slow_only: all the wave's channels decay slowly
+    float slow;            // scale softplus(decay)
+    float input2, decay2;  // -log2(e) times the biases
     template <int L>
     __device__ __forceinline__ static GateLane of(const GateParams &p, uint32_t group) {
         GateLane l;
@@ -158,36 +241,35 @@ struct GateLane {
         l.live = d < p.channels;
         l.d = l.live ? d : p.channels - 1;
         l.slow = slow_of(p.scale, p.decay[l.d]);
-        l.input_bias = p.input_bias == nullptr ? 0.f : p.input_bias[l.d];
-        l.decay_bias = p.decay_bias == nullptr ? 0.f : p.decay_bias[l.d];
+        l.slow_only = whole_wave(l.slow <= kSlow);
+        l.input2 = p.input_bias == nullptr ? 0.f : -kLog2e * p.input_bias[l.d];
+        l.decay2 = p.decay_bias == nullptr ? 0.f : -kLog2e * p.decay_bias[l.d];
         return l;
     }
 };
 
 // A lane's episode starts in its steps from t on, as bits; none from `end` on.
 __device__ __forceinline__ uint32_t gate_starts(const GateParams &p, uint32_t n, int t, int end) {
+    if (t >= end) return 0;
     uint32_t s = start_bits<kGateK>(p.flags + (int64_t)n * p.T, t, p.T, p.after_done);
-    if (t + kGateK > end) s &= t < end ? (1u << (end - t)) - 1 : 0u;
+    if (t + kGateK > end) s &= (1u << (end - t)) - 1;
     return s;
 }
 
-// A lane's 8 steps: the gates, and the maps (a, b) of the recurrence.
+// sigmoid(x + bias), shift = -log2(e) bias.
+__device__ __forceinline__ float gate_of(float x, float shift) {
+    return __builtin_amdgcn_rcpf(1.f + exp2_fast(fmaf(x, -kLog2e, shift)));
+}
+
+// A lane's 8 steps: the gates, and a and 1 - a^2 of the recurrence's maps.
 struct GateSteps {
-    float x[kGateK], i[kGateK], r[kGateK], a[kGateK], rest[kGateK];
+    float r[kGateK], a[kGateK], rest[kGateK];
     template <typename E>
-    __device__ __forceinline__ void make(const GateLane &l, const Steps<kGateK, E> &xs,
-                                         const Steps<kGateK, E> &igs, const Steps<kGateK, E> &dgs) {
-        xs.widen(x);
-        igs.widen(i);
+    __device__ __forceinline__ void decays(const GateLane &l, const Steps<kGateK, E> &dgs) {
         dgs.widen(r);
-        bool small = true;
 #pragma unroll
-        for (int k = 0; k < kGateK; ++k) {
-            i[k] = sigmoid(i[k] + l.input_bias);
-            r[k] = sigmoid(r[k] + l.decay_bias);
-            small &= l.slow * r[k] <= 0.5f;
-        }
-        if (whole_wave(small)) {
+        for (int k = 0; k < kGateK; ++k) r[k] = gate_of(r[k], l.decay2);
+        if (l.slow_only) {
 #pragma unroll
             for (int k = 0; k < kGateK; ++k) decay_of<true>(l.slow * r[k], a[k], rest[k]);
         } else {
@@ -196,6 +278,14 @@ struct GateSteps {
         }
     }
 };
+
+template <typename E>
+__device__ __forceinline__ void input_gates(const GateLane &l, const Steps<kGateK, E> &igs,
+                                            float (&i)[kGateK]) {
+    igs.widen(i);
+#pragma unroll
+    for (int k = 0; k < kGateK; ++k) i[k] = gate_of(i[k], l.input2);
+}
 
 // The state that enters a chunk: the row's state through the maps of the chunks
 // before it.  (REVERSE: the gradient that enters from the chunks after it.)
@@ -213,17 +303,34 @@ __device__ __forceinline__ float enter_chunk(const GateParams &p, uint32_t n, ui
     return x;
 }
 
+// Whether the step after a sequence's last one starts an episode: no state leaves it.
+template <bool FLAGS>
+__device__ __forceinline__ bool ends_over(const GateParams &p, uint32_t n, int end) {
+    return FLAGS && p.after_done && end > 0 && p.flags[(int64_t)n * p.T + end - 1] != 0;
+}
+
+constexpr int threads_of(int waves) { return waves > 1 ? waves * kWave : kGateThreads; }
+
+// Which of the launch's units of work a wave is: waves that work apart, or a workgroup.
+template <int WAVES>
+__device__ __forceinline__ uint32_t gate_worker(int &wave) {
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    wave = WAVES > 1 ? w : 0;
+    return WAVES > 1 ? blockIdx.x : blockIdx.x * kGateWaves + w;
+}
+
 // ------------------------------------------------------------------- forward
 // MAPS: leave each chunk's map only.
-template <typename E, bool FLAGS, int L, bool MAPS>
-__global__ __launch_bounds__(kGateThreads) void gated_rows(GateParams p) {
+template <typename E, bool FLAGS, int L, int WAVES, bool MAPS>
+__global__ __launch_bounds__(threads_of(WAVES)) void gated_rows(GateParams p) {
     constexpr int K = kGateK, kTile = gate_tile(L);
-    const uint32_t wave = blockIdx.x * kGateWaves +
-                          __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const uint32_t walker = wave / p.groups, group = wave - walker * p.groups;
+    __shared__ float lds[2][WAVES][2];
+    int wave, parity = 0;
+    const uint32_t worker = gate_worker<WAVES>(wave);
+    const uint32_t walker = worker / p.groups, group = worker - walker * p.groups;
     if (walker >= p.walkers) return;
     const GateLane l = GateLane::of<L>(p, group);
-    const int own = l.lane * K;
+    const int own = wave * kTile + l.lane * K;
 
     struct Loads {
         Steps<K, E> x, ig, dg;
@@ -235,10 +342,13 @@ __global__ __launch_bounds__(kGateThreads) void gated_rows(GateParams p) {
         next.dg.load(static_cast<const E *>(p.decay_gate) + at.n * p.dg_n + l.d * p.dg_d + t, left);
     };
     // The last chunk's map is not needed.
-    const auto wanted = [&](const Place &at) { return !MAPS || at.chunk + 1 < p.chunks; };
+    const auto next_unit = [&](Place &at, uint32_t u) {
+        at.set_unit(p, u);
+        while (MAPS && at.unit < p.units && at.chunk + 1 == p.chunks)
+            at.set_unit(p, at.unit + p.walkers);
+    };
     Place at;
-    at.set_unit(p, walker);
-    while (at.unit < p.units && !wanted(at)) at.set_unit(p, at.unit + p.walkers);
+    next_unit(at, walker);
     if (at.unit >= p.units) return;
     at.tile = at.first(p);
     load(at);
@@ -246,7 +356,7 @@ __global__ __launch_bounds__(kGateThreads) void gated_rows(GateParams p) {
     bool fresh = true;
     while (true) {
         const int64_t row = (int64_t)at.n * p.channels + l.d;
-        const int t0 = at.tile * kTile, t = t0 + own;
+        const int t0 = at.tile * kTile + wave * kTile, t = at.tile * kTile + own;
         if (fresh) {
             if constexpr (MAPS) {
                 carry = 0.f;
@@ -261,71 +371,69 @@ __global__ __launch_bounds__(kGateThreads) void gated_rows(GateParams p) {
         if constexpr (FLAGS) starts = gate_starts(p, at.n, t, at.end);
         // the place after this one, and its loads
         Place ahead = at;
-        const bool last = at.tile + 1 == at.past(p);
+        const bool last = at.tile == at.last(p, WAVES);
         if (last) {
-            do ahead.set_unit(p, ahead.unit + p.walkers);
-            while (ahead.unit < p.units && !wanted(ahead));
+            next_unit(ahead, ahead.unit + p.walkers);
             ahead.tile = ahead.unit < p.units ? ahead.first(p) : 0;
         } else {
-            ++ahead.tile;
+            ahead.tile += WAVES;
         }
         if (ahead.unit < p.units) load(ahead);
 
         GateSteps s;
-        s.make(l, now.x, now.ig, now.dg);
-        float b[K], h[K];
+        float x[K], i[K], b[K];
+        s.decays(l, now.dg);
+        now.x.widen(x);
+        input_gates(l, now.ig, i);
 #pragma unroll
-        for (int k = 0; k < K; ++k) b[k] = __builtin_amdgcn_sqrtf(s.rest[k]) * (s.i[k] * s.x[k]);
-        if (t0 + kTile > at.end)
+        for (int k = 0; k < K; ++k) b[k] = __builtin_amdgcn_sqrtf(s.rest[k]) * (i[k] * x[k]);
+        const bool partial = t0 + kTile > at.end;
+        if (partial)
 #pragma unroll
             for (int k = 0; k < K; ++k)
                 if (t + k >= at.end) s.a[k] = 1.f, b[k] = 0.f;
-        float a = 1.f, fold = 0.f;
+        float a = s.a[0], fold = b[0];
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
+        for (int k = 1; k < K; ++k) {
             if (FLAGS && (starts >> k & 1)) fold = 0.f;
             fold = fmaf(s.a[k], fold, b[k]);
             a *= s.a[k];
         }
         if (FLAGS && starts != 0) a = -0.f;
-        if (!MAPS && p.checkpoints != nullptr && l.live && l.lane == 0)
-            p.checkpoints[row * p.tiles + at.tile] = carry;
-        float leave;
-        const float in = enter_lanes<FLAGS, false, L>(a, fold, carry, l.lane, leave);
-        carry = leave;
+        lanes_scan<FLAGS, false, L>(a, fold, l.lane);
+        float enter = carry;
+        if constexpr (WAVES > 1)
+            enter = enter_wave<FLAGS, false, WAVES>(last_lane<false, L>(a), last_lane<false, L>(fold),
+                                                    lds, parity, wave, carry);
+        if (!MAPS && p.checkpoints != nullptr && l.live && l.lane == 0 &&
+            (WAVES == 1 || at.tile + wave < p.tiles))
+            p.checkpoints[row * p.tiles + at.tile + wave] = enter;
+        const float after = step_map<FLAGS>(a, fold, enter);
+        float h = next_lane<false, L>(after, enter, l.lane);
+        if constexpr (WAVES == 1) carry = last_lane<false, L>(after);
         if constexpr (MAPS) {
-            // the tile's product of a's, from the row's lanes
-            float whole = a;
-            if constexpr (L > 1) {
-                float unused = 0.f;
-                lanes_scan<FLAGS, false, L>(whole, unused, l.lane);
-                whole = row_last<false, L>(whole);
-            }
-            map = product<FLAGS>(whole, map);
+            map = product<FLAGS>(last_lane<false, L>(a), map);
             if (last && l.live && l.lane == 0) {
                 float *m = p.maps + ((int64_t)at.n * p.chunks + at.chunk) * 2 * p.channels + l.d;
                 m[0] = map;
                 m[p.channels] = carry;
             }
         } else {
-            float x = in;
+            float out[K];
 #pragma unroll
             for (int k = 0; k < K; ++k) {
-                if (FLAGS && (starts >> k & 1)) x = 0.f;
-                x = fmaf(s.a[k], x, b[k]);
-                h[k] = x;
+                if (FLAGS && (starts >> k & 1)) h = 0.f;
+                h = fmaf(s.a[k], h, b[k]);
+                out[k] = h;
             }
-            if (t0 + kTile > at.end)
+            if (partial)
 #pragma unroll
                 for (int k = 0; k < K; ++k)
-                    if (t + k >= at.end) h[k] = 0.f;
-            if (l.live) store_steps<K>(static_cast<E *>(p.out) + row * p.T + t, p.T - t, h);
+                    if (t + k >= at.end) out[k] = 0.f;
+            if (l.live) store_steps<K>(static_cast<E *>(p.out) + row * p.T + t, p.T - t, out);
             if (last && at.chunk + 1 == p.chunks && p.final_state != nullptr && l.live &&
-                l.lane == 0) {
-                const bool over = FLAGS && p.after_done && at.end > 0 &&
-                                  p.flags[(int64_t)at.n * p.T + at.end - 1] != 0;
-                p.final_state[row] = over ? 0.f : carry;
-            }
+                l.lane == 0 && wave == 0)
+                p.final_state[row] = ends_over<FLAGS>(p, at.n, at.end) ? 0.f : carry;
         }
         if (ahead.unit >= p.units) return;
         fresh = last;
@@ -342,15 +450,16 @@ __global__ __launch_bounds__(kGateThreads) void gated_rows(GateParams p) {
 // The states are computed again, from the state that entered the tile.  What passes a
 // step to the left is a_t lambda_t, so a lane's map is r -> a_k (grad_k + r) over its
 // steps from the last.
-template <typename E, bool FLAGS, int L, bool MAPS>
-__global__ __launch_bounds__(kGateThreads) void gated_rows_backward(GateParams p) {
+template <typename E, bool FLAGS, int L, int WAVES, bool MAPS>
+__global__ __launch_bounds__(threads_of(WAVES), sizeof(E) == 2 ? 4 : 3) void gated_rows_backward(GateParams p) {
     constexpr int K = kGateK, kTile = gate_tile(L);
-    const uint32_t wave = blockIdx.x * kGateWaves +
-                          __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const uint32_t walker = wave / p.groups, group = wave - walker * p.groups;
+    __shared__ float lds[2][WAVES][2];
+    int wave, parity = 0;
+    const uint32_t worker = gate_worker<WAVES>(wave);
+    const uint32_t walker = worker / p.groups, group = worker - walker * p.groups;
     if (walker >= p.walkers) return;
     const GateLane l = GateLane::of<L>(p, group);
-    const int own = l.lane * K;
+    const int own = wave * kTile + l.lane * K;
 
     struct Loads {
         Steps<K, E> x, ig, dg, g;
@@ -358,38 +467,44 @@ __global__ __launch_bounds__(kGateThreads) void gated_rows_backward(GateParams p
     } next;
     const auto load = [&](const Place &at) {
         const int t = at.tile * kTile + own, left = at.end - t;
-        next.dg.load(static_cast<const E *>(p.decay_gate) + at.n * p.dg_n + l.d * p.dg_d + t, left);
-        next.g.load(static_cast<const E *>(p.grad_out) + at.n * p.g_n + l.d * p.g_d + t, left);
+        // formed here each time: kept, the rows' addresses would take registers from a wave
+        const uint32_t d = here(l.d);
+        next.dg.load(static_cast<const E *>(p.decay_gate) + at.n * p.dg_n + d * p.dg_d + t, left);
+        next.g.load(static_cast<const E *>(p.grad_out) + at.n * p.g_n + d * p.g_d + t, left);
         if constexpr (!MAPS) {
-            next.x.load(static_cast<const E *>(p.x) + at.n * p.x_n + l.d * p.x_d + t, left);
-            next.ig.load(static_cast<const E *>(p.input_gate) + at.n * p.ig_n + l.d * p.ig_d + t,
+            next.x.load(static_cast<const E *>(p.x) + at.n * p.x_n + d * p.x_d + t, left);
+            next.ig.load(static_cast<const E *>(p.input_gate) + at.n * p.ig_n + d * p.ig_d + t,
                          left);
-            next.enter = p.checkpoints[((int64_t)at.n * p.channels + l.d) * p.tiles + at.tile];
+            next.enter = 0.f;
+            if (WAVES == 1 || at.tile + wave < p.tiles)
+                next.enter = p.checkpoints[((int64_t)at.n * p.channels + l.d) * p.tiles + at.tile +
+                                           wave];
         }
     };
     // The first chunk's map is not needed.
-    const auto wanted = [&](const Place &at) { return !MAPS || at.chunk > 0; };
+    const auto next_unit = [&](Place &at, uint32_t u) {
+        at.set_unit(p, u);
+        while (MAPS && at.unit < p.units && at.chunk == 0) at.set_unit(p, at.unit + p.walkers);
+    };
     float sum_decay = 0.f, sum_rate = 0.f, sum_input = 0.f;
     Place at;
-    at.set_unit(p, walker);
-    while (at.unit < p.units && !wanted(at)) at.set_unit(p, at.unit + p.walkers);
+    next_unit(at, walker);
     if (MAPS && at.unit >= p.units) return;
     if (at.unit < p.units) {
-        at.tile = at.past(p) - 1;
+        at.tile = at.last(p, WAVES);
         load(at);
     }
     float carry = 0.f, map = 1.f;
     bool fresh = true;
     while (at.unit < p.units) {
         const int64_t row = (int64_t)at.n * p.channels + l.d;
-        const int t0 = at.tile * kTile, t = t0 + own;
+        const int t0 = at.tile * kTile + wave * kTile, t = at.tile * kTile + own;
         if (fresh) {
             carry = 0.f;
             map = 1.f;
             if constexpr (!MAPS) {
-                const bool over = FLAGS && p.after_done && at.end > 0 &&
-                                  p.flags[(int64_t)at.n * p.T + at.end - 1] != 0;
-                if (p.grad_final != nullptr && !over) carry = p.grad_final[row];
+                if (p.grad_final != nullptr && !ends_over<FLAGS>(p, at.n, at.end))
+                    carry = p.grad_final[row];
                 if (p.chunks > 1) carry = enter_chunk<true>(p, at.n, at.chunk, l.d, carry);
             }
         }
@@ -399,81 +514,89 @@ __global__ __launch_bounds__(kGateThreads) void gated_rows_backward(GateParams p
         Place ahead = at;
         const bool last = at.tile == at.first(p);
         if (last) {
-            do ahead.set_unit(p, ahead.unit + p.walkers);
-            while (ahead.unit < p.units && !wanted(ahead));
-            ahead.tile = ahead.unit < p.units ? ahead.past(p) - 1 : 0;
+            next_unit(ahead, ahead.unit + p.walkers);
+            ahead.tile = ahead.unit < p.units ? ahead.last(p, WAVES) : 0;
         } else {
-            --ahead.tile;
+            ahead.tile -= WAVES;
         }
         if (ahead.unit < p.units) load(ahead);
 
         float g[K];
         now.g.widen(g);
         GateSteps s;
-        if constexpr (MAPS)
-            s.make(l, now.dg, now.dg, now.dg);
-        else
-            s.make(l, now.x, now.ig, now.dg);
+        s.decays(l, now.dg);
         const bool partial = t0 + kTile > at.end;
         if (partial)
 #pragma unroll
             for (int k = 0; k < K; ++k)
                 if (t + k >= at.end) s.a[k] = 1.f;
-        float a = 1.f;
+        float whole = s.a[0];
 #pragma unroll
-        for (int k = 0; k < K; ++k) a *= s.a[k];
-        if (FLAGS && starts != 0) a = -0.f;
-        float back = 0.f;
+        for (int k = 1; k < K; ++k) whole *= s.a[k];
+        if (FLAGS && starts != 0) whole = -0.f;
+        float a = whole, back = 0.f;
 #pragma unroll
         for (int k = K - 1; k >= 0; --k) {
             back = s.a[k] * (g[k] + back);
             if (FLAGS && (starts >> k & 1)) back = 0.f;
         }
-        float leave;
-        float pass = enter_lanes<FLAGS, true, L>(a, back, carry, l.lane, leave);
-        carry = leave;
+        lanes_scan<FLAGS, true, L>(a, back, l.lane);
+        float right = carry;
+        if constexpr (WAVES > 1)
+            right = enter_wave<FLAGS, true, WAVES>(last_lane<true, L>(a), last_lane<true, L>(back),
+                                                   lds, parity, wave, carry);
+        const float after = step_map<FLAGS>(a, back, right);
+        float pass = next_lane<true, L>(after, right, l.lane);
+        if constexpr (WAVES == 1) carry = last_lane<true, L>(after);
         if constexpr (MAPS) {
-            float whole = a;
-            if constexpr (L > 1) {
-                float unused = 0.f;
-                lanes_scan<FLAGS, true, L>(whole, unused, l.lane);
-                whole = row_last<true, L>(whole);
-            }
-            map = product<FLAGS>(whole, map);
+            map = product<FLAGS>(last_lane<true, L>(a), map);
             if (last && l.live && l.lane == 0) {
                 float *m = p.maps + ((int64_t)at.n * p.chunks + at.chunk) * 2 * p.channels + l.d;
                 m[0] = map;
                 m[p.channels] = carry;
             }
         } else {
-            float beta[K], inv[K], before[K];
+            // lambda's factors in grad_x, and grad_x's in grad_input_gate; the input
+            float beta_i[K], rest_x[K], in[K], q[K];
+            {
+                float x[K], i[K];
+                now.x.widen(x);
+                input_gates(l, now.ig, i);
+#pragma unroll
+                for (int k = 0; k < K; ++k) {
+                    const float rest = s.rest[k];
+                    const float inv = __builtin_amdgcn_rsqf(rest < 1.2e-38f ? 1.2e-38f : rest);
+                    beta_i[k] = rest * inv * i[k];
+                    if (partial && t + k >= at.end) beta_i[k] = 0.f;
+                    in[k] = beta_i[k] * x[k];
+                    q[k] = s.a[k] * inv * (i[k] * x[k]);
+                    rest_x[k] = x[k] * (1.f - i[k]);
+                }
+            }
             float fold = 0.f;
 #pragma unroll
             for (int k = 0; k < K; ++k) {
-                inv[k] = __builtin_amdgcn_rsqf(s.rest[k] < 1.2e-38f ? 1.2e-38f : s.rest[k]);
-                beta[k] = s.rest[k] * inv[k];
-                if (partial && t + k >= at.end) beta[k] = 0.f;
                 if (FLAGS && (starts >> k & 1)) fold = 0.f;
-                fold = fmaf(s.a[k], fold, beta[k] * (s.i[k] * s.x[k]));
+                fold = fmaf(s.a[k], fold, in[k]);
             }
-            float unused, h = enter_lanes<FLAGS, false, L>(a, fold, now.enter, l.lane, unused);
+            a = whole;
+            lanes_scan<FLAGS, false, L>(a, fold, l.lane);
+            float h = next_lane<false, L>(step_map<FLAGS>(a, fold, now.enter), now.enter, l.lane);
 #pragma unroll
             for (int k = 0; k < K; ++k) {
                 if (FLAGS && (starts >> k & 1)) h = 0.f;
-                before[k] = h;
-                h = fmaf(s.a[k], h, beta[k] * (s.i[k] * s.x[k]));
+                q[k] -= h;
+                h = fmaf(s.a[k], h, in[k]);
             }
             float gx[K], gi[K], gr[K];
 #pragma unroll
             for (int k = K - 1; k >= 0; --k) {
-                float lambda = g[k] + pass;
+                const float lambda = g[k] + pass;
                 pass = s.a[k] * lambda;
+                const float e = pass * (l.slow * s.r[k]) * q[k];
                 if (FLAGS && (starts >> k & 1)) pass = 0.f;
-                if (partial && t + k >= at.end) lambda = 0.f;
-                const float gain = s.a[k] * inv[k] * (s.i[k] * s.x[k]);
-                const float e = lambda * (l.slow * s.r[k] * s.a[k] * (gain - before[k]));
-                gx[k] = lambda * beta[k] * s.i[k];
-                gi[k] = gx[k] * s.x[k] * (1.f - s.i[k]);
+                gx[k] = lambda * beta_i[k];
+                gi[k] = gx[k] * rest_x[k];
                 gr[k] = e * (1.f - s.r[k]);
                 if (partial && t + k >= at.end) {
                     gx[k] = gi[k] = gr[k] = 0.f;
@@ -488,7 +611,8 @@ __global__ __launch_bounds__(kGateThreads) void gated_rows_backward(GateParams p
                 store_steps<K>(static_cast<E *>(p.grad_input) + row * p.T + t, p.T - t, gi);
                 store_steps<K>(static_cast<E *>(p.grad_decay) + row * p.T + t, p.T - t, gr);
             }
-            if (last && at.chunk == 0 && p.grad_state != nullptr && l.live && l.lane == 0)
+            if (last && at.chunk == 0 && p.grad_state != nullptr && l.live && l.lane == 0 &&
+                wave == 0)
                 p.grad_state[row] = carry;
         }
         fresh = last;
@@ -502,7 +626,7 @@ __global__ __launch_bounds__(kGateThreads) void gated_rows_backward(GateParams p
             sum_input += __shfl_xor(sum_input, m);
         }
         if (l.live && l.lane == 0) {
-            float *to = p.partials + (int64_t)walker * 3 * p.channels + l.d;
+            float *to = p.partials + ((int64_t)walker * WAVES + wave) * 3 * p.channels + l.d;
             to[0] = sum_decay;
             to[p.channels] = sum_rate;
             to[2 * (int64_t)p.channels] = sum_input;
@@ -592,7 +716,10 @@ __global__ __launch_bounds__(kGateStepThreads) void gated_step(GateStepParams p)
     if (p.input_bias != nullptr) load_steps<VEC>(p.input_bias + d, left, ib);
     if (p.decay_bias != nullptr) load_steps<VEC>(p.decay_bias + d, left, db);
 #pragma unroll
-    for (int c = 0; c < VEC; ++c) slow[c] = slow_of(p.scale, slow[c]);
+    for (int c = 0; c < VEC; ++c) {
+        slow[c] = slow_of(p.scale, slow[c]);
+        ib[c] *= -kLog2e, db[c] *= -kLog2e;
+    }
     for (uint32_t n = blockIdx.y; n < p.num_seqs; n += gridDim.y) {
         const Loads now = next;
         if (n + gridDim.y < p.num_seqs) load(n + gridDim.y);
@@ -606,8 +733,8 @@ __global__ __launch_bounds__(kGateStepThreads) void gated_step(GateStepParams p)
 #pragma unroll
             for (int c = 0; c < VEC; ++c) {
                 float a, rest;
-                decay_of<false>(slow[c] * sigmoid(dg[c] + db[c]), a, rest);
-                const float in = __builtin_amdgcn_sqrtf(rest) * (sigmoid(ig[c] + ib[c]) * x[c]);
+                decay_of<false>(slow[c] * gate_of(dg[c], db[c]), a, rest);
+                const float in = __builtin_amdgcn_sqrtf(rest) * (gate_of(ig[c], ib[c]) * x[c]);
                 out[c] = fmaf(a, h[c], in);
             }
             store_steps<VEC>(p.state + now.place * p.channels + d, left, out);
@@ -617,38 +744,61 @@ __global__ __launch_bounds__(kGateStepThreads) void gated_step(GateStepParams p)
 }
 
 // ------------------------------------------------------------------- host side
-// Lanes of a row: rows of up to 8 steps take one, up to 32 four.
-static int gate_lanes(int64_t T) { return T <= gate_tile(1) ? 1 : T <= gate_tile(4) ? 4 : 16; }
+// How a call is launched.  Rows of up to 8 steps take a lane, up to 32 four, others 16,
+// as long as that makes waves enough; from `kFewWaves` down a whole wave takes a row,
+// from `kFewRows` rows down the kShared waves of a workgroup do, and from `kFewestRows`
+// down rows are cut into chunks of at least kFewestTiles tiles, at most kMostChunks.
+// Waves that a launch wants: 4 a SIMD, or what the registers of the backward kernel leave.
+static int64_t gate_wanted(const rlca_gated_call &c, bool backward) {
+    return backward && c.dtype == RLCA_F32 ? 3072 : 4096;
+}
 
-// Waves that a launch wants; below half of them rows are cut into chunks of at
-// least kFewestTiles tiles, at most kMostChunks.
-constexpr int64_t kGateWanted = 4096;
+constexpr int64_t kFewWaves = 2048;
+constexpr int64_t kFewRows = 1024;
+constexpr int64_t kFewestRows = 96;
 constexpr int64_t kFewestTiles = 4;
 constexpr int64_t kMostChunks = 64;
+constexpr int kShared = 8;
 
 struct GatePlan {
-    int L;
+    int L, waves;
     int64_t tiles, groups, chunks, chunk_tiles, units, walkers;
 };
 
-static GatePlan gate_plan(const rlca_gated_call &c) {
+static GatePlan gate_plan(const rlca_gated_call &c, bool backward) {
     GatePlan g = {};
-    g.L = gate_lanes(c.T);
+    const int64_t wanted = gate_wanted(c, backward);
+    const int64_t rows = c.num_seqs * c.channels;
+    const auto per_wave = [&](int lanes) { return kWave / lanes; };
+    const auto groups = [&](int lanes) {
+        return (c.channels + per_wave(lanes) - 1) / per_wave(lanes);
+    };
+    g.L = c.T <= gate_tile(1) ? 1 : c.T <= gate_tile(4) ? 4 : 16;
+    g.waves = 1;
+    const bool few = groups(16) * c.num_seqs <= kFewWaves;
+    const bool chunked = few && rows <= kFewestRows && c.T >= 2 * kFewestTiles * gate_tile(16);
+    if (few && !chunked && c.T > gate_tile(16)) {
+        g.L = 64;
+        if (rows <= kFewRows && c.T > kShared / 2 * gate_tile(64)) g.waves = kShared;
+    }
     g.tiles = (c.T + gate_tile(g.L) - 1) / gate_tile(g.L);
-    g.groups = (c.channels + kWave / g.L - 1) / (kWave / g.L);
+    g.groups = groups(g.L);
     g.chunks = 1;
-    const int64_t waves = g.groups * c.num_seqs;
-    if (waves > 0 && waves <= kGateWanted / 2 && g.tiles >= 2 * kFewestTiles) {
-        int64_t want = kGateWanted / waves;
+    if (chunked && rows > 0) {
+        int64_t want = 4096 / (g.groups * c.num_seqs);
         if (want > g.tiles / kFewestTiles) want = g.tiles / kFewestTiles;
         if (want > kMostChunks) want = kMostChunks;
         g.chunks = want;
     }
-    g.chunk_tiles = g.chunks == 0 ? 0 : (g.tiles + g.chunks - 1) / g.chunks;
+    g.chunk_tiles = (g.tiles + g.chunks - 1) / g.chunks;
     if (g.chunk_tiles > 0) g.chunks = (g.tiles + g.chunk_tiles - 1) / g.chunk_tiles;
     g.units = c.num_seqs * g.chunks;
-    g.walkers = g.groups == 0 ? 0 : (kGateWanted + g.groups - 1) / g.groups;
+    g.walkers = g.groups == 0 ? 0 : (wanted / g.waves + g.groups - 1) / g.groups;
     if (g.walkers > g.units) g.walkers = g.units;
+    if (g.walkers > 0) {  // as many units for each, as far as possible
+        const int64_t rounds = (g.units + g.walkers - 1) / g.walkers;
+        g.walkers = (g.units + rounds - 1) / rounds;
+    }
     return g;
 }
 
@@ -681,33 +831,40 @@ static GateParams gate_params(const rlca_gated_call &c, const GatePlan &g) {
     return p;
 }
 
-template <typename E, bool MAPS, int L>
+template <typename E, int L, int WAVES, bool MAPS>
 static const void *gate_kernel(bool backward, bool flags) {
     if (backward)
-        return flags ? (const void *)gated_rows_backward<E, true, L, MAPS>
-                     : (const void *)gated_rows_backward<E, false, L, MAPS>;
-    return flags ? (const void *)gated_rows<E, true, L, MAPS>
-                 : (const void *)gated_rows<E, false, L, MAPS>;
+        return flags ? (const void *)gated_rows_backward<E, true, L, WAVES, MAPS>
+                     : (const void *)gated_rows_backward<E, false, L, WAVES, MAPS>;
+    return flags ? (const void *)gated_rows<E, true, L, WAVES, MAPS>
+                 : (const void *)gated_rows<E, false, L, WAVES, MAPS>;
 }
 
 // Chunks exist for rows of 16 lanes only.
 template <typename E>
-static const void *gate_kernel(bool backward, bool flags, int L, bool maps) {
-    return maps      ? gate_kernel<E, true, 16>(backward, flags)
-           : L == 16 ? gate_kernel<E, false, 16>(backward, flags)
-           : L == 4  ? gate_kernel<E, false, 4>(backward, flags)
-                     : gate_kernel<E, false, 1>(backward, flags);
+static const void *gate_kernel(bool backward, bool flags, const GatePlan &g, bool maps) {
+    return maps          ? gate_kernel<E, 16, 1, true>(backward, flags)
+           : g.waves > 1 ? gate_kernel<E, 64, kShared, false>(backward, flags)
+           : g.L == 64   ? gate_kernel<E, 64, 1, false>(backward, flags)
+           : g.L == 16   ? gate_kernel<E, 16, 1, false>(backward, flags)
+           : g.L == 4    ? gate_kernel<E, 4, 1, false>(backward, flags)
+                         : gate_kernel<E, 1, 1, false>(backward, flags);
 }
 
 static rlca_status gate_launch(const rlca_gated_call &c, const GatePlan &g, GateParams &p,
                                bool backward, bool maps, hipStream_t stream) {
     const bool flags = c.flags != nullptr;
-    const void *kernel = c.dtype == RLCA_F32    ? gate_kernel<float>(backward, flags, g.L, maps)
-                         : c.dtype == RLCA_BF16 ? gate_kernel<__bf16>(backward, flags, g.L, maps)
-                                                : gate_kernel<_Float16>(backward, flags, g.L, maps);
-    const uint64_t waves = (uint64_t)g.groups * g.walkers;
-    return launch(kernel, dim3((uint32_t)((waves + kGateWaves - 1) / kGateWaves)), kGateThreads, 0,
-                  p, stream);
+    const void *kernel = c.dtype == RLCA_F32    ? gate_kernel<float>(backward, flags, g, maps)
+                         : c.dtype == RLCA_BF16 ? gate_kernel<__bf16>(backward, flags, g, maps)
+                                                : gate_kernel<_Float16>(backward, flags, g, maps);
+    const uint64_t workers = (uint64_t)g.groups * g.walkers;
+    const uint64_t blocks = g.waves > 1 ? workers : (workers + kGateWaves - 1) / kGateWaves;
+    return launch(kernel, dim3((uint32_t)blocks), threads_of(g.waves), 0, p, stream);
+}
+
+// The walkers' sums.
+static size_t gate_partials_bytes(const rlca_gated_call &c, const GatePlan &g) {
+    return (size_t)g.walkers * g.waves * 3 * c.channels * sizeof(float);
 }
 
 static size_t gate_maps_bytes(const rlca_gated_call &c, const GatePlan &g) {
@@ -793,18 +950,18 @@ extern "C" {
 
 size_t rlca_gated_recurrence_checkpoints_size(const rlca_gated_call *call) {
     if (call == nullptr || !gate_sizes_ok(*call)) return 0;
-    return gate_checkpoints_bytes(*call, gate_plan(*call));
+    return gate_checkpoints_bytes(*call, gate_plan(*call, false));
 }
 
 size_t rlca_gated_recurrence_workspace_size(const rlca_gated_call *call) {
     if (call == nullptr || !gate_sizes_ok(*call)) return 0;
-    return gate_maps_bytes(*call, gate_plan(*call));
+    return gate_maps_bytes(*call, gate_plan(*call, false));
 }
 
 size_t rlca_gated_recurrence_backward_workspace_size(const rlca_gated_call *call) {
     if (call == nullptr || !gate_sizes_ok(*call)) return 0;
-    const GatePlan g = gate_plan(*call);
-    return gate_maps_bytes(*call, g) + (size_t)g.walkers * 3 * call->channels * sizeof(float);
+    const GatePlan g = gate_plan(*call, true);
+    return gate_maps_bytes(*call, g) + gate_partials_bytes(*call, g);
 }
 
 rlca_status rlca_gated_recurrence(const rlca_gated_call *call, void *workspace,
@@ -814,7 +971,7 @@ rlca_status rlca_gated_recurrence(const rlca_gated_call *call, void *workspace,
     Arrays a;
     rlca_status st = check_gated(c, false, a);
     if (st != RLCA_OK) return st;
-    const GatePlan g = gate_plan(c);
+    const GatePlan g = gate_plan(c, false);
     const int64_t N = c.num_seqs, D = c.channels, T = c.T;
     const size_t need = gate_maps_bytes(c, g);
     a.out(c.out, element_bytes(c.dtype), true, {{N, D * T}, {D, T}, {T, 1}});
@@ -838,10 +995,10 @@ rlca_status rlca_gated_recurrence_backward(const rlca_gated_call *call, void *wo
     Arrays a;
     rlca_status st = check_gated(c, true, a);
     if (st != RLCA_OK) return st;
-    const GatePlan g = gate_plan(c);
+    const GatePlan g = gate_plan(c, true);
     const int64_t N = c.num_seqs, D = c.channels, T = c.T;
     const size_t e = element_bytes(c.dtype), maps = gate_maps_bytes(c, g);
-    const size_t need = maps + (size_t)g.walkers * 3 * D * sizeof(float);
+    const size_t need = maps + gate_partials_bytes(c, g);
     a.in(c.grad_out, e, true, {{N, c.grad_stride_seq}, {D, c.grad_stride_channel}, {T, 1}});
     a.in(c.grad_final_state, 4, false, {{N, D}, {D, 1}});
     a.in(c.checkpoints, 4, true, {{(int64_t)(gate_checkpoints_bytes(c, g) / 4), 1}});
@@ -863,7 +1020,7 @@ rlca_status rlca_gated_recurrence_backward(const rlca_gated_call *call, void *wo
     if (N > 0 && T == 0) {
         if ((st = copy_state(c.grad_final_state, c.grad_state, N * D, stream)) != RLCA_OK) return st;
     } else if (N > 0) {
-        walkers = p.walkers;
+        walkers = p.walkers * (uint32_t)g.waves;
         if (g.chunks > 1 && (st = gate_launch(c, g, p, true, true, stream)) != RLCA_OK) return st;
         if ((st = gate_launch(c, g, p, true, false, stream)) != RLCA_OK) return st;
     }

@@ -5,9 +5,9 @@ As in sequence_reference.py, every function returns {output: (value, bound)},
 and the bounds are running error analyses: beside each quantity its magnitude
 and the error that float32 roundings of u = 2^-24 relative can have built up.
 The counts for the gated recurrence, relative unless said otherwise:
-  * a sigmoid: the argument's error, (4 |raw| + 4) u (its sum, the constant and
-    product of its exponential, the exponential's own two) times 1 - sigmoid, and
-    4 for sum and reciprocal;
+  * a sigmoid: the argument's error, (|raw| + 3 (|gate| + |bias|) + 4) u (the constant
+    and products that its two parts meet in one sum, that sum, the exponential's own
+    two) times 1 - sigmoid, and 4 for sum and reciprocal;
   * the rate scale softplus(decay): 8; L = rate times r: r's, the rate's and 2;
   * a = exp(-L): L times L's error and 2, and 6; and 2^-126 absolute, since the
     exponential of less than float32's smallest normal number is 0;
@@ -37,11 +37,12 @@ def gated(x, input_gate, decay_gate, decay, input_bias=None, decay_bias=None, sc
     raw_i, raw_r = ig + ib[:, None], dg + db[:, None]
     # of what is masked nothing is used
     raw_i, raw_r = torch.where(inside, raw_i, 0.0), torch.where(inside, raw_r, 0.0)
+    ig, dg = torch.where(inside, ig, 0.0), torch.where(inside, dg, 0.0)
     x = torch.where(inside, x, 0.0)
     i, r = sigmoid(raw_i), sigmoid(raw_r)
 
     def sig_err(s, raw, v, b):
-        return U * ((1 - s) * (4 * raw.abs() + 4) + 4)
+        return U * ((1 - s) * (raw.abs() + 3 * (v.abs() + b.abs()[:, None]) + 4) + 4)
 
     ei, er = sig_err(i, raw_i, ig, ib), sig_err(r, raw_r, dg, db)
     rate = scale * softplus(decay)[:, None]

@@ -745,20 +745,25 @@ __global__ __launch_bounds__(kGateStepThreads) void gated_step(GateStepParams p)
 
 // ------------------------------------------------------------------- host side
 // How a call is launched.  Rows of up to 8 steps take a lane, up to 32 four, others 16,
-// as long as that makes waves enough; from `kFewWaves` down a whole wave takes a row,
-// from `kFewRows` rows down the kShared waves of a workgroup do, and from `kFewestRows`
-// down rows are cut into chunks of at least kFewestTiles tiles, at most kMostChunks.
-// Waves that a launch wants: 4 a SIMD, or what the registers of the backward kernel leave.
-static int64_t gate_wanted(const rlca_gated_call &c, bool backward) {
-    return backward && c.dtype == RLCA_F32 ? 3072 : 4096;
-}
-
+// or a whole wave where its wider tiles waste less than a fifth more lanes at the row's
+// end (8x2048 channels of 2048 steps, bf16: forward 53 us against 63, gradients 99
+// against 113; 32x1024 of 600 steps the other way 57 against 41 and 87 against 67), or
+// where waves are few, up to kFewWaves of 16-lane rows.  From kFewRows rows down the
+// kShared waves of a workgroup share a row (512 rows of 65535 steps: 71 us against 198
+// apart and 114 in chunks; 4096 rows of 8191 steps 74 against 56 apart); from
+// kFewestRows down rows are cut into chunks of at least kFewestTiles tiles, at most
+// kMostChunks.
 constexpr int64_t kFewWaves = 2048;
-constexpr int64_t kFewRows = 1024;
+constexpr int64_t kFewRows = 2048;
 constexpr int64_t kFewestRows = 96;
 constexpr int64_t kFewestTiles = 4;
 constexpr int64_t kMostChunks = 64;
 constexpr int kShared = 8;
+
+// Waves that a launch wants: 4 a SIMD, or what the registers of the backward kernel leave.
+static int64_t gate_wanted(const rlca_gated_call &c, bool backward) {
+    return backward && c.dtype == RLCA_F32 ? 3072 : 4096;
+}
 
 struct GatePlan {
     int L, waves;
@@ -777,7 +782,11 @@ static GatePlan gate_plan(const rlca_gated_call &c, bool backward) {
     g.waves = 1;
     const bool few = groups(16) * c.num_seqs <= kFewWaves;
     const bool chunked = few && rows <= kFewestRows && c.T >= 2 * kFewestTiles * gate_tile(16);
-    if (few && !chunked && c.T > gate_tile(16)) {
+    const auto padded = [&](int lanes) {
+        return (c.T + gate_tile(lanes) - 1) / gate_tile(lanes) * gate_tile(lanes);
+    };
+    if (g.L == 16 && !chunked &&
+        ((few && c.T > gate_tile(16)) || 5 * padded(64) <= 6 * padded(16))) {
         g.L = 64;
         if (rows <= kFewRows && c.T > kShared / 2 * gate_tile(64)) g.waves = kShared;
     }

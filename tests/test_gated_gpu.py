@@ -52,7 +52,7 @@ def run_all(a, which, flags, lengths, go, gf, scale=8.0):
 # several chunks
 SHAPES = [(5, 3, 1), (5, 70, 2), (6, 65, 7), (5, 5, 8), (5, 17, 9), (5, 3, 31), (5, 18, 32),
           (5, 3, 33), (5, 5, 127), (5, 4, 128), (5, 3, 130), (5, 6, 515), (3, 5, 1031),
-          (2, 3, 2051), (1, 2, 4100), (2100, 2, 300), (5, 30, 1100), (2, 60, 2600),
+          (2, 3, 2051), (1, 2, 4100), (2100, 2, 300), (2100, 3, 500), (5, 30, 1100), (2, 60, 2600),
           (1, 100, 8200)]
 
 

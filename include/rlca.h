@@ -725,7 +725,7 @@ rlca_status rlca_rms_norm_backward(const rlca_norm_call *call, void *workspace,
  * may be).  A NaN or +infinity among a beam's logits, or as its score, makes its
  * totals NaN, and NaN ranks first.  beams and picks are 1 .. RLCA_MAX_BEAMS, picks at
  * most beams * vocab, beams * vocab < 2^31, and num_searches * beams *
- * ceil(vocab / 8192) < 2^24. */
+ * ceil(vocab / 2048) < 2^24. */
 #define RLCA_MAX_BEAMS 64
 
 typedef struct {

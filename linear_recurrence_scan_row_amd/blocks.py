@@ -120,15 +120,22 @@ _pack_gated, _pack_gated_step, _pack_norm, _pack_beam = (
     _packer(cls) for cls in (GatedCall, GatedStepCall, NormCall, BeamCall))
 
 
+# The current device's index: torch's own getter is several times cheaper than the
+# public function's wrapper around it.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _run(name, dev, *args):
     """One library call on the current stream of the inputs' device.  Its default
     stream has no handle of its own, so another device is made the current one."""
-    if torch.cuda.current_device() == dev.index:
-        status = getattr(lib(), name)(*args, _current_stream(dev))
+    call = getattr(lib(), name)
+    if _current_device() == dev.index:
+        status = call(*args, _current_stream(dev))
     else:
         with torch.cuda.device(dev):
-            status = getattr(lib(), name)(*args, _current_stream(dev))
-    _check(status, name)
+            status = call(*args, _current_stream(dev))
+    if status:
+        _check(status, name)
 
 
 # -------------------------------------------------------- the gated recurrence
@@ -294,14 +301,15 @@ def _norm_inputs(x, weight, eps, lengths):
 
 def _norm(x, weight, residual, eps, lengths, total, out, scale, bits8):
     head, tail, shape, dev, dtype = _norm_inputs(x, weight, eps, lengths)
-    o = _new(out, shape, torch.float8_e4m3fn if bits8 else dtype, dev)
+    o = _new(out, shape, torch.float8_e4m3fn, dev) if bits8 \
+        else _new_step(out, x, shape, dtype, dev, "out")
     sc = _new(scale, (shape[0], *shape[2:]), torch.float32, dev, "scale") if bits8 else None
     s = None
     if residual is not None:
-        s = _new(total, shape, dtype, dev, "total")
+        s = _new_step(total, x, shape, dtype, dev, "total")
     elif total is not None:
         raise ValueError("total is given without a residual")
-    call = _pack_norm(*head, *_rows("x", x, shape, dtype, dev),
+    call = _pack_norm(*head, x.data_ptr(), x.stride(0), x.stride(1),
                       *_rows("residual", residual, shape, dtype, dev), *tail,
                       0 if bits8 else o.data_ptr(), o.data_ptr() if bits8 else 0, _ptr(sc),
                       _ptr(s), *(0,) * 8)
@@ -340,7 +348,7 @@ def rms_norm_backward(grad_out, x, weight=None, eps=1e-6, grad_sum=None, lengths
         raise ValueError("grad_out is required")
     grads = NormGrads(x=_new(None, shape, dtype, dev),
                       weight=None if weight is None else _new(None, shape[1:2], torch.float32, dev))
-    call = _pack_norm(*head, *_rows("x", x, shape, dtype, dev), 0, 0, 0, *tail, 0, 0, 0, 0,
+    call = _pack_norm(*head, x.data_ptr(), x.stride(0), x.stride(1), 0, 0, 0, *tail, 0, 0, 0, 0,
                       *_rows("grad_out", grad_out, shape, dtype, dev),
                       *_rows("grad_sum", grad_sum, shape, dtype, dev), grads.x.data_ptr(),
                       _ptr(grads.weight))
@@ -390,9 +398,9 @@ def beam_select(logits, scores, picks=None, finished=None, pad_token=0):
             logits.stride(1), _dense_in("scores", scores, (N, K), torch.float32, dev),
             0 if finished is None else _flags_in(finished, (N, K), dev))
     # one allocation: the scores' bits and the whole numbers are of one size
-    out = torch.empty((3, N, P), dtype=torch.int32, device=dev)
-    choice = BeamChoice(out[0].view(torch.float32), out[1], out[2])
-    call = _pack_beam(*head, *(t.data_ptr() for t in choice))
+    bits, tokens, parents = torch.empty((3, N, P), dtype=torch.int32, device=dev).unbind()
+    choice = BeamChoice(bits.view(torch.float32), tokens, parents)
+    call = _pack_beam(*head, bits.data_ptr(), tokens.data_ptr(), parents.data_ptr())
     ws = _scratch(lib().rlca_beam_select_workspace_size(call), dev)
     _run("rlca_beam_select", dev, call, ws.data_ptr(), ws.numel())
     return choice
@@ -428,7 +436,7 @@ def beam_reorder(pools, slots, parents, out=None):
         if t.get_device() != dev.index or not t.is_contiguous():
             raise ValueError(f"pools[{i}] must be contiguous and on {dev}")
         packed[2 * i] = t.data_ptr()
-        packed[2 * i + 1] = t[0].numel() * t.element_size() if places > 0 else 0
+        packed[2 * i + 1] = t.numel() * t.element_size() // places if places > 0 else 0
     o = _new(out, (N, K), torch.int32, dev)
     _run("rlca_beam_reorder", dev, packed.buffer_info()[0], len(pools), N, K, places, s, f,
          o.data_ptr())

@@ -11,6 +11,11 @@ backward calls); the advantages come from gae_stats, the surrogate and its
 gradient from ppo_clip_loss, and clip_grad_norm bounds the step.  The matrix
 products between them are torch's.
 
+With --core gated the policy is a residual stack of gated recurrences instead:
+rms_norm adds each block's output to the stream and norms it, gated_recurrence and
+gated_step carry the memory, and plan() searches for its likeliest sequences of
+actions with beam_select and beam_reorder, the states of all beams in pools.
+
 The task cannot be solved without memory: a cue is shown at an episode's first
 step, and its last step is rewarded if the action names it.
 """
@@ -21,8 +26,10 @@ import argparse
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import (causal_conv, causal_conv_backward, causal_conv_step, clip_grad_norm, gae_stats,
-               ppo_clip_loss, selective_scan, selective_scan_backward, selective_step)
+from . import (beam_reorder, beam_select, causal_conv, causal_conv_backward, causal_conv_step,
+               clip_grad_norm, gae_stats, gated_recurrence, gated_recurrence_backward, gated_step,
+               ppo_clip_loss, rms_norm, rms_norm_backward, selective_scan,
+               selective_scan_backward, selective_step)
 
 
 class _Conv(torch.autograd.Function):
@@ -54,6 +61,42 @@ class _Scan(torch.autograd.Function):
         g = selective_scan_backward(grad.contiguous(), *ctx.saved_tensors)
         return (g.u, g.delta, g.A, g.B.view(B.shape), g.C.view(C.shape), g.D, g.z, g.delta_bias,
                 g.state, None)
+
+
+class _Norm(torch.autograd.Function):
+    """(normed, s) of s = x + residual."""
+
+    @staticmethod
+    def forward(ctx, x, residual, weight):
+        out, s = rms_norm(x, weight, residual)
+        ctx.save_for_backward(s, weight)
+        return out, s
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad, grad_sum):
+        s, weight = ctx.saved_tensors
+        g = rms_norm_backward(grad.contiguous(), s, weight, grad_sum=grad_sum.contiguous())
+        return g.x, g.x, g.weight
+
+
+class _Gated(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, input_gate, decay_gate, decay, input_bias, decay_bias, state, flags):
+        h, _, checkpoints = gated_recurrence(x, input_gate, decay_gate, decay, input_bias,
+                                             decay_bias, state=state, flags=flags,
+                                             with_checkpoints=True)
+        ctx.save_for_backward(x, input_gate, decay_gate, decay, checkpoints, input_bias,
+                              decay_bias, state, flags)
+        return h
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad):
+        *inputs, state, flags = ctx.saved_tensors
+        g = gated_recurrence_backward(grad.contiguous(), *inputs, state=state, flags=flags)
+        return (g.x, g.input_gate, g.decay_gate, g.decay, g.input_bias, g.decay_bias, g.state,
+                None)
 
 
 class RecurrentPolicy(torch.nn.Module):
@@ -117,6 +160,98 @@ class RecurrentPolicy(torch.nn.Module):
         return out[:, :-1], out[:, -1]
 
 
+class GatedPolicy(torch.nn.Module):
+    """Logits and value from a residual stack of gated recurrences (float32)."""
+
+    def __init__(self, observations, actions, channels=64, blocks=2, device="cuda"):
+        super().__init__()
+        self.channels = channels
+
+        def matrix(rows, cols, scale=1.0):
+            w = torch.randn(rows, cols, device=device) * (scale / cols ** 0.5)
+            return torch.nn.Parameter(w)
+
+        def each(make):
+            return torch.nn.ParameterList([make() for _ in range(blocks)])
+
+        def constant(value, n=channels):
+            return torch.nn.Parameter(torch.full((n,), value, device=device))
+
+        self.w_in = matrix(channels, observations, observations ** 0.5)
+        self.norms = torch.nn.ParameterList([constant(1.0) for _ in range(blocks + 1)])
+        self.w_gates = each(lambda: matrix(3 * channels, channels))
+        # a between 0.5 and 0.99 with an open decay gate: 8 softplus(decay) = -log(a)
+        slow = -torch.logspace(-0.3, -0.005, channels, device=device).log() / 8
+        self.decays = each(lambda: torch.nn.Parameter(torch.log(torch.expm1(slow))))
+        self.input_biases = each(lambda: constant(0.0))
+        self.decay_biases = each(lambda: constant(0.0))
+        self.w_blocks = each(lambda: matrix(channels, channels, 0.5))
+        self.w_out = matrix(actions + 1, channels, 0.1)
+
+    def new_state(self, num_envs):
+        """What acting carries from step to step: each block's states."""
+        return tuple(torch.zeros(num_envs, self.channels, device=self.w_in.device)
+                     for _ in self.decays)
+
+    @torch.no_grad()
+    def step(self, obs, starts, state, slots=None):
+        """One step of every environment: obs [num_envs, observations], starts
+        [num_envs] marks new episodes (or None); state, at the places that slots give,
+        is updated in place."""
+        new, stream = obs @ self.w_in.t(), None
+        for norm, w, decay, ib, db, w_block, pool in zip(
+                self.norms, self.w_gates, self.decays, self.input_biases, self.decay_biases,
+                self.w_blocks, state):
+            y, total = rms_norm(new, norm, stream)
+            stream = new if stream is None else total
+            x, ig, dg = (y @ w.t()).split(self.channels, dim=1)
+            new = gated_step(x, ig, dg, decay, pool, ib, db, slots=slots,
+                             flags=starts) @ w_block.t()
+        out = rms_norm(new, self.norms[-1], stream)[0] @ self.w_out.t()
+        return out[:, :-1], out[:, -1]
+
+    def rows(self, obs, starts, state):
+        """The same over a window: obs [num_envs, observations, T], starts
+        [num_envs, T], state as it was when the window began."""
+        new = torch.matmul(self.w_in, obs)
+        stream = torch.zeros_like(new)
+        for norm, w, decay, ib, db, w_block, begin in zip(
+                self.norms, self.w_gates, self.decays, self.input_biases, self.decay_biases,
+                self.w_blocks, state):
+            y, stream = _Norm.apply(new, stream, norm)
+            x, ig, dg = torch.matmul(w, y).split(self.channels, dim=1)
+            new = torch.matmul(w_block, _Gated.apply(x, ig, dg, decay, ib, db, begin, starts))
+        out = torch.matmul(self.w_out, _Norm.apply(new, stream, self.norms[-1])[0])
+        return out[:, :-1], out[:, -1]
+
+
+@torch.no_grad()
+def plan(policy, obs, model, steps, beams=4):
+    """The likeliest sequences of actions of a GatedPolicy from new episodes: obs
+    [N, observations] is what each episode begins with, and model(actions), actions
+    [N * beams] int64, gives the observations that follow.  Returns the actions
+    [N, beams, steps] and their log probabilities [N, beams], the likeliest first.
+    The beams' states and their actions so far lie in pools that beam_reorder keeps in
+    order."""
+    N = len(obs)
+    dev = obs.device
+    pools = policy.new_state(N * beams)
+    taken = torch.zeros(N * beams, steps, dtype=torch.int64, device=dev)
+    slots = torch.arange(N * beams, dtype=torch.int32, device=dev).view(N, beams)
+    # at first the beams of an episode are alike, so one of them counts
+    scores = torch.full((N, beams), -float("inf"), device=dev)
+    scores[:, 0] = 0.0
+    obs = obs.repeat_interleave(beams, 0)
+    for t in range(steps):
+        logits, _ = policy.step(obs, None, pools, slots=slots.view(-1))
+        choice = beam_select(logits.view(N, beams, -1), scores)
+        slots = beam_reorder([*pools, taken], slots, choice.parents)
+        scores, actions = choice.scores, choice.tokens.view(-1).long()
+        taken[slots.view(-1).long(), t] = actions
+        obs = model(actions)
+    return taken[slots.view(-1).long()].view(N, beams, steps), scores
+
+
 class Recall:
     """Environments whose observation is the cue (one-hot) at an episode's first
     step, zero after it, and a last entry that is 1 at its last step."""
@@ -177,11 +312,14 @@ def update(policy, optimizer, window, bootstrap, state, epochs=2, gamma=0.95, la
     return norm
 
 
-def train(updates=60, num_envs=256, T=48, lr=1e-2, seed=0, report=None):
+CORES = {"selective": RecurrentPolicy, "gated": GatedPolicy}
+
+
+def train(updates=60, num_envs=256, T=48, lr=1e-2, seed=0, report=None, core="selective"):
     """Mean reward per episode of each window."""
     torch.manual_seed(seed)
     env = Recall(num_envs)
-    policy = RecurrentPolicy(env.cues + 1, env.cues)
+    policy = CORES[core](env.cues + 1, env.cues)
     optimizer = torch.optim.Adam(policy.parameters(), lr=lr)
     state = policy.new_state(num_envs)
     history = []
@@ -201,8 +339,9 @@ def main():
     parser.add_argument("--updates", type=int, default=60)
     parser.add_argument("--envs", type=int, default=256)
     parser.add_argument("--steps", type=int, default=48, help="steps of a window")
+    parser.add_argument("--core", choices=sorted(CORES), default="selective")
     args = parser.parse_args()
-    train(args.updates, args.envs, args.steps, report=lambda i, r, norm: print(
+    train(args.updates, args.envs, args.steps, core=args.core, report=lambda i, r, norm: print(
         f"update {i:3d}  reward per episode {r:.3f}  gradient norm {norm:.3f}", flush=True))
 
 

@@ -35,25 +35,39 @@ import sys
 ROOT = os.path.dirname(os.path.abspath(__file__))
 
 
-# Sources of the operators of a recurrent policy or model, whose summary has a
-# digest of its own; the rest are the estimators'.
+# Sources of the operators of a recurrent policy or model, and of those of a block
+# and of a search, whose summaries have digests of their own; the rest are the
+# estimators'.
 _SEQUENCE_SOURCES = ("seq", "grad_clip")
+_BLOCK_SOURCES = ("seq_gated", "norm", "beams")
+_BLOCK_HEADER = (b"/* ------------------------------------------- operators of a block",
+                 b"/* Static description of a status code")
 
 
-def _kernel_sources(sequence=False):
+def _kernel_sources(sequence=False, blocks=False):
     csrc = sorted(glob.glob(os.path.join(ROOT, "linear_recurrence_scan_row_amd", "csrc", "*")))
-    return [os.path.relpath(p, ROOT) for p in csrc
-            if os.path.basename(p).startswith(_SEQUENCE_SOURCES) == sequence] + ["include/rlca.h"]
+
+    def wanted(name):
+        if name.startswith(_BLOCK_SOURCES) or blocks:
+            return blocks and name.startswith(_BLOCK_SOURCES + ("seq.", "seq_scan.hpp"))
+        return name.startswith(_SEQUENCE_SOURCES) == sequence
+    return [os.path.relpath(p, ROOT) for p in csrc if wanted(os.path.basename(p))] \
+        + ["include/rlca.h"]
 
 
-def source_digest(sequence=False) -> str:
+def source_digest(sequence=False, blocks=False) -> str:
     """Digest of the estimators' kernel sources (sequence: of the sequence
-    operators'); stored with a counter summary so that a summary taken on
+    operators', blocks: of the block and beam operators', whose part of the header
+    the others leave out); stored with a counter summary so that a summary taken on
     other code is not reported for this code."""
     h = hashlib.sha256()
-    for rel in _kernel_sources(sequence):
+    for rel in _kernel_sources(sequence, blocks):
         with open(os.path.join(ROOT, rel), "rb") as f:
-            h.update(f.read())
+            text = f.read()
+        if rel.endswith("rlca.h") and not blocks:
+            begin, end = (text.index(mark) for mark in _BLOCK_HEADER)
+            text = text[:begin] + text[end:]
+        h.update(text)
     return h.hexdigest()[:16]
 
 

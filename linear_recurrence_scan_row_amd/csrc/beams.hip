@@ -298,7 +298,9 @@ __global__ __launch_bounds__(kThreads) void beam_merge(SelectParams p) {
     __shared__ uint32_t most_of[kThreads], ranked_index[kRanked], bound, reached;
     __shared__ uint32_t indexes[kCandidates];
     const uint32_t search = blockIdx.x, tid = threadIdx.x, wave = tid / kWave, lane = tid % kWave;
-    for (uint32_t b = wave; b < p.beams; b += kWaves) {
+    // 16 lanes a beam
+    for (uint32_t b = tid / 16; b < p.beams; b += kThreads / 16) {
+        const uint32_t part = tid % 16;
         const uint32_t row = search * p.beams + b;
         const float score = p.scores[row];
         const bool finished = p.finished != nullptr && p.finished[row] != 0;
@@ -310,17 +312,17 @@ __global__ __launch_bounds__(kThreads) void beam_merge(SelectParams p) {
         if (kind == kLogits) {
             const ChunkSum *sums = p.sums + (int64_t)row * p.chunks;
             float most = -INFINITY;
-            for (uint32_t c = lane; c < p.chunks; c += kWave) most = fmaxf(most, sums[c].most);
+            for (uint32_t c = part; c < p.chunks; c += 16) most = fmaxf(most, sums[c].most);
 #pragma unroll
-            for (int m = 1; m < kWave; m <<= 1) most = fmaxf(most, __shfl_xor(most, m));
+            for (int m = 1; m < 16; m <<= 1) most = fmaxf(most, __shfl_xor(most, m));
             double sum = 0.0;
-            for (uint32_t c = lane; c < p.chunks; c += kWave) {
+            for (uint32_t c = part; c < p.chunks; c += 16) {
                 const ChunkSum s = sums[c];
                 // a chunk of -infinity alone has sum 0; a NaN stays one
                 sum += s.most == -INFINITY ? s.sum : s.sum * exp((double)s.most - (double)most);
             }
 #pragma unroll
-            for (int m = 1; m < kWave; m <<= 1) sum += __shfl_xor(sum, m);
+            for (int m = 1; m < 16; m <<= 1) sum += __shfl_xor(sum, m);
             if (sum != sum)
                 kind = kNan;
             else if (sum == 0.0)
@@ -328,7 +330,7 @@ __global__ __launch_bounds__(kThreads) void beam_merge(SelectParams p) {
             else
                 off = (double)score - log(sum), top = most;
         }
-        if (lane == 0) {
+        if (part == 0) {
             offset[b] = off;
             largest[b] = top;
             kinds[b] = kind;

@@ -879,7 +879,8 @@ static const void *forward_kernel(const Shape &s) {
 
 // Both arrays of the backward call do not fit the registers from 1024 channels on; few
 // are kept there, since what is read again matters less than waves to hide it (2048
-// channels: 2 blocks a thread 80 us, 8 86, 16 and half the threads 87).
+// channels: 2 blocks a thread 80 us, 6 77, which is what fits 1024 threads; 16 with half
+// the threads 83).
 template <typename E>
 static const void *backward_kernel(const Shape &s) {
     if (s.dense)
@@ -887,8 +888,8 @@ static const void *backward_kernel(const Shape &s) {
                             : (const void *)rms_norm_dense_backward<E, 4, 4>;
     return s.threads == 256 ? (const void *)rms_norm_rows_backward<E, 256, 8, 4>
            : s.threads == 512 ? (const void *)rms_norm_rows_backward<E, 512, 8, 8>
-           : s.lanes == 8     ? (const void *)rms_norm_rows_backward<E, 1024, 8, 2>
-           : s.lanes == 4     ? (const void *)rms_norm_rows_backward<E, 1024, 4, 2>
+           : s.lanes == 8     ? (const void *)rms_norm_rows_backward<E, 1024, 8, 6>
+           : s.lanes == 4     ? (const void *)rms_norm_rows_backward<E, 1024, 4, 6>
                               : (const void *)rms_norm_rows_backward<E, 1024, 1, 2>;
 }
 

@@ -760,9 +760,11 @@ constexpr int64_t kFewestTiles = 4;
 constexpr int64_t kMostChunks = 64;
 constexpr int kShared = 8;
 
-// Waves that a launch wants: 4 a SIMD, or what the registers of the backward kernel leave.
+// Waves that a launch wants: 4 on each of the 1024 SIMDs, or the 3 that the registers of
+// the backward kernel leave where values are float32.
+constexpr int64_t kSimds = 1024;
 static int64_t gate_wanted(const rlca_gated_call &c, bool backward) {
-    return backward && c.dtype == RLCA_F32 ? 3072 : 4096;
+    return (backward && c.dtype == RLCA_F32 ? 3 : 4) * kSimds;
 }
 
 struct GatePlan {
@@ -794,7 +796,7 @@ static GatePlan gate_plan(const rlca_gated_call &c, bool backward) {
     g.groups = groups(g.L);
     g.chunks = 1;
     if (chunked && rows > 0) {
-        int64_t want = 4096 / (g.groups * c.num_seqs);
+        int64_t want = 4 * kSimds / (g.groups * c.num_seqs);
         if (want > g.tiles / kFewestTiles) want = g.tiles / kFewestTiles;
         if (want > kMostChunks) want = kMostChunks;
         g.chunks = want;

@@ -468,13 +468,14 @@ struct ReorderParams {
     uint32_t num_pools, searches, beams;
 };
 
-// PIECES accesses a thread: a workgroup copies a tile of kThreads * PIECES * kPiece
-// bytes of a place, for every copy of its searches.
-template <int PIECES>
+// A workgroup copies a tile of 4 KB of a place, 16 bytes a thread, for every copy of its
+// searches.  (Tiles of 16 KB: 32 searches of 8 beams with 18 pools 80 us against 67, 4
+// searches with 12 pools 18 against 5.)
+constexpr int64_t kTile = (int64_t)kThreads * kPiece;
+
 __global__ __launch_bounds__(kThreads) void beam_reorder(ReorderParams p) {
     __shared__ int32_t free_slots[RLCA_MAX_BEAMS], from[RLCA_MAX_BEAMS], to[RLCA_MAX_BEAMS];
     __shared__ uint32_t copies;
-    constexpr int64_t kTile = (int64_t)kThreads * PIECES * kPiece;
     const uint32_t tid = threadIdx.x, lane = tid % kWave;
     uint32_t pool = 0, past = p.num_pools;  // the last pool whose first tile is not after ours
     while (past - pool > 1) {
@@ -527,22 +528,14 @@ __global__ __launch_bounds__(kThreads) void beam_reorder(ReorderParams p) {
         for (uint32_t c = 0; c < count; ++c) {
             const char *source = data + from[c] * place + mine;
             char *target = data + to[c] * place + mine;
-            typedef uint32_t piece __attribute__((ext_vector_type(4)));
-            piece v[PIECES];
-#pragma unroll
-            for (int i = 0; i < PIECES; ++i)
-                if (mine + (int64_t)i * kThreads * kPiece + kPiece <= place)
-                    __builtin_memcpy(&v[i], source + (int64_t)i * kThreads * kPiece, kPiece);
-#pragma unroll
-            for (int i = 0; i < PIECES; ++i) {
-                const int64_t begin = mine + (int64_t)i * kThreads * kPiece;
-                if (begin + kPiece <= place) {
-                    __builtin_memcpy(target + (int64_t)i * kThreads * kPiece, &v[i], kPiece);
-                } else {
-                    // a place's last bytes
-                    for (int64_t b = begin; b < place; ++b)
-                        target[b - mine] = source[b - mine];
-                }
+            if (mine + kPiece <= place) {
+                typedef uint32_t piece __attribute__((ext_vector_type(4)));
+                piece v;
+                __builtin_memcpy(&v, source, kPiece);
+                __builtin_memcpy(target, &v, kPiece);
+            } else {
+                // a place's last bytes
+                for (int64_t i = mine; i < place; ++i) target[i - mine] = source[i - mine];
             }
         }
     }
@@ -550,11 +543,11 @@ __global__ __launch_bounds__(kThreads) void beam_reorder(ReorderParams p) {
 
 // ------------------------------------------------------------------- host side
 // Blocks of kVec logits a thread: chunks of 2048 logits where 6144 would make too few
-// workgroups for the chip (64 searches of 8 beams and 100003 tokens, bf16: 39 us, 42
-// with 4096 or 8192).
+// workgroups for the chip (4 beams of 32000 tokens, fp32: 9.7 us against 10.8; 32 of
+// 50000, bf16: 14.8 against 12.3; 512 of 100003: 39 us, 42 with 4096 or 8192).
 static int blocks_of(const rlca_beam_call &c) {
     const int64_t rows = c.num_searches * c.beams;
-    return rows * ((c.vocab + 6143) / 6144) < 512 ? 1 : 3;
+    return rows * ((c.vocab + 6143) / 6144) < 128 ? 1 : 3;
 }
 
 static int64_t chunks_of(const rlca_beam_call &c) {
@@ -687,12 +680,6 @@ rlca_status rlca_beam_reorder(const rlca_state_pool *pools, int64_t num_pools,
                 return RLCA_ERR_ALIASING;
     }
     if (N == 0) return RLCA_OK;
-    // Tiles of 16 KB of a place, or of 4 KB where those would be too few for the chip.
-    const auto tiles_of = [&](int64_t bytes, int64_t tile) { return (bytes + tile - 1) / tile; };
-    int64_t tiles = 0;
-    for (int64_t i = 0; i < num_pools; ++i) tiles += tiles_of(pools[i].place_bytes, 1 << 14);
-    const int pieces = tiles * N >= 2048 ? 4 : 1;
-    const int64_t tile = (int64_t)kThreads * kPiece * pieces;
     ReorderParams p;
     p.slots = slots;
     p.parents = parents;
@@ -705,7 +692,7 @@ rlca_status rlca_beam_reorder(const rlca_state_pool *pools, int64_t num_pools,
         int64_t blocks = 0;
         p.num_pools = 0;
         for (; i < num_pools && p.num_pools < kMaxPools; ++i) {
-            const int64_t more = tiles_of(pools[i].place_bytes, tile);
+            const int64_t more = (pools[i].place_bytes + kTile - 1) / kTile;
             if (more == 0 || places == 0) continue;
             if (blocks + more > (int64_t)1 << 23) break;
             p.pools[p.num_pools++] =
@@ -713,8 +700,7 @@ rlca_status rlca_beam_reorder(const rlca_state_pool *pools, int64_t num_pools,
             blocks += more;
         }
         const dim3 grid((uint32_t)(blocks < 1 ? 1 : blocks), (uint32_t)(N < 65535 ? N : 65535));
-        st = launch(pieces == 4 ? (const void *)beam_reorder<4> : (const void *)beam_reorder<1>,
-                    grid, kThreads, 0, p, stream);
+        st = launch((const void *)beam_reorder, grid, kThreads, 0, p, stream);
         if (st != RLCA_OK) return st;
     } while (i < num_pools);
     return RLCA_OK;

@@ -852,7 +852,10 @@ static Shape shape_of(const rlca_norm_call &c, bool backward) {
                               row(c.grad_sum, c.grad_sum_stride_channel)
                         : row(c.residual, c.residual_stride_channel));
     if (s.dense) {
-        s.waves = D <= 4 * kWave * vec ? 1 : 4;
+        // a wave a row where it holds the row and there are rows enough for the chip, or
+        // one block a lane is all of it (2048 channels, bf16: one row 4.4 us against 3.9
+        // with four waves, 64 rows 5.1 against 3.4, 2048 rows 8.8 against 9.4)
+        s.waves = D <= kWave * vec || (D <= 4 * kWave * vec && N >= 1024) ? 1 : 4;
         s.work = N;
         const int64_t rows = 4 / s.waves;
         s.groups = (N + rows - 1) / rows;
@@ -863,8 +866,12 @@ static Shape shape_of(const rlca_norm_call &c, bool backward) {
     // 128 bytes of a channel's steps side by side, a whole cache line (64 bytes: 78 us
     // against 58 forward and 101 against 80 backward for 8x2048 channels of 2048 steps,
     // bf16 with residual).  64 with more channels than registers hold then (4096 of 1024
-    // steps: 70 against 94, and 99 against 115).  16 where there are too few tiles.
-    s.lanes = N * tiles(8) < 128 ? 1 : D <= 2048 ? 8 : 4;
+    // steps: 70 against 94, and 99 against 115), or with fewer tiles than compute units
+    // (1x2048 channels of 4096 steps: 22 against 27), unless they share lines for want of
+    // alignment (6x1536 of 2049 steps 45 against 38).  16 where tiles are fewest (2048 of
+    // 512 steps: 10.8 against 13.5 and 20; not for 64 of 1024: 6.5 against 4.6).
+    const bool few = N * tiles(8) < 256 && T % (4 * vec) == 0;
+    s.lanes = D <= 512 ? 8 : N * tiles(4) < 64 ? 1 : D <= 2048 && !few ? 8 : 4;
     s.threads = s.lanes != 8 || D > 512 ? 1024 : D > 128 ? 512 : 256;
     s.tiles = tiles(s.lanes);
     s.work = N * s.tiles;

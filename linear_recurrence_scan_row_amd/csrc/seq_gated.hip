@@ -19,7 +19,7 @@
 // whose issue takes as long as the bytes where values have 16 bits.  Measured: 8x2048
 // channels of 2048 steps bf16 forward 52 to 62 us (5.1 to 4.3 TB/s), gradients 87 (5.4);
 // 4096x64 of 128 steps fp32 with flags 112 and 179 (4.8 and 5.3); one row set of 512x65535
-// bf16 58 (4.6); a step of 512x8192 bf16 14 (4.7); a large copy reaches 5.05 TB/s.
+// bf16 58 (4.6); a step of 512x8192 bf16 13 (5.1); a large copy reaches 5.05 TB/s.
 #include "seq_scan.hpp"
 
 namespace rlca {
@@ -696,57 +696,43 @@ __device__ __forceinline__ int64_t gate_place(const GateStepParams &p, uint32_t 
     return s >= 0 && s < p.places ? s : -1;
 }
 
-// A thread takes VEC neighbouring channels of the sequences blockIdx.y, blockIdx.y +
-// gridDim.y, ..., the next one's loads issued before one is computed.
-template <typename E, int VEC>
+// A thread takes a channel of the sequences blockIdx.y, blockIdx.y + gridDim.y, ..., the
+// next one's loads issued before one is computed.  (Four channels a thread: 512x8192
+// bf16 14.2 us against 13.2, 64x4096 3.7 against 3.3.)
+template <typename E>
 __global__ __launch_bounds__(kGateStepThreads) void gated_step(GateStepParams p) {
-    const uint32_t d = (blockIdx.x * blockDim.x + threadIdx.x) * VEC;
+    const uint32_t d = blockIdx.x * blockDim.x + threadIdx.x;
     if (d >= p.channels) return;
-    const int left = p.channels - d < (uint32_t)VEC ? (int)(p.channels - d) : VEC;
     struct Loads {
         int64_t place;
-        Steps<VEC, E> x, ig, dg;
-        Steps<VEC, float> h;
+        E x, ig, dg;
+        float h;
     } next;
     const auto load = [&](uint32_t n) {
         next.place = gate_place(p, n);
         if (next.place < 0) return;
-        next.x.load(static_cast<const E *>(p.x) + n * p.x_n + d, left);
-        next.ig.load(static_cast<const E *>(p.input_gate) + n * p.ig_n + d, left);
-        next.dg.load(static_cast<const E *>(p.decay_gate) + n * p.dg_n + d, left);
-        next.h.load(p.state + next.place * p.channels + d,
-                    p.starts != nullptr && p.starts[n] != 0 ? 0 : left);
+        next.x = static_cast<const E *>(p.x)[n * p.x_n + d];
+        next.ig = static_cast<const E *>(p.input_gate)[n * p.ig_n + d];
+        next.dg = static_cast<const E *>(p.decay_gate)[n * p.dg_n + d];
+        next.h = p.starts != nullptr && p.starts[n] != 0 ? 0.f
+                                                         : p.state[next.place * p.channels + d];
     };
     load(blockIdx.y);
-    float slow[VEC], ib[VEC] = {}, db[VEC] = {};
-    load_steps<VEC>(p.decay + d, left, slow);
-    if (p.input_bias != nullptr) load_steps<VEC>(p.input_bias + d, left, ib);
-    if (p.decay_bias != nullptr) load_steps<VEC>(p.decay_bias + d, left, db);
-#pragma unroll
-    for (int c = 0; c < VEC; ++c) {
-        slow[c] = slow_of(p.scale, slow[c]);
-        ib[c] *= -kLog2e, db[c] *= -kLog2e;
-    }
+    const float slow = slow_of(p.scale, p.decay[d]);
+    const float input2 = p.input_bias == nullptr ? 0.f : -kLog2e * p.input_bias[d];
+    const float decay2 = p.decay_bias == nullptr ? 0.f : -kLog2e * p.decay_bias[d];
     for (uint32_t n = blockIdx.y; n < p.num_seqs; n += gridDim.y) {
         const Loads now = next;
         if (n + gridDim.y < p.num_seqs) load(n + gridDim.y);
-        float out[VEC] = {};
+        float out = 0.f;
         if (now.place >= 0) {
-            float x[VEC], ig[VEC], dg[VEC], h[VEC];
-            now.x.widen(x);
-            now.ig.widen(ig);
-            now.dg.widen(dg);
-            now.h.widen(h);
-#pragma unroll
-            for (int c = 0; c < VEC; ++c) {
-                float a, rest;
-                decay_of<false>(slow[c] * gate_of(dg[c], db[c]), a, rest);
-                const float in = __builtin_amdgcn_sqrtf(rest) * (gate_of(ig[c], ib[c]) * x[c]);
-                out[c] = fmaf(a, h[c], in);
-            }
-            store_steps<VEC>(p.state + now.place * p.channels + d, left, out);
+            float a, rest;
+            decay_of<false>(slow * gate_of((float)now.dg, decay2), a, rest);
+            const float in = __builtin_amdgcn_sqrtf(rest) * (gate_of((float)now.ig, input2) * (float)now.x);
+            out = fmaf(a, now.h, in);
+            p.state[now.place * p.channels + d] = out;
         }
-        store_steps<VEC>(static_cast<E *>(p.out) + (int64_t)n * p.channels + d, left, out);
+        static_cast<E *>(p.out)[(int64_t)n * p.channels + d] = (E)out;
     }
 }
 
@@ -759,7 +745,8 @@ __global__ __launch_bounds__(kGateStepThreads) void gated_step(GateStepParams p)
 // kShared waves of a workgroup share a row (512 rows of 65535 steps: 71 us against 198
 // apart and 114 in chunks; 4096 rows of 8191 steps 74 against 56 apart); from
 // kFewestRows down rows are cut into chunks of at least kFewestTiles tiles, at most
-// kMostChunks.
+// kMostChunks (64 rows of 131072 steps 48 us against 60 shared, 96 of 65536 33 and 33,
+// 128 36 against 33).
 constexpr int64_t kFewWaves = 2048;
 constexpr int64_t kFewRows = 2048;
 constexpr int64_t kFewestRows = 96;
@@ -1080,22 +1067,15 @@ rlca_status rlca_gated_step(const rlca_gated_step_call *call, hipStream_t stream
     p.num_seqs = (uint32_t)N;
     p.channels = (uint32_t)D;
     p.scale = (float)c.scale;
-    constexpr int kVec = 4;
-    const bool wide = N * D >= (int64_t)1 << 18;
-    const int vec = wide ? kVec : 1;
-    const uint32_t threads = (uint32_t)((D + vec - 1) / vec);
+    const uint32_t threads = (uint32_t)D;
     const uint32_t size =
         threads >= (uint32_t)kGateStepThreads ? kGateStepThreads : (threads + 63) / 64 * 64;
     const uint32_t across = (threads + size - 1) / size;
-    const uint32_t most = (2048 + across - 1) / across;
+    const uint32_t most = (2048 + across - 1) / across;  // enough to fill the chip
     const int64_t all = N < 32768 ? N : 32768;
-    const void *kernel =
-        c.dtype == RLCA_F32    ? (wide ? (const void *)gated_step<float, kVec>
-                                       : (const void *)gated_step<float, 1>)
-        : c.dtype == RLCA_BF16 ? (wide ? (const void *)gated_step<__bf16, kVec>
-                                       : (const void *)gated_step<__bf16, 1>)
-                               : (wide ? (const void *)gated_step<_Float16, kVec>
-                                       : (const void *)gated_step<_Float16, 1>);
+    const void *kernel = c.dtype == RLCA_F32    ? (const void *)gated_step<float>
+                         : c.dtype == RLCA_BF16 ? (const void *)gated_step<__bf16>
+                                                : (const void *)gated_step<_Float16>;
     return launch(kernel, dim3(across, all < most ? (uint32_t)all : most), size, 0, p, stream);
 }
 

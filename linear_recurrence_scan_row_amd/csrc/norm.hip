@@ -12,8 +12,8 @@
 // channels (T = 1) take a wave or a workgroup a row.
 //
 // Measured, where a large copy reaches 5.05 TB/s: 8x2048 channels of 2048 steps bf16 with
-// residual 58 to 63 us (4.6 to 4.3 TB/s), gradients 72 (285 MB read for the 201 of the
-// inputs: not all of both arrays stays in registers; 4.9 TB/s); prompts of 6x1536x2049
+// residual 58 to 63 us (4.6 to 4.3 TB/s), gradients 70 (285 MB read for the 201 of the
+// inputs: not all of both arrays stays in registers; 5.1 TB/s); prompts of 6x1536x2049
 // fp16 to 8 bits, of different lengths, 39 (2.9: rows that begin at any 2 bytes, and
 // fewer tiles than compute units); 4096x64 of 128 steps fp32 107 (5.0); one row of 4096
 // channels 3.8.

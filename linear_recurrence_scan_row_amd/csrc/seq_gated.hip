@@ -19,7 +19,8 @@
 // whose issue takes as long as the bytes where values have 16 bits.  Measured: 8x2048
 // channels of 2048 steps bf16 forward 52 to 62 us (5.1 to 4.3 TB/s), gradients 87 (5.4);
 // 4096x64 of 128 steps fp32 with flags 112 and 179 (4.8 and 5.3); one row set of 512x65535
-// bf16 58 (4.6); a step of 512x8192 bf16 13 (5.1); a large copy reaches 5.05 TB/s.
+// bf16 58 (4.6); a step of 512x8192 bf16 13 to 14 (5.1 to 4.6); a large copy reaches
+// 5.05 TB/s.
 #include "seq_scan.hpp"
 
 namespace rlca {

@@ -24,6 +24,7 @@ constexpr int kWaves = kThreads / kWave;
 constexpr int kVec = 8;          // neighbouring logits of a thread
 constexpr int kRanked = kThreads;  // logits that are ranked, one a thread
 constexpr int kHeld = 80;          // threads whose logits are looked through for those
+constexpr float kNear = 0x1p22f;   // logits whose products with log2(e) are rounded by <= 1/4
 
 struct Best {
     float logit;
@@ -140,14 +141,15 @@ __global__ __launch_bounds__(kThreads) void beam_chunks(SelectParams p) {
     }
     // the thread's largest, and its sum of exponentials from there (a NaN or +infinity
     // makes that sum NaN): 2^(x log2(e) - from), where `low`, what the product for `from`
-    // was rounded by, is put right in the sum
+    // was rounded by, is put right in the sum.  `low` grows with the largest, and is at most
+    // 1/4 up to 2^22; further out, where 2^low would leave float32's range, and for
+    // infinities, the difference is formed first, an instruction more a logit.
     float most = -INFINITY;
 #pragma unroll
     for (int j = 0; j < BLOCKS; ++j)
 #pragma unroll
         for (int k = 0; k < kVec; ++k) most = fmaxf(most, x[j][k]);
-    // where the product overflows, the few exponentials that are not 0 are 1 by it
-    const float top = fmaxf(fminf(most, 1e37f), -1e37f);
+    const float top = fmaxf(fminf(most, kNear), -kNear);
     const float from = top * seq::kLog2e, low = fmaf(top, seq::kLog2e, -from);
     float sum = 0.f;
     if (most == top) {

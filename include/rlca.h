@@ -716,9 +716,10 @@ rlca_status rlca_rms_norm_backward(const rlca_norm_call *call, void *workspace,
 /* A beam search's selection.  For each of num_searches searches, over all `beams`
  * beams and `vocab` tokens, the `picks` candidates with the highest
  *   total = score_b + (logit_bv - log sum_v exp(logit_bv)),
- * best first, equal ones by beam and then token (the lower first).  Exponentials are
- * float32, their sums over a beam and the totals float64: totals are good to 1e-6,
- * and they are compared before the one rounding to float32.  A beam that is finished has one candidate, pad_token
+ * best first, equal ones by beam (the lower first), those of one beam by logit and then
+ * token (the lower first).  Exponentials are float32, their sums over a beam and the
+ * totals float64: totals are good to 1e-6, and they are compared before the one
+ * rounding to float32.  A beam that is finished has one candidate, pad_token
  * at its own score; its other totals are -infinity.  So are all totals of a beam
  * whose score is -infinity (an unused one: its logits do not count, whatever they
  * hold) and those of logits of -infinity (tokens that are not allowed; all of them

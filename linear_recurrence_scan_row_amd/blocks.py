@@ -370,7 +370,7 @@ class BeamChoice(NamedTuple):
 def beam_select(logits, scores, picks=None, finished=None, pad_token=0):
     """The best continuations of each search, over all its beams and the vocabulary:
     the `picks` (default: one a beam) highest of score + log_softmax(logits), equal
-    ones by the lower beam, then the lower token.
+    ones by the lower beam, those of one beam by the higher logit, then the lower token.
 
     logits [num_searches, beams, vocab] (float32, bfloat16 or float16; contiguous in
     its last dimension), scores [num_searches, beams] float32 the beams' totals so

@@ -49,7 +49,7 @@ struct SelectParams {
     int64_t by_search, by_beam;
     uint32_t searches, beams, vocab, picks, chunks;
     int32_t pad_token;
-    seq::FastDiv by_chunks, by_beams, by_each;  // each: chunks * picks
+    seq::FastDiv by_chunks, by_beams, by_each, by_vocab;  // each: chunks * picks
 };
 
 // A beam whose logits count: not finished, and of a finite score.
@@ -255,13 +255,20 @@ __global__ __launch_bounds__(kThreads) void beam_chunks(SelectParams p) {
     }
 }
 
-// A candidate of a search: its total's order (a NaN above all, 0 for none), and its
-// place among beams * vocab, the lower first.
+// A candidate of a search: its total's order (a NaN above all, 0 for none), its place
+// among beams * vocab, and its logit's order (0 where the beam's logits do not count).
+// Totals that float64 does not tell apart (about a score of -1e30, say) are ordered by
+// beam, those of one beam by logit, as the chunks' lists are, then by token: which
+// logits reach the lists depends on the chunks' size, so no other order of one beam's
+// would be the same for every launch.
 struct Candidate {
     uint64_t order;
-    uint32_t index;
-    __device__ __forceinline__ bool before(const Candidate &c) const {
-        return order > c.order || (order == c.order && index < c.index);
+    uint32_t index, logit;
+    __device__ __forceinline__ bool before(const Candidate &c, seq::FastDiv by_vocab) const {
+        if (order != c.order) return order > c.order;
+        return logit != c.logit && by_vocab.div(index) == by_vocab.div(c.index)
+                   ? logit > c.logit
+                   : index < c.index;
     }
 };
 
@@ -275,14 +282,15 @@ __device__ __forceinline__ double double_of(uint64_t order) {
     return __builtin_bit_cast(double, order >> 63 ? order ^ 0x8000000000000000ull : ~order);
 }
 
-__device__ __forceinline__ Candidate wave_first(Candidate c) {
+__device__ __forceinline__ Candidate wave_first(Candidate c, seq::FastDiv by_vocab) {
 #pragma unroll
     for (int m = 1; m < kWave; m <<= 1) {
         Candidate d;
         d.order = (uint64_t)(uint32_t)__shfl_xor((int)(c.order >> 32), m) << 32 |
                   (uint32_t)__shfl_xor((int)c.order, m);
         d.index = (uint32_t)__shfl_xor((int)c.index, m);
-        if (d.before(c)) c = d;
+        d.logit = (uint32_t)__shfl_xor((int)c.logit, m);
+        if (d.before(c, by_vocab)) c = d;
     }
     return c;
 }
@@ -299,8 +307,8 @@ __global__ __launch_bounds__(kThreads) void beam_merge(SelectParams p) {
     __shared__ Candidate firsts[kWaves];
     __shared__ uint32_t chosen[RLCA_MAX_BEAMS];
     __shared__ uint64_t orders[kCandidates], ranked[kRanked];
-    __shared__ uint32_t most_of[kThreads], ranked_index[kRanked], bound, reached;
-    __shared__ uint32_t indexes[kCandidates];
+    __shared__ uint32_t most_of[kThreads], ranked_index[kRanked], ranked_logit[kRanked];
+    __shared__ uint32_t indexes[kCandidates], logits[kCandidates], bound, reached;
     const uint32_t search = blockIdx.x, tid = threadIdx.x, wave = tid / kWave, lane = tid % kWave;
     // 16 lanes a beam
     for (uint32_t b = tid / 16; b < p.beams; b += kThreads / 16) {
@@ -346,12 +354,13 @@ __global__ __launch_bounds__(kThreads) void beam_merge(SelectParams p) {
     const Best *best = p.best + (int64_t)search * count;
     const auto candidate = [&](uint32_t i) {
         const uint32_t b = p.by_each.div(i), of_beam = i - b * each, kind = kinds[b];
-        Candidate c = {0, b * p.vocab};
+        Candidate c = {0, b * p.vocab, 0};
         if (kind == kLogits) {
             const Best x = best[i];
             if (x.token >= 0) {
                 c.order = order_of(offset[b] + ((double)x.logit - largest[b]));
                 c.index += (uint32_t)x.token;
+                c.logit = order_of(x.logit);
             }
         } else if (kind == kFinished && of_beam == 0 && !(offset[b] == -INFINITY)) {
             c.order = order_of(offset[b]);
@@ -370,12 +379,13 @@ __global__ __launch_bounds__(kThreads) void beam_merge(SelectParams p) {
             const Candidate c = candidate(i);
             orders[i] = c.order;
             indexes[i] = c.index;
+            logits[i] = c.logit;
         }
     const auto at = [&](uint32_t i) {
-        return fits ? Candidate{orders[i], indexes[i]} : candidate(i);
+        return fits ? Candidate{orders[i], indexes[i], logits[i]} : candidate(i);
     };
     const auto choose = [&](const Candidate &c, uint32_t n) {
-        const uint32_t b = c.index / p.vocab;
+        const uint32_t b = p.by_vocab.div(c.index);
         const int64_t to = (int64_t)search * p.picks + n;
         p.out_scores[to] = (float)double_of(c.order);
         p.out_tokens[to] = (int32_t)(c.index - b * p.vocab);
@@ -399,17 +409,20 @@ __global__ __launch_bounds__(kThreads) void beam_merge(SelectParams p) {
         const Candidate c = at(i);
         if (c.order != 0 && (uint32_t)(c.order >> 32) >= bound) {
             const uint32_t to = atomicAdd(&reached, 1u);
-            if (to < kRanked) ranked[to] = c.order, ranked_index[to] = c.index;
+            if (to < kRanked)
+                ranked[to] = c.order, ranked_index[to] = c.index, ranked_logit[to] = c.logit;
         }
     }
     __syncthreads();
     uint32_t n = reached;
     if (n <= kRanked) {
         if (tid < n) {
-            const Candidate mine = {ranked[tid], ranked_index[tid]};
+            const auto one = [&](uint32_t i) {
+                return Candidate{ranked[i], ranked_index[i], ranked_logit[i]};
+            };
+            const Candidate mine = one(tid);
             uint32_t rank = 0;
-            for (uint32_t i = 0; i < n; ++i)
-                rank += Candidate{ranked[i], ranked_index[i]}.before(mine) ? 1u : 0u;
+            for (uint32_t i = 0; i < n; ++i) rank += one(i).before(mine, p.by_vocab) ? 1u : 0u;
             if (rank < p.picks) choose(mine, rank);
         }
         n = n < p.picks ? n : p.picks;
@@ -417,21 +430,23 @@ __global__ __launch_bounds__(kThreads) void beam_merge(SelectParams p) {
     } else {
         // many equal ones: one after the other, the thread's first after the last one
         const auto next_after = [&](const Candidate &last, bool any) {
-            Candidate found = {0, ~0u};
+            Candidate found = {0, ~0u, 0};
             for (uint32_t i = tid; i < count; i += kThreads) {
                 const Candidate c = at(i);
-                if (c.order != 0 && (any || last.before(c)) && c.before(found)) found = c;
+                if (c.order != 0 && (any || last.before(c, p.by_vocab)) &&
+                    c.before(found, p.by_vocab))
+                    found = c;
             }
             return found;
         };
-        Candidate mine = next_after(Candidate{0, 0}, true);
+        Candidate mine = next_after(Candidate{0, 0, 0}, true);
         for (n = 0; n < p.picks; ++n) {
-            Candidate first = wave_first(mine);
+            Candidate first = wave_first(mine, p.by_vocab);
             if (lane == 0) firsts[wave] = first;
             __syncthreads();
 #pragma unroll
             for (int w = 0; w < kWaves; ++w)
-                if (firsts[w].before(first)) first = firsts[w];
+                if (firsts[w].before(first, p.by_vocab)) first = firsts[w];
             __syncthreads();
             if (first.order == 0) break;  // the same in all threads
             if (tid == 0) choose(first, n);
@@ -633,6 +648,7 @@ rlca_status rlca_beam_select(const rlca_beam_call *call, void *workspace, size_t
     p.by_chunks = fast_div(p.chunks);
     p.by_beams = fast_div(p.beams);
     p.by_each = fast_div(p.chunks * p.picks);
+    p.by_vocab = fast_div(p.vocab);
     const uint32_t groups = p.searches * p.beams * p.chunks;
     p.sums = static_cast<ChunkSum *>(workspace);
     p.best = reinterpret_cast<Best *>(p.sums + groups);

@@ -80,9 +80,9 @@ __device__ __forceinline__ uint32_t magnitude(float x) {
 }
 __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return a > b ? a : b; }
 
-// r, from the sum of squares of values times factor; and a step's scale.
+// r / factor, from the sum of squares of values times factor; and a step's scale.
 __device__ __forceinline__ float rsqrt_of(const NormParams &p, float sum, float factor) {
-    return factor * __builtin_amdgcn_rsqf(fmaf(sum, p.per_channel, p.eps * factor * factor));
+    return __builtin_amdgcn_rsqf(fmaf(sum, p.per_channel, p.eps * factor * factor));
 }
 __device__ __forceinline__ float scale_of(uint32_t most, float r) {
     const float s = __builtin_bit_cast(float, most) * r / kMostE4m3;
@@ -90,12 +90,18 @@ __device__ __forceinline__ float scale_of(uint32_t most, float r) {
 }
 // What s and the weight are multiplied by for the 8-bit value: 448 / max|s weight|, since
 // r is in both (each rounding left out is a value less that falls on the other side of
-// a border); r / scale at the least scale; NaN where the scale is.
+// a border); NaN where the scale is.  Where all products are 0 anything finite will do.
 __device__ __forceinline__ float gain_of(uint32_t most, float factor, float r, float scale) {
-    float g = scale == kLeastScale ? r / kLeastScale
-                                   : kMostE4m3 / __builtin_bit_cast(float, most) * factor;
-    g = g > 3.4e38f ? 3.4e38f : g;  // 0 times it is 0
-    return scale != scale ? scale : g;
+    const float g = kMostE4m3 / __builtin_bit_cast(float, most) * factor;
+    return scale != scale ? scale : most == 0 ? r : g;
+}
+// Whether a step's 8-bit values have to be formed from y itself, with passes of their own:
+// near the least scale, and where s weight is so small that its largest is no normal
+// number or 448 / it too large a one, or that all of them have underflowed and r is
+// large enough to bring them back (eps below 2^-36).
+__device__ __forceinline__ bool small_values(uint32_t most, float factor, float r, float scale) {
+    const uint32_t least = __builtin_bit_cast(uint32_t, kMostE4m3 * 0x1p-126f);
+    return most == 0 ? r > 0x1p18f : scale < 0x1p-100f || (factor == 1.f && most < least);
 }
 
 // K values in e4m3, rounded to nearest even.  Those of one step are at most 448 up to
@@ -209,14 +215,15 @@ __global__ __launch_bounds__(THREADS) void rms_norm_rows(NormParams p) {
     __shared__ __attribute__((aligned(16))) float sums[WAVES][Mine::STEPS];
     __shared__ __attribute__((aligned(16))) uint32_t mosts[Q8 ? WAVES : 1][Mine::STEPS];
     __shared__ uint32_t large[WAVES];
+    __shared__ float factors[Q8 ? Mine::STEPS : 1];  // of the steps, where told(large)
     Mine at;
     at.set(p, blockIdx.x);
-    const E *x = static_cast<const E *>(p.x) + at.n * p.x_n + at.t;
-    const E *res = p.residual == nullptr
-                       ? nullptr
-                       : static_cast<const E *>(p.residual) + at.n * p.r_n + at.t;
-    const int64_t to = (int64_t)at.n * p.channels * p.T + at.t;
-    E *sum_out = static_cast<E *>(p.sum) + to;
+    const E *x = static_cast<const E *>(p.x) + at.n * p.x_n;
+    const E *res =
+        p.residual == nullptr ? nullptr : static_cast<const E *>(p.residual) + at.n * p.r_n;
+    const int64_t out_row = (int64_t)at.n * p.channels * p.T;
+    E *sum_out = static_cast<E *>(p.sum) + out_row;
+    const auto to = [&](uint32_t d) { return out_row + (int64_t)d * p.T + at.t; };
 
     // kBatch channels' steps, every load issued before the first value is used; their
     // sums are stored the first time
@@ -225,19 +232,21 @@ __global__ __launch_bounds__(THREADS) void rms_norm_rows(NormParams p) {
 #pragma unroll
         for (int u = 0; u < N; ++u)
             if (d + u * ACROSS < p.channels)
-                b[u].load(x + (d + u * ACROSS) * p.x_d, at.left);
+                b[u].load(x + ((d + u * ACROSS) * p.x_d + at.t), at.left);
             else
                 clear(b[u]);
         if (res == nullptr) return;
         Steps<VEC, E> r[N];
 #pragma unroll
         for (int u = 0; u < N; ++u)
-            if (d + u * ACROSS < p.channels) r[u].load(res + (d + u * ACROSS) * p.r_d, at.left);
+            if (d + u * ACROSS < p.channels)
+                r[u].load(res + ((d + u * ACROSS) * p.r_d + at.t), at.left);
 #pragma unroll
         for (int u = 0; u < N; ++u)
             if (d + u * ACROSS < p.channels) {
                 add_residual(b[u], r[u]);
-                if (store) store_block(sum_out + (int64_t)(d + u * ACROSS) * p.T, at.room, b[u]);
+                if (store)
+                    store_block(sum_out + ((int64_t)(d + u * ACROSS) * p.T + at.t), at.room, b[u]);
             }
     };
     const auto weight = [&](uint32_t d) { return p.weight == nullptr ? 1.f : p.weight[d]; };
@@ -311,6 +320,7 @@ __global__ __launch_bounds__(THREADS) void rms_norm_rows(NormParams p) {
 #pragma unroll
         for (int k = 0; k < VEC; ++k) {
             factor[k] = s[k] >= kMuch ? kDown : 1.f;
+            if (Q8 && threadIdx.x < LT) factors[at.column + k] = factor[k];
             s[k] = 0.f, most[k] = 0;
         }
         // read again, so that this costs the usual case no registers
@@ -325,22 +335,93 @@ __global__ __launch_bounds__(THREADS) void rms_norm_rows(NormParams p) {
         all();
     }
     float r[VEC], scale[VEC];
+    bool small = false;
 #pragma unroll
     for (int k = 0; k < VEC; ++k) {
-        r[k] = rsqrt_of(p, s[k], factor[k]);
+        const float root = rsqrt_of(p, s[k], factor[k]);
+        r[k] = factor[k] * root;
         if constexpr (Q8) {
             // `most` has the factor too
-            scale[k] = scale_of(most[k], r[k] / factor[k]);
+            scale[k] = scale_of(most[k], root);
+            small |= small_values(most[k], factor[k], r[k], scale[k]);
             r[k] = gain_of(most[k], factor[k], r[k], scale[k]);
         }
     }
-    if constexpr (Q8)
+    const auto store_scales = [&] {
         if (threadIdx.x < LT)
 #pragma unroll
             for (int k = 0; k < VEC; ++k)
                 if (k < at.room)
                     p.scale[(int64_t)at.n * p.T + at.t + k] = k < at.left ? scale[k] : 0.f;
+    };
+    if constexpr (Q8) {
+        store_scales();
+        // every wave has all columns, so all of the workgroup's agree
+        if (__builtin_amdgcn_ballot_w64(small) != 0) {
+            // the steps that need it: their largest |y|, and y / scale; the others as
+            // below.  All is formed anew, so that this costs the usual case no registers.
+            at.first = here(at.first);
+            at.t = (int)here((uint32_t)at.t);
+            all();
+            const bool down = overflows<E>() && told<WAVES>(large);
+            float by[VEC];
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) {
+                const float f = down ? factors[at.column + k] : 1.f, root = rsqrt_of(p, s[k], f);
+                scale[k] = scale_of(most[k], root);
+                by[k] = 1.f;
+                if (small_values(most[k], f, f * root, scale[k])) {
+                    r[k] = f * root;
+                    by[k] = 0.f;
+                    most[k] = 0;
+                }
+            }
+            const auto value = [&](const Steps<VEC, E> &b, uint32_t d, float(&v)[VEC]) {
+                b.widen(v);
+                const float w = weight(d);
+#pragma unroll
+                for (int k = 0; k < VEC; ++k) v[k] = v[k] * r[k] * w;
+            };
+#pragma unroll 1
+            for (uint32_t d = at.first; d < p.channels; d += ACROSS) {
+                Steps<VEC, E> b[1];
+                float v[VEC];
+                fetch_batch(d, b, Count<1>{}, false);
+                value(b[0], d, v);
+#pragma unroll
+                for (int k = 0; k < VEC; ++k)
+                    if (by[k] == 0.f) most[k] = larger(most[k], magnitude(v[k]));
+            }
+            wave_most<VEC, LT>(most);
+            __syncthreads();  // the sums have been read
+            if (threadIdx.x % kWave < LT)
+#pragma unroll
+                for (int k = 0; k < VEC; ++k) mosts[wave][at.column + k] = most[k];
+            __syncthreads();
+#pragma unroll
+            for (int k = 0; k < VEC; ++k)
+                if (by[k] == 0.f) {
+                    for (int w = 0; w < WAVES; ++w)
+                        most[k] = larger(most[k], mosts[w][at.column + k]);
+                    scale[k] = scale_of(most[k], 1.f);
+                    by[k] = 1.f / scale[k];
+                }
+            store_scales();
+#pragma unroll 1
+            for (uint32_t d = at.first; d < p.channels; d += ACROSS) {
+                Steps<VEC, E> b[1];
+                float v[VEC];
+                fetch_batch(d, b, Count<1>{}, false);
+                value(b[0], d, v);
+#pragma unroll
+                for (int k = 0; k < VEC; ++k) v[k] = k < at.left ? v[k] * by[k] : 0.f;
+                store_e4m3<VEC>(p.out8 + to(d), at.room, v);
+            }
+            return;
+        }
+    }
     at.first = here(at.first);
+    at.t = (int)here((uint32_t)at.t);
 #pragma unroll
     for (int j = 0; j < R; ++j) here(kept[j]);
     const auto finish = [&](const Steps<VEC, E> &b, uint32_t d) {
@@ -353,9 +434,9 @@ __global__ __launch_bounds__(THREADS) void rms_norm_rows(NormParams p) {
             if (k >= at.left) v[k] = 0.f;
         }
         if constexpr (Q8)
-            store_e4m3<VEC>(p.out8 + to + (int64_t)d * p.T, at.room, v);
+            store_e4m3<VEC>(p.out8 + to(d), at.room, v);
         else
-            seq::store_steps<VEC>(static_cast<E *>(p.out) + to + (int64_t)d * p.T, at.room, v);
+            seq::store_steps<VEC>(static_cast<E *>(p.out) + to(d), at.room, v);
     };
 #pragma unroll
     for (int j = 0; j < R; ++j) {
@@ -503,8 +584,9 @@ __global__ __launch_bounds__(THREADS) void rms_norm_rows_backward(NormParams p) 
         float r[VEC];
 #pragma unroll
         for (int k = 0; k < VEC; ++k) {
-            r[k] = rsqrt_of(p, s[k], factor[k]);
-            c[k] = c[k] * (r[k] / factor[k]) * p.per_channel;  // mean(g w s r)
+            const float root = rsqrt_of(p, s[k], factor[k]);
+            r[k] = factor[k] * root;
+            c[k] = c[k] * root * p.per_channel;  // mean(g w s r)
         }
         at.first = here(at.first);
 #pragma unroll
@@ -666,9 +748,42 @@ __global__ __launch_bounds__(kRowThreads) void rms_norm_dense(NormParams p) {
         }
         row_sums<WAVES>(s, unused, most, lds, lds_most);
     }
-    float r = rsqrt_of(p, s, factor);
+    const float root = rsqrt_of(p, s, factor);
+    float r = factor * root;
     if constexpr (Q8) {
-        const float scale = scale_of(most, r / factor);
+        float scale = scale_of(most, root);
+        if (small_values(most, factor, r, scale)) {  // the same in all of a row's threads
+            const auto value = [&](uint32_t i, float(&v)[VEC]) {
+                Steps<VEC, E> b;
+                float w[VEC];
+                fetch(i, b, false);
+                b.widen(v);
+                weights(i, w);
+#pragma unroll
+                for (int k = 0; k < VEC; ++k) v[k] = v[k] * r * w[k];
+            };
+            most = 0;
+#pragma unroll 1
+            for (uint32_t i = first; i < blocks; i += ACROSS) {
+                float v[VEC];
+                value(i, v);
+#pragma unroll
+                for (int k = 0; k < VEC; ++k) most = larger(most, magnitude(v[k]));
+            }
+            row_sums<WAVES>(s, unused, most, lds, lds_most);
+            scale = scale_of(most, 1.f);
+            const float by = 1.f / scale;
+            if (first == 0) p.scale[n] = counts ? scale : 0.f;
+#pragma unroll 1
+            for (uint32_t i = first; i < blocks; i += ACROSS) {
+                float v[VEC];
+                value(i, v);
+#pragma unroll
+                for (int k = 0; k < VEC; ++k) v[k] = counts ? v[k] * by : 0.f;
+                store_e4m3<VEC>(p.out8 + to + (int64_t)i * VEC, (int)p.channels - (int)i * VEC, v);
+            }
+            return;
+        }
         if (first == 0) p.scale[n] = counts ? scale : 0.f;
         r = gain_of(most, factor, r, scale);
     }
@@ -763,8 +878,8 @@ __global__ __launch_bounds__(kRowThreads) void rms_norm_dense_backward(NormParam
             s = c = 0.f;
             all_channels(factor);
         }
-        const float r = rsqrt_of(p, s, factor);
-        c = c * (r / factor) * p.per_channel;
+        const float root = rsqrt_of(p, s, factor), r = factor * root;
+        c = c * root * p.per_channel;
         const auto finish = [&](const Steps<VEC, E> &xb, const Steps<VEC, E> &gb, uint32_t i,
                                 float(&total)[VEC]) {
             float v[VEC], g[VEC], w[VEC], more[VEC] = {};

@@ -678,9 +678,10 @@ rlca_status rlca_gated_step(const rlca_gated_step_call *call, hipStream_t stream
  * step, for an 8-bit matrix product: scale = max(max over channels of |y| / 448,
  * 2^-120), out8 = y / scale rounded to nearest even.  Squares and sums are float32,
  * and are scaled down where they would overflow.  Steps past a row's length get
- * output, sum, scale and gradient 0.  T = 1 with x_stride_channel = 1 (and the
- * residual's and gradients' too) is the norm of dense rows of channels: a generated
- * token's, or any [tokens, channels] array's.  eps is within 1e-30 .. 1e30. */
+ * output, sum, scale and gradient 0; with no channels all scales are 0.  T = 1 with
+ * x_stride_channel = 1 (and the residual's and gradients' too) is the norm of dense
+ * rows of channels: a generated token's, or any [tokens, channels] array's.  eps is
+ * within 1e-30 .. 1e30. */
 typedef struct {
     int64_t num_seqs, channels, T;
     int32_t dtype;

@@ -944,6 +944,17 @@ __global__ __launch_bounds__(kSumWaves *kWave) void rms_norm_sums(SumParams p) {
     p.out[d] = sum;
 }
 
+// With no channels: the scales.
+struct EmptyParams {
+    float *scale;
+    uint64_t count;
+};
+
+__global__ __launch_bounds__(256) void rms_norm_empty(EmptyParams p) {
+    for (uint64_t i = blockIdx.x * 256ull + threadIdx.x; i < p.count; i += gridDim.x * 256ull)
+        p.scale[i] = 0.f;
+}
+
 // ------------------------------------------------------------------- host side
 // How a call is launched.
 struct Shape {
@@ -1100,9 +1111,16 @@ rlca_status rlca_rms_norm(const rlca_norm_call *call, hipStream_t stream) {
          {{N, c.residual_stride_seq}, {D, c.residual_stride_channel}, {T, 1}});
     a.out(c.out, e, false, {{N, D * T}, {D, T}, {T, 1}});
     a.out(c.out8, 1, false, {{N, D * T}, {D, T}, {T, 1}});
-    a.out(c.scale, 4, c.out8 != nullptr, {{D == 0 ? 0 : N, T}, {T, 1}});
+    a.out(c.scale, 4, c.out8 != nullptr, {{N, T}, {T, 1}});
     a.out(c.sum, e, c.residual != nullptr, {{N, D * T}, {D, T}, {T, 1}});
-    if ((st = a.status()) != RLCA_OK || N * D == 0 || T == 0) return st;
+    if ((st = a.status()) != RLCA_OK || N == 0 || T == 0) return st;
+    if (D == 0) {
+        if (c.scale == nullptr) return RLCA_OK;
+        EmptyParams p = {c.scale, (uint64_t)N * T};
+        const uint64_t blocks = (p.count + 255) / 256;
+        return launch((const void *)rms_norm_empty, dim3((uint32_t)(blocks < 4096 ? blocks : 4096)),
+                      256, 0, p, stream);
+    }
     const Shape s = shape_of(c, false);
     NormParams p = params_of(c, s);
     const bool q8 = c.out8 != nullptr;

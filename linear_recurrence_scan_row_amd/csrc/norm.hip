@@ -919,29 +919,34 @@ __global__ __launch_bounds__(kRowThreads) void rms_norm_dense_backward(NormParam
         }
 }
 
-// The walkers' sums in order: a workgroup takes 64 channels, its 16 waves every 16th
-// walker each.
+// The walkers' sums in order: a workgroup takes 64 channels (and, of more than 2^26, more
+// of them: a launch holds fewer than 2^32 threads), its 16 waves every 16th walker each.
 struct SumParams {
     const float *partials;
     float *out;
     uint32_t walkers, channels;
 };
 constexpr int kSumWaves = 16;
+constexpr uint32_t kSumGroups = 1u << 20;
 
 __global__ __launch_bounds__(kSumWaves *kWave) void rms_norm_sums(SumParams p) {
     __shared__ float sums[kSumWaves][kWave];
     const uint32_t wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
-    const uint32_t d = blockIdx.x * kWave + lane;
-    float sum = 0.f;
-    if (d < p.channels)
+    for (uint32_t first = blockIdx.x * kWave; first < p.channels; first += gridDim.x * kWave) {
+        const uint32_t d = first + lane;
+        float sum = 0.f;
+        if (d < p.channels)
 #pragma unroll 8
-        for (uint32_t w = wave; w < p.walkers; w += kSumWaves)
-            sum += p.partials[(int64_t)w * p.channels + d];
-    sums[wave][lane] = sum;
-    __syncthreads();
-    if (wave != 0 || d >= p.channels) return;
-    for (int w = 1; w < kSumWaves; ++w) sum += sums[w][lane];
-    p.out[d] = sum;
+            for (uint32_t w = wave; w < p.walkers; w += kSumWaves)
+                sum += p.partials[(int64_t)w * p.channels + d];
+        __syncthreads();  // the channels before have been read
+        sums[wave][lane] = sum;
+        __syncthreads();
+        if (wave == 0 && d < p.channels) {
+            for (int w = 1; w < kSumWaves; ++w) sum += sums[w][lane];
+            p.out[d] = sum;
+        }
+    }
 }
 
 // With no channels: the scales.
@@ -1166,7 +1171,8 @@ rlca_status rlca_rms_norm_backward(const rlca_norm_call *call, void *workspace,
     }
     if (c.grad_weight == nullptr) return RLCA_OK;
     SumParams sum = {static_cast<const float *>(workspace), c.grad_weight, walkers, (uint32_t)D};
-    return launch((const void *)rms_norm_sums, dim3((uint32_t)((D + kWave - 1) / kWave)),
+    const uint32_t groups = (uint32_t)((D + kWave - 1) / kWave);
+    return launch((const void *)rms_norm_sums, dim3(groups < kSumGroups ? groups : kSumGroups),
                   kSumWaves * kWave, 0, sum, stream);
 }
 

@@ -608,7 +608,10 @@ rlca_status rlca_clip_grad_norm(const rlca_grad_tensor *tensors, int64_t num_ten
  *   L_t = scale softplus(decay) r_t,  a_t = exp(-L_t),
  *   h_t = a_t h_{t-1} + sqrt(1 - a_t^2) i_t x_t      (h_{t-1} = 0 at a start);
  * out_t is h_t, rounded once.  A state decays at every step and cannot grow; a_t is
- * float32, so steps with L_t below 1e-7 do not decay.  The checkpoints (nullable)
+ * float32, so steps with L_t below 1e-7 do not decay.  An infinite state does not stay
+ * infinity for certain: where a run's decays multiply to less than float32 holds, 0
+ * times it is NaN.  Either stays, in the states and back through the gradients, until
+ * an episode starts.  The checkpoints (nullable)
  * are the states that the backward call starts from.  scale is within 1e-30 ..
  * 1e30, channels below 2^25.  The workspaces need no initialisation; the forward
  * call's may be of size 0. */

@@ -34,7 +34,7 @@ struct NormParams {
     float *scale;
     float *partials;  // [workgroups or waves][channels]: sums for grad_weight
     int64_t x_n, x_d, r_n, r_d, g_n, g_d, s_n, s_d;
-    uint32_t num_seqs, channels;
+    uint32_t channels;
     int32_t T;
     uint32_t tiles;       // of a sequence
     uint32_t work;        // tiles, or rows, of the call
@@ -1063,7 +1063,6 @@ static NormParams params_of(const rlca_norm_call &c, const Shape &s) {
     p.r_n = c.residual_stride_seq, p.r_d = c.residual_stride_channel;
     p.g_n = c.grad_stride_seq, p.g_d = c.grad_stride_channel;
     p.s_n = c.grad_sum_stride_seq, p.s_d = c.grad_sum_stride_channel;
-    p.num_seqs = (uint32_t)c.num_seqs;
     p.channels = (uint32_t)c.channels;
     p.T = (int32_t)c.T;
     p.tiles = (uint32_t)(s.dense ? 1 : s.tiles);

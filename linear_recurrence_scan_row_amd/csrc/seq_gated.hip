@@ -45,7 +45,7 @@ struct GateParams {
     float *maps;      // [num_seqs][chunks][2][channels]: each chunk's map
     float *partials;  // [walkers * WAVES][3][channels]: sums for decay, decay_bias, input_bias
     int64_t x_n, x_d, ig_n, ig_d, dg_n, dg_d, g_n, g_d;
-    uint32_t num_seqs, channels;
+    uint32_t channels;
     uint32_t groups;      // waves that share a sequence's channels
     uint32_t walkers;     // waves (or workgroups) that share a group's sequences and chunks
     uint32_t units;       // num_seqs * chunks
@@ -649,7 +649,6 @@ struct GateSums {
     const float *partials, *decay;
     float *grad_decay, *grad_rate, *grad_input;
     uint32_t walkers, channels;
-    float scale;
 };
 constexpr int kGateSumWaves = 16;
 
@@ -823,7 +822,6 @@ static GateParams gate_params(const rlca_gated_call &c, const GatePlan &g) {
     p.ig_n = c.input_stride_seq, p.ig_d = c.input_stride_channel;
     p.dg_n = c.decay_stride_seq, p.dg_d = c.decay_stride_channel;
     p.g_n = c.grad_stride_seq, p.g_d = c.grad_stride_channel;
-    p.num_seqs = (uint32_t)c.num_seqs;
     p.channels = (uint32_t)c.channels;
     p.groups = (uint32_t)g.groups;
     p.walkers = (uint32_t)g.walkers;

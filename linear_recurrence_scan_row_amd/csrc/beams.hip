@@ -422,7 +422,18 @@ __global__ __launch_bounds__(kThreads) void beam_merge(SelectParams p) {
             };
             const Candidate mine = one(tid);
             uint32_t rank = 0;
-            for (uint32_t i = 0; i < n; ++i) rank += one(i).before(mine, p.by_vocab) ? 1u : 0u;
+            bool by_logit = false;  // equal totals of unequal logits: hardly ever
+            for (uint32_t i = 0; i < n; ++i) {
+                const Candidate c = one(i);
+                const bool equal = c.order == mine.order;
+                rank += c.order > mine.order || (equal && c.index < mine.index) ? 1u : 0u;
+                by_logit |= equal && c.logit != mine.logit;
+            }
+            if (by_logit) {
+                rank = 0;
+                for (uint32_t i = 0; i < n; ++i)
+                    rank += one(i).before(mine, p.by_vocab) ? 1u : 0u;
+            }
             if (rank < p.picks) choose(mine, rank);
         }
         n = n < p.picks ? n : p.picks;

@@ -970,6 +970,7 @@ struct Shape {
 };
 
 constexpr int64_t kBackwardGroups = 512;  // workgroups that walk in the backward call
+constexpr int64_t kCompute = 256;         // compute units
 
 static Shape shape_of(const rlca_norm_call &c, bool backward) {
     Shape s = {};
@@ -997,11 +998,14 @@ static Shape shape_of(const rlca_norm_call &c, bool backward) {
     // 128 bytes of a channel's steps side by side, a whole cache line (64 bytes: 78 us
     // against 58 forward and 101 against 80 backward for 8x2048 channels of 2048 steps,
     // bf16 with residual).  64 with more channels than registers hold then (4096 of 1024
-    // steps: 70 against 94, and 99 against 115), or with fewer tiles than compute units
-    // (1x2048 channels of 4096 steps: 22 against 27), unless they share lines for want of
-    // alignment (6x1536 of 2049 steps 45 against 38).  16 where tiles are fewest (2048 of
-    // 512 steps: 10.8 against 13.5 and 20; not for 64 of 1024: 6.5 against 4.6).
-    const bool few = N * tiles(8) < 256 && T % (4 * vec) == 0;
+    // steps: 70 against 94, and 99 against 115), or where even those make no more
+    // workgroups than there are compute units, one on each: 1x2048 channels of 8192 steps,
+    // 256 of them, 27.0 against 29.7, and of 8256, with two more, 38.0 against 29.4; with
+    // gradients 35.6 against 41.5 and 50.8 against 39.8.  (So it is wherever rows begin:
+    // 8191 steps 54.0 against 58.8, 6x1536 of 2049, 390 workgroups, 38.2 against 30.2.)
+    // 16 where tiles are fewest (2048 of 512 steps: 10.8 against 13.5 and 20; not for 64 of
+    // 1024: 6.5 against 4.6).
+    const bool few = N * tiles(4) <= kCompute;
     s.lanes = D <= 512 ? 8 : N * tiles(4) < 64 ? 1 : D <= 2048 && !few ? 8 : 4;
     s.threads = s.lanes != 8 || D > 512 ? 1024 : D > 128 ? 512 : 256;
     s.tiles = tiles(s.lanes);

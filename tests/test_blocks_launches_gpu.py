@@ -93,7 +93,8 @@ def test_gated_step_walks_sequences(slots, dtype, gpu_device):
 
 # (sequences, channels, steps by type): tiles of 4 x 16 bytes of a channel's steps, for few
 # whole rows and for many channels; and those and wider ones that walk in the backward call
-ROWS = [((4, 600), {4: 512, 2: 1024}, False), ((5, 2100), {4: 230, 2: 460}, False),
+ROWS = [((4, 600), {4: 512, 2: 1024}, False), ((4, 601), {4: 515, 2: 1027}, False),
+        ((5, 530), {4: 832, 2: 1664}, False), ((5, 2100), {4: 230, 2: 460}, False),
         ((600, 2100), {4: 5, 2: 5}, True), ((600, 520), {4: 7, 2: 7}, True),
         ((9, 530), {4: 1900, 2: 3700}, True), ((600, 300), {4: 9, 2: 9}, True),
         ((600, 100), {4: 9, 2: 9}, True)]

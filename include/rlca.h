@@ -678,13 +678,14 @@ rlca_status rlca_gated_step(const rlca_gated_step_call *call, hipStream_t stream
  *   y = s / sqrt(mean over channels of s^2 + eps) * weight.
  * s is the residual stream that goes on, and it is normed as it is stored.  The
  * output is y in the storage type, or in 8 bits (OCP e4m3) with one float32 scale a
- * step, for an 8-bit matrix product: scale = max(max over channels of |y| / 448,
- * 2^-120), out8 = y / scale rounded to nearest even.  Squares and sums are float32,
- * and are scaled down where they would overflow.  Steps past a row's length get
- * output, sum, scale and gradient 0; with no channels all scales are 0.  T = 1 with
- * x_stride_channel = 1 (and the residual's and gradients' too) is the norm of dense
- * rows of channels: a generated token's, or any [tokens, channels] array's.  eps is
- * within 1e-30 .. 1e30. */
+ * step: scale = max(max over channels of |y| / 448, 2^-120), out8 = y / scale rounded
+ * to nearest even.  Squares and sums are float32, and are scaled down where they would
+ * overflow.  Steps past a row's length get output, sum, scale and gradient 0; with no
+ * channels all scales are 0.  T = 1 with x_stride_channel = 1 (and the residual's and
+ * gradients' too) is the norm of dense rows of channels: a generated token's, or any
+ * [tokens, channels] array's.  Their 8-bit output is what an 8-bit matrix product takes
+ * as it is; in rows over time a step's channels lie T apart, and a product that wants
+ * them side by side takes a transposed copy.  eps is within 1e-30 .. 1e30. */
 typedef struct {
     int64_t num_seqs, channels, T;
     int32_t dtype;
@@ -722,8 +723,8 @@ rlca_status rlca_rms_norm_backward(const rlca_norm_call *call, void *workspace,
  *   total = score_b + (logit_bv - log sum_v exp(logit_bv)),
  * best first, equal ones by beam (the lower first), those of one beam by logit and then
  * token (the lower first).  Exponentials are float32, their sums over a beam and the
- * totals float64: totals are good to 1e-6, and they are compared before the one
- * rounding to float32.  A beam that is finished has one candidate, pad_token
+ * totals float64: totals are good to 2e-6 and usually to 1e-7, and they are compared
+ * before the one rounding to float32.  A beam that is finished has one candidate, pad_token
  * at its own score; its other totals are -infinity.  So are all totals of a beam
  * whose score is -infinity (an unused one: its logits do not count, whatever they
  * hold) and those of logits of -infinity (tokens that are not allowed; all of them

@@ -333,9 +333,11 @@ def rms_norm(x, weight=None, residual=None, eps=1e-6, lengths=None, total=None, 
 
 def rms_norm_8bit(x, weight=None, residual=None, eps=1e-6, lengths=None, total=None, out=None,
                   scale=None):
-    """rms_norm with its output in 8 bits for a matrix product: (out, scale, s), out
-    float8_e4m3fn like x, scale [num_seqs, T] (or [num_seqs]) float32, the largest
-    magnitude of a step's channels / 448, so that out * scale is the norm."""
+    """rms_norm with its output in 8 bits: (out, scale, s), out float8_e4m3fn like x,
+    scale [num_seqs, T] (or [num_seqs]) float32, the largest magnitude of a step's
+    channels / 448 (at least 2^-120), so that out * scale is the norm.  [tokens,
+    channels] goes into an 8-bit matrix product as it is; of rows over time, whose
+    steps' channels lie T apart, such a product wants a transposed copy."""
     return _norm(x, weight, residual, eps, lengths, total, out, scale, True)
 
 

@@ -7,7 +7,10 @@
 // its exponentials and its best logits: the K-th largest of the threads' own largest
 // logits is a bound that at least K logits reach, and few more than K do, so only
 // those are ranked.  A second launch forms the beams' sums and takes the best of the
-// chunks' best, in float64.
+// chunks' best, in float64.  A thread's exponentials and their sum, of up to 24, are
+// float32: at most 2e-6 off, relative, in all 24 roundings' worst case, and about 1e-8
+// over a beam's threads, so only beams whose totals lie that close can change places.
+// (Exponentials in float64: 64 searches of 8 beams and 100003 tokens, bf16, 55 us for 29.)
 //
 // Reordering: bound by the states that have to move.  A parent's first child keeps its
 // place, so only further children's states are copied, to the places of beams without

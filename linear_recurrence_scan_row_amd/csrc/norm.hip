@@ -12,11 +12,12 @@
 // channels (T = 1) take a wave or a workgroup a row.
 //
 // Measured, where a large copy reaches 5.05 TB/s: 8x2048 channels of 2048 steps bf16 with
-// residual 58 to 63 us (4.6 to 4.3 TB/s), gradients 70 (285 MB read for the 201 of the
-// inputs: not all of both arrays stays in registers; 5.1 TB/s); prompts of 6x1536x2049
-// fp16 to 8 bits, of different lengths, 39 (2.9: rows that begin at any 2 bytes, and
-// fewer tiles than compute units); 4096x64 of 128 steps fp32 107 (5.0); one row of 4096
-// channels 3.8.
+// residual 43 us and gradients 62, each alone in a row, where part of the arrays stays in
+// the last-level cache, 63 and 71 in turn (4.3 and 5.0 TB/s; the gradients read 286 MB for
+// the 201 of the inputs, since not all of both arrays stays in registers); prompts of
+// 6x1536x2049 fp16 to 8 bits, of different lengths, 37 to 47 (rows that begin at any 2
+// bytes, and fewer tiles than compute units); 4096x64 of 128 steps fp32 107 (5.0).  Dense
+// rows: one of 4096 channels 3.8; 16384 of 2048, bf16 with residual, 43 and 71 + 8, alone.
 #include "seq.hpp"
 
 namespace rlca {
@@ -1026,10 +1027,9 @@ static const void *forward_kernel(const Shape &s) {
                               : (const void *)rms_norm_rows<E, 1024, 1, 4, Q8>;
 }
 
-// Both arrays of the backward call do not fit the registers from 1024 channels on; few
-// are kept there, since what is read again matters less than waves to hide it (2048
-// channels: 2 blocks a thread 80 us, 6 77, which is what fits 1024 threads; 16 with half
-// the threads 83).
+// Both arrays of the backward call do not fit the registers from 1024 channels on, of
+// which 1024 threads take all; as many blocks are kept as fit (8x2048 channels of 2048
+// steps, bf16, alone in a row: 2 blocks a thread 67 us, 6 62).
 template <typename E>
 static const void *backward_kernel(const Shape &s) {
     if (s.dense)

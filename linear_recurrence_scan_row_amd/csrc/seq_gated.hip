@@ -17,7 +17,9 @@
 // Bound by memory: three or four values are read for each that is computed, beside 5
 // transcendental instructions and about 26 others a step forward (5 and 67 backward),
 // whose issue takes as long as the bytes where values have 16 bits.  Measured: 8x2048
-// channels of 2048 steps bf16 forward 52 to 62 us (5.1 to 4.3 TB/s), gradients 87 (5.4);
+// channels of 2048 steps bf16 forward 54 us and gradients 99 (5.0 and 4.7 TB/s), each
+// alone, 62 and 87 (4.3 and 5.4) in turn, where the gradients find the forward call's
+// inputs in the last-level cache;
 // 4096x64 of 128 steps fp32 with flags 112 and 179 (4.8 and 5.3); one row set of 512x65535
 // bf16 58 (4.6); a step of 512x8192 bf16 13 to 14 (5.1 to 4.6); a large copy reaches
 // 5.05 TB/s.
@@ -66,9 +68,10 @@ __device__ __forceinline__ float slow_of(float scale, float decay) {
 
 // A step's a = exp(-L) and 1 - a^2 = (1 - a)(1 + a).  Near L = 0 the difference 1 - a
 // would lose digits, so up to 1/2 it is L times the polynomial that interpolates
-// (1 - exp(-L)) / L there at 6 Chebyshev points (error 1.5e-9), and a is 1 minus it;
-// from there on a is the exponential, and the difference of at least 0.39 loses none.
-// SLOW: no L of the wave's channels is above 1/8, where 4 points do (error 3.2e-8).
+// (1 - exp(-L)) / L there at 6 Chebyshev points (error 2.6e-9, with its coefficients in
+// float32), and a is 1 minus it; from there on a is the exponential, and the difference
+// of at least 0.39 loses none.  SLOW: no L of the wave's channels is above 1/8, where 4
+// points do (error 3.1e-8).
 constexpr float kSlow = 0.125f;
 template <bool SLOW>
 __device__ __forceinline__ void decay_of(float L, float &a, float &rest) {
@@ -740,9 +743,9 @@ __global__ __launch_bounds__(kGateStepThreads) void gated_step(GateStepParams p)
 // ------------------------------------------------------------------- host side
 // How a call is launched.  Rows of up to 8 steps take a lane, up to 32 four, others 16,
 // or a whole wave where its wider tiles waste less than a fifth more lanes at the row's
-// end (8x2048 channels of 2048 steps, bf16: forward 53 us against 63, gradients 99
-// against 113; 32x1024 of 600 steps the other way 57 against 41 and 87 against 67), or
-// where waves are few, up to kFewWaves of 16-lane rows.  From kFewRows rows down the
+// end (8x2048 channels of 2048 steps, bf16, each call alone in a row: forward 54 us
+// against 58, gradients 99 against 131; 32x1024 of 600 steps the other way 55 against 37
+// and 86 against 69), or where waves are few, up to kFewWaves of 16-lane rows.  From kFewRows rows down the
 // kShared waves of a workgroup share a row (512 rows of 65535 steps: 71 us against 198
 // apart and 114 in chunks; 4096 rows of 8191 steps 74 against 56 apart); from
 // kFewestRows down rows are cut into chunks of at least kFewestTiles tiles, at most

@@ -1123,7 +1123,7 @@ rlca_status rlca_rms_norm(const rlca_norm_call *call, hipStream_t stream) {
     a.out(c.sum, e, c.residual != nullptr, {{N, D * T}, {D, T}, {T, 1}});
     if ((st = a.status()) != RLCA_OK || N == 0 || T == 0) return st;
     if (D == 0) {
-        if (c.scale == nullptr) return RLCA_OK;
+        if (c.scale == nullptr || c.out != nullptr) return RLCA_OK;
         EmptyParams p = {c.scale, (uint64_t)N * T};
         const uint64_t blocks = (p.count + 255) / 256;
         return launch((const void *)rms_norm_empty, dim3((uint32_t)(blocks < 4096 ? blocks : 4096)),
